@@ -1,4 +1,4 @@
-"""Build libdan.so (the CUDA kernels behind the C ABI in include/dan.h).
+"""Build libdan.so (the CUDA kernels behind the C ABI in include/).
 
 nvcc compiles each translation unit for sm_103a in parallel, then links one
 shared library in the package directory.  Numerics flags: -fmad=false (no
@@ -18,8 +18,10 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdan.so")
 SOURCES = ["dan_rows_rms.cu", "dan_rows_gated.cu", "dan_rows_ln.cu", "dan_rows_lnfp8.cu",
-           "dan_rows_gatedln.cu", "dan_qk.cu", "dan_resid_t.cu", "dan_abi.cu", "dan_noalloc.cu"]
-HEADERS = ["dan_device.cuh", "dan_internal.h", "dan_ring.cuh", "dan_rows.cuh"]
+           "dan_rows_gatedln.cu", "dan_qk.cu", "dan_resid_t.cu", "dan_abi.cu", "dan_noalloc.cu",
+           "dan_cache_rope.cu", "dan_attn_step.cu", "dan_cache_abi.cu"]
+HEADERS = ["dan_device.cuh", "dan_internal.h", "dan_ring.cuh", "dan_rows.cuh",
+           "dan_attn.cuh", "dan_attn_tma.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NUMERICS = ["-fmad=false", "-prec-div=true", "-prec-sqrt=true", "-ftz=false"]
@@ -39,7 +41,8 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps += [os.path.join(ROOT, "include", "dan.h"), os.path.abspath(__file__)]
+    deps += [os.path.join(ROOT, "include", h) for h in ("dan.h", "dan_cache.h")]
+    deps += [os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -1,0 +1,194 @@
+// dan_attn.cuh -- what the paged-cache operators share: their problems as
+// the shim validated them, which keys a query row sees, how a sequence's
+// keys are split, and the partial results of the splits.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace dan {
+
+constexpr unsigned kStatusIndex = 8u; // an index in a caller's array was out of its range
+
+inline int page_shift(int64_t page_size)
+{
+    int s = 0;
+    while ((int64_t(1) << s) < page_size) ++s;
+    return s;
+}
+
+struct CacheRopeProblem {
+    const void *q, *k, *v;
+    int64_t N, q_stride, kv_stride, heads, kv_heads, head_dim;
+    const void *wq, *wk;
+    const float *rope;
+    int64_t table_rows;
+    const int32_t *positions, *slots;
+    float eps;
+    bool neox;
+    void *q_out;
+    int64_t qo_stride;
+    void *k_cache, *v_cache;
+    int64_t num_pages, page_size;
+};
+
+struct AttnProblem {
+    const void *q;
+    int64_t N, q_stride;
+    const void *k_cache, *v_cache;
+    int64_t num_pages, page_size;
+    const int32_t *page_table;
+    int64_t table_stride, max_pages;
+    const int32_t *q_start, *kv_len;
+    int64_t S, heads, kv_heads, head_dim, window, sinks, chunk, max_q;
+    float scale;
+    void *out;
+    float *lse;
+    void *workspace;
+};
+
+cudaError_t launch_qk_norm_rope_cache(const CacheRopeProblem &p, cudaStream_t s);
+cudaError_t launch_window_attention(const AttnProblem &p, cudaStream_t s);
+int64_t window_attention_workspace(int64_t N, int64_t S, int64_t heads, int64_t kv_heads,
+                                   int64_t head_dim, int64_t max_pages, int64_t page_size,
+                                   int64_t max_q);
+
+// Launch with programmatic stream serialization (see launch_overlapped) on a
+// two-dimensional grid.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_overlapped_2d(void (*fn)(KArgs...), dim3 grid, int block, int smem,
+                                 cudaStream_t s, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+// ----------------------------------------------------------- device side
+
+struct AttnParams {
+    const uint4 *q;
+    int64_t N, q_stride8; // query row stride in 16-byte fragments
+    const int32_t *table;
+    int64_t table_stride;
+    int max_pages, num_pages, page_shift;
+    const int32_t *q_start, *kv_len;
+    int S, H, Hkv, g; // g = H / Hkv query heads share a key head
+    int window, sinks, chunk;
+    int max_q;
+    float scale_log2; // scale * log2(e): the softmax is taken in base 2
+    uint4 *out;
+    float *lse;
+    // partial results (see PartLayout)
+    float *part_o;
+    float2 *part_ml;
+    int64_t part_cap; // rows of a (sequence, key head), or 0: rows by query token
+    unsigned *status;
+    unsigned long long limit_ns;
+};
+
+// A sequence as the arrays say it, with what is out of range cut off; n == 0
+// where nothing is to be done.
+struct SeqInfo {
+    int q0, n, L;
+    bool bad; // an entry was out of its range
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const AttnParams &p, int s)
+{
+    SeqInfo q;
+    const int a = __ldg(p.q_start + s), b = __ldg(p.q_start + s + 1);
+    int L = __ldg(p.kv_len + s);
+    const int cap = p.max_pages << p.page_shift;
+    q.bad = L < 0 || L > cap;
+    q.L = L < 0 ? 0 : L > cap ? cap : L;
+    q.q0 = a;
+    q.n = b - a;
+    if (a < 0 || b < a || b > p.N || q.n > p.max_q) {
+        q.bad = true;
+        q.n = 0;
+    }
+    return q;
+}
+
+// Keys that the query at position `pos` sees: [0, sink) and [lo, hi).
+struct RowRange {
+    int sink, lo, hi;
+};
+
+__device__ __forceinline__ RowRange row_range(const AttnParams &p, int pos, int L)
+{
+    RowRange r = {0, 0, 0};
+    if (pos < 0) return r;
+    const int p0 = pos - pos % p.chunk;
+    r.hi = min(L, p0 + p.chunk);
+    r.sink = min(p.sinks, r.hi);
+    r.lo = p.window ? min(r.hi, max(0, p0 + 1 - p.window)) : r.hi;
+    return r;
+}
+
+// Keys that some query at positions first..last of one sequence sees.  The
+// ranges of successive positions overlap or touch (lo never passes the
+// previous hi when there is a window), so their union is again [0, sink) and
+// [lo, hi).
+__device__ __forceinline__ RowRange rows_union(const AttnParams &p, int first, int last, int L)
+{
+    if (last < 0) return RowRange{0, 0, 0};
+    RowRange r = row_range(p, last, L);
+    if (p.window) r.lo = row_range(p, max(first, 0), L).lo;
+    return r;
+}
+
+// The union's keys in blocks of 2^SHIFT, each block once: the sinks' blocks
+// from 0, then the window's.
+template <int SHIFT>
+struct KeyBlocks {
+    int nsink, first, count; // block i is i < nsink ? i : i - nsink + first
+    __device__ __forceinline__ explicit KeyBlocks(const RowRange &r)
+    {
+        constexpr int M = (1 << SHIFT) - 1;
+        nsink = (r.sink + M) >> SHIFT;
+        first = max(r.lo >> SHIFT, nsink);
+        const int end = r.lo < r.hi ? (r.hi + M) >> SHIFT : 0;
+        count = nsink + max(0, end - first);
+    }
+    __device__ __forceinline__ int block(int i) const { return i < nsink ? i : i - nsink + first; }
+};
+
+// How a step sequence's keys are split: by its own number of blocks alone, so
+// that a row's bits do not depend on the batch.  Splits of at least 256 keys,
+// at most 32 of them.
+constexpr int kStepRows = 16;     // query rows (tokens x g) that the step kernel takes
+constexpr int kStepShift = 4;     // its key blocks: 16 keys, the smallest page
+constexpr int kMaxSplits = 32;
+constexpr int kStepMinBlocks = 256 >> kStepShift;
+
+__device__ __forceinline__ int step_split_blocks(int count)
+{
+    const int b = (count + kMaxSplits - 1) / kMaxSplits;
+    return b < kStepMinBlocks ? kStepMinBlocks : b;
+}
+
+// First partial row of (sequence, key head); its rows are [split][row].  With
+// part_cap each has room for part_cap rows; otherwise room goes by the query
+// rows, H * kMaxSplits for each.
+__device__ __forceinline__ int64_t part_base(const AttnParams &p, int s, const SeqInfo &q, int u)
+{
+    if (p.part_cap) return ((int64_t)s * p.Hkv + u) * p.part_cap;
+    return ((int64_t)q.q0 * p.H + (int64_t)u * q.n * p.g) * kMaxSplits;
+}
+
+// Launch the step kernel and, where a sequence may be split, the join.
+cudaError_t launch_attention_step(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
+                                  const CUtensorMap &vmap, int splits, cudaStream_t s);
+
+} // namespace dan

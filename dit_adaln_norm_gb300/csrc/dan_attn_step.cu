@@ -1,0 +1,345 @@
+// dan_attn_step.cu -- attention over the paged cache for sequences with few
+// query rows (n_s * heads/kv_heads <= 16): a decoded token, or a few drafted
+// ones; and the join of split results.
+//
+// Mathematics: o = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m) with
+// x_j = scale * log2(e) * q.k_j and a running maximum m, one pass over the
+// keys.  Every key and value is read once for all query heads that share it;
+// at 16 rows the arithmetic per byte is small and the bound is memory.
+//
+// One CTA has one (sequence, key head, tile of 16 rows, split).  Its four warps take blocks of
+// 16 keys in turn, each with its own ring of TMA-filled slots, its own running
+// maximum, sum and output; nothing but the end joins them.  The 16 query rows
+// are the rows of m16n8k16 products.  TMA brings a block's K and V with the
+// 128-byte swizzle, so that the matrix loads are free of bank conflicts.
+#include "dan_device.cuh"
+#include "dan_internal.h"
+#include "dan_attn.cuh"
+#include "dan_attn_tma.cuh"
+#include "dan_ring.cuh"
+
+namespace dan {
+
+constexpr int kStepWarps = 4;
+constexpr int kStepSlots = 3;
+constexpr int kStepKeys = 1 << kStepShift;
+
+template <int HD>
+struct StepShape {
+    static constexpr int HALVES = HD / 64;               // 128-byte columns of a row
+    static constexpr int HALF = kStepKeys * 128;         // bytes of one box
+    static constexpr int TILE = HALVES * HALF;           // K or V of a block
+    static constexpr int SLOT = 2 * TILE;
+    static constexpr int RING = kStepWarps * kStepSlots * SLOT;
+    static constexpr int SMEM = RING + kStepWarps * kStepSlots * 8 + kStepWarps * 16 * 8 + 1024;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(32 * kStepWarps)
+    window_attention_step_kernel(const AttnParams p, int tiles, const __grid_constant__ CUtensorMap kmap,
+                                 const __grid_constant__ CUtensorMap vmap)
+{
+    using Sh = StepShape<HD>;
+    using Pipe = WarpPipe<kStepSlots>;
+    constexpr int KS = HD / 16; // products over the head's columns
+    constexpr int NT = HD / 8;  // output column tiles
+    extern __shared__ char smem_raw[];
+    char *ring = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + Sh::RING);
+    float2 *s_ml = reinterpret_cast<float2 *>(full + kStepWarps * kStepSlots);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStepWarps * kStepSlots; ++i) mbar_init(full + i, 1);
+        mbar_init_fence();
+    }
+    grid_dependency_wait();
+    allow_dependents();
+
+    const int u = blockIdx.x % p.Hkv;
+    const int tile = blockIdx.x / p.Hkv % tiles, s = blockIdx.x / p.Hkv / tiles, split = blockIdx.y;
+    const SeqInfo q = seq_info(p, s);
+    if (q.bad && split == 0 && u == 0 && tile == 0 && threadIdx.x == 0)
+        set_status(p.status, kStatusIndex);
+    const int64_t R64 = (int64_t)q.n * p.g - (int64_t)tile * kStepRows;
+    if (R64 <= 0) return;
+    const bool few = (int64_t)q.n * p.g <= kStepRows;
+    const int R = R64 < kStepRows ? (int)R64 : kStepRows, rb = tile * kStepRows;
+    const int pos0 = q.L - q.n;
+    const RowRange all = rows_union(p, pos0 + rb / p.g, pos0 + (rb + R - 1) / p.g, q.L);
+    const KeyBlocks<kStepShift> kb(all);
+    const int per = few ? step_split_blocks(kb.count) : max(1, kb.count);
+    const int nsplit = max(1, (kb.count + per - 1) / per);
+    if (split >= nsplit) return;
+    const int b0 = split * per, b1 = min(kb.count, b0 + per);
+
+    // the lane's two rows of the products, and its two columns of each tile
+    const int r0 = lane >> 2, r1 = r0 + 8, c2 = (lane & 3) * 2;
+    const RowRange rr0 = r0 < R ? row_range(p, pos0 + (rb + r0) / p.g, q.L) : RowRange{0, 0, 0};
+    const RowRange rr1 = r1 < R ? row_range(p, pos0 + (rb + r1) / p.g, q.L) : RowRange{0, 0, 0};
+
+    uint32_t qf[KS][4];
+    {
+        const uint32_t *qb = reinterpret_cast<const uint32_t *>(p.q);
+        const int64_t a0 = ((int64_t)(q.q0 + (rb + r0) / p.g) * p.q_stride8 + (u * p.g + (rb + r0) % p.g) * (HD / 8)) * 4;
+        const int64_t a1 = ((int64_t)(q.q0 + (rb + r1) / p.g) * p.q_stride8 + (u * p.g + (rb + r1) % p.g) * (HD / 8)) * 4;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int c = k * 8 + (lane & 3);
+            qf[k][0] = r0 < R ? __ldg(qb + a0 + c) : 0u;
+            qf[k][1] = r1 < R ? __ldg(qb + a1 + c) : 0u;
+            qf[k][2] = r0 < R ? __ldg(qb + a0 + c + 4) : 0u;
+            qf[k][3] = r1 < R ? __ldg(qb + a1 + c + 4) : 0u;
+        }
+    }
+    __syncthreads(); // barriers initialised
+
+    char *slots = ring + warp * kStepSlots * Sh::SLOT;
+    uint64_t *bar = full + warp * kStepSlots;
+    const int nblk = b1 - b0 > warp ? (b1 - b0 - warp + kStepWarps - 1) / kStepWarps : 0;
+    const int32_t *trow = p.table + (int64_t)s * p.table_stride;
+    const int rows_total = (p.num_pages * p.Hkv) << p.page_shift; // < 2^31 (host)
+    auto my_block = [&](int i) { return kb.block(b0 + warp + i * kStepWarps); };
+    // First cache row of the warp's i-th block, or rows_total (filled with
+    // zeros by the copy) for a page id that is out of range.
+    auto cache_row = [&](int i) {
+        if (i >= nblk) return 0;
+        const int key = my_block(i) << kStepShift;
+        const int page = __ldg(trow + (key >> p.page_shift));
+        if (page < 0 || page >= p.num_pages) {
+            set_status(p.status, kStatusIndex);
+            return rows_total;
+        }
+        return ((page * p.Hkv + u) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+    };
+    auto request = [&](int i, int row) { // lane 0 only
+        uint64_t *b = bar + Pipe::slot(i);
+        char *dst = slots + Pipe::slot(i) * Sh::SLOT;
+        mbar_arrive_expect_tx(b, Sh::SLOT);
+#pragma unroll
+        for (int hf = 0; hf < Sh::HALVES; ++hf) {
+            tma_load_2d(dst + hf * Sh::HALF, &kmap, hf * 64, row, b);
+            tma_load_2d(dst + Sh::TILE + hf * Sh::HALF, &vmap, hf * 64, row, b);
+        }
+    };
+    int rows = cache_row(lane); // lane l holds the row of block (32 * round + l)
+#pragma unroll
+    for (int i = 0; i < kStepSlots; ++i) {
+        const int row = __shfl_sync(kFull, rows, i);
+        if (lane == 0 && i < nblk) request(i, row);
+    }
+
+    float o[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    for (int i = 0; i < nblk; ++i) {
+        if (!__all_sync(kFull, Pipe::wait(bar, i, p.limit_ns))) {
+            Pipe::abort(bar, i, nblk, p.status, p.limit_ns);
+            break;
+        }
+        char *kt = slots + Pipe::slot(i) * Sh::SLOT, *vt = kt + Sh::TILE;
+        const int key0 = my_block(i) << kStepShift;
+        // value rows that no query of the sequence sees may hold anything: zeros
+        if (key0 + kStepKeys > all.hi || (key0 < all.lo && key0 + kStepKeys > all.sink)) {
+            for (int r = lane; r < kStepKeys; r += 32) {
+                const int key = key0 + r;
+                if (key >= all.hi || (key >= all.sink && key < all.lo))
+                    for (int c = 0; c < Sh::HALVES * 8; ++c)
+                        *reinterpret_cast<uint4 *>(vt + (c >> 3) * Sh::HALF + r * 128 + (c & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+        }
+        float x[2][4]; // scores: keys 8t + c2, +1 of rows r0 and r1
+        x[0][0] = x[0][1] = x[0][2] = x[0][3] = x[1][0] = x[1][1] = x[1][2] = x[1][3] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            // matrices: keys 0-7 and 8-15, columns 16k..+7 and +8..+15
+            const int key = (lane & 7) + ((lane >> 4) << 3), chunk = (2 * k + ((lane >> 3) & 1)) & 7;
+            uint32_t b[4];
+            ldmatrix4(b, kt + (k >> 2) * Sh::HALF + key * 128 + ((chunk ^ (key & 7)) << 4));
+            mma_bf16(x[0], qf[k], b[0], b[1]);
+            mma_bf16(x[1], qf[k], b[2], b[3]);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = key0 + 8 * t + c2 + (e & 1);
+                const RowRange &r = e < 2 ? rr0 : rr1;
+                const bool see = key < r.hi && (key < r.sink || key >= r.lo);
+                x[t][e] = see ? __fmul_rn(x[t][e], p.scale_log2) : -INFINITY;
+            }
+        float a0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+        float a1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+        a0 = fmaxf(a0, __shfl_xor_sync(kFull, a0, 1));
+        a1 = fmaxf(a1, __shfl_xor_sync(kFull, a1, 1));
+        a0 = fmaxf(a0, __shfl_xor_sync(kFull, a0, 2));
+        a1 = fmaxf(a1, __shfl_xor_sync(kFull, a1, 2));
+        const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
+        // a row that has seen no key yet keeps -infinity and adds zeros
+        const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
+        if (__any_sync(kFull, n0 != m0 || n1 != m1)) {
+            const float f0 = exp2_fast(m0 - z0), f1 = exp2_fast(m1 - z1);
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                o[n][0] *= f0;
+                o[n][1] *= f0;
+                o[n][2] *= f1;
+                o[n][3] *= f1;
+            }
+            m0 = n0;
+            m1 = n1;
+        }
+        float e0[4], e1[4]; // keys c2, c2+1, 8+c2, 8+c2+1
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                e0[2 * t + e] = exp2_fast(x[t][e] - z0);
+                e1[2 * t + e] = exp2_fast(x[t][2 + e] - z1);
+            }
+        l0 += (e0[0] + e0[1]) + (e0[2] + e0[3]); // this lane's keys; the quad's at the end
+        l1 += (e1[0] + e1[1]) + (e1[2] + e1[3]);
+        // rounded to bf16 for the product with V (relative 2^-9 each, of either
+        // sign); the sum above is of the unrounded ones
+        const uint32_t pf[4] = {pack_bf16(e0[0], e0[1]), pack_bf16(e1[0], e1[1]),
+                                pack_bf16(e0[2], e0[3]), pack_bf16(e1[2], e1[3])};
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+            // matrices: keys 0-7 and 8-15 of columns 8n..+7, then of 8n+8..+15
+            const int key = lane & 15, chunk = (n + (lane >> 4)) & 7;
+            uint32_t b[4];
+            ldmatrix4_trans(b, vt + (n >> 3) * Sh::HALF + key * 128 + ((chunk ^ (key & 7)) << 4));
+            mma_bf16(o[n], pf, b[0], b[1]);
+            mma_bf16(o[n + 1], pf, b[2], b[3]);
+        }
+        slot_reads_done();
+        const int nx = i + kStepSlots;
+        if ((nx & 31) == 0) rows = cache_row(nx + lane);
+        const int row = __shfl_sync(kFull, rows, nx & 31);
+        if (lane == 0 && nx < nblk) request(nx, row);
+    }
+    l0 += __shfl_xor_sync(kFull, l0, 1);
+    l1 += __shfl_xor_sync(kFull, l1, 1);
+    l0 += __shfl_xor_sync(kFull, l0, 2);
+    l1 += __shfl_xor_sync(kFull, l1, 2);
+
+    // Join the warps in shared memory, in warp order: each puts its output in
+    // its own ring (its copies have all landed), [row][column] fp32.
+    __syncwarp();
+    float *mine = reinterpret_cast<float *>(slots);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        *reinterpret_cast<float2 *>(mine + r0 * HD + 8 * n + c2) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2 *>(mine + r1 * HD + 8 * n + c2) = make_float2(o[n][2], o[n][3]);
+    }
+    if ((lane & 3) == 0) {
+        s_ml[warp * 16 + r0] = make_float2(m0, l0);
+        s_ml[warp * 16 + r1] = make_float2(m1, l1);
+    }
+    __syncthreads();
+    constexpr int CT = HD / 4; // threads of a row, four columns each
+    const int64_t base = part_base(p, s, q, u) + (int64_t)split * R;
+    for (int r = threadIdx.x / CT; r < R; r += 32 * kStepWarps / CT) {
+        const int c = (threadIdx.x % CT) * 4;
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kStepWarps; ++w) m = fmaxf(m, s_ml[w * 16 + r].x);
+        const float z = m == -INFINITY ? 0.0f : m;
+        float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < kStepWarps; ++w) {
+            const float2 ml = s_ml[w * 16 + r];
+            const float f = exp2_fast(ml.x - z);
+            const float4 v = *reinterpret_cast<const float4 *>(
+                reinterpret_cast<const float *>(ring + w * kStepSlots * Sh::SLOT) + r * HD + c);
+            l = fmaf(f, ml.y, l);
+            a.x = fmaf(f, v.x, a.x);
+            a.y = fmaf(f, v.y, a.y);
+            a.z = fmaf(f, v.z, a.z);
+            a.w = fmaf(f, v.w, a.w);
+        }
+        if (nsplit == 1) {
+            write_row<HD>(p, q.q0 + (rb + r) / p.g, u * p.g + (rb + r) % p.g, c, a, m, l);
+        } else {
+            *reinterpret_cast<float4 *>(p.part_o + (base + r) * HD + c) = a;
+            if (c == 0) p.part_ml[base + r] = make_float2(m, l);
+        }
+    }
+}
+
+// Join a sequence's split results, one warp per row, in split order.
+template <int HD>
+__global__ void __launch_bounds__(128) window_attention_join_kernel(const AttnParams p)
+{
+    grid_dependency_wait();
+    allow_dependents();
+    const int u = blockIdx.x % p.Hkv, s = blockIdx.x / p.Hkv;
+    const SeqInfo q = seq_info(p, s);
+    const int64_t R64 = (int64_t)q.n * p.g;
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 5);
+    if (r >= R64 || R64 > kStepRows) return;
+    const int R = (int)R64;
+    const KeyBlocks<kStepShift> kb(rows_union(p, q.L - q.n, q.L - 1, q.L));
+    const int per = step_split_blocks(kb.count);
+    const int nsplit = max(1, (kb.count + per - 1) / per);
+    if (nsplit == 1) return;
+    const int64_t base = part_base(p, s, q, u) + r;
+    const float2 ml = lane < nsplit ? p.part_ml[base + (int64_t)lane * R] : make_float2(-INFINITY, 0.0f);
+    float m = ml.x;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+    const float f = exp2_fast(ml.x - (m == -INFINITY ? 0.0f : m));
+    float l = 0.0f;
+    float4 a = make_float4(0, 0, 0, 0);
+    const int c = lane * 4;
+    for (int k = 0; k < nsplit; ++k) {
+        const float fk = __shfl_sync(kFull, f, k);
+        l = fmaf(fk, __shfl_sync(kFull, ml.y, k), l);
+        if (c < HD) {
+            const float4 v = *reinterpret_cast<const float4 *>(p.part_o + (base + (int64_t)k * R) * HD + c);
+            a.x = fmaf(fk, v.x, a.x);
+            a.y = fmaf(fk, v.y, a.y);
+            a.z = fmaf(fk, v.z, a.z);
+            a.w = fmaf(fk, v.w, a.w);
+        }
+    }
+    if (c < HD) write_row<HD>(p, q.q0 + (int)r / p.g, u * p.g + (int)r % p.g, c, a, m, l);
+}
+
+namespace {
+
+template <int HD>
+cudaError_t launch_step_hd(const AttnParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                           int splits, cudaStream_t s)
+{
+    auto fn = window_attention_step_kernel<HD>;
+    const int smem = StepShape<HD>::SMEM;
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = ((int64_t)p.max_q * p.g + kStepRows - 1) / kStepRows;
+    if (tiles * p.S * p.Hkv > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    e = launch_overlapped_2d(fn, dim3((unsigned)(tiles * p.S * p.Hkv), (unsigned)splits),
+                             32 * kStepWarps, smem, s, p, (int)tiles, kmap, vmap);
+    if (e != cudaSuccess || splits == 1) return e;
+    const int rows = (int)(p.max_q * (int64_t)p.g < kStepRows ? p.max_q * p.g : kStepRows);
+    return launch_overlapped_2d(window_attention_join_kernel<HD>,
+                                dim3((unsigned)(p.S * p.Hkv), (unsigned)((rows + 3) / 4)), 128, 0,
+                                s, p);
+}
+
+} // namespace
+
+cudaError_t launch_attention_step(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
+                                  const CUtensorMap &vmap, int splits, cudaStream_t s)
+{
+    return head_dim == 64 ? launch_step_hd<64>(p, kmap, vmap, splits, s)
+                          : launch_step_hd<128>(p, kmap, vmap, splits, s);
+}
+
+} // namespace dan

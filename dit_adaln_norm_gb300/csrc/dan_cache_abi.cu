@@ -1,0 +1,351 @@
+// dan_cache_abi.cu -- the extern "C" boundary of the paged-cache operators
+// (include/dan_cache.h): argument validation, tensor maps, launches.
+#include "../../include/dan_cache.h"
+#include "dan_attn.cuh"
+#include "dan_internal.h"
+
+#include <cmath>
+#include <mutex>
+
+namespace dan {
+namespace {
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once (the library does not link
+// the driver, so that it loads on machines without one).
+EncodeTiled encode_tiled()
+{
+    static std::mutex mu;
+    static EncodeTiled fn = nullptr;
+    std::lock_guard<std::mutex> lk(mu);
+    if (!fn) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &found) == cudaSuccess &&
+            found == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiled>(ptr);
+    }
+    return fn;
+}
+
+// A cache as a matrix of `rows` token rows of one head, read in boxes of 64
+// columns x box_rows tokens with the 128-byte swizzle.
+bool cache_map(CUtensorMap *map, const void *cache, int64_t rows, int64_t hd, int box_rows)
+{
+    const EncodeTiled enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)hd * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t step[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(cache), dims, strides, box,
+               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Most splits that a step sequence over a table of this size can have.
+int step_splits(int64_t max_pages, int64_t page_size)
+{
+    // the sinks' last block and the window's first may both be partly used
+    const int64_t blocks = ((max_pages * page_size) >> kStepShift) + 1;
+    const int64_t n = (blocks + kStepMinBlocks - 1) / kStepMinBlocks;
+    return (int)(n < kMaxSplits ? n : kMaxSplits);
+}
+
+// Room for partial results: rows for each (sequence, key head) (cap), or for
+// each query row, whichever is less in all.
+struct PartRoom {
+    int64_t rows, cap;
+};
+
+PartRoom part_room(int64_t N, int64_t S, int64_t heads, int64_t kv_heads, int64_t max_pages,
+                   int64_t page_size)
+{
+    const int splits = step_splits(max_pages, page_size);
+    if (splits == 1 || N == 0 || S == 0) return {0, 0};
+    const int64_t cap = (int64_t)kStepRows * splits;
+    const int64_t by_seq = S * kv_heads * cap, by_row = N * heads * kMaxSplits;
+    return by_seq <= by_row ? PartRoom{by_seq, cap} : PartRoom{by_row, 0};
+}
+
+} // namespace
+
+int64_t window_attention_workspace(int64_t N, int64_t S, int64_t heads, int64_t kv_heads,
+                                   int64_t head_dim, int64_t max_pages, int64_t page_size, int64_t)
+{
+    return part_room(N, S, heads, kv_heads, max_pages, page_size).rows * (head_dim * 4 + 8);
+}
+
+cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
+{
+    AttnParams p = {};
+    p.q = static_cast<const uint4 *>(a.q);
+    p.N = a.N;
+    p.q_stride8 = a.q_stride / 8;
+    p.table = a.page_table;
+    p.table_stride = a.table_stride;
+    p.max_pages = (int)a.max_pages;
+    p.num_pages = (int)a.num_pages;
+    p.page_shift = page_shift(a.page_size);
+    p.q_start = a.q_start;
+    p.kv_len = a.kv_len;
+    p.S = (int)a.S;
+    p.H = (int)a.heads;
+    p.Hkv = (int)a.kv_heads;
+    p.g = (int)(a.heads / a.kv_heads);
+    const int64_t big = int64_t(1) << 30; // past every position
+    p.window = (int)(a.window < big ? a.window : big);
+    p.sinks = (int)(a.sinks < big ? a.sinks : big);
+    p.chunk = (int)(a.chunk < big ? a.chunk : big);
+    p.max_q = (int)(a.max_q < a.N ? a.max_q : a.N);
+    p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+    p.out = static_cast<uint4 *>(a.out);
+    p.lse = a.lse;
+    const PartRoom room = part_room(a.N, a.S, a.heads, a.kv_heads, a.max_pages, a.page_size);
+    p.part_o = static_cast<float *>(a.workspace);
+    p.part_ml = reinterpret_cast<float2 *>(p.part_o + room.rows * a.head_dim);
+    p.part_cap = room.cap;
+    p.status = device_status();
+    p.limit_ns = 1000000000ull;
+    const int64_t rows = a.num_pages * a.kv_heads * a.page_size;
+    CUtensorMap kmap, vmap;
+    if (!cache_map(&kmap, a.k_cache, rows, a.head_dim, 1 << kStepShift) ||
+        !cache_map(&vmap, a.v_cache, rows, a.head_dim, 1 << kStepShift))
+        return cudaErrorInvalidValue;
+    return launch_attention_step(p, (int)a.head_dim, kmap, vmap,
+                                 step_splits(a.max_pages, a.page_size), s);
+}
+
+} // namespace dan
+
+namespace {
+
+constexpr int64_t kMaxElems = int64_t(1) << 40;
+constexpr int64_t kMaxCacheRows = (int64_t(1) << 31) - 256;
+constexpr int64_t kMaxInt = 0x7FFFFFFF;
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+struct Range {
+    uintptr_t lo, hi;
+    Range(const void *p, int64_t bytes)
+        : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + static_cast<uintptr_t>(bytes))
+    {
+    }
+};
+
+bool overlap(const Range &a, const Range &b)
+{
+    return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
+}
+
+// Shared checks of sizes: heads, head_dim, pages.
+int check_cache(int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t num_pages,
+                int64_t page_size)
+{
+    if (head_dim != 64 && head_dim != 128) return DAN_EUNSUPPORTED;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+        return DAN_EUNSUPPORTED;
+    if (heads < 1 || kv_heads < 1 || num_pages < 1 || heads % kv_heads) return DAN_EINVAL;
+    if (heads > 1024) return DAN_EUNSUPPORTED;
+    if (num_pages > kMaxCacheRows / (kv_heads * page_size)) return DAN_EUNSUPPORTED;
+    return DAN_OK;
+}
+
+// Bytes of N rows of `width` elements at `stride`; -1 if out of bounds.
+int64_t rows_bytes(int64_t N, int64_t width, int64_t stride)
+{
+    if (stride < width || stride > kMaxElems || N > kMaxElems / stride) return -1;
+    return ((N - 1) * stride + width) * 2;
+}
+
+int validate_rope(const dan_bf16 *q, const dan_bf16 *k, const dan_bf16 *v, int64_t N,
+                  int64_t q_row_stride, int64_t kv_row_stride, int64_t heads, int64_t kv_heads,
+                  int64_t hd, const dan_bf16 *wq, const dan_bf16 *wk, const float *rope,
+                  int64_t table_rows, const int32_t *positions, const int32_t *slots, float eps,
+                  const dan_bf16 *q_out, int64_t qo_row_stride, const dan_bf16 *k_cache,
+                  const dan_bf16 *v_cache, int64_t num_pages, int64_t page_size)
+{
+    const int st = check_cache(heads, kv_heads, hd, num_pages, page_size);
+    if (st != DAN_OK) return st;
+    if (N < 0 || table_rows < 1 || table_rows > kMaxInt || !std::isfinite(eps) || eps < 0.0f)
+        return DAN_EINVAL;
+    if (N == 0) return DAN_OK;
+    const int64_t qb = rows_bytes(N, heads * hd, q_row_stride);
+    const int64_t kb = rows_bytes(N, kv_heads * hd, kv_row_stride);
+    const int64_t ob = rows_bytes(N, heads * hd, qo_row_stride);
+    if (qb < 0 || kb < 0 || ob < 0) return DAN_EINVAL;
+    if (!q || !k || !v || !wq || !wk || !rope || !positions || !slots || !q_out || !k_cache || !v_cache)
+        return DAN_EINVAL;
+    const void *p16[] = {q, k, v, wq, wk, rope, q_out, k_cache, v_cache};
+    for (const void *p : p16)
+        if (!aligned(p, 16)) return DAN_EALIGN;
+    if (!aligned(positions, 4) || !aligned(slots, 4)) return DAN_EALIGN;
+    if (q_row_stride % 8 || kv_row_stride % 8 || qo_row_stride % 8) return DAN_EALIGN;
+    const int64_t cb = num_pages * kv_heads * page_size * hd * 2;
+    const Range outs[] = {{q_out, ob}, {k_cache, cb}, {v_cache, cb}};
+    const Range ins[] = {{q, qb},         {k, kb},          {v, kb},        {wq, hd * 2},
+                         {wk, hd * 2},    {rope, table_rows * hd * 4}, {positions, N * 4}, {slots, N * 4}};
+    const bool in_place = q_out == q && qo_row_stride == q_row_stride;
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 8; ++i) {
+            if (o == 0 && i == 0 && in_place) continue;
+            // the columns of one packed buffer: in-place q rows lie beside k and v rows
+            if (o == 0 && in_place && (i == 1 || i == 2)) {
+                const uintptr_t row = (uintptr_t)(heads * hd * 2), krow = (uintptr_t)(kv_heads * hd * 2);
+                const uintptr_t step = (uintptr_t)q_row_stride * 2;
+                if (q_row_stride == kv_row_stride && ins[i].lo > outs[0].lo &&
+                    ins[i].lo - outs[0].lo >= row && ins[i].lo - outs[0].lo + krow <= step)
+                    continue;
+            }
+            if (overlap(outs[o], ins[i])) return DAN_EALIAS;
+        }
+        for (int o2 = o + 1; o2 < 3; ++o2)
+            if (overlap(outs[o], outs[o2])) return DAN_EALIAS;
+    }
+    return DAN_OK;
+}
+
+int validate_attention(const dan_bf16 *q, int64_t N, int64_t q_row_stride, const dan_bf16 *k_cache,
+                       const dan_bf16 *v_cache, int64_t num_pages, int64_t page_size,
+                       const int32_t *page_table, int64_t table_stride, int64_t max_pages,
+                       const int32_t *q_start, const int32_t *kv_len, int64_t S, int64_t heads,
+                       int64_t kv_heads, int64_t hd, int64_t window, int64_t sinks, int64_t chunk,
+                       int64_t max_q, float scale, const dan_bf16 *out, const float *lse,
+                       const void *workspace, int64_t workspace_bytes)
+{
+    const int st = check_cache(heads, kv_heads, hd, num_pages, page_size);
+    if (st != DAN_OK) return st;
+    if (N < 0 || S < 0 || max_pages < 1 || max_q < 0) return DAN_EINVAL;
+    if (window < 0 || window > kMaxInt || sinks < 0 || sinks > kMaxInt || chunk < 1 || chunk > kMaxInt)
+        return DAN_EINVAL;
+    if (!std::isfinite(scale) || scale <= 0.0f) return DAN_EINVAL;
+    if (N > (int64_t(1) << 30) || S > (int64_t(1) << 20) ||
+        max_pages > (int64_t(1) << 30) / page_size)
+        return DAN_EUNSUPPORTED;
+    if (N == 0 || S == 0) return DAN_OK;
+    if (table_stride < max_pages || table_stride > kMaxElems / S) return DAN_EINVAL;
+    const int64_t qb = rows_bytes(N, heads * hd, q_row_stride);
+    if (qb < 0) return DAN_EINVAL;
+    if (!q || !k_cache || !v_cache || !page_table || !q_start || !kv_len || !out) return DAN_EINVAL;
+    const int64_t need = dan::window_attention_workspace(N, S, heads, kv_heads, hd, max_pages,
+                                                         page_size, max_q);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return DAN_EINVAL;
+    const void *p16[] = {q, k_cache, v_cache, out, workspace};
+    for (const void *p : p16)
+        if (!aligned(p, 16)) return DAN_EALIGN;
+    const void *p4[] = {page_table, q_start, kv_len, lse};
+    for (const void *p : p4)
+        if (!aligned(p, 4)) return DAN_EALIGN;
+    if (q_row_stride % 8) return DAN_EALIGN;
+    const int64_t cb = num_pages * kv_heads * page_size * hd * 2;
+    const Range outs[] = {{out, N * heads * hd * 2},
+                          {lse, lse ? N * heads * 4 : 0},
+                          {workspace, need}};
+    const Range ins[] = {{q, qb},
+                         {k_cache, cb},
+                         {v_cache, cb},
+                         {page_table, ((S - 1) * table_stride + max_pages) * 4},
+                         {q_start, (S + 1) * 4},
+                         {kv_len, S * 4}};
+    for (int o = 0; o < 3; ++o) {
+        for (const Range &in : ins)
+            if (overlap(outs[o], in)) return DAN_EALIAS;
+        for (int o2 = o + 1; o2 < 3; ++o2)
+            if (overlap(outs[o], outs[o2])) return DAN_EALIAS;
+    }
+    return DAN_OK;
+}
+
+int status_of(cudaError_t e) { return e == cudaSuccess ? DAN_OK : DAN_ECUDA; }
+
+} // namespace
+
+extern "C" {
+
+int dan_can_use_qk_norm_rope_cache(const dan_bf16 *q, const dan_bf16 *k, const dan_bf16 *v,
+                                   int64_t N, int64_t q_row_stride, int64_t kv_row_stride,
+                                   int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                   const dan_bf16 *wq, const dan_bf16 *wk, const float *rope,
+                                   int64_t table_rows, const int32_t *positions,
+                                   const int32_t *slots, float eps, int neox,
+                                   const dan_bf16 *q_out, int64_t qo_row_stride,
+                                   const dan_bf16 *k_cache, const dan_bf16 *v_cache,
+                                   int64_t num_pages, int64_t page_size)
+{
+    (void)neox;
+    return validate_rope(q, k, v, N, q_row_stride, kv_row_stride, heads, kv_heads, head_dim, wq, wk,
+                         rope, table_rows, positions, slots, eps, q_out, qo_row_stride, k_cache,
+                         v_cache, num_pages, page_size);
+}
+
+int dan_qk_norm_rope_cache(const dan_bf16 *q, const dan_bf16 *k, const dan_bf16 *v, int64_t N,
+                           int64_t q_row_stride, int64_t kv_row_stride, int64_t heads,
+                           int64_t kv_heads, int64_t head_dim, const dan_bf16 *wq,
+                           const dan_bf16 *wk, const float *rope, int64_t table_rows,
+                           const int32_t *positions, const int32_t *slots, float eps, int neox,
+                           dan_bf16 *q_out, int64_t qo_row_stride, dan_bf16 *k_cache,
+                           dan_bf16 *v_cache, int64_t num_pages, int64_t page_size, void *stream)
+{
+    const int st = validate_rope(q, k, v, N, q_row_stride, kv_row_stride, heads, kv_heads, head_dim,
+                                 wq, wk, rope, table_rows, positions, slots, eps, q_out,
+                                 qo_row_stride, k_cache, v_cache, num_pages, page_size);
+    if (st != DAN_OK || N == 0) return st;
+    const dan::CacheRopeProblem c{q, k, v, N, q_row_stride, kv_row_stride, heads, kv_heads, head_dim,
+                                  wq, wk, rope, table_rows, positions, slots, eps, neox != 0, q_out,
+                                  qo_row_stride, k_cache, v_cache, num_pages, page_size};
+    return status_of(dan::launch_qk_norm_rope_cache(c, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t dan_window_attention_workspace(int64_t N, int64_t S, int64_t heads, int64_t kv_heads,
+                                       int64_t head_dim, int64_t max_pages, int64_t page_size,
+                                       int64_t max_q)
+{
+    if (N < 0 || S < 0 || N > (int64_t(1) << 30) || S > (int64_t(1) << 20) || max_q < 0 ||
+        check_cache(heads, kv_heads, head_dim, 1, page_size) != DAN_OK || max_pages < 1 ||
+        max_pages > (int64_t(1) << 30) / page_size)
+        return 0; // the call itself refuses these sizes
+    return dan::window_attention_workspace(N, S, heads, kv_heads, head_dim, max_pages, page_size, max_q);
+}
+
+int dan_can_use_window_attention(const dan_bf16 *q, int64_t N, int64_t q_row_stride,
+                                 const dan_bf16 *k_cache, const dan_bf16 *v_cache,
+                                 int64_t num_pages, int64_t page_size, const int32_t *page_table,
+                                 int64_t table_stride, int64_t max_pages, const int32_t *q_start,
+                                 const int32_t *kv_len, int64_t S, int64_t heads, int64_t kv_heads,
+                                 int64_t head_dim, int64_t window, int64_t sinks, int64_t chunk,
+                                 int64_t max_q, float scale, const dan_bf16 *out, const float *lse,
+                                 const void *workspace, int64_t workspace_bytes)
+{
+    return validate_attention(q, N, q_row_stride, k_cache, v_cache, num_pages, page_size, page_table,
+                              table_stride, max_pages, q_start, kv_len, S, heads, kv_heads, head_dim,
+                              window, sinks, chunk, max_q, scale, out, lse, workspace,
+                              workspace_bytes);
+}
+
+int dan_window_attention(const dan_bf16 *q, int64_t N, int64_t q_row_stride,
+                         const dan_bf16 *k_cache, const dan_bf16 *v_cache, int64_t num_pages,
+                         int64_t page_size, const int32_t *page_table, int64_t table_stride,
+                         int64_t max_pages, const int32_t *q_start, const int32_t *kv_len,
+                         int64_t S, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                         int64_t window, int64_t sinks, int64_t chunk, int64_t max_q, float scale,
+                         dan_bf16 *out, float *lse, void *workspace, int64_t workspace_bytes,
+                         void *stream)
+{
+    const int st = validate_attention(q, N, q_row_stride, k_cache, v_cache, num_pages, page_size,
+                                      page_table, table_stride, max_pages, q_start, kv_len, S, heads,
+                                      kv_heads, head_dim, window, sinks, chunk, max_q, scale, out, lse,
+                                      workspace, workspace_bytes);
+    if (st != DAN_OK || N == 0 || S == 0) return st;
+    const dan::AttnProblem a{q, N, q_row_stride, k_cache, v_cache, num_pages, page_size, page_table,
+                             table_stride, max_pages, q_start, kv_len, S, heads, kv_heads, head_dim,
+                             window, sinks, chunk, max_q, scale, out, lse, workspace};
+    return status_of(dan::launch_window_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+} // extern "C"

@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libdan.so (include/dan.h): argument marshalling only.
+"""Thin ctypes binding of libdan.so (include/dan.h and include/dan_cache.h):
+argument marshalling only.
 
 Every function takes CUDA bf16 torch tensors, checks the layout the C ABI
 expects, passes raw pointers, strides and the current CUDA stream, and turns
@@ -19,6 +20,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdan.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "dan.h")
+CACHE_HEADER = os.path.join(os.path.dirname(HERE), "include", "dan_cache.h")
 
 DAN_OK, DAN_EINVAL, DAN_EUNSUPPORTED, DAN_EALIGN, DAN_EALIAS, DAN_ECUDA = range(6)
 
@@ -47,6 +49,16 @@ _SIGS = {
                                        _P, _P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P],
     "dan_can_use_qk_norm_rope_neox_epilogue": [_P, _P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I,
                                                _P, _P, _P, _P, _P, _P, _F, _F, _P, _P, _P],
+    "dan_qk_norm_rope_cache": [_P, _P, _P] + [_I] * 6 + [_P, _P, _P, _I, _P, _P, _F, ctypes.c_int,
+                                                         _P, _I, _P, _P, _I, _I, _P],
+    "dan_can_use_qk_norm_rope_cache": [_P, _P, _P] + [_I] * 6 + [_P, _P, _P, _I, _P, _P, _F,
+                                                                 ctypes.c_int, _P, _I, _P, _P, _I,
+                                                                 _I],
+    "dan_window_attention": [_P, _I, _I, _P, _P, _I, _I, _P, _I, _I, _P, _P] + [_I] * 8
+                            + [_F, _P, _P, _P, _I, _P],
+    "dan_can_use_window_attention": [_P, _I, _I, _P, _P, _I, _I, _P, _I, _I, _P, _P] + [_I] * 8
+                                    + [_F, _P, _P, _P, _I],
+    "dan_window_attention_workspace": [_I] * 8,
 }
 
 _lib = None
@@ -69,6 +81,7 @@ def load():
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
+        lib.dan_window_attention_workspace.restype = ctypes.c_int64
         lib.dan_status_string.argtypes = [ctypes.c_int]
         lib.dan_status_string.restype = ctypes.c_char_p
         lib.dan_get_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -79,9 +92,10 @@ def load():
     return _lib
 
 
-def declared_symbols() -> list[str]:
-    """Function names declared in include/dan.h."""
-    text = open(HEADER).read()
+def declared_symbols(header: str = HEADER) -> list[str]:
+    """Function names declared in a header (include/dan.h by default)."""
+    text = open(header).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S) if header != HEADER else text
     return sorted(set(re.findall(r"\b(dan_\w+)\s*\(", text)))
 
 
@@ -92,7 +106,8 @@ def status_string(status: int) -> str:
 def device_status() -> int:
     """Read and clear the current device's status word (bit 1: a warp gave
     up waiting for a row it requested, 4: it then also gave up on its other
-    copies in flight).  Synchronous; 0 when every wait completed."""
+    copies in flight, 8: an index array of a cache operation held an entry out
+    of its range).  Synchronous; 0 when every wait completed."""
     v = ctypes.c_uint(0)
     _check(load().dan_get_device_status(ctypes.byref(v)), "dan_get_device_status")
     return v.value
@@ -289,3 +304,154 @@ def qk_norm_rope_epilogue(txt, img, wq_txt, wk_txt, wq_img, wk_img, rope_txt, ro
         _ptr(wq_txt), _ptr(wk_txt), _ptr(wq_img), _ptr(wk_img), _ptr(rope_txt), _ptr(rope_img),
         float(eps_txt), float(eps_img), _ptr(qo), _ptr(ko), _ptr(vo), _stream()), name)
     return qo, ko, vo
+
+
+# ------------------------------------------------------ paged-cache operators
+
+def _one_device(named):
+    """The CUDA device that every given tensor lies on."""
+    devs = {}
+    for name, t in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name}: expected a CUDA tensor")
+        devs[t.device] = name
+    if len(devs) != 1:
+        raise ValueError(f"tensors lie on several devices: {sorted(map(str, devs))}")
+    return next(iter(devs))
+
+
+def _caches(k_cache, v_cache):
+    for c, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _bf16_cuda(c, n)
+        if c.dim() != 4 or not c.is_contiguous():
+            raise ValueError(f"{n}: expected a contiguous [pages, kv_heads, page_size, head_dim] tensor")
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    return k_cache.shape
+
+
+def _int32(t, name, shape):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+        raise TypeError(f"{name}: expected a CUDA int32 tensor")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {list(shape)} tensor")
+
+
+def _token_rows(t, name, N, heads, hd):
+    """A [N, heads, hd] or [N, heads*hd] view whose tokens' rows are dense;
+    returns its row stride."""
+    _bf16_cuda(t, name)
+    dense = (hd, 1) if t.dim() == 3 else (1,)
+    shape = (N, heads, hd) if t.dim() == 3 else (N, heads * hd)
+    strides_ok = all(st == want or n == 1
+                     for n, st, want in zip(t.shape[1:], t.stride()[1:], dense))
+    if tuple(t.shape) != shape or (t.numel() and not strides_ok):
+        raise ValueError(f"{name}: expected [{N}, {heads}, {hd}] (or [{N}, {heads * hd}]) with dense rows")
+    return t.stride(0) if N > 1 else heads * hd
+
+
+def qk_norm_rope_cache(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache, eps: float,
+                       neox: bool = False, q_out=None):
+    """RMSNorm per head and RoPE of Q and K at given positions; K and V go to
+    the paged cache (include/dan_cache.h).
+
+    q [N, heads*hd], k, v [N, kv_heads*hd]: views with dense rows, k and v with
+    one row stride (e.g. column slices of a packed projection); wq, wk [hd];
+    rope fp32 [rows, hd], row p the cosines then sines of position p; positions,
+    slots int32 [N], a negative slot storing nothing; k_cache, v_cache
+    [pages, kv_heads, page_size, hd], written in place.  Returns the queries
+    [N, heads, hd] (q_out if given; q_out may be q itself)."""
+    pages, Hkv, page, hd = _caches(k_cache, v_cache)
+    _bf16_cuda(q, "q")
+    N = q.shape[0]
+    width = q[0].numel() if N else q.shape[1:].numel()
+    if hd == 0 or width % hd:
+        raise ValueError(f"q: rows of {width} elements are not whole heads of {hd}")
+    H = width // hd
+    qs = _token_rows(q, "q", N, H, hd)
+    ks, vs = _token_rows(k, "k", N, Hkv, hd), _token_rows(v, "v", N, Hkv, hd)
+    if ks != vs:
+        raise ValueError("k and v must share one row stride")
+    for w, n in ((wq, "wq"), (wk, "wk")):
+        _bf16_cuda(w, n)
+        if tuple(w.shape) != (hd,) or not w.is_contiguous():
+            raise ValueError(f"{n}: expected a contiguous [{hd}] tensor")
+    if not isinstance(rope, torch.Tensor) or not rope.is_cuda or rope.dtype != torch.float32:
+        raise TypeError("rope: expected a CUDA float32 tensor")
+    if rope.dim() != 2 or rope.shape[1] != hd or not rope.is_contiguous():
+        raise ValueError(f"rope: expected a contiguous [rows, {hd}] tensor")
+    _int32(positions, "positions", (N,))
+    _int32(slots, "slots", (N,))
+    dev = _one_device([("q", q), ("k", k), ("v", v), ("wq", wq), ("wk", wk), ("rope", rope),
+                       ("positions", positions), ("slots", slots), ("k_cache", k_cache),
+                       ("v_cache", v_cache), ("q_out", q_out)])
+    with torch.cuda.device(dev):
+        if q_out is None:
+            q_out = torch.empty((N, H, hd), dtype=torch.bfloat16, device=dev)
+        os_ = _token_rows(q_out, "q_out", N, H, hd)
+        _check(load().dan_qk_norm_rope_cache(
+            _ptr(q), _ptr(k), _ptr(v), N, qs, ks, H, Hkv, hd, _ptr(wq), _ptr(wk), _ptr(rope),
+            rope.shape[0], _ptr(positions), _ptr(slots), float(eps), int(bool(neox)), _ptr(q_out),
+            os_, _ptr(k_cache), _ptr(v_cache), pages, page, _stream()), "dan_qk_norm_rope_cache")
+    return q_out if q_out.dim() == 3 else q_out.unflatten(1, (H, hd))
+
+
+def window_attention(q, k_cache, v_cache, page_table, q_start, kv_len, window: int, sinks: int = 0,
+                     chunk: int = 1, scale: float | None = None, max_q: int | None = None, out=None,
+                     lse=None):
+    """Attention of ragged sequences over the paged cache
+    (include/dan_cache.h): each query sees the first ``sinks`` tokens, the
+    ``window`` tokens up to the first of its chunk, and its chunk of ``chunk``
+    tokens (chunk=1: causal).
+
+    q [N, heads, hd] with dense rows; page_table int32 [S, max_pages] (rows may
+    be strided); q_start int32 [S+1], kv_len int32 [S]: sequence s has the
+    query rows q_start[s]..q_start[s+1]-1, its last tokens, and kv_len[s] keys
+    in the cache.  scale defaults to hd**-0.5; max_q is a bound on the rows of
+    one sequence.  Returns out [N, heads, hd] (rows outside every sequence are
+    not written), or (out, lse) when ``lse`` is a float32 [N, heads] tensor or
+    True."""
+    pages, Hkv, page, hd = _caches(k_cache, v_cache)
+    _bf16_cuda(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q: expected a [N, heads, head_dim] tensor")
+    N, H, _ = q.shape
+    qs = _token_rows(q, "q", N, H, hd)
+    if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda or page_table.dtype != torch.int32:
+        raise TypeError("page_table: expected a CUDA int32 tensor")
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table: expected [S, max_pages] with unit column stride")
+    S, M = page_table.shape
+    ts = page_table.stride(0) if S > 1 else M
+    _int32(q_start, "q_start", (S + 1,))
+    _int32(kv_len, "kv_len", (S,))
+    want_lse = lse is not None and lse is not False
+    given_lse = lse if isinstance(lse, torch.Tensor) else None
+    dev = _one_device([("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
+                       ("page_table", page_table), ("q_start", q_start), ("kv_len", kv_len),
+                       ("out", out), ("lse", given_lse)])
+    max_q = N if max_q is None else int(max_q)
+    lib = load()
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((N, H, hd), dtype=torch.bfloat16, device=dev)
+        _bf16_cuda(out, "out")
+        if tuple(out.shape) != (N, H, hd) or not out.is_contiguous():
+            raise ValueError("out: expected a contiguous [N, heads, head_dim] tensor")
+        if want_lse:
+            lse = given_lse if given_lse is not None else torch.empty((N, H), dtype=torch.float32, device=dev)
+            if lse.dtype != torch.float32 or tuple(lse.shape) != (N, H) or not lse.is_contiguous():
+                raise ValueError("lse: expected a contiguous float32 [N, heads] tensor")
+        else:
+            lse = None
+        size = lib.dan_window_attention_workspace(N, S, H, Hkv, hd, M, page, max_q)
+        # of this call alone: the allocator hands it on in the stream's order
+        work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        _check(lib.dan_window_attention(
+            _ptr(q), N, qs, _ptr(k_cache), _ptr(v_cache), pages, page, _ptr(page_table), ts, M,
+            _ptr(q_start), _ptr(kv_len), S, H, Hkv, hd, int(window), int(sinks), int(chunk), max_q,
+            float(hd ** -0.5 if scale is None else scale), _ptr(out), _ptr(lse), _ptr(work), size,
+            _stream()), "dan_window_attention")
+    return (out, lse) if want_lse else out

@@ -1,0 +1,416 @@
+"""GPU tests of the paged-cache operators: values against 64-bit references
+with tolerances from the arithmetic (tests/_cache.py), the rotation bit for
+bit against single fp32 steps, untouched rows and slots, index checks, batch
+invariance, graphs, streams, and both operators together over several steps."""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from dit_adaln_norm_gb300 import ops, synth
+from _cache import SENTINEL, Problem
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    assert torch.cuda.is_available(), "GPU tests need CUDA"
+    ops.load()
+    ops.device_status()
+    yield
+    torch.cuda.synchronize()
+    assert ops.device_status() == 0
+
+
+# ------------------------------------------------------- rotation + cache
+
+def bits(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def rotate_steps(x, w, table, pos, eps, neox):
+    """The documented fp32 steps on heads x [N, heads, hd] (float32 arrays)."""
+    f = np.float32
+    N, H, hd = x.shape
+    part = np.zeros((N, H, hd // 8), f)
+    for e in range(8):
+        part = part + x[..., e::8] * x[..., e::8]
+    while part.shape[-1] > 1:
+        part = part[..., 0::2] + part[..., 1::2]
+    r = f(1) / np.sqrt(part / f(hd) + f(eps))
+    n = (x * r) * w
+    c, s = table[pos][:, None, :hd // 2], table[pos][:, None, hd // 2:]
+    out = np.empty_like(n)
+    a, b = (n[..., :hd // 2], n[..., hd // 2:]) if neox else (n[..., 0::2], n[..., 1::2])
+    ra, rb = a * c - b * s, a * s + b * c
+    if neox:
+        out[..., :hd // 2], out[..., hd // 2:] = ra, rb
+    else:
+        out[..., 0::2], out[..., 1::2] = ra, rb
+    return synth.to_bf16_bits(out)
+
+
+def rope_problem(N, H, Hkv, hd, page, seed, pad=0, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    qkv = (torch.randn(N, (H + 2 * Hkv) * hd + 8, generator=g, device="cuda") * std).bfloat16()
+    w = (1 + 0.1 * torch.randn(2, hd, generator=g, device="cuda")).bfloat16()
+    pages = -(-max(N, 1) // page) + 2
+    slots = rng.permutation(pages * page)[:N].astype(np.int32)
+    slots[rng.permutation(N)[:pad]] = -1 - rng.integers(0, 5, pad)
+    pos = rng.integers(0, 500, N).astype(np.int32)
+    caches = [torch.full((pages, Hkv, page, hd), v, dtype=torch.bfloat16, device="cuda") for v in (3.5, -2.5)]
+    table = synth.rope_table(500, hd)
+    return dict(q=qkv[:, :H * hd], k=qkv[:, H * hd:(H + Hkv) * hd], v=qkv[:, (H + Hkv) * hd:-8], w=w,
+                table=table, pos=pos, slots=slots, caches=caches)
+
+
+def rope_call(p, neox, q_out=None):
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    return ops.qk_norm_rope_cache(p["q"], p["k"], p["v"], p["w"][0], p["w"][1], dev(p["table"]),
+                                  dev(p["pos"]), dev(p["slots"]), *p["caches"], EPS, neox=neox, q_out=q_out)
+
+
+def rope_check(p, got, neox, q_in=None, k_in=None, v_in=None):
+    kc, vc = p["caches"]
+    pages, Hkv, page, hd = kc.shape
+    N = len(p["pos"])
+    x = lambda t: t.float().cpu().numpy().reshape(N, -1, hd)  # noqa: E731
+    wq, wk = (p["w"][i].float().cpu().numpy() for i in (0, 1))
+    q_in = p["q"] if q_in is None else q_in
+    with np.errstate(invalid="ignore", over="ignore"):
+        wantq = rotate_steps(x(q_in), wq, p["table"], p["pos"], EPS, neox)
+        wantk = rotate_steps(x(p["k"]), wk, p["table"], p["pos"], EPS, neox)
+    nan = lambda b: (b & 0x7FFF) > 0x7F80  # noqa: E731
+    gq = bits(got)
+    assert ((gq == wantq) | (nan(gq) & nan(wantq))).all()
+    ek = np.full((pages * page, Hkv, hd), bits(torch.tensor([3.5]).bfloat16())[0], np.uint16)
+    ev = np.full((pages * page, Hkv, hd), bits(torch.tensor([-2.5]).bfloat16())[0], np.uint16)
+    live = p["slots"] >= 0
+    ek[p["slots"][live]] = wantk[live]
+    ev[p["slots"][live]] = bits(p["v"]).reshape(N, Hkv, hd)[live]
+    gk = bits(kc).reshape(pages, Hkv, page, hd).transpose(0, 2, 1, 3).reshape(pages * page, Hkv, hd)
+    gv = bits(vc).reshape(pages, Hkv, page, hd).transpose(0, 2, 1, 3).reshape(pages * page, Hkv, hd)
+    assert ((gk == ek) | (nan(gk) & nan(ek))).all()
+    assert (gv == ev).all()
+
+
+@pytest.mark.parametrize("hd,neox", [(128, False), (128, True), (64, False), (64, True)])
+@pytest.mark.parametrize("N,H,Hkv,page", [(1, 1, 1, 16), (1, 32, 8, 64), (3, 6, 2, 32), (37, 20, 4, 16),
+                                          (130, 5, 5, 128), (515, 32, 8, 64)])
+def test_rope_cache(N, H, Hkv, page, hd, neox):
+    p = rope_problem(N, H, Hkv, hd, page, 7 * N + H + hd, pad=N // 5)
+    rope_check(p, rope_call(p, neox), neox)
+
+
+@pytest.mark.parametrize("neox", [False, True])
+def test_rope_cache_extreme_values(neox):
+    p = rope_problem(64, 4, 2, 128, 16, 5)
+    p["q"][0], p["k"][0] = 0.0, 0.0
+    p["q"][1], p["k"][1] = 1e-38, -1e-38
+    p["q"][2], p["k"][2] = 3e38, 3e38            # squares overflow
+    p["q"][3, 5], p["k"][3, 7], p["v"][3, 1] = float("inf"), float("nan"), float("nan")
+    p["q"][4, ::2] = -0.0
+    rope_check(p, rope_call(p, neox), neox)
+
+
+@pytest.mark.parametrize("neox", [False, True])
+def test_rope_cache_in_place_beside_k_and_v(neox):
+    p = rope_problem(70, 6, 2, 128, 32, 6)
+    q_in = p["q"].clone()
+    got = rope_call(p, neox, q_out=p["q"])
+    assert got.data_ptr() == p["q"].data_ptr()
+    rope_check(p, got, neox, q_in=q_in)
+
+
+def test_rope_cache_bad_indices_are_left_out():
+    p = rope_problem(40, 4, 2, 64, 16, 8)
+    total = p["caches"][0].shape[0] * 16
+    p["pos"][3], p["pos"][4], p["slots"][5], p["slots"][6] = -1, 500, total, 0x7FFFFFFF
+    out = torch.full((40, 4, 64), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    rope_call(p, True, q_out=out)
+    torch.cuda.synchronize()
+    assert ops.device_status() == 8
+    assert (out[3:5] == SENTINEL).all()
+    good = np.ones(40, bool)
+    good[3:5] = False
+    p["pos"][3:5] = 0
+    x = p["q"].float().cpu().numpy().reshape(40, -1, 64)
+    want = rotate_steps(x, p["w"][0].float().cpu().numpy(), p["table"], p["pos"], EPS, True)
+    assert (bits(out)[good] == want[good]).all()
+    slots = p["slots"].copy()
+    slots[3:7] = -1  # none of the four stored anything
+    p2 = dict(p, slots=slots)
+    rope_check(p2, torch.from_numpy(want.view(np.int16)).view(torch.bfloat16).cuda(), True)
+
+
+def test_rope_cache_empty_call():
+    p = rope_problem(0, 4, 2, 64, 16, 9)
+    assert rope_call(p, True).shape == (0, 4, 64)
+
+
+# -------------------------------------------------------------- attention
+
+def run(p, what="", **kw):
+    p.check(p.call(ops, **kw), what)
+
+
+GROUPS = [(1, 1), (4, 2), (8, 1), (6, 2), (16, 1), (32, 1), (5, 5)]
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("H,Hkv", GROUPS)
+def test_single_tokens(H, Hkv, hd):
+    lens = [1, 2, 15, 16, 17, 63, 255, 256, 257, 300, 777, 1030]
+    run(Problem([1] * len(lens), lens, H, Hkv, hd, page=16, seed=H + hd), max_q=1)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (17, 0), (100, 4), (256, 64), (0, 5), (0, 0), (5, 1000),
+                                          (300, 130)])
+def test_step_windows_and_sinks(window, sinks, page):
+    lens = [1, 5, 6, 64, 129, 400, 1000]
+    run(Problem([1] * len(lens), lens, 8, 2, 128, page, window, sinks, seed=window + page), max_q=1)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("H,Hkv", GROUPS)
+def test_drafted_tokens(H, Hkv, hd):
+    q = [1, 2, 3, 4, 0, 5, 1, 16]
+    kv = [1, 2, 300, 64, 0, 5, 700, 1029]
+    run(Problem(q, kv, H, Hkv, hd, 32, 200, 7, seed=H * hd, pad=3))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q,kv", [(17, 17), (40, 40), (128, 128), (129, 200), (255, 1000), (300, 300),
+                                  (513, 513), (700, 1500)])
+def test_prefill(q, kv, hd):
+    run(Problem([q], [kv], 4, 2, hd, 16, seed=q + kv))
+
+
+@pytest.mark.parametrize("window,sinks,chunk", [(1, 0, 1), (50, 0, 1), (128, 4, 1), (129, 130, 1), (0, 9, 1),
+                                                (0, 0, 1), (1, 0, 100), (201, 37, 100), (64, 3, 7),
+                                                (0, 5, 33), (1 << 30, 0, 1 << 30), (1000, 300, 256)])
+@pytest.mark.parametrize("H,Hkv,hd,page", [(4, 4, 128, 64), (6, 2, 64, 16), (8, 1, 128, 128)])
+def test_prefill_masks(window, sinks, chunk, H, Hkv, hd, page):
+    run(Problem([400, 90, 300], [400, 1000, 333], H, Hkv, hd, page, window, sinks, chunk,
+                seed=window + chunk + hd))
+
+
+def test_mixed_batch_with_empty_sequences_and_rows_behind():
+    run(Problem([0, 1, 300, 0, 2, 70, 1, 0], [0, 1, 500, 40, 900, 70, 1300, 0], 8, 2, 128, 32, 250, 5,
+                seed=3, pad=9))
+
+
+def test_queries_before_the_first_key_give_zeros():
+    # kv_len < n: the first rows have negative positions
+    run(Problem([5, 40, 3], [2, 30, 0], 4, 2, 64, 16, seed=4))
+
+
+@pytest.mark.parametrize("max_q", [None, 300])
+def test_max_q_bound_is_only_a_hint(max_q):
+    run(Problem([1, 300, 7], [50, 300, 1000], 4, 2, 128, 16, seed=5), max_q=max_q)
+
+
+@pytest.mark.parametrize("q", [1, 60])
+def test_large_scores_and_values(q):
+    run(Problem([q, q], [400, 257], 4, 2, 128, 16, seed=6, q_std=30.0, v_mean=1000.0))
+    run(Problem([q, q], [400, 257], 4, 2, 128, 16, seed=7, q_std=1e-3, scale=3.0))
+
+
+@pytest.mark.parametrize("q", [1, 50])
+def test_rising_scores_rescale(q):
+    """Keys that grow along the sequence: the running maximum moves at every block."""
+    p = Problem([q], [900], 4, 2, 64, 16, seed=8)
+    ramp = torch.linspace(0.01, 4, 900, device="cuda")[None, :, None]
+    p2 = Problem([q], [900], 4, 2, 64, 16, seed=8)
+    for b in range(-(-900 // 16)):
+        a, e = 16 * b, min(900, 16 * b + 16)
+        pid = int(p2.table[0, b])
+        if pid < 0 or pid >= p2.k_cache.shape[0]:
+            continue
+        p2.k_cache[pid, :, :e - a] = (p.K[0][:, a:e].float() * ramp[:, a:e]).bfloat16()
+    p2.K[0] = (p.K[0].float() * ramp).bfloat16()
+    run(p2)
+
+
+@pytest.mark.parametrize("q", [1, 40])
+def test_visible_nan_and_infinite_keys_reach_only_their_rows(q):
+    p = Problem([q], [200], 2, 1, 64, 16, window=60, seed=9)
+    base = [t.clone() for t in p.call(ops)]
+    pid = int(p.table[0, 150 // 16])
+    p.k_cache[pid, 0, 150 % 16, 3] = float("nan")
+    got = p.call(ops)
+    torch.cuda.synchronize()
+    for i in range(q):
+        pos = 200 - q + i
+        hit = pos - 60 < 150 <= pos
+        assert got[0][i].isnan().all() == hit and got[1][i].isnan().all() == hit
+        if not hit:
+            assert torch.equal(got[0][i], base[0][i]) and torch.equal(got[1][i], base[1][i])
+
+
+def test_long_context_split():
+    run(Problem([1, 1, 2], [20000, 9000, 12345], 4, 1, 128, 64, seed=10), max_q=2)
+    run(Problem([48, 20], [9000, 5000], 4, 1, 128, 64, seed=11))
+
+
+def test_lse_is_optional_and_out_is_made():
+    p = Problem([3, 20], [50, 60], 4, 2, 64, 16, seed=12)
+    out = ops.window_attention(p.q, p.k_cache, p.v_cache, p.table, p.q_start, p.kv_len, p.window)
+    both = ops.window_attention(p.q, p.k_cache, p.v_cache, p.table, p.q_start, p.kv_len, p.window, lse=True)
+    assert torch.equal(out, both[0])
+    p.check(both)
+
+
+def test_bad_indices_leave_their_sequence_out():
+    p = Problem([1, 1, 1, 1], [40, 40, 40, 40], 4, 2, 64, 16, seed=13, poison=False)
+    want = p.call(ops)[0].clone()
+    p.table[1, 1] = p.k_cache.shape[0]       # one past the last page
+    got = p.call(ops)[0]
+    torch.cuda.synchronize()
+    assert ops.device_status() == 8
+    keep = [0, 2, 3]
+    assert torch.equal(got[keep], want[keep]) and got[1].isfinite().all()
+    p.table[1, 1] = -1
+    p.call(ops)
+    torch.cuda.synchronize()
+    assert ops.device_status() == 8
+
+
+@pytest.mark.parametrize("starts", [[0, 2, 1, 3, 4], [0, 1, 2, 3, 5], [-1, 1, 2, 3, 4], [0, 1, 2, 3, 1 << 30]])
+def test_bad_query_starts_leave_their_sequence_out(starts):
+    p = Problem([1] * 4, [40] * 4, 4, 2, 64, 16, seed=14)
+    want = p.call(ops)[0].clone()
+    p.q_start.copy_(torch.tensor(starts, dtype=torch.int32))
+    out = p.call(ops)[0]
+    torch.cuda.synchronize()
+    assert ops.device_status() == 8
+    if starts[:3] == [0, 1, 2]:
+        assert torch.equal(out[:3], want[:3]) and (out[3] == SENTINEL).all()
+
+
+def test_bad_lengths_and_max_q():
+    p = Problem([1, 1, 20], [40, 40, 40], 4, 2, 64, 16, seed=15, poison=False)
+    p.kv_len.copy_(torch.tensor([-5, 40, 1 << 30], dtype=torch.int32))
+    out, lse = p.call(ops, max_q=19)
+    torch.cuda.synchronize()
+    assert ops.device_status() == 8
+    assert (out[0] == 0).all() and (lse[0] == float("-inf")).all()   # no keys
+    assert (out[2:] == SENTINEL).all()                               # more than max_q rows
+    assert not (out[1] == SENTINEL).any()
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_batch_invariance(hd):
+    """A sequence's bits are the same alone, in a batch, with another page size
+    and with another bound."""
+    q, kv = [1, 300, 3, 40, 1], [777, 900, 2000, 1500, 5000]
+    kw = dict(H=8, Hkv=2, hd=hd, window=1100, sinks=20, seed=16)
+    p = Problem(q, kv, page=16, **kw)
+    out, lse = p.call(ops)
+    p2 = Problem(q, kv, page=128, **kw)
+    out2, lse2 = p2.call(ops, max_q=300)
+    assert same(out, out2) and torch.equal(lse, lse2)
+    t0 = 0
+    for s, n in enumerate(q):
+        o1 = torch.empty_like(out[t0:t0 + n])
+        l1 = torch.empty_like(lse[t0:t0 + n])
+        ops.window_attention(p.q[t0:t0 + n], p.k_cache, p.v_cache, p.table[s:s + 1],
+                             torch.tensor([0, n], dtype=torch.int32, device="cuda"), p.kv_len[s:s + 1],
+                             1100, sinks=20, scale=p.scale, max_q=n, out=o1, lse=l1)
+        assert same(o1, out[t0:t0 + n]) and torch.equal(l1, lse[t0:t0 + n]), s
+        t0 += n
+
+
+@pytest.mark.parametrize("q,kv", [([1] * 5, [700, 1, 64, 5000, 333]), ([1, 200, 30], [900, 300, 4000])])
+def test_graph_replay_and_other_stream(q, kv):
+    p = Problem(q, kv, 8, 2, 128, 32, 800, 4, seed=17)
+    want = [t.clone() for t in p.call(ops)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = p.call(ops)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    outs = [torch.zeros_like(want[0]), torch.zeros_like(want[1])]
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            p.call(ops, out=outs[0], lse=outs[1])
+        graphs.append(gr)
+    for gr in graphs + graphs:
+        outs[0].fill_(SENTINEL)
+        outs[1].fill_(SENTINEL)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("chunk,window,sinks", [(1, 40, 4), (1, 1 << 20, 0), (24, 49, 10)])
+def test_steps_with_the_cache_writer(chunk, window, sinks):
+    """Both operators as a model uses them: two sequences advance by prompts,
+    single tokens or chunks; every output against the attention of the whole
+    sequence so far in 64 bits, keys as the cache holds them."""
+    H, Hkv, hd, page, S, M = 4, 2, 64, 16, 2, 20
+    rng = random.Random(18)
+    g = torch.Generator(device="cuda").manual_seed(18)
+    pages = list(range(S * M))
+    rng.shuffle(pages)
+    table = torch.tensor(pages, dtype=torch.int32, device="cuda").view(S, M)
+    kc, vc = (torch.full((S * M, Hkv, page, hd), float("nan"), dtype=torch.bfloat16, device="cuda")
+              for _ in range(2))
+    rope = torch.from_numpy(synth.rope_table(512, hd)).cuda()
+    w = (1 + 0.1 * torch.randn(2, hd, generator=g, device="cuda")).bfloat16()
+    lens = [0, 0]
+    keep_k, keep_v = [[], []], [[], []]
+    steps = [(48, 24), (24, 24), (24, 24), (24, 48)] if chunk > 1 else [(70, 3), (1, 1), (1, 1), (2, 30), (1, 1)]
+    for add in steps:
+        N = sum(add)
+        qkv = torch.randn(N, (H + 2 * Hkv) * hd, generator=g, device="cuda").bfloat16()
+        pos = [lens[s] + i for s in range(S) for i in range(add[s])]
+        slot = [int(table[s, (lens[s] + i) // page]) * page + (lens[s] + i) % page
+                for s in range(S) for i in range(add[s])]
+        lens = [a + b for a, b in zip(lens, add)]
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+        q = ops.qk_norm_rope_cache(qkv[:, :H * hd], qkv[:, H * hd:(H + Hkv) * hd], qkv[:, (H + Hkv) * hd:],
+                                   w[0], w[1], rope, i32(pos), i32(slot), kc, vc, EPS, neox=True)
+        out, lse = ops.window_attention(q, kc, vc, table, i32([0, add[0], N]), i32(lens), window,
+                                        sinks=sinks, chunk=chunk, lse=True)
+        p = Problem(add, lens, H, Hkv, hd, page, window, sinks, chunk, seed=0, poison=False)
+        p.q = q
+        for s in range(S):
+            ids = table[s, :-(-lens[s] // page)].long()
+            p.K[s] = kc[ids].transpose(0, 1).reshape(Hkv, -1, hd)[:, :lens[s]]
+            p.V[s] = vc[ids].transpose(0, 1).reshape(Hkv, -1, hd)[:, :lens[s]]
+            assert p.K[s].isfinite().all() and p.V[s].isfinite().all()
+        p.check((out, lse), f"after {lens}")
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^32 bytes whose used pages lie at its end."""
+    hd, page, Hkv = 128, 64, 8
+    pages = (1 << 32) // (Hkv * page * hd * 2) + 40
+    kc = torch.zeros((pages, Hkv, page, hd), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    p = Problem([1, 30], [500, 100], 16, Hkv, hd, page, seed=19)
+    n = p.k_cache.shape[0]
+    kc[-n:], vc[-n:] = p.k_cache, p.v_cache
+    live = (p.table >= 0) & (p.table < n)
+    p.table.copy_(torch.where(live, p.table + (pages - n), p.table))
+    p.k_cache, p.v_cache = kc, vc
+    run(p)
+    r = rope_problem(20, 16, Hkv, hd, page, 20)
+    small = r["caches"][0].shape[0]
+    kc[-small:], vc[-small:] = r["caches"][0], r["caches"][1]
+    first = dict(r, caches=[kc, vc], slots=(r["slots"] + (pages - small) * page).astype(np.int32))
+    got = rope_call(first, True)
+    rope_check(dict(r, caches=[kc[-small:].clone(), vc[-small:].clone()]), got, True)
