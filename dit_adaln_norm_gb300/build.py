@@ -19,7 +19,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdan.so")
 SOURCES = ["dan_rows_rms.cu", "dan_rows_gated.cu", "dan_rows_ln.cu", "dan_rows_lnfp8.cu",
            "dan_rows_gatedln.cu", "dan_qk.cu", "dan_resid_t.cu", "dan_abi.cu", "dan_noalloc.cu",
-           "dan_cache_rope.cu", "dan_attn_step.cu", "dan_cache_abi.cu"]
+           "dan_cache_rope.cu", "dan_attn_step.cu", "dan_attn_tile.cu",
+           "dan_cache_abi.cu"]
 HEADERS = ["dan_device.cuh", "dan_internal.h", "dan_ring.cuh", "dan_rows.cuh",
            "dan_attn.cuh", "dan_attn_tma.cuh"]
 

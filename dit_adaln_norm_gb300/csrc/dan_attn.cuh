@@ -91,7 +91,13 @@ struct AttnParams {
     // partial results (see PartLayout)
     float *part_o;
     float2 *part_ml;
-    int64_t part_cap; // rows of a (sequence, key head), or 0: rows by query token
+    int64_t part_cap; // rows of a (sequence, key head), or 0: room by query row,
+    int part_splits;  // that many for each
+    // work of the tile kernel (see its plan)
+    int4 *items;
+    int2 *split_tiles;
+    int *plan_head;
+    int items_cap, split_tiles_cap;
     unsigned *status;
     unsigned long long limit_ns;
 };
@@ -184,11 +190,41 @@ __device__ __forceinline__ int step_split_blocks(int count)
 __device__ __forceinline__ int64_t part_base(const AttnParams &p, int s, const SeqInfo &q, int u)
 {
     if (p.part_cap) return ((int64_t)s * p.Hkv + u) * p.part_cap;
-    return ((int64_t)q.q0 * p.H + (int64_t)u * q.n * p.g) * kMaxSplits;
+    return ((int64_t)q.q0 * p.H + (int64_t)u * q.n * p.g) * p.part_splits;
 }
 
-// Launch the step kernel and, where a sequence may be split, the join.
+// The tile kernel's rows: tiles of 256 of a sequence's (token, query head)
+// rows.  Keys that some row of a tile sees:
+constexpr int kTileRows = 256;
+constexpr int kPlanBuckets = 2048;
+
+__device__ __forceinline__ RowRange tile_union(const AttnParams &p, const SeqInfo &q, int tile)
+{
+    const int rb = tile * kTileRows, end = min(q.n * p.g, rb + kTileRows), pos0 = q.L - q.n;
+    return rows_union(p, pos0 + rb / p.g, pos0 + (end - 1) / p.g, q.L);
+}
+
+// Key blocks (128 keys) of a split of a tile that sees `count` of them, in a
+// sequence of `tiles` tiles: split only where the sequence alone has fewer
+// than half of kTileSplitTarget items, and not below 8 blocks.
+constexpr int kTileSplitTarget = 128;
+constexpr int kTileMaxSplits = 16;
+constexpr int kTileMinBlocks = 8;
+
+__device__ __forceinline__ int tile_split_blocks(const AttnParams &p, int tiles, int count)
+{
+    const int64_t items = (int64_t)tiles * p.Hkv;
+    int n = items > kTileSplitTarget ? 1 : min(kTileMaxSplits, kTileSplitTarget / (int)items);
+    n = min(n, count / kTileMinBlocks);
+    return n <= 1 ? max(1, count) : (count + n - 1) / n;
+}
+
+// Launch one kernel each: sequences of at most kStepRows rows, split at most
+// `splits` ways; the others (with the plan before it); the join of splits.
 cudaError_t launch_attention_step(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
                                   const CUtensorMap &vmap, int splits, cudaStream_t s);
+cudaError_t launch_attention_tile(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
+                                  const CUtensorMap &vmap, cudaStream_t s);
+cudaError_t launch_attention_join(const AttnParams &p, int head_dim, bool tiles, cudaStream_t s);
 
 } // namespace dan

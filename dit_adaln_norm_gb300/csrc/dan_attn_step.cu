@@ -1,13 +1,14 @@
 // dan_attn_step.cu -- attention over the paged cache for sequences with few
 // query rows (n_s * heads/kv_heads <= 16): a decoded token, or a few drafted
-// ones; and the join of split results.
+// ones; and the join of split
+// results of both kernels.
 //
 // Mathematics: o = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m) with
 // x_j = scale * log2(e) * q.k_j and a running maximum m, one pass over the
 // keys.  Every key and value is read once for all query heads that share it;
 // at 16 rows the arithmetic per byte is small and the bound is memory.
 //
-// One CTA has one (sequence, key head, tile of 16 rows, split).  Its four warps take blocks of
+// One CTA has one (sequence, key head, split).  Its four warps take blocks of
 // 16 keys in turn, each with its own ring of TMA-filled slots, its own running
 // maximum, sum and output; nothing but the end joins them.  The 16 query rows
 // are the rows of m16n8k16 products.  TMA brings a block's K and V with the
@@ -36,7 +37,7 @@ struct StepShape {
 
 template <int HD>
 __global__ void __launch_bounds__(32 * kStepWarps)
-    window_attention_step_kernel(const AttnParams p, int tiles, const __grid_constant__ CUtensorMap kmap,
+    window_attention_step_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap,
                                  const __grid_constant__ CUtensorMap vmap)
 {
     using Sh = StepShape<HD>;
@@ -57,32 +58,29 @@ __global__ void __launch_bounds__(32 * kStepWarps)
     allow_dependents();
 
     const int u = blockIdx.x % p.Hkv;
-    const int tile = blockIdx.x / p.Hkv % tiles, s = blockIdx.x / p.Hkv / tiles, split = blockIdx.y;
+    const int s = blockIdx.x / p.Hkv, split = blockIdx.y;
     const SeqInfo q = seq_info(p, s);
-    if (q.bad && split == 0 && u == 0 && tile == 0 && threadIdx.x == 0)
-        set_status(p.status, kStatusIndex);
-    const int64_t R64 = (int64_t)q.n * p.g - (int64_t)tile * kStepRows;
-    if (R64 <= 0) return;
-    const bool few = (int64_t)q.n * p.g <= kStepRows;
-    const int R = R64 < kStepRows ? (int)R64 : kStepRows, rb = tile * kStepRows;
+    if (q.bad && split == 0 && u == 0 && threadIdx.x == 0) set_status(p.status, kStatusIndex);
+    const int R = q.n * p.g;
+    if (R == 0 || R > kStepRows) return;
     const int pos0 = q.L - q.n;
-    const RowRange all = rows_union(p, pos0 + rb / p.g, pos0 + (rb + R - 1) / p.g, q.L);
+    const RowRange all = rows_union(p, pos0, q.L - 1, q.L);
     const KeyBlocks<kStepShift> kb(all);
-    const int per = few ? step_split_blocks(kb.count) : max(1, kb.count);
+    const int per = step_split_blocks(kb.count);
     const int nsplit = max(1, (kb.count + per - 1) / per);
     if (split >= nsplit) return;
     const int b0 = split * per, b1 = min(kb.count, b0 + per);
 
     // the lane's two rows of the products, and its two columns of each tile
     const int r0 = lane >> 2, r1 = r0 + 8, c2 = (lane & 3) * 2;
-    const RowRange rr0 = r0 < R ? row_range(p, pos0 + (rb + r0) / p.g, q.L) : RowRange{0, 0, 0};
-    const RowRange rr1 = r1 < R ? row_range(p, pos0 + (rb + r1) / p.g, q.L) : RowRange{0, 0, 0};
+    const RowRange rr0 = r0 < R ? row_range(p, pos0 + r0 / p.g, q.L) : RowRange{0, 0, 0};
+    const RowRange rr1 = r1 < R ? row_range(p, pos0 + r1 / p.g, q.L) : RowRange{0, 0, 0};
 
     uint32_t qf[KS][4];
     {
         const uint32_t *qb = reinterpret_cast<const uint32_t *>(p.q);
-        const int64_t a0 = ((int64_t)(q.q0 + (rb + r0) / p.g) * p.q_stride8 + (u * p.g + (rb + r0) % p.g) * (HD / 8)) * 4;
-        const int64_t a1 = ((int64_t)(q.q0 + (rb + r1) / p.g) * p.q_stride8 + (u * p.g + (rb + r1) % p.g) * (HD / 8)) * 4;
+        const int64_t a0 = ((int64_t)(q.q0 + r0 / p.g) * p.q_stride8 + (u * p.g + r0 % p.g) * (HD / 8)) * 4;
+        const int64_t a1 = ((int64_t)(q.q0 + r1 / p.g) * p.q_stride8 + (u * p.g + r1 % p.g) * (HD / 8)) * 4;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
             const int c = k * 8 + (lane & 3);
@@ -264,7 +262,7 @@ __global__ void __launch_bounds__(32 * kStepWarps)
             a.w = fmaf(f, v.w, a.w);
         }
         if (nsplit == 1) {
-            write_row<HD>(p, q.q0 + (rb + r) / p.g, u * p.g + (rb + r) % p.g, c, a, m, l);
+            write_row<HD>(p, q.q0 + r / p.g, u * p.g + r % p.g, c, a, m, l);
         } else {
             *reinterpret_cast<float4 *>(p.part_o + (base + r) * HD + c) = a;
             if (c == 0) p.part_ml[base + r] = make_float2(m, l);
@@ -272,23 +270,12 @@ __global__ void __launch_bounds__(32 * kStepWarps)
     }
 }
 
-// Join a sequence's split results, one warp per row, in split order.
+// Join one row's split results, in split order: a warp, four columns a lane.
 template <int HD>
-__global__ void __launch_bounds__(128) window_attention_join_kernel(const AttnParams p)
+__device__ __forceinline__ void join_row(const AttnParams &p, int s, const SeqInfo &q, int u, int r,
+                                         int nsplit)
 {
-    grid_dependency_wait();
-    allow_dependents();
-    const int u = blockIdx.x % p.Hkv, s = blockIdx.x / p.Hkv;
-    const SeqInfo q = seq_info(p, s);
-    const int64_t R64 = (int64_t)q.n * p.g;
-    const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 5);
-    if (r >= R64 || R64 > kStepRows) return;
-    const int R = (int)R64;
-    const KeyBlocks<kStepShift> kb(rows_union(p, q.L - q.n, q.L - 1, q.L));
-    const int per = step_split_blocks(kb.count);
-    const int nsplit = max(1, (kb.count + per - 1) / per);
-    if (nsplit == 1) return;
+    const int lane = threadIdx.x & 31, c = lane * 4, R = q.n * p.g;
     const int64_t base = part_base(p, s, q, u) + r;
     const float2 ml = lane < nsplit ? p.part_ml[base + (int64_t)lane * R] : make_float2(-INFINITY, 0.0f);
     float m = ml.x;
@@ -297,7 +284,6 @@ __global__ void __launch_bounds__(128) window_attention_join_kernel(const AttnPa
     const float f = exp2_fast(ml.x - (m == -INFINITY ? 0.0f : m));
     float l = 0.0f;
     float4 a = make_float4(0, 0, 0, 0);
-    const int c = lane * 4;
     for (int k = 0; k < nsplit; ++k) {
         const float fk = __shfl_sync(kFull, f, k);
         l = fmaf(fk, __shfl_sync(kFull, ml.y, k), l);
@@ -309,7 +295,43 @@ __global__ void __launch_bounds__(128) window_attention_join_kernel(const AttnPa
             a.w = fmaf(fk, v.w, a.w);
         }
     }
-    if (c < HD) write_row<HD>(p, q.q0 + (int)r / p.g, u * p.g + (int)r % p.g, c, a, m, l);
+    if (c < HD) write_row<HD>(p, q.q0 + r / p.g, u * p.g + r % p.g, c, a, m, l);
+}
+
+// The first step_blocks blocks take four rows each of a (sequence, key head)
+// of the step kernel; the others the split tiles of the tile kernel.
+template <int HD>
+__global__ void __launch_bounds__(128) window_attention_join_kernel(const AttnParams p, int step_blocks)
+{
+    grid_dependency_wait();
+    allow_dependents();
+    const int warp = threadIdx.x >> 5;
+    if ((int)blockIdx.x < step_blocks) {
+        constexpr int RB = kStepRows / 4;
+        const int r = (int)(blockIdx.x % RB) * 4 + warp, su = blockIdx.x / RB;
+        const int u = su % p.Hkv, s = su / p.Hkv;
+        const SeqInfo q = seq_info(p, s);
+        const int R = q.n * p.g;
+        if (r >= R || R > kStepRows) return;
+        const KeyBlocks<kStepShift> kb(rows_union(p, q.L - q.n, q.L - 1, q.L));
+        const int per = step_split_blocks(kb.count);
+        const int nsplit = (kb.count + per - 1) / per;
+        if (nsplit > 1) join_row<HD>(p, s, q, u, r, nsplit);
+        return;
+    }
+    constexpr int RB = kTileRows / 4;
+    const int64_t work = (int64_t)p.plan_head[1] * p.Hkv * RB;
+    for (int64_t w = blockIdx.x - step_blocks; w < work; w += gridDim.x - step_blocks) {
+        const int2 st = p.split_tiles[w / RB / p.Hkv];
+        if (st.x < 0) continue;
+        const int u = (int)(w / RB % p.Hkv);
+        const SeqInfo q = seq_info(p, st.x);
+        const int total = q.n * p.g, r = st.y * kTileRows + (int)(w % RB) * 4 + warp;
+        if (r >= total) continue;
+        const int count = KeyBlocks<7>(tile_union(p, q, st.y)).count;
+        const int per = tile_split_blocks(p, (total + kTileRows - 1) / kTileRows, count);
+        join_row<HD>(p, st.x, q, u, r, (count + per - 1) / per);
+    }
 }
 
 namespace {
@@ -320,17 +342,20 @@ cudaError_t launch_step_hd(const AttnParams &p, const CUtensorMap &kmap, const C
 {
     auto fn = window_attention_step_kernel<HD>;
     const int smem = StepShape<HD>::SMEM;
-    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
+    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = ((int64_t)p.max_q * p.g + kStepRows - 1) / kStepRows;
-    if (tiles * p.S * p.Hkv > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    e = launch_overlapped_2d(fn, dim3((unsigned)(tiles * p.S * p.Hkv), (unsigned)splits),
-                             32 * kStepWarps, smem, s, p, (int)tiles, kmap, vmap);
-    if (e != cudaSuccess || splits == 1) return e;
-    const int rows = (int)(p.max_q * (int64_t)p.g < kStepRows ? p.max_q * p.g : kStepRows);
-    return launch_overlapped_2d(window_attention_join_kernel<HD>,
-                                dim3((unsigned)(p.S * p.Hkv), (unsigned)((rows + 3) / 4)), 128, 0,
-                                s, p);
+    return launch_overlapped_2d(fn, dim3((unsigned)(p.S * p.Hkv), (unsigned)splits), 32 * kStepWarps,
+                                smem, s, p, kmap, vmap);
+}
+
+template <int HD>
+cudaError_t launch_join_hd(const AttnParams &p, bool tiles, cudaStream_t s)
+{
+    const int64_t step = (int64_t)p.S * p.Hkv * (kStepRows / 4);
+    const int64_t grid = step + (tiles ? 4 * sm_count() : 0);
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    return launch_overlapped_2d(window_attention_join_kernel<HD>, dim3((unsigned)grid), 128, 0, s, p,
+                                (int)step);
 }
 
 } // namespace
@@ -340,6 +365,11 @@ cudaError_t launch_attention_step(const AttnParams &p, int head_dim, const CUten
 {
     return head_dim == 64 ? launch_step_hd<64>(p, kmap, vmap, splits, s)
                           : launch_step_hd<128>(p, kmap, vmap, splits, s);
+}
+
+cudaError_t launch_attention_join(const AttnParams &p, int head_dim, bool tiles, cudaStream_t s)
+{
+    return head_dim == 64 ? launch_join_hd<64>(p, tiles, s) : launch_join_hd<128>(p, tiles, s);
 }
 
 } // namespace dan

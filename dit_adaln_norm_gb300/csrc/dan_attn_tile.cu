@@ -1,0 +1,733 @@
+// dan_attn_tile.cu -- attention over the paged cache for sequences with more
+// than 16 query rows (n_s * heads/kv_heads): prompts, chunks, long drafts.
+//
+// Mathematics: the same one-pass softmax as the step kernel.  Rows are
+// (token, query head of the group) pairs, tokens outermost, so that a tile
+// of rows shares its keys; 4 * hd flops per (row, key) against 2 * 2 * hd
+// bytes per key for 256 rows: the bound is the tensor cores, and beside them
+// one exponential per (row, key).
+//
+// One persistent CTA per SM, work items (sequence, 256-row tile, split, key
+// head) from a list that a planning kernel wrote, longest first, taken in
+// turn from a counter.  Roles:
+//   warps 0-3, 4-7  softmax of row tiles A and B (128 rows each, a row per
+//                   thread): scores out of TMEM, probabilities back into it
+//   warp 8          issues every tcgen05 product
+//   warp 9          takes the items and brings K and V by TMA (128 keys each)
+//   warps 10, 11    bring the item's query rows
+// Per 128 keys and row tile: S = Q K^T (operands in shared memory, result in
+// TMEM), softmax, P (bf16) over S's columns in TMEM, O += P V with P read
+// from TMEM.  The tensor pipe runs in issue order: O_A(j), S_A(j+1), O_B(j),
+// S_B(j+1), so each tile's softmax has the other tile's two products to hide
+// behind.  The completion of S(j+1) implies that of O(j).
+//
+// The running maximum is raised only when a row's new maximum passes it by
+// more than 8 (a factor of 256 in the sums, far inside fp32 and bf16 range):
+// a choice of each row alone, so bits do not depend on its neighbours.
+#include "dan_device.cuh"
+#include "dan_internal.h"
+#include "dan_attn.cuh"
+#include "dan_attn_tma.cuh"
+#include "dan_ring.cuh"
+
+namespace dan {
+
+constexpr int kTileThreads = 384;
+constexpr int kTileItems = 2; // item slots between warp 9 and the others
+
+template <int HD>
+struct TileShape {
+    static constexpr int HALVES = HD / 64;
+    static constexpr int HALF = 128 * 128;       // 128 rows of 128 bytes
+    static constexpr int MAT = HALVES * HALF;    // Q tile, K tile or V tile
+    static constexpr int STAGES = HD == 128 ? 5 : 10;
+    static constexpr int Q_OFF = 0;
+    static constexpr int KV_OFF = 2 * MAT;
+    static constexpr int BAR_OFF = KV_OFF + STAGES * MAT;
+    static constexpr int SMEM = BAR_OFF + 512 + 1024;
+    // TMEM columns
+    static constexpr int S_COL = 0;   // S_A, S_B: 128 each; P over the first 64 of each
+    static constexpr int O_COL = 256; // O_A, O_B: HD each
+};
+
+struct TileBars {
+    uint64_t kv_full[10], kv_empty[10];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t item_full[kTileItems], item_empty[kTileItems];
+    uint64_t drain;
+    int4 item[kTileItems]; // sequence (-1: no more), tile, split, key head
+    uint32_t tmem;
+};
+static_assert(sizeof(TileBars) <= 512, "barrier area");
+
+// What a role needs to know of an item.
+struct TileItem {
+    int s, u, tile, split, nsplit;
+    SeqInfo q;
+    int rb, R;          // first row of the sequence, rows of this tile (1..256)
+    int pos0;           // position of the sequence's first query
+    RowRange all;       // keys that the tile's rows see
+    KeyBlocks<7> kb;
+    int b0, b1;         // key blocks of this split
+    __device__ __forceinline__ TileItem(const AttnParams &p, const int4 &it)
+        : s(it.x), u(it.w), tile(it.y), split(it.z), q(seq_info(p, it.x)), rb(it.y * 256),
+          pos0(q.L - q.n), all(tile_union(p, q, it.y)), kb(all)
+    {
+        const int total = q.n * p.g;
+        R = min(256, total - rb);
+        const int per = tile_split_blocks(p, (total + 255) / 256, kb.count);
+        nsplit = max(1, (kb.count + per - 1) / per);
+        b0 = split * per;
+        b1 = min(kb.count, b0 + per);
+    }
+};
+
+// ------------------------------------------------------- tcgen05 primitives
+
+__device__ __forceinline__ void tc_fence_before()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after()
+{
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// Arrive on `bar` when every product issued so far by this thread is done.
+__device__ __forceinline__ void tc_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle.  sbo: bytes between
+// groups of 8 rows of 128 bytes; lbo: bytes between 64-column blocks of a
+// matrix whose columns are the contiguous dimension (else unused).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(lbo >> 4) << 16) |
+           ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: bf16 x bf16 -> fp32, M = 128; b_cols: B's columns
+// are its contiguous dimension.
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_cols)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_cols ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           (8u << 24);
+}
+
+#define DAN_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), \
+                     "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
+#define DAN_I8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), \
+                     "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+
+// 32 columns of this warp's 32 lanes (a lane per thread).
+__device__ __forceinline__ void tc_ld32(uint32_t *r, uint32_t addr)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : DAN_R8(r, 0), DAN_R8(r, 8), DAN_R8(r, 16), DAN_R8(r, 24)
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+                 DAN_I8(r, 0), DAN_I8(r, 8), DAN_I8(r, 16), DAN_I8(r, 24)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+                 DAN_I8(r, 0), DAN_I8(r, 8)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk2(a)), "l"(pk2(b)), "l"(pk2(c)));
+    return upk2(r);
+}
+
+// ------------------------------------------------------------------- plan
+
+// Work lists: items (sequence, tile, split, -) longest first, and the tiles
+// that are split.  head: [0] items, [1] split tiles, [2] next item * Hkv + u.
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads) window_attention_plan_kernel(const AttnParams p)
+{
+    __shared__ int s_first[kPlanThreads + 1]; // first tile of each sequence of the chunk
+    __shared__ int s_warp[32];
+    __shared__ int s_hist[kPlanBuckets];
+    __shared__ int s_split;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < kPlanBuckets; i += kPlanThreads) s_hist[i] = 0;
+    if (tid == 0) s_split = 0;
+    grid_dependency_wait();
+    allow_dependents();
+    __syncthreads();
+    for (int pass = 0; pass < 2; ++pass) { // count by length, then place
+        for (int s0 = 0; s0 < p.S; s0 += kPlanThreads) {
+            const int s = s0 + tid;
+            int tiles = 0;
+            if (s < p.S) {
+                const SeqInfo q = seq_info(p, s);
+                if (q.bad && pass == 0) set_status(p.status, kStatusIndex);
+                const int64_t rows = (int64_t)q.n * p.g;
+                tiles = rows > kStepRows ? (int)((rows + 255) / 256) : 0;
+            }
+            int x = tiles; // inclusive sum over the chunk
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) s_warp[warp] = x;
+            __syncthreads();
+            if (warp == 0) {
+                int w = s_warp[lane];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(kFull, w, o);
+                    if (lane >= o) w += y;
+                }
+                s_warp[lane] = w;
+            }
+            __syncthreads();
+            x += warp ? s_warp[warp - 1] : 0;
+            s_first[tid + 1] = x;
+            if (tid == 0) s_first[0] = 0;
+            __syncthreads();
+            const int total = s_first[kPlanThreads];
+            for (int e = tid; e < total; e += kPlanThreads) {
+                int lo = 0, hi = kPlanThreads; // the sequence whose tiles hold e
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_first[mid] <= e) lo = mid;
+                    else hi = mid;
+                }
+                const int seq = s0 + lo, tile = e - s_first[lo];
+                const SeqInfo q = seq_info(p, seq);
+                const int count = KeyBlocks<7>(tile_union(p, q, tile)).count;
+                const int per = tile_split_blocks(p, (q.n * p.g + 255) / 256, count);
+                const int nsplit = max(1, (count + per - 1) / per);
+                const int bucket = kPlanBuckets - 1 - min(kPlanBuckets - 1, min(per, count));
+                if (pass == 0) {
+                    atomicAdd(&s_hist[bucket], nsplit);
+                } else {
+                    // query starts that let sequences overlap may ask for more items
+                    // than N rows can have: what is past the lists is left out
+                    const int at = atomicAdd(&s_hist[bucket], nsplit);
+                    const int sp = nsplit > 1 ? atomicAdd(&s_split, 1) : 0;
+                    if (at + nsplit <= p.items_cap && (nsplit == 1 || sp < p.split_tiles_cap)) {
+                        for (int k = 0; k < nsplit; ++k) p.items[at + k] = make_int4(seq, tile, k, 0);
+                        if (nsplit > 1) p.split_tiles[sp] = make_int2(seq, tile);
+                    } else {
+                        set_status(p.status, kStatusIndex);
+                        for (int k = at; k < min(at + nsplit, p.items_cap); ++k)
+                            p.items[k] = make_int4(-2, 0, 0, 0);
+                        if (nsplit > 1 && sp < p.split_tiles_cap) p.split_tiles[sp] = make_int2(-1, 0);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        if (pass == 0) { // first place of each bucket
+            int v[kPlanBuckets / kPlanThreads], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kPlanBuckets / kPlanThreads; ++i) {
+                v[i] = s_hist[tid * (kPlanBuckets / kPlanThreads) + i];
+                sum += v[i];
+            }
+            int x = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) s_warp[warp] = x;
+            __syncthreads();
+            int before = x - sum;
+            for (int w = 0; w < warp; ++w) before += s_warp[w];
+#pragma unroll
+            for (int i = 0; i < kPlanBuckets / kPlanThreads; ++i) {
+                s_hist[tid * (kPlanBuckets / kPlanThreads) + i] = before;
+                before += v[i];
+            }
+            if (tid == kPlanThreads - 1) p.plan_head[0] = min(before, p.items_cap);
+            __syncthreads();
+        }
+    }
+    if (tid == 0) {
+        p.plan_head[1] = min(s_split, p.split_tiles_cap);
+        p.plan_head[2] = 0;
+    }
+}
+
+// ------------------------------------------------------------------- main
+
+// A wait of a role: false when it ran out (the role then leaves).
+__device__ __forceinline__ bool role_wait(const AttnParams &p, uint64_t *bar, unsigned parity)
+{
+    if (__all_sync(kFull, mbar_wait(bar, parity, p.limit_ns))) return true;
+    if ((threadIdx.x & 31) == 0) set_status(p.status, kStatusWaitFull);
+    return false;
+}
+
+template <int HD>
+__device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, uint32_t tmem)
+{
+    using Sh = TileShape<HD>;
+    const int t = threadIdx.x >> 7, wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int row = t * 128 + (threadIdx.x & 127);
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + Sh::S_COL + t * 128;
+    const uint32_t o_addr = tmem + lanes + Sh::O_COL + t * HD;
+    unsigned s_phase = 0, o_phase = 0;
+    for (int k = 0;; ++k) {
+        const int slot = k % kTileItems;
+        if (!role_wait(p, &B.item_full[slot], (k / kTileItems) & 1)) return;
+        const int4 raw = B.item[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.item_empty[slot]);
+        if (raw.x < 0) return;
+        const TileItem it(p, raw);
+        if (t == 1 && it.R <= 128) continue; // no rows in tile B
+        const int r = it.rb + row;           // row of the sequence
+        const bool live = row < it.R;
+        const RowRange rr = live ? row_range(p, it.pos0 + r / p.g, it.q.L) : RowRange{0, 0, 0};
+        float m = -INFINITY, l = 0.0f;
+        for (int j = it.b0; j < it.b1; ++j) {
+            const int key0 = it.kb.block(j) << 7;
+            if (!role_wait(p, &B.s_full[t], s_phase)) return;
+            s_phase ^= 1;
+            tc_fence_after();
+            uint32_t xs[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc_ld32(xs + 32 * c, s_addr + 32 * c);
+            tc_wait_ld();
+            float x[128];
+#pragma unroll
+            for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(xs[c]);
+            const int hi = rr.hi - key0, lo = rr.lo - key0, sink = rr.sink - key0;
+            const bool whole = hi >= 128 && (lo <= 0 || sink >= 128);
+            if (!__all_sync(kFull, whole)) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (!(c < hi && (c < sink || c >= lo))) x[c] = -INFINITY;
+            }
+            float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int c = 4; c < 128; c += 4)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[c + e]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+            const bool raise = top > m + 8.0f || (m == -INFINITY && top > m);
+            if (j > it.b0 && __any_sync(kFull, raise)) { // O(j-1) is complete (see above)
+                const float f = raise ? exp2_fast(m - top) : 1.0f;
+                l *= f;
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 32) {
+                    uint32_t o[32];
+                    tc_ld32(o, o_addr + c);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tc_st32(o_addr + c, o);
+                }
+            }
+            if (raise) m = top;
+            const float z = m == -INFINITY ? 0.0f : m;
+            const float2 sc = dup2(p.scale_log2), nz = dup2(-z);
+            float2 sum0 = make_float2(0, 0), sum1 = make_float2(0, 0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t pk[16]; // rounded to bf16 for the product with V; the sums are of the unrounded
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float2 v = fma2(make_float2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), sc, nz);
+                    v.x = exp2_fast(v.x);
+                    v.y = exp2_fast(v.y);
+                    if (e & 1) sum1 = add2(sum1, v);
+                    else sum0 = add2(sum0, v);
+                    pk[e] = pack_bf16(v.x, v.y);
+                }
+                tc_st16(s_addr + 16 * c, pk);
+            }
+            sum0 = add2(sum0, sum1);
+            l += sum0.x + sum0.y;
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.p_full[t]);
+        }
+        // The row's output, straight from TMEM: whole, or a split's part.
+        const bool any = it.b1 > it.b0;
+        if (any) {
+            if (!role_wait(p, &B.o_full[t], o_phase)) return;
+            o_phase ^= 1;
+            tc_fence_after();
+        }
+        const bool part = it.nsplit > 1;
+        const float inv = part ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t orow = (int64_t)(it.q.q0 + r / p.g) * p.H + it.u * p.g + r % p.g;
+        const int64_t prow = part_base(p, it.s, it.q, it.u) + (int64_t)it.split * it.q.n * p.g + r;
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+            uint32_t o[32];
+            __syncwarp();
+            if (any) { // warp-uniform
+                tc_ld32(o, o_addr + c);
+                tc_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
+            if (live && part) {
+                float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * HD + c);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                         __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            } else if (live) {
+                uint4 *dst = p.out + (orow * HD + c) / 8;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint4 w;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        set_word(w, i, pack_bf16(__uint_as_float(o[8 * e + 2 * i]) * inv,
+                                                 __uint_as_float(o[8 * e + 2 * i + 1]) * inv));
+                    dst[e] = w;
+                }
+            }
+        }
+        if (live) {
+            if (part) p.part_ml[prow] = make_float2(m, l);
+            else if (p.lse) p.lse[orow] = row_lse(m, l);
+        }
+        if (any) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.o_empty[t]);
+        }
+    }
+}
+
+template <int HD>
+__device__ __forceinline__ void tile_mma(const AttnParams &p, TileBars &B, char *smem, uint32_t tmem)
+{
+    using Sh = TileShape<HD>;
+    const int lane = threadIdx.x & 31;
+    constexpr uint32_t id_s = tc_idesc(128, false), id_o = tc_idesc(HD, true);
+    const uint32_t base = smem_addr(smem);
+    uint64_t qd[2];
+    for (int t = 0; t < 2; ++t) qd[t] = tc_desc(base + Sh::Q_OFF + t * Sh::MAT, 16, 1024);
+    unsigned kv = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {1, 1};
+    auto full = [&](unsigned i) { return role_wait(p, &B.kv_full[i % Sh::STAGES], (i / Sh::STAGES) & 1); };
+    auto product_s = [&](int t, unsigned i) { // lane 0
+        const uint64_t kd = tc_desc(base + Sh::KV_OFF + (i % Sh::STAGES) * Sh::MAT, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+            const uint64_t off = (uint64_t)(((k >> 2) * Sh::HALF + (k & 3) * 32) >> 4);
+            tc_mma_ss(tmem + Sh::S_COL + t * 128, qd[t] + off, kd + off, id_s, k > 0);
+        }
+        tc_commit(&B.s_full[t]);
+    };
+    for (int k = 0;; ++k) {
+        const int slot = k % kTileItems;
+        if (!role_wait(p, &B.item_full[slot], (k / kTileItems) & 1)) return;
+        const int4 raw = B.item[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.item_empty[slot]);
+        if (raw.x < 0) return;
+        const TileItem it(p, raw);
+        const int nt = it.b1 - it.b0, last = it.R > 128 ? 1 : 0; // last active row tile
+        // every loaded query tile is released, used or not
+        for (int t = 0; t <= last; ++t) {
+            if (!role_wait(p, &B.q_full[t], q_phase[t])) return;
+            q_phase[t] ^= 1;
+            if (nt <= 0) {
+                if (lane == 0) mbar_arrive(&B.q_empty[t]);
+                continue;
+            }
+            if (t == 0 && !full(kv)) return;
+            tc_fence_after();
+            if (lane == 0) {
+                product_s(t, kv);
+                if (nt == 1) tc_commit(&B.q_empty[t]);
+                if (t == last) tc_commit(&B.kv_empty[kv % Sh::STAGES]);
+            }
+            __syncwarp();
+        }
+        for (int j = 0; j < nt; ++j) {
+            const unsigned vi = kv + 2 * j + 1, ki = vi + 1;
+            if (!full(vi)) return;
+            // value rows that no row of the tile sees may hold anything: zeros
+            const int key0 = it.kb.block(it.b0 + j) << 7;
+            if (key0 + 128 > it.all.hi || (key0 < it.all.lo && key0 + 128 > it.all.sink)) {
+                char *v = smem + Sh::KV_OFF + (vi % Sh::STAGES) * Sh::MAT;
+                for (int r = lane; r < 128; r += 32) {
+                    const int key = key0 + r;
+                    if (key >= it.all.hi || (key >= it.all.sink && key < it.all.lo))
+                        for (int c = 0; c < Sh::HALVES * 8; ++c)
+                            *reinterpret_cast<uint4 *>(v + (c >> 3) * Sh::HALF + r * 128 + (c & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            }
+            const uint64_t vd = tc_desc(base + Sh::KV_OFF + (vi % Sh::STAGES) * Sh::MAT, Sh::HALF, 1024);
+            for (int t = 0; t <= last; ++t) {
+                if (j == 0) { // the previous item's output of this tile has been read
+                    if (!role_wait(p, &B.o_empty[t], o_phase[t])) return;
+                    o_phase[t] ^= 1;
+                }
+                if (!role_wait(p, &B.p_full[t], p_phase[t])) return;
+                p_phase[t] ^= 1;
+                if (t == 0 && j + 1 < nt && !full(ki)) return;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma_ts(tmem + Sh::O_COL + t * HD, tmem + Sh::S_COL + t * 128 + k * 8,
+                                  vd + (uint64_t)(k * 2048 >> 4), id_o, j > 0 || k > 0);
+                    if (j + 1 == nt) tc_commit(&B.o_full[t]);
+                    if (t == last) tc_commit(&B.kv_empty[vi % Sh::STAGES]);
+                    if (j + 1 < nt) {
+                        product_s(t, ki);
+                        if (j + 2 == nt) tc_commit(&B.q_empty[t]);
+                        if (t == last) tc_commit(&B.kv_empty[ki % Sh::STAGES]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        kv += 2 * (nt > 0 ? nt : 0);
+    }
+}
+
+template <int HD>
+__device__ __forceinline__ void tile_load(const AttnParams &p, TileBars &B, char *smem,
+                                          const CUtensorMap &kmap, const CUtensorMap &vmap)
+{
+    using Sh = TileShape<HD>;
+    const int lane = threadIdx.x & 31;
+    const int total = p.plan_head[0] * p.Hkv;
+    const int box = min(128, 1 << p.page_shift), per = 128 / box; // pages of a key block
+    const int rows_total = (p.num_pages * p.Hkv) << p.page_shift;
+    unsigned kv = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+        int4 raw = make_int4(-1, 0, 0, 0);
+        do { // the next item (-2: one that the plan left out)
+            int w = 0;
+            if (lane == 0) w = atomicAdd(p.plan_head + 2, 1);
+            w = __shfl_sync(kFull, w, 0);
+            raw.x = -1;
+            if (w < total) {
+                raw = p.items[w / p.Hkv];
+                raw.w = w % p.Hkv;
+            }
+        } while (raw.x == -2);
+        const int slot = k % kTileItems;
+        if (!role_wait(p, &B.item_empty[slot], ((k / kTileItems) & 1) ^ 1)) break;
+        if (lane == 0) {
+            B.item[slot] = raw;
+            mbar_arrive(&B.item_full[slot]);
+        }
+        if (raw.x < 0) break;
+        const TileItem it(p, raw);
+        const int32_t *trow = p.table + (int64_t)it.s * p.table_stride;
+        // Lane l < per: first cache row of page l of key block j (a page that no
+        // row sees, or an id out of range: past the end, where the copy gives zeros)
+        auto cache_row = [&](int j) {
+            if (lane >= per || j >= it.b1) return rows_total;
+            const int key = (it.kb.block(j) << 7) + lane * box, end = key + box;
+            const bool see = (key < it.all.hi && end > it.all.lo) || key < it.all.sink;
+            if (!see) return rows_total;
+            const int page = __ldg(trow + (key >> p.page_shift));
+            if (page < 0 || page >= p.num_pages) {
+                set_status(p.status, kStatusIndex);
+                return rows_total;
+            }
+            return ((page * p.Hkv + it.u) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+        };
+        int rows = cache_row(it.b0);
+        for (int j = it.b0; j < it.b1 && ok; ++j) {
+            const int next = cache_row(j + 1); // in flight while this block's copies start
+#pragma unroll
+            for (int m = 0; m < 2; ++m, ++kv) {
+                const int st = kv % Sh::STAGES;
+                if (!role_wait(p, &B.kv_empty[st], ((kv / Sh::STAGES) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&B.kv_full[st], Sh::MAT);
+                __syncwarp();
+                if (lane < per) {
+                    char *dst = smem + Sh::KV_OFF + st * Sh::MAT + lane * box * 128;
+#pragma unroll
+                    for (int h = 0; h < Sh::HALVES; ++h)
+                        tma_load_2d(dst + h * Sh::HALF, m ? &vmap : &kmap, h * 64, rows, &B.kv_full[st]);
+                }
+                __syncwarp();
+            }
+            rows = next;
+        }
+    }
+    // copies still in flight (after a wait that ran out) land before the CTA ends
+    for (unsigned i = kv > Sh::STAGES ? kv - Sh::STAGES : 0; i < kv; ++i)
+        if (!mbar_wait(&B.kv_full[i % Sh::STAGES], (i / Sh::STAGES) & 1, p.limit_ns))
+            set_status(p.status, kStatusWaitDrain);
+}
+
+// Query rows into the swizzled tiles, rows past the sequence as zeros.
+template <int HD>
+__device__ __forceinline__ void tile_queries(const AttnParams &p, TileBars &B, char *smem)
+{
+    using Sh = TileShape<HD>;
+    constexpr int CH = HD / 8; // 16-byte chunks of a row
+    const int th = threadIdx.x - 320, lane = threadIdx.x & 31;
+    unsigned phase[2] = {1, 1};
+    for (int k = 0;; ++k) {
+        const int slot = k % kTileItems;
+        if (!role_wait(p, &B.item_full[slot], (k / kTileItems) & 1)) return;
+        const int4 raw = B.item[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.item_empty[slot]);
+        if (raw.x < 0) return;
+        const TileItem it(p, raw);
+        for (int t = 0; t < (it.R > 128 ? 2 : 1); ++t) {
+            if (!role_wait(p, &B.q_empty[t], phase[t])) return;
+            phase[t] ^= 1;
+            char *dst = smem + Sh::Q_OFF + t * Sh::MAT;
+            const int c = th % CH;
+            for (int r = th / CH; r < 128; r += 64 / CH) {
+                const int sr = it.rb + t * 128 + r;
+                char *at = dst + (c >> 3) * Sh::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                if (t * 128 + r < it.R)
+                    cp_async16(at, p.q + (int64_t)(it.q.q0 + sr / p.g) * p.q_stride8 +
+                                       (it.u * p.g + sr % p.g) * CH + c);
+                else
+                    *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
+            }
+            cp_async_commit();
+            cp_async_wait_all();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.q_full[t]);
+        }
+    }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    window_attention_tile_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                                 const __grid_constant__ CUtensorMap vmap)
+{
+    using Sh = TileShape<HD>;
+    extern __shared__ char smem_raw[];
+    char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    TileBars &B = *reinterpret_cast<TileBars *>(smem + Sh::BAR_OFF);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Sh::STAGES; ++i) {
+            mbar_init(&B.kv_full[i], 1);
+            mbar_init(&B.kv_empty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&B.q_full[t], 2);  // warps 10, 11
+            mbar_init(&B.q_empty[t], 1);
+            mbar_init(&B.s_full[t], 1);
+            mbar_init(&B.p_full[t], 4);  // the four softmax warps
+            mbar_init(&B.o_full[t], 1);
+            mbar_init(&B.o_empty[t], 4);
+        }
+        for (int i = 0; i < kTileItems; ++i) {
+            mbar_init(&B.item_full[i], 1);
+            mbar_init(&B.item_empty[i], 11); // every warp but 9
+        }
+        mbar_init(&B.drain, 1);
+        mbar_init_fence();
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_addr(&B.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = B.tmem;
+    grid_dependency_wait(); // the plan, and what came before it
+    allow_dependents();
+    if (warp < 8) {
+        tile_softmax<HD>(p, B, tmem);
+    } else if (warp == 8) {
+        tile_mma<HD>(p, B, smem, tmem);
+        // every product is done before the TMEM is given back
+        if ((threadIdx.x & 31) == 0) tc_commit(&B.drain);
+        __syncwarp();
+        if (!mbar_wait(&B.drain, 0, p.limit_ns)) set_status(p.status, kStatusWaitDrain);
+    } else if (warp == 9) {
+        tile_load<HD>(p, B, smem, kmap, vmap);
+    } else {
+        tile_queries<HD>(p, B, smem);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+namespace {
+
+template <int HD>
+cudaError_t launch_tile_hd(const AttnParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                           cudaStream_t s)
+{
+    auto fn = window_attention_tile_kernel<HD>;
+    const int smem = TileShape<HD>::SMEM;
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
+    if (e != cudaSuccess) return e;
+    e = launch_overlapped_2d(window_attention_plan_kernel, dim3(1), kPlanThreads, 0, s, p);
+    if (e != cudaSuccess) return e;
+    const int64_t work = (int64_t)p.items_cap * p.Hkv;
+    const int grid = (int)(work < sm_count() ? work : sm_count());
+    return launch_overlapped_2d(fn, dim3((unsigned)grid), kTileThreads, smem, s, p, kmap, vmap);
+}
+
+} // namespace
+
+cudaError_t launch_attention_tile(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
+                                  const CUtensorMap &vmap, cudaStream_t s)
+{
+    return head_dim == 64 ? launch_tile_hd<64>(p, kmap, vmap, s) : launch_tile_hd<128>(p, kmap, vmap, s);
+}
+
+} // namespace dan

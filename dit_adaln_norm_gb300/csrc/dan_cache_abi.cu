@@ -57,28 +57,51 @@ int step_splits(int64_t max_pages, int64_t page_size)
     return (int)(n < kMaxSplits ? n : kMaxSplits);
 }
 
-// Room for partial results: rows for each (sequence, key head) (cap), or for
-// each query row, whichever is less in all.
-struct PartRoom {
-    int64_t rows, cap;
+// What a call needs of the workspace: partial results of splits, with room
+// by (sequence, key head) (cap rows each) or by query row, whichever is less
+// in all, and the tile kernel's work lists.
+struct Room {
+    int splits = 1;     // most splits of a step sequence
+    bool tiles = false; // a sequence may have more rows than the step kernel takes
+    int64_t part_rows = 0, part_cap = 0, items = 0, split_tiles = 0;
+    int64_t part_bytes = 0, bytes = 0;
 };
 
-PartRoom part_room(int64_t N, int64_t S, int64_t heads, int64_t kv_heads, int64_t max_pages,
-                   int64_t page_size)
+Room room_for(int64_t N, int64_t S, int64_t heads, int64_t kv_heads, int64_t head_dim,
+              int64_t max_pages, int64_t page_size, int64_t max_q)
 {
-    const int splits = step_splits(max_pages, page_size);
-    if (splits == 1 || N == 0 || S == 0) return {0, 0};
-    const int64_t cap = (int64_t)kStepRows * splits;
-    const int64_t by_seq = S * kv_heads * cap, by_row = N * heads * kMaxSplits;
-    return by_seq <= by_row ? PartRoom{by_seq, cap} : PartRoom{by_row, 0};
+    Room r;
+    if (N == 0 || S == 0) return r;
+    const int64_t g = heads / kv_heads;
+    max_q = max_q < N ? max_q : N;
+    r.splits = step_splits(max_pages, page_size);
+    r.tiles = max_q * g > kStepRows;
+    int64_t cap = (int64_t)kStepRows * r.splits;
+    if (r.tiles) {
+        // sequences that the tile kernel takes, and the tiles of one that may be split
+        const int64_t long_seqs = S < N * g / kStepRows ? S : N * g / kStepRows;
+        const int64_t split_target = kTileSplitTarget / kv_heads;
+        r.items = N * g / kTileRows + long_seqs * (1 + split_target);
+        r.split_tiles = long_seqs * (1 + split_target / 2);
+        cap = cap > split_target * kTileRows ? cap : split_target * kTileRows;
+    }
+    if (r.splits > 1) {
+        const int64_t by_seq = S * kv_heads * cap, by_row = N * heads * r.splits;
+        r.part_cap = by_seq <= by_row ? cap : 0;
+        r.part_rows = by_seq <= by_row ? by_seq : by_row;
+        r.part_bytes = (r.part_rows * (head_dim * 4 + 8) + 15) / 16 * 16;
+    }
+    r.bytes = r.part_bytes + (r.tiles ? 16 * (r.items + 1) + 8 * r.split_tiles : 0);
+    return r;
 }
 
 } // namespace
 
 int64_t window_attention_workspace(int64_t N, int64_t S, int64_t heads, int64_t kv_heads,
-                                   int64_t head_dim, int64_t max_pages, int64_t page_size, int64_t)
+                                   int64_t head_dim, int64_t max_pages, int64_t page_size,
+                                   int64_t max_q)
 {
-    return part_room(N, S, heads, kv_heads, max_pages, page_size).rows * (head_dim * 4 + 8);
+    return room_for(N, S, heads, kv_heads, head_dim, max_pages, page_size, max_q).bytes;
 }
 
 cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
@@ -106,19 +129,36 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
     p.out = static_cast<uint4 *>(a.out);
     p.lse = a.lse;
-    const PartRoom room = part_room(a.N, a.S, a.heads, a.kv_heads, a.max_pages, a.page_size);
+    const Room room = room_for(a.N, a.S, a.heads, a.kv_heads, a.head_dim, a.max_pages, a.page_size,
+                               a.max_q);
+    if (room.items > 0x7FFFFFFF || room.split_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.part_o = static_cast<float *>(a.workspace);
-    p.part_ml = reinterpret_cast<float2 *>(p.part_o + room.rows * a.head_dim);
-    p.part_cap = room.cap;
+    p.part_ml = reinterpret_cast<float2 *>(p.part_o + room.part_rows * a.head_dim);
+    p.part_cap = room.part_cap;
+    p.part_splits = room.splits;
+    p.plan_head = reinterpret_cast<int *>(static_cast<char *>(a.workspace) + room.part_bytes);
+    p.items = reinterpret_cast<int4 *>(p.plan_head + 4);
+    p.split_tiles = reinterpret_cast<int2 *>(p.items + room.items);
+    p.items_cap = (int)room.items;
+    p.split_tiles_cap = (int)room.split_tiles;
     p.status = device_status();
     p.limit_ns = 1000000000ull;
     const int64_t rows = a.num_pages * a.kv_heads * a.page_size;
     CUtensorMap kmap, vmap;
-    if (!cache_map(&kmap, a.k_cache, rows, a.head_dim, 1 << kStepShift) ||
-        !cache_map(&vmap, a.v_cache, rows, a.head_dim, 1 << kStepShift))
+    const int hd = (int)a.head_dim;
+    if (room.tiles) {
+        const int box = (int)(a.page_size < 128 ? a.page_size : 128);
+        if (!cache_map(&kmap, a.k_cache, rows, hd, box) || !cache_map(&vmap, a.v_cache, rows, hd, box))
+            return cudaErrorInvalidValue;
+        const cudaError_t e = launch_attention_tile(p, hd, kmap, vmap, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (!cache_map(&kmap, a.k_cache, rows, hd, 1 << kStepShift) ||
+        !cache_map(&vmap, a.v_cache, rows, hd, 1 << kStepShift))
         return cudaErrorInvalidValue;
-    return launch_attention_step(p, (int)a.head_dim, kmap, vmap,
-                                 step_splits(a.max_pages, a.page_size), s);
+    const cudaError_t e = launch_attention_step(p, hd, kmap, vmap, room.splits, s);
+    if (e != cudaSuccess || room.splits == 1) return e;
+    return launch_attention_join(p, hd, room.tiles, s);
 }
 
 } // namespace dan
@@ -226,7 +266,7 @@ int validate_attention(const dan_bf16 *q, int64_t N, int64_t q_row_stride, const
         return DAN_EINVAL;
     if (!std::isfinite(scale) || scale <= 0.0f) return DAN_EINVAL;
     if (N > (int64_t(1) << 30) || S > (int64_t(1) << 20) ||
-        max_pages > (int64_t(1) << 30) / page_size)
+        N > (int64_t(1) << 30) / heads || max_pages > (int64_t(1) << 30) / page_size)
         return DAN_EUNSUPPORTED;
     if (N == 0 || S == 0) return DAN_OK;
     if (table_stride < max_pages || table_stride > kMaxElems / S) return DAN_EINVAL;
@@ -308,6 +348,7 @@ int64_t dan_window_attention_workspace(int64_t N, int64_t S, int64_t heads, int6
 {
     if (N < 0 || S < 0 || N > (int64_t(1) << 30) || S > (int64_t(1) << 20) || max_q < 0 ||
         check_cache(heads, kv_heads, head_dim, 1, page_size) != DAN_OK || max_pages < 1 ||
+        N > (int64_t(1) << 30) / heads ||
         max_pages > (int64_t(1) << 30) / page_size)
         return 0; // the call itself refuses these sizes
     return dan::window_attention_workspace(N, S, heads, kv_heads, head_dim, max_pages, page_size, max_q);
