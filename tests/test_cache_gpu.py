@@ -19,6 +19,10 @@ EPS = 1e-6
 def _setup():
     assert torch.cuda.is_available(), "GPU tests need CUDA"
     ops.load()
+
+
+@pytest.fixture(autouse=True)
+def _no_status_left():
     ops.device_status()
     yield
     torch.cuda.synchronize()
