@@ -23,7 +23,9 @@
 //
 // The running maximum is raised only when a row's new maximum passes it by
 // more than 8 (a factor of 256 in the sums, far inside fp32 and bf16 range):
-// a choice of each row alone, so bits do not depend on its neighbours.
+// a choice of each row alone, so bits do not depend on its neighbours.  So a
+// block's exponentials are taken with the standing maximum while the block's
+// own is still being found, and taken again in the rare block that raises it.
 #include "dan_device.cuh"
 #include "dan_internal.h"
 #include "dan_attn.cuh"
@@ -34,6 +36,7 @@ namespace dan {
 
 constexpr int kTileThreads = 384;
 constexpr int kTileItems = 2; // item slots between warp 9 and the others
+constexpr int kTileBarBytes = 768;
 
 template <int HD>
 struct TileShape {
@@ -44,10 +47,24 @@ struct TileShape {
     static constexpr int Q_OFF = 0;
     static constexpr int KV_OFF = 2 * MAT;
     static constexpr int BAR_OFF = KV_OFF + STAGES * MAT;
-    static constexpr int SMEM = BAR_OFF + 512 + 1024;
+    static constexpr int SMEM = BAR_OFF + kTileBarBytes + 1024;
     // TMEM columns
     static constexpr int S_COL = 0;   // S_A, S_B: 128 each; P over the first 64 of each
     static constexpr int O_COL = 256; // O_A, O_B: HD each
+};
+
+// What the roles need to know of an item; warp 9 works it out once.
+struct __align__(16) TileItem {
+    int s, u, split, nsplit; // s < 0: no more items
+    int q0, n, L, rb;        // the sequence; the tile's first row in it
+    int R, b0, b1, pos0;     // rows of the tile, its split's key blocks, first query's position
+    int sink, lo, hi, nsink; // keys that some row sees, blocks of the sinks
+    int first, pad[3];       // first block of the window
+
+    __device__ __forceinline__ int key_of(int j) const
+    {
+        return (j < nsink ? j : j - nsink + first) << 7;
+    }
 };
 
 struct TileBars {
@@ -55,32 +72,26 @@ struct TileBars {
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
     uint64_t item_full[kTileItems], item_empty[kTileItems];
     uint64_t drain;
-    int4 item[kTileItems]; // sequence (-1: no more), tile, split, key head
+    TileItem item[kTileItems];
     uint32_t tmem;
 };
-static_assert(sizeof(TileBars) <= 512, "barrier area");
+static_assert(sizeof(TileBars) <= kTileBarBytes, "barrier area");
 
-// What a role needs to know of an item.
-struct TileItem {
-    int s, u, tile, split, nsplit;
-    SeqInfo q;
-    int rb, R;          // first row of the sequence, rows of this tile (1..256)
-    int pos0;           // position of the sequence's first query
-    RowRange all;       // keys that the tile's rows see
-    KeyBlocks<7> kb;
-    int b0, b1;         // key blocks of this split
-    __device__ __forceinline__ TileItem(const AttnParams &p, const int4 &it)
-        : s(it.x), u(it.w), tile(it.y), split(it.z), q(seq_info(p, it.x)), rb(it.y * 256),
-          pos0(q.L - q.n), all(tile_union(p, q, it.y)), kb(all)
-    {
-        const int total = q.n * p.g;
-        R = min(256, total - rb);
-        const int per = tile_split_blocks(p, (total + 255) / 256, kb.count);
-        nsplit = max(1, (kb.count + per - 1) / per);
-        b0 = split * per;
-        b1 = min(kb.count, b0 + per);
-    }
-};
+__device__ __forceinline__ TileItem make_item(const AttnParams &p, const int4 &w)
+{
+    TileItem it;
+    const SeqInfo q = seq_info(p, w.x);
+    const int total = q.n * p.g;
+    const RowRange all = tile_union(p, q, w.y);
+    const KeyBlocks<7> kb(all);
+    const int per = tile_split_blocks(p, (total + kTileRows - 1) / kTileRows, kb.count);
+    it.s = w.x, it.u = w.w, it.split = w.z, it.nsplit = max(1, (kb.count + per - 1) / per);
+    it.q0 = q.q0, it.n = q.n, it.L = q.L, it.rb = w.y * kTileRows;
+    it.R = min(kTileRows, total - it.rb), it.b0 = w.z * per, it.b1 = min(kb.count, it.b0 + per);
+    it.pos0 = q.L - q.n;
+    it.sink = all.sink, it.lo = all.lo, it.hi = all.hi, it.nsink = kb.nsink, it.first = kb.first;
+    return it;
+}
 
 // ------------------------------------------------------- tcgen05 primitives
 
@@ -163,6 +174,13 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r)
                  DAN_I8(r, 0), DAN_I8(r, 8), DAN_I8(r, 16), DAN_I8(r, 24)
                  : "memory");
 }
+__device__ __forceinline__ void tc_ld16(uint32_t *r, uint32_t addr)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : DAN_R8(r, 0), DAN_R8(r, 8)
+                 : "r"(addr));
+}
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -172,6 +190,13 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r)
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -243,7 +268,9 @@ __global__ void __launch_bounds__(kPlanThreads) window_attention_plan_kernel(con
                 const int count = KeyBlocks<7>(tile_union(p, q, tile)).count;
                 const int per = tile_split_blocks(p, (q.n * p.g + 255) / 256, count);
                 const int nsplit = max(1, (count + per - 1) / per);
-                const int bucket = kPlanBuckets - 1 - min(kPlanBuckets - 1, min(per, count));
+                const int rows = min(kTileRows, q.n * p.g - tile * kTileRows);
+                const int cost = min(per, count) * (rows > 128 ? 2 : 1);
+                const int bucket = kPlanBuckets - 1 - min(kPlanBuckets - 1, cost);
                 if (pass == 0) {
                     atomicAdd(&s_hist[bucket], nsplit);
                 } else {
@@ -312,93 +339,142 @@ __device__ __forceinline__ uint32_t low_bits(int n)
     return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
 }
 
+// Take the next item from its slot; false when there is none or the wait ran out.
+__device__ __forceinline__ bool next_item(const AttnParams &p, TileBars &B, int k, TileItem &it)
+{
+    const int slot = k % kTileItems;
+    if (!role_wait(p, &B.item_full[slot], (k / kTileItems) & 1)) return false;
+    it = B.item[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&B.item_empty[slot]);
+    return it.s >= 0;
+}
+
+// Four lanes with four 16-byte chunks each of their own row: afterwards v[k]
+// is chunk (lane & 3) of the row of lane k of the four.
+__device__ __forceinline__ void transpose4(uint4 (&v)[4])
+{
+    const int lane = threadIdx.x & 31;
+    auto swap = [&](uint4 &a, uint4 &b, int bit) { // lanes with the bit clear give b for the other's a
+        const bool up = lane & bit;
+        uint4 s = up ? a : b;
+        s.x = __shfl_xor_sync(kFull, s.x, bit);
+        s.y = __shfl_xor_sync(kFull, s.y, bit);
+        s.z = __shfl_xor_sync(kFull, s.z, bit);
+        s.w = __shfl_xor_sync(kFull, s.w, bit);
+        if (up) a = s;
+        else b = s;
+    };
+    swap(v[0], v[1], 1);
+    swap(v[2], v[3], 1);
+    swap(v[0], v[2], 2);
+    swap(v[1], v[3], 2);
+}
+
+// Probabilities 2^(x * scale - z) of 64 scores, packed to bf16 for the product
+// with V; the sums are of the unrounded ones.
+__device__ __forceinline__ void exp_half(uint32_t *pk, const float *x, float2 scale, float2 minus_z,
+                                         float2 &sum0, float2 &sum1)
+{
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        float2 v = fma2(make_float2(x[2 * e], x[2 * e + 1]), scale, minus_z);
+        v.x = exp2_fast(v.x);
+        v.y = exp2_fast(v.y);
+        if (e & 1) sum1 = add2(sum1, v);
+        else sum0 = add2(sum0, v);
+        pk[e] = pack_bf16(v.x, v.y);
+    }
+}
+
 template <int HD>
 __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, uint32_t tmem)
 {
     using Sh = TileShape<HD>;
-    const int t = threadIdx.x >> 7, wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-    const int row = t * 128 + (threadIdx.x & 127);
+    const int t = threadIdx.x >> 7, wq = (threadIdx.x >> 5) & 3;
+    const int lane = threadIdx.x & 31, trow = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t s_addr = tmem + lanes + Sh::S_COL + t * 128;
     const uint32_t o_addr = tmem + lanes + Sh::O_COL + t * HD;
     unsigned s_phase = 0, o_phase = 0;
-    for (int k = 0;; ++k) {
-        const int slot = k % kTileItems;
-        if (!role_wait(p, &B.item_full[slot], (k / kTileItems) & 1)) return;
-        const int4 raw = B.item[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B.item_empty[slot]);
-        if (raw.x < 0) return;
-        const TileItem it(p, raw);
+    TileItem it;
+    for (int k = 0; next_item(p, B, k, it); ++k) {
         if (t == 1 && it.R <= 128) continue; // no rows in tile B
-        const int r = it.rb + row;           // row of the sequence
+        const int row = t * 128 + trow, r = it.rb + row;
+        const int tok = r / p.g;
         const bool live = row < it.R;
-        const RowRange rr = live ? row_range(p, it.pos0 + r / p.g, it.q.L) : RowRange{0, 0, 0};
+        const RowRange rr = live ? row_range(p, it.pos0 + tok, it.L) : RowRange{0, 0, 0};
         float m = -INFINITY, l = 0.0f;
         for (int j = it.b0; j < it.b1; ++j) {
-            const int key0 = it.kb.block(j) << 7;
+            const int key0 = it.key_of(j);
+            const int hi = rr.hi - key0, lo = rr.lo - key0, sink = rr.sink - key0;
+            const bool part = __any_sync(kFull, hi < 128 || (lo > 0 && sink < 128));
             if (!role_wait(p, &B.s_full[t], s_phase)) return;
             s_phase ^= 1;
             tc_fence_after();
-            uint32_t xs[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tc_ld32(xs + 32 * c, s_addr + 32 * c);
-            tc_wait_ld();
             float x[128];
+            auto load = [&](int c) { // scores 32c .. 32c+31, those not seen as -infinity
+                uint32_t raw[32];
+                tc_ld32(raw, s_addr + 32 * c);
+                tc_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(xs[c]);
-            const int hi = rr.hi - key0, lo = rr.lo - key0, sink = rr.sink - key0;
-            const bool whole = hi >= 128 && (lo <= 0 || sink >= 128);
-            if (!__all_sync(kFull, whole)) {
-                // a bit per key and no branch per key (measured: branches took
-                // about 9000 cycles a block)
+                for (int e = 0; e < 32; ++e) x[32 * c + e] = __uint_as_float(raw[e]);
+            };
+            auto mask = [&](int c) { // a bit per key and no branch per key
+                const uint32_t see = low_bits(hi - 32 * c) &
+                                     (low_bits(sink - 32 * c) | ~low_bits(lo - 32 * c));
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t see = low_bits(hi - 32 * w) &
-                                         (low_bits(sink - 32 * w) | ~low_bits(lo - 32 * w));
+                for (int e = 0; e < 32; ++e)
+                    x[32 * c + e] = (see >> e) & 1u ? x[32 * c + e] : -INFINITY;
+            };
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        x[32 * w + c] = (see >> c) & 1u ? x[32 * w + c] : -INFINITY;
-                }
+            for (int c = 0; c < 4; ++c) load(c);
+            if (part) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mask(c);
             }
+            const float2 scale = dup2(p.scale_log2);
+            float z = m == -INFINITY ? 0.0f : m;
+            float2 sum0 = make_float2(0, 0), sum1 = make_float2(0, 0);
+            uint32_t pk[32];
+            exp_half(pk, x, scale, dup2(-z), sum0, sum1);
             float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int c = 4; c < 128; c += 4)
+            for (int c = 4; c < 124; c += 8)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[c + e]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[c + e], x[c + 4 + e]);
+            const float top = fmaxf(max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(x[124], x[125], x[126])),
+                                    x[127]) * p.scale_log2;
             const bool raise = top > m + 8.0f || (m == -INFINITY && top > m);
-            if (j > it.b0 && __any_sync(kFull, raise)) { // O(j-1) is complete (see above)
+            if (__any_sync(kFull, raise)) {
                 const float f = raise ? exp2_fast(m - top) : 1.0f;
                 l *= f;
+                if (j > it.b0) { // O(j-1) is complete (see above)
 #pragma unroll 1
-                for (int c = 0; c < HD; c += 32) {
-                    uint32_t o[32];
-                    tc_ld32(o, o_addr + c);
-                    tc_wait_ld();
+                    for (int c = 0; c < HD; c += 16) {
+                        uint32_t o[16];
+                        tc_ld16(o, o_addr + c);
+                        tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tc_st32(o_addr + c, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc_st16(o_addr + c, o);
+                    }
                 }
-            }
-            if (raise) m = top;
-            const float z = m == -INFINITY ? 0.0f : m;
-            const float2 sc = dup2(p.scale_log2), nz = dup2(-z);
-            float2 sum0 = make_float2(0, 0), sum1 = make_float2(0, 0);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pk[16]; // rounded to bf16 for the product with V; the sums are of the unrounded
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 v = fma2(make_float2(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), sc, nz);
-                    v.x = exp2_fast(v.x);
-                    v.y = exp2_fast(v.y);
-                    if (e & 1) sum1 = add2(sum1, v);
-                    else sum0 = add2(sum0, v);
-                    pk[e] = pack_bf16(v.x, v.y);
+                if (raise) m = top;
+                z = m == -INFINITY ? 0.0f : m;
+                // the first half once more, from TMEM, where it still stands
+                load(0);
+                load(1);
+                if (part) {
+                    mask(0);
+                    mask(1);
                 }
-                tc_st16(s_addr + 16 * c, pk);
+                sum0 = sum1 = make_float2(0, 0);
+                exp_half(pk, x, scale, dup2(-z), sum0, sum1);
             }
+            tc_st32(s_addr, pk);
+            exp_half(pk, x + 64, scale, dup2(-z), sum0, sum1);
+            tc_st32(s_addr + 32, pk);
             sum0 = add2(sum0, sum1);
             l += sum0.x + sum0.y;
             tc_wait_st();
@@ -407,16 +483,24 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
             if (lane == 0) mbar_arrive(&B.p_full[t]);
         }
         // The row's output, straight from TMEM: whole, or a split's part.
-        const bool any = it.b1 > it.b0;
+        const bool any = it.b1 > it.b0, part = it.nsplit > 1;
+        const float inv = part ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+        const SeqInfo q = {it.q0, it.n, it.L, false};
+        const int64_t orow = live ? (int64_t)(it.q0 + tok) * p.H + it.u * p.g + (r - tok * p.g) : -1;
+        const int64_t prow = live ? part_base(p, it.s, q, it.u) + (int64_t)it.split * it.n * p.g + r : -1;
+        const int64_t base = part ? prow : orow;
+        if (live) {
+            if (part) p.part_ml[prow] = make_float2(m, l);
+            else if (p.lse) p.lse[orow] = row_lse(m, l);
+        }
         if (any) {
             if (!role_wait(p, &B.o_full[t], o_phase)) return;
             o_phase ^= 1;
             tc_fence_after();
         }
-        const bool part = it.nsplit > 1;
-        const float inv = part ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-        const int64_t orow = (int64_t)(it.q.q0 + r / p.g) * p.H + it.u * p.g + r % p.g;
-        const int64_t prow = part_base(p, it.s, it.q, it.u) + (int64_t)it.split * it.q.n * p.g + r;
+        int64_t rows4[4]; // the rows that this lane's four stores go to
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows4[i] = __shfl_sync(kFull, base, (lane & ~3) + i);
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
             uint32_t o[32];
@@ -428,28 +512,37 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = 0u;
             }
-            if (live && part) {
-                float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * HD + c);
+            // Four lanes trade chunks so that each store writes 64 bytes of a row
+            // (a row per lane wrote 16 at a time: an item's epilogue took 6600 cycles,
+            // now 2600).
+            if (part) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                         __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-            } else if (live) {
-                uint4 *dst = p.out + (orow * HD + c) / 8;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint4 w;
+                for (int hc = 0; hc < 2; ++hc) {
+                    uint4 v[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        set_word(w, i, pack_bf16(__uint_as_float(o[8 * e + 2 * i]) * inv,
-                                                 __uint_as_float(o[8 * e + 2 * i + 1]) * inv));
-                    dst[e] = w;
+                        v[i] = make_uint4(o[16 * hc + 4 * i], o[16 * hc + 4 * i + 1],
+                                          o[16 * hc + 4 * i + 2], o[16 * hc + 4 * i + 3]);
+                    transpose4(v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (rows4[i] >= 0)
+                            *reinterpret_cast<uint4 *>(p.part_o + rows4[i] * HD + c + 16 * hc +
+                                                       4 * (lane & 3)) = v[i];
                 }
+            } else {
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        set_word(v[i], e, pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                                    __uint_as_float(o[8 * i + 2 * e + 1]) * inv));
+                transpose4(v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (rows4[i] >= 0) p.out[(rows4[i] * HD + c) / 8 + (lane & 3)] = v[i];
             }
-        }
-        if (live) {
-            if (part) p.part_ml[prow] = make_float2(m, l);
-            else if (p.lse) p.lse[orow] = row_lse(m, l);
         }
         if (any) {
             tc_fence_before();
@@ -480,14 +573,8 @@ __device__ __forceinline__ void tile_mma(const AttnParams &p, TileBars &B, char 
         }
         tc_commit(&B.s_full[t]);
     };
-    for (int k = 0;; ++k) {
-        const int slot = k % kTileItems;
-        if (!role_wait(p, &B.item_full[slot], (k / kTileItems) & 1)) return;
-        const int4 raw = B.item[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B.item_empty[slot]);
-        if (raw.x < 0) return;
-        const TileItem it(p, raw);
+    TileItem it;
+    for (int k = 0; next_item(p, B, k, it); ++k) {
         const int nt = it.b1 - it.b0, last = it.R > 128 ? 1 : 0; // last active row tile
         // every loaded query tile is released, used or not
         for (int t = 0; t <= last; ++t) {
@@ -510,12 +597,12 @@ __device__ __forceinline__ void tile_mma(const AttnParams &p, TileBars &B, char 
             const unsigned vi = kv + 2 * j + 1, ki = vi + 1;
             if (!full(vi)) return;
             // value rows that no row of the tile sees may hold anything: zeros
-            const int key0 = it.kb.block(it.b0 + j) << 7;
-            if (key0 + 128 > it.all.hi || (key0 < it.all.lo && key0 + 128 > it.all.sink)) {
+            const int key0 = it.key_of(it.b0 + j);
+            if (key0 + 128 > it.hi || (key0 < it.lo && key0 + 128 > it.sink)) {
                 char *v = smem + Sh::KV_OFF + (vi % Sh::STAGES) * Sh::MAT;
                 for (int r = lane; r < 128; r += 32) {
                     const int key = key0 + r;
-                    if (key >= it.all.hi || (key >= it.all.sink && key < it.all.lo))
+                    if (key >= it.hi || (key >= it.sink && key < it.lo))
                         for (int c = 0; c < Sh::HALVES * 8; ++c)
                             *reinterpret_cast<uint4 *>(v + (c >> 3) * Sh::HALF + r * 128 + (c & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
@@ -529,9 +616,9 @@ __device__ __forceinline__ void tile_mma(const AttnParams &p, TileBars &B, char 
                     if (!role_wait(p, &B.o_empty[t], o_phase[t])) return;
                     o_phase[t] ^= 1;
                 }
+                if (t == 0 && j + 1 < nt && !full(ki)) return;
                 if (!role_wait(p, &B.p_full[t], p_phase[t])) return;
                 p_phase[t] ^= 1;
-                if (t == 0 && j + 1 < nt && !full(ki)) return;
                 tc_fence_after();
                 if (issuer) {
 #pragma unroll
@@ -577,21 +664,22 @@ __device__ __forceinline__ void tile_load(const AttnParams &p, TileBars &B, char
             }
         } while (raw.x == -2);
         const int slot = k % kTileItems;
+        TileItem it;
+        it.s = -1;
+        if (raw.x >= 0) it = make_item(p, raw);
         if (!role_wait(p, &B.item_empty[slot], ((k / kTileItems) & 1) ^ 1)) break;
         if (lane == 0) {
-            B.item[slot] = raw;
+            B.item[slot] = it;
             mbar_arrive(&B.item_full[slot]);
         }
-        if (raw.x < 0) break;
-        const TileItem it(p, raw);
+        if (it.s < 0) break;
         const int32_t *trow = p.table + (int64_t)it.s * p.table_stride;
         // Lane l < per: first cache row of page l of key block j (a page that no
         // row sees, or an id out of range: past the end, where the copy gives zeros)
         auto cache_row = [&](int j) {
             if (lane >= per || j >= it.b1) return rows_total;
-            const int key = (it.kb.block(j) << 7) + lane * box, end = key + box;
-            const bool see = (it.all.lo < it.all.hi && key < it.all.hi && end > it.all.lo) ||
-                             key < it.all.sink;
+            const int key = it.key_of(j) + lane * box, end = key + box;
+            const bool see = (it.lo < it.hi && key < it.hi && end > it.lo) || key < it.sink;
             if (!see) return rows_total;
             const int page = __ldg(trow + (key >> p.page_shift));
             if (page < 0 || page >= p.num_pages) {
@@ -634,30 +722,27 @@ template <int HD>
 __device__ __forceinline__ void tile_queries(const AttnParams &p, TileBars &B, char *smem)
 {
     using Sh = TileShape<HD>;
-    constexpr int CH = HD / 8; // 16-byte chunks of a row
-    const int th = threadIdx.x - 320, lane = threadIdx.x & 31;
+    constexpr int CH = HD / 8, STEP = 64 / CH; // 16-byte chunks of a row, rows of a step
+    const int th = threadIdx.x - 10 * 32, lane = threadIdx.x & 31;
+    const int dt = STEP / p.g, dh = STEP - dt * p.g; // a step in tokens and heads
     unsigned phase[2] = {1, 1};
-    for (int k = 0;; ++k) {
-        const int slot = k % kTileItems;
-        if (!role_wait(p, &B.item_full[slot], (k / kTileItems) & 1)) return;
-        const int4 raw = B.item[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B.item_empty[slot]);
-        if (raw.x < 0) return;
-        const TileItem it(p, raw);
+    TileItem it;
+    for (int k = 0; next_item(p, B, k, it); ++k) {
         for (int t = 0; t < (it.R > 128 ? 2 : 1); ++t) {
             if (!role_wait(p, &B.q_empty[t], phase[t])) return;
             phase[t] ^= 1;
-            char *dst = smem + Sh::Q_OFF + t * Sh::MAT;
-            const int c = th % CH;
-            for (int r = th / CH; r < 128; r += 64 / CH) {
-                const int sr = it.rb + t * 128 + r;
-                char *at = dst + (c >> 3) * Sh::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-                if (t * 128 + r < it.R)
-                    cp_async16(at, p.q + (int64_t)(it.q.q0 + sr / p.g) * p.q_stride8 +
-                                       (it.u * p.g + sr % p.g) * CH + c);
-                else
-                    *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
+            const int c = th % CH, r0 = th / CH, left = it.R - t * 128;
+            int tok = (it.rb + t * 128 + r0) / p.g, head = it.rb + t * 128 + r0 - tok * p.g;
+            char *dst = smem + Sh::Q_OFF + t * Sh::MAT + (c >> 3) * Sh::HALF;
+            const uint4 *src = p.q + (int64_t)it.q0 * p.q_stride8 + (int64_t)it.u * p.g * CH + c;
+#pragma unroll 4
+            for (int r = r0; r < 128; r += STEP) {
+                char *at = dst + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                if (r < left) cp_async16(at, src + tok * p.q_stride8 + head * CH);
+                else *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
+                tok += dt;
+                head += dh;
+                if (head >= p.g) head -= p.g, ++tok;
             }
             cp_async_commit();
             cp_async_wait_all();
@@ -684,10 +769,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(&B.kv_empty[i], 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&B.q_full[t], 2);  // warps 10, 11
+            mbar_init(&B.q_full[t], 2); // warps 10, 11
             mbar_init(&B.q_empty[t], 1);
             mbar_init(&B.s_full[t], 1);
-            mbar_init(&B.p_full[t], 4);  // the four softmax warps
+            mbar_init(&B.p_full[t], 4); // the four softmax warps
             mbar_init(&B.o_full[t], 1);
             mbar_init(&B.o_empty[t], 4);
         }
