@@ -21,11 +21,13 @@
 // S_B(j+1), so each tile's softmax has the other tile's two products to hide
 // behind.  The completion of S(j+1) implies that of O(j).
 //
-// The running maximum is raised only when a row's new maximum passes it by
-// more than 8 (a factor of 256 in the sums, far inside fp32 and bf16 range):
-// a choice of each row alone, so bits do not depend on its neighbours.  So a
-// block's exponentials are taken with the standing maximum while the block's
-// own is still being found, and taken again in the rare block that raises it.
+// The reference m of a row's exponentials need not be its maximum, only near
+// enough for fp32 and bf16 range.  A block's exponentials are taken with the
+// standing m; only where a row's block then sums to more than 1024 (or the row
+// has seen no key before) is the block's maximum found, m raised to it and the
+// block taken again.  The choice is each row's own, so bits do not depend on
+// its neighbours.  Finding every block's maximum first cost a third of the
+// softmax's time.
 #include "dan_device.cuh"
 #include "dan_internal.h"
 #include "dan_attn.cuh"
@@ -190,13 +192,6 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r)
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -371,21 +366,77 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4])
     swap(v[1], v[3], 2);
 }
 
-// Probabilities 2^(x * scale - z) of 64 scores, packed to bf16 for the product
-// with V; the sums are of the unrounded ones.
-__device__ __forceinline__ void exp_half(uint32_t *pk, const float *x, float2 scale, float2 minus_z,
-                                         float2 &sum0, float2 &sum1)
+// Keys of a block that a row sees: below `sink` or in [lo, hi), and below hi.
+struct BlockMask {
+    int hi, lo, sink;
+    __device__ __forceinline__ bool whole() const { return hi >= 128 && (lo <= 0 || sink >= 128); }
+    __device__ __forceinline__ bool some() const { return hi > 0 && (sink > 0 || lo < min(hi, 128)); }
+    // keys 32c .. 32c+31, a bit each
+    __device__ __forceinline__ uint32_t bits(int c) const
+    {
+        return low_bits(hi - 32 * c) & (low_bits(sink - 32 * c) | ~low_bits(lo - 32 * c));
+    }
+};
+
+// -infinity in place of the scores that the row does not see: a bit per key
+// and no branch per key (measured: branches took about 9000 cycles a block).
+__device__ __forceinline__ void mask_chunk(uint32_t (&x)[32], uint32_t see)
 {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-        float2 v = fma2(make_float2(x[2 * e], x[2 * e + 1]), scale, minus_z);
-        v.x = exp2_fast(v.x);
-        v.y = exp2_fast(v.y);
-        if (e & 1) sum1 = add2(sum1, v);
-        else sum0 = add2(sum0, v);
-        pk[e] = pack_bf16(v.x, v.y);
-    }
+    for (int e = 0; e < 32; ++e) x[e] = (see >> e) & 1u ? x[e] : 0xFF800000u;
 }
+
+// A row's block: pk = 2^(x * scale - z) of its 128 scores, in pairs rounded to
+// bf16 for the product with V; returns the sum of the unrounded ones.  A chunk
+// of 32 scores is on its way from TMEM while the one before it is worked on.
+__device__ __forceinline__ float block_exp(uint32_t (&pk)[64], uint32_t s_addr, const BlockMask &bm,
+                                           bool part, float scale_log2, float z)
+{
+    const float2 scale = dup2(scale_log2), minus_z = dup2(-z);
+    float2 sum0 = make_float2(0, 0), sum1 = make_float2(0, 0);
+    uint32_t x[2][32];
+    tc_ld32(x[0], s_addr);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        tc_wait_ld();
+        if (c < 3) tc_ld32(x[(c + 1) & 1], s_addr + 32 * (c + 1));
+        uint32_t(&xc)[32] = x[c & 1];
+        if (part) mask_chunk(xc, bm.bits(c));
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float2 v = fma2(make_float2(__uint_as_float(xc[2 * e]), __uint_as_float(xc[2 * e + 1])),
+                            scale, minus_z);
+            v.x = exp2_fast(v.x);
+            v.y = exp2_fast(v.y);
+            if (e & 1) sum1 = add2(sum1, v);
+            else sum0 = add2(sum0, v);
+            pk[16 * c + e] = pack_bf16(v.x, v.y);
+        }
+    }
+    sum0 = add2(sum0, sum1);
+    return sum0.x + sum0.y;
+}
+
+// The largest of a row's visible scores in a block.
+__device__ __forceinline__ float block_max(uint32_t s_addr, const BlockMask &bm, bool part)
+{
+    float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        tc_ld32(x, s_addr + 32 * c);
+        tc_wait_ld();
+        if (part) mask_chunk(x, bm.bits(c));
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            m0 = fmaxf(m0, __uint_as_float(x[e]));
+            m1 = fmaxf(m1, __uint_as_float(x[e + 1]));
+        }
+    }
+    return fmaxf(m0, m1);
+}
+
+constexpr float kRaiseSum = 1024.0f;
 
 template <int HD>
 __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, uint32_t tmem)
@@ -407,46 +458,21 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
         float m = -INFINITY, l = 0.0f;
         for (int j = it.b0; j < it.b1; ++j) {
             const int key0 = it.key_of(j);
-            const int hi = rr.hi - key0, lo = rr.lo - key0, sink = rr.sink - key0;
-            const bool part = __any_sync(kFull, hi < 128 || (lo > 0 && sink < 128));
+            const BlockMask bm = {rr.hi - key0, rr.lo - key0, rr.sink - key0};
+            const bool part = !__all_sync(kFull, bm.whole()), some = bm.some();
             if (!role_wait(p, &B.s_full[t], s_phase)) return;
             s_phase ^= 1;
             tc_fence_after();
-            float x[128];
-            auto load = [&](int c) { // scores 32c .. 32c+31, those not seen as -infinity
-                uint32_t raw[32];
-                tc_ld32(raw, s_addr + 32 * c);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[32 * c + e] = __uint_as_float(raw[e]);
-            };
-            auto mask = [&](int c) { // a bit per key and no branch per key
-                const uint32_t see = low_bits(hi - 32 * c) &
-                                     (low_bits(sink - 32 * c) | ~low_bits(lo - 32 * c));
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    x[32 * c + e] = (see >> e) & 1u ? x[32 * c + e] : -INFINITY;
-            };
-#pragma unroll
-            for (int c = 0; c < 4; ++c) load(c);
-            if (part) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) mask(c);
+            uint32_t pk[64];
+            float sum = 0.0f;
+            bool raise = m == -INFINITY && some;
+            if (j > it.b0) { // (a first block always finds its maximum)
+                sum = block_exp(pk, s_addr, bm, part, p.scale_log2, m == -INFINITY ? 0.0f : m);
+                raise = raise || sum > kRaiseSum;
             }
-            const float2 scale = dup2(p.scale_log2);
-            float z = m == -INFINITY ? 0.0f : m;
-            float2 sum0 = make_float2(0, 0), sum1 = make_float2(0, 0);
-            uint32_t pk[32];
-            exp_half(pk, x, scale, dup2(-z), sum0, sum1);
-            float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int c = 4; c < 124; c += 8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[c + e], x[c + 4 + e]);
-            const float top = fmaxf(max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(x[124], x[125], x[126])),
-                                    x[127]) * p.scale_log2;
-            const bool raise = top > m + 8.0f || (m == -INFINITY && top > m);
-            if (__any_sync(kFull, raise)) {
+            if (j == it.b0 || __any_sync(kFull, raise)) {
+                const float top = block_max(s_addr, bm, part) * p.scale_log2;
+                raise = raise && top > m;
                 const float f = raise ? exp2_fast(m - top) : 1.0f;
                 l *= f;
                 if (j > it.b0) { // O(j-1) is complete (see above)
@@ -461,22 +487,12 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
                     }
                 }
                 if (raise) m = top;
-                z = m == -INFINITY ? 0.0f : m;
-                // the first half once more, from TMEM, where it still stands
-                load(0);
-                load(1);
-                if (part) {
-                    mask(0);
-                    mask(1);
-                }
-                sum0 = sum1 = make_float2(0, 0);
-                exp_half(pk, x, scale, dup2(-z), sum0, sum1);
+                sum = block_exp(pk, s_addr, bm, part, p.scale_log2, m == -INFINITY ? 0.0f : m);
             }
+            // P over the scores
             tc_st32(s_addr, pk);
-            exp_half(pk, x + 64, scale, dup2(-z), sum0, sum1);
-            tc_st32(s_addr + 32, pk);
-            sum0 = add2(sum0, sum1);
-            l += sum0.x + sum0.y;
+            tc_st32(s_addr + 32, pk + 32);
+            l += sum;
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
