@@ -14,7 +14,9 @@
 //                   thread): scores out of TMEM, probabilities back into it
 //   warp 8          issues every tcgen05 product
 //   warp 9          takes the items and brings K and V by TMA (128 keys each)
-//   warps 10, 11    bring the item's query rows
+//   warp 10         brings the item's query rows
+//   warp 11         follows the blocks: clears value rows that no query sees,
+//                   vouches for a block's K and V, gives its stages back
 // Per 128 keys and row tile: S = Q K^T (operands in shared memory, result in
 // TMEM), softmax, P (bf16) over S's columns in TMEM, O += P V with P read
 // from TMEM.  The tensor pipe runs in issue order: O_A(j), S_A(j+1), O_B(j),
@@ -75,7 +77,7 @@ struct TileBars {
     uint64_t item_full[kTileItems], item_empty[kTileItems];
     uint64_t drain;
     TileItem item[kTileItems];
-    uint32_t tmem;
+    uint32_t tmem, dead; // dead: a wait ran out
 };
 static_assert(sizeof(TileBars) <= kTileBarBytes, "barrier area");
 
@@ -320,12 +322,37 @@ __global__ void __launch_bounds__(kPlanThreads) window_attention_plan_kernel(con
 
 // ------------------------------------------------------------------- main
 
-// A wait of a role: false when it ran out (the role then leaves).
-__device__ __forceinline__ bool role_wait(const AttnParams &p, uint64_t *bar, unsigned parity)
+// A wait of a role, each lane by itself.  One that runs out marks the CTA dead;
+// from then on every wait returns at once and the roles run to their end (on
+// whatever the buffers hold; no address depends on it but an item's, and no
+// item is taken any more).
+__device__ __forceinline__ void role_wait(const AttnParams &p, TileBars &B, uint64_t *bar, unsigned parity)
 {
-    if (__all_sync(kFull, mbar_wait(bar, parity, p.limit_ns))) return true;
-    if ((threadIdx.x & 31) == 0) set_status(p.status, kStatusWaitFull);
-    return false;
+    if (mbar_try_wait(bar, parity)) return;
+    const unsigned long long t0 = global_ns();
+    volatile uint32_t *dead = &B.dead;
+#pragma unroll 1
+    while (!*dead) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return;
+        if (global_ns() - t0 > p.limit_ns) {
+            *dead = 1;
+            set_status(p.status, kStatusWaitFull);
+        }
+    }
+}
+
+// The same for a whole warp, converged afterwards.
+__device__ __forceinline__ void warp_wait(const AttnParams &p, TileBars &B, uint64_t *bar, unsigned parity)
+{
+    role_wait(p, B, bar, parity);
+    __syncwarp();
+}
+
+__device__ __forceinline__ bool is_dead(TileBars &B)
+{
+    return __any_sync(kFull, *reinterpret_cast<volatile uint32_t *>(&B.dead) != 0);
 }
 
 // A word whose lowest n bits are set (n of any size).
@@ -338,7 +365,8 @@ __device__ __forceinline__ uint32_t low_bits(int n)
 __device__ __forceinline__ bool next_item(const AttnParams &p, TileBars &B, int k, TileItem &it)
 {
     const int slot = k % kTileItems;
-    if (!role_wait(p, &B.item_full[slot], (k / kTileItems) & 1)) return false;
+    warp_wait(p, B, &B.item_full[slot], (k / kTileItems) & 1);
+    if (is_dead(B)) return false;
     it = B.item[slot];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&B.item_empty[slot]);
@@ -460,7 +488,7 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
             const int key0 = it.key_of(j);
             const BlockMask bm = {rr.hi - key0, rr.lo - key0, rr.sink - key0};
             const bool part = !__all_sync(kFull, bm.whole()), some = bm.some();
-            if (!role_wait(p, &B.s_full[t], s_phase)) return;
+            warp_wait(p, B, &B.s_full[t], s_phase);
             s_phase ^= 1;
             tc_fence_after();
             uint32_t pk[64];
@@ -510,7 +538,7 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
             else if (p.lse) p.lse[orow] = row_lse(m, l);
         }
         if (any) {
-            if (!role_wait(p, &B.o_full[t], o_phase)) return;
+            warp_wait(p, B, &B.o_full[t], o_phase);
             o_phase ^= 1;
             tc_fence_after();
         }
@@ -568,54 +596,117 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
     }
 }
 
+// All of it in one elected lane, and as little as can be between a wait and
+// its products.  A commit holds the lane until the products before it have
+// been taken up (about 300 cycles), so each tile's block has one: the scores'.
 template <int HD>
 __device__ __forceinline__ void tile_mma(const AttnParams &p, TileBars &B, char *smem, uint32_t tmem)
 {
     using Sh = TileShape<HD>;
-    const int lane = threadIdx.x & 31;
-    const bool issuer = elect_one();
     constexpr uint32_t id_s = tc_idesc(128, false), id_o = tc_idesc(HD, true);
     const uint32_t base = smem_addr(smem);
-    uint64_t qd[2];
-    for (int t = 0; t < 2; ++t) qd[t] = tc_desc(base + Sh::Q_OFF + t * Sh::MAT, 16, 1024);
-    unsigned kv = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {1, 1};
-    auto full = [&](unsigned i) { return role_wait(p, &B.kv_full[i % Sh::STAGES], (i / Sh::STAGES) & 1); };
-    auto product_s = [&](int t, unsigned i) { // the issuer
-        const uint64_t kd = tc_desc(base + Sh::KV_OFF + (i % Sh::STAGES) * Sh::MAT, 16, 1024);
+    const uint64_t q0 = tc_desc(base + Sh::Q_OFF, 16, 1024);
+    const uint64_t k0 = tc_desc(base + Sh::KV_OFF, 16, 1024);
+    const uint64_t v0 = tc_desc(base + Sh::KV_OFF, Sh::HALF, 1024);
+    unsigned stage = 0, kv_phase = 0;               // of the next block, keys or values
+    unsigned q_phase = 0, p_phase = 0, o_phase = 3; // a bit for each row tile
+    auto wait_tile = [&](uint64_t *bars, int t, unsigned &phase) {
+        role_wait(p, B, bars + t, (phase >> t) & 1);
+        phase ^= 1u << t;
+    };
+    auto advance = [&] {
+        const unsigned st = stage;
+        if (++stage == Sh::STAGES) stage = 0, kv_phase ^= 1;
+        return st;
+    };
+    auto product_s = [&](int t, unsigned st) {
+        const uint64_t qd = q0 + (uint64_t)((t * Sh::MAT) >> 4), kd = k0 + (uint64_t)((st * Sh::MAT) >> 4);
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k) {
             const uint64_t off = (uint64_t)(((k >> 2) * Sh::HALF + (k & 3) * 32) >> 4);
-            tc_mma_ss(tmem + Sh::S_COL + t * 128, qd[t] + off, kd + off, id_s, k > 0);
+            tc_mma_ss(tmem + Sh::S_COL + t * 128, qd + off, kd + off, id_s, k > 0);
         }
         tc_commit(&B.s_full[t]);
     };
     TileItem it;
-    for (int k = 0; next_item(p, B, k, it); ++k) {
+    for (int n = 0; next_item(p, B, n, it); ++n) {
         const int nt = it.b1 - it.b0, last = it.R > 128 ? 1 : 0; // last active row tile
-        // every loaded query tile is released, used or not
-        for (int t = 0; t <= last; ++t) {
-            if (!role_wait(p, &B.q_full[t], q_phase[t])) return;
-            q_phase[t] ^= 1;
-            if (nt <= 0) {
-                if (lane == 0) mbar_arrive(&B.q_empty[t]);
-                continue;
-            }
-            if (t == 0 && !full(kv)) return;
-            tc_fence_after();
-            if (issuer) {
-                product_s(t, kv);
+        if (elect_one()) {
+            if (nt > 0) role_wait(p, B, &B.kv_full[stage], kv_phase);
+            unsigned kst = nt > 0 ? advance() : 0; // the key block's stage
+            // every loaded query tile is released, used or not
+            for (int t = 0; t <= last; ++t) {
+                wait_tile(B.q_full, t, q_phase);
+                if (nt <= 0) {
+                    mbar_arrive(&B.q_empty[t]);
+                    continue;
+                }
+                tc_fence_after();
+                product_s(t, kst);
                 if (nt == 1) tc_commit(&B.q_empty[t]);
-                if (t == last) tc_commit(&B.kv_empty[kv % Sh::STAGES]);
             }
-            __syncwarp();
+            for (int j = 0; j < nt; ++j) {
+                const unsigned vst = advance();
+                const bool more = j + 1 < nt;
+                if (more) kst = advance();
+                const uint64_t vd = v0 + (uint64_t)((vst * Sh::MAT) >> 4);
+                for (int t = 0; t <= last; ++t) {
+                    if (j == 0) wait_tile(B.o_empty, t, o_phase); // the previous item's output has been read
+                    wait_tile(B.p_full, t, p_phase); // P, and V(j) and K(j+1) too
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma_ts(tmem + Sh::O_COL + t * HD, tmem + Sh::S_COL + t * 128 + k * 8,
+                                  vd + (uint64_t)(k * 2048 >> 4), id_o, j > 0 || k > 0);
+                    if (more) {
+                        product_s(t, kst);
+                        if (j + 2 == nt) tc_commit(&B.q_empty[t]);
+                    } else {
+                        tc_commit(&B.o_full[t]);
+                    }
+                }
+            }
         }
-        for (int j = 0; j < nt; ++j) {
-            const unsigned vi = kv + 2 * j + 1, ki = vi + 1;
-            if (!full(vi)) return;
-            // value rows that no row of the tile sees may hold anything: zeros
-            const int key0 = it.key_of(it.b0 + j);
+        __syncwarp();
+    }
+    // every product is done before the TMEM is given back
+    if (elect_one()) tc_commit(&B.drain); // the lane that issued them
+    __syncwarp();
+    if (!mbar_wait(&B.drain, 0, p.limit_ns)) set_status(p.status, kStatusWaitDrain);
+}
+
+// Follows the blocks of an item.  Before the products of block j may run (its
+// arrival on p_full beside the softmax's): V(j) and K(j+1) have landed, and
+// value rows that no row of the tile sees, which may hold anything, are zeros.
+// When the last tile's scores of block j are there, its products have read
+// K(j) and V(j-1): those stages go back to the loader.
+template <int HD>
+__device__ __forceinline__ void tile_follow(const AttnParams &p, TileBars &B, char *smem)
+{
+    using Sh = TileShape<HD>;
+    const int lane = threadIdx.x & 31;
+    unsigned stage = 0, phase = 0;                  // of the next block that lands
+    unsigned given = 0;                             // the next stage to give back
+    unsigned s_phase = 0, o_phase = 0;              // a bit for each row tile
+    auto landed = [&] {
+        warp_wait(p, B, &B.kv_full[stage], phase);
+        const unsigned st = stage;
+        if (++stage == Sh::STAGES) stage = 0, phase ^= 1;
+        return st;
+    };
+    auto give_back = [&] {
+        if (lane == 0) mbar_arrive(&B.kv_empty[given]);
+        if (++given == Sh::STAGES) given = 0;
+    };
+    TileItem it;
+    for (int n = 0; next_item(p, B, n, it); ++n) {
+        const int last = it.R > 128 ? 1 : 0;
+        if (it.b0 < it.b1) landed(); // K of the first block
+        for (int j = it.b0; j < it.b1; ++j) {
+            const unsigned vst = landed();
+            const int key0 = it.key_of(j);
             if (key0 + 128 > it.hi || (key0 < it.lo && key0 + 128 > it.sink)) {
-                char *v = smem + Sh::KV_OFF + (vi % Sh::STAGES) * Sh::MAT;
+                char *v = smem + Sh::KV_OFF + vst * Sh::MAT;
                 for (int r = lane; r < 128; r += 32) {
                     const int key = key0 + r;
                     if (key >= it.hi || (key >= it.sink && key < it.lo))
@@ -626,33 +717,20 @@ __device__ __forceinline__ void tile_mma(const AttnParams &p, TileBars &B, char 
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             }
-            const uint64_t vd = tc_desc(base + Sh::KV_OFF + (vi % Sh::STAGES) * Sh::MAT, Sh::HALF, 1024);
+            if (j + 1 < it.b1) landed();
             for (int t = 0; t <= last; ++t) {
-                if (j == 0) { // the previous item's output of this tile has been read
-                    if (!role_wait(p, &B.o_empty[t], o_phase[t])) return;
-                    o_phase[t] ^= 1;
-                }
-                if (t == 0 && j + 1 < nt && !full(ki)) return;
-                if (!role_wait(p, &B.p_full[t], p_phase[t])) return;
-                p_phase[t] ^= 1;
-                tc_fence_after();
-                if (issuer) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tc_mma_ts(tmem + Sh::O_COL + t * HD, tmem + Sh::S_COL + t * 128 + k * 8,
-                                  vd + (uint64_t)(k * 2048 >> 4), id_o, j > 0 || k > 0);
-                    if (j + 1 == nt) tc_commit(&B.o_full[t]);
-                    if (t == last) tc_commit(&B.kv_empty[vi % Sh::STAGES]);
-                    if (j + 1 < nt) {
-                        product_s(t, ki);
-                        if (j + 2 == nt) tc_commit(&B.q_empty[t]);
-                        if (t == last) tc_commit(&B.kv_empty[ki % Sh::STAGES]);
-                    }
-                }
-                __syncwarp();
+                warp_wait(p, B, &B.s_full[t], (s_phase >> t) & 1);
+                s_phase ^= 1u << t;
+                if (lane == 0) mbar_arrive(&B.p_full[t]);
             }
+            if (j > it.b0) give_back(); // V(j-1)
+            give_back();                // K(j)
         }
-        kv += 2 * (nt > 0 ? nt : 0);
+        if (it.b0 < it.b1) {
+            warp_wait(p, B, &B.o_full[last], (o_phase >> last) & 1);
+            give_back(); // the last V
+            o_phase ^= last ? 3 : 1;
+        }
     }
 }
 
@@ -666,8 +744,7 @@ __device__ __forceinline__ void tile_load(const AttnParams &p, TileBars &B, char
     const int box = min(128, 1 << p.page_shift), per = 128 / box; // pages of a key block
     const int rows_total = (p.num_pages * p.Hkv) << p.page_shift;
     unsigned kv = 0;
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
+    for (int k = 0; !is_dead(B); ++k) {
         int4 raw = make_int4(-1, 0, 0, 0);
         do { // the next item (-2: one that the plan left out)
             int w = 0;
@@ -683,7 +760,7 @@ __device__ __forceinline__ void tile_load(const AttnParams &p, TileBars &B, char
         TileItem it;
         it.s = -1;
         if (raw.x >= 0) it = make_item(p, raw);
-        if (!role_wait(p, &B.item_empty[slot], ((k / kTileItems) & 1) ^ 1)) break;
+        warp_wait(p, B, &B.item_empty[slot], ((k / kTileItems) & 1) ^ 1);
         if (lane == 0) {
             B.item[slot] = it;
             mbar_arrive(&B.item_full[slot]);
@@ -705,15 +782,13 @@ __device__ __forceinline__ void tile_load(const AttnParams &p, TileBars &B, char
             return ((page * p.Hkv + it.u) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
         };
         int rows = cache_row(it.b0);
-        for (int j = it.b0; j < it.b1 && ok; ++j) {
+        for (int j = it.b0; j < it.b1; ++j) {
             const int next = cache_row(j + 1); // in flight while this block's copies start
 #pragma unroll
-            for (int m = 0; m < 2; ++m, ++kv) {
+            for (int m = 0; m < 2; ++m) {
                 const int st = kv % Sh::STAGES;
-                if (!role_wait(p, &B.kv_empty[st], ((kv / Sh::STAGES) & 1) ^ 1)) {
-                    ok = false;
-                    break;
-                }
+                warp_wait(p, B, &B.kv_empty[st], ((kv / Sh::STAGES) & 1) ^ 1);
+                if (is_dead(B)) break;
                 if (lane == 0) mbar_arrive_expect_tx(&B.kv_full[st], Sh::MAT);
                 __syncwarp();
                 if (lane < per) {
@@ -722,6 +797,7 @@ __device__ __forceinline__ void tile_load(const AttnParams &p, TileBars &B, char
                     for (int h = 0; h < Sh::HALVES; ++h)
                         tma_load_2d(dst + h * Sh::HALF, m ? &vmap : &kmap, h * 64, rows, &B.kv_full[st]);
                 }
+                ++kv;
                 __syncwarp();
             }
             rows = next;
@@ -738,16 +814,16 @@ template <int HD>
 __device__ __forceinline__ void tile_queries(const AttnParams &p, TileBars &B, char *smem)
 {
     using Sh = TileShape<HD>;
-    constexpr int CH = HD / 8, STEP = 64 / CH; // 16-byte chunks of a row, rows of a step
-    const int th = threadIdx.x - 10 * 32, lane = threadIdx.x & 31;
+    constexpr int CH = HD / 8, STEP = 32 / CH; // 16-byte chunks of a row, rows of a step
+    const int lane = threadIdx.x & 31;
     const int dt = STEP / p.g, dh = STEP - dt * p.g; // a step in tokens and heads
     unsigned phase[2] = {1, 1};
     TileItem it;
     for (int k = 0; next_item(p, B, k, it); ++k) {
         for (int t = 0; t < (it.R > 128 ? 2 : 1); ++t) {
-            if (!role_wait(p, &B.q_empty[t], phase[t])) return;
+            warp_wait(p, B, &B.q_empty[t], phase[t]);
             phase[t] ^= 1;
-            const int c = th % CH, r0 = th / CH, left = it.R - t * 128;
+            const int c = lane % CH, r0 = lane / CH, left = it.R - t * 128;
             int tok = (it.rb + t * 128 + r0) / p.g, head = it.rb + t * 128 + r0 - tok * p.g;
             char *dst = smem + Sh::Q_OFF + t * Sh::MAT + (c >> 3) * Sh::HALF;
             const uint4 *src = p.q + (int64_t)it.q0 * p.q_stride8 + (int64_t)it.u * p.g * CH + c;
@@ -785,10 +861,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(&B.kv_empty[i], 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&B.q_full[t], 2); // warps 10, 11
+            mbar_init(&B.q_full[t], 1);
             mbar_init(&B.q_empty[t], 1);
             mbar_init(&B.s_full[t], 1);
-            mbar_init(&B.p_full[t], 4); // the four softmax warps
+            mbar_init(&B.p_full[t], 5); // the four softmax warps and warp 11
             mbar_init(&B.o_full[t], 1);
             mbar_init(&B.o_empty[t], 4);
         }
@@ -797,6 +873,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(&B.item_empty[i], 11); // every warp but 9
         }
         mbar_init(&B.drain, 1);
+        B.dead = 0;
         mbar_init_fence();
     }
     if (warp == 8) {
@@ -815,14 +892,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tile_softmax<HD>(p, B, tmem);
     } else if (warp == 8) {
         tile_mma<HD>(p, B, smem, tmem);
-        // every product is done before the TMEM is given back
-        if (elect_one()) tc_commit(&B.drain); // the lane that issued them
-        __syncwarp();
-        if (!mbar_wait(&B.drain, 0, p.limit_ns)) set_status(p.status, kStatusWaitDrain);
     } else if (warp == 9) {
         tile_load<HD>(p, B, smem, kmap, vmap);
-    } else {
+    } else if (warp == 10) {
         tile_queries<HD>(p, B, smem);
+    } else {
+        tile_follow<HD>(p, B, smem);
     }
     __syncwarp();
     tc_fence_before();
