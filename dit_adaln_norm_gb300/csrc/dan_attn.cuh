@@ -75,6 +75,19 @@ cudaError_t launch_overlapped_2d(void (*fn)(KArgs...), dim3 grid, int block, int
 
 // ----------------------------------------------------------- device side
 
+// One piece of work of the tile kernel: a split of the keys of a tile of
+// query tokens, for one key head.
+struct __align__(16) TileItem {
+    int s, u, split, nsplit; // sequence, key head (set when taken); s < 0: none
+    int q0, n, L, tok0;      // the sequence; the tile's first token in it
+    int ntok, b0, b1, pos0;  // tokens of the tile, its split's key blocks, first query's position
+    int sink, lo, hi, nsink; // keys that some row sees, blocks of the sinks
+    int first, pad[3];       // first block of the window
+
+    // first key of block j
+    __host__ __device__ int key_of(int j) const { return (j < nsink ? j : j - nsink + first) << 7; }
+};
+
 struct AttnParams {
     const uint4 *q;
     int64_t N, q_stride8; // query row stride in 16-byte fragments
@@ -94,7 +107,7 @@ struct AttnParams {
     int64_t part_cap; // rows of a (sequence, key head), or 0: room by query row,
     int part_splits;  // that many for each
     // work of the tile kernel (see its plan)
-    int4 *items;
+    TileItem *items;
     int2 *split_tiles;
     int *plan_head;
     int items_cap, split_tiles_cap;
@@ -193,15 +206,25 @@ __device__ __forceinline__ int64_t part_base(const AttnParams &p, int s, const S
     return ((int64_t)q.q0 * p.H + (int64_t)u * q.n * p.g) * p.part_splits;
 }
 
-// The tile kernel's rows: tiles of 256 of a sequence's (token, query head)
-// rows.  Keys that some row of a tile sees:
+// The tile kernel's rows: two row tiles of 128 / g whole tokens each, at most
+// 256 (token, query head) rows.
 constexpr int kTileRows = 256;
+constexpr int kMaxGroup = 128; // most query heads of a key head
 constexpr int kPlanBuckets = 2048;
 
+__host__ __device__ __forceinline__ int tile_tokens(int g) { return 2 * (128 / g); }
+
+// Keys that some row of a tile sees:
 __device__ __forceinline__ RowRange tile_union(const AttnParams &p, const SeqInfo &q, int tile)
 {
-    const int rb = tile * kTileRows, end = min(q.n * p.g, rb + kTileRows), pos0 = q.L - q.n;
-    return rows_union(p, pos0 + rb / p.g, pos0 + (end - 1) / p.g, q.L);
+    const int nt = tile_tokens(p.g), first = tile * nt, end = min(q.n, first + nt), pos0 = q.L - q.n;
+    return rows_union(p, pos0 + first, pos0 + end - 1, q.L);
+}
+
+__device__ __forceinline__ int seq_tiles(const AttnParams &p, const SeqInfo &q)
+{
+    const int nt = tile_tokens(p.g);
+    return (q.n + nt - 1) / nt;
 }
 
 // Key blocks (128 keys) of a split of a tile that sees `count` of them, in a
@@ -223,8 +246,8 @@ __device__ __forceinline__ int tile_split_blocks(const AttnParams &p, int tiles,
 // `splits` ways; the others (with the plan before it); the join of splits.
 cudaError_t launch_attention_step(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
                                   const CUtensorMap &vmap, int splits, cudaStream_t s);
-cudaError_t launch_attention_tile(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
-                                  const CUtensorMap &vmap, cudaStream_t s);
+cudaError_t launch_attention_tile(const AttnParams &p, int head_dim, const CUtensorMap &qmap,
+                                  const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t s);
 cudaError_t launch_attention_join(const AttnParams &p, int head_dim, bool tiles, cudaStream_t s);
 
 } // namespace dan

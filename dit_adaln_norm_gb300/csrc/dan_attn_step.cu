@@ -326,10 +326,10 @@ __global__ void __launch_bounds__(128) window_attention_join_kernel(const AttnPa
         if (st.x < 0) continue;
         const int u = (int)(w / RB % p.Hkv);
         const SeqInfo q = seq_info(p, st.x);
-        const int total = q.n * p.g, r = st.y * kTileRows + (int)(w % RB) * 4 + warp;
-        if (r >= total) continue;
+        const int rows = tile_tokens(p.g) * p.g, rt = (int)(w % RB) * 4 + warp, r = st.y * rows + rt;
+        if (rt >= rows || r >= q.n * p.g) continue;
         const int count = KeyBlocks<7>(tile_union(p, q, st.y)).count;
-        const int per = tile_split_blocks(p, (total + kTileRows - 1) / kTileRows, count);
+        const int per = tile_split_blocks(p, seq_tiles(p, q), count);
         join_row<HD>(p, st.x, q, u, r, (count + per - 1) / per);
     }
 }

@@ -14,7 +14,7 @@
 //                   thread): scores out of TMEM, probabilities back into it
 //   warp 8          issues every tcgen05 product
 //   warp 9          takes the items and brings K and V by TMA (128 keys each)
-//   warp 10         brings the item's query rows
+//   warp 10         brings the item's query rows by TMA
 //   warp 11         follows the blocks: clears value rows that no query sees,
 //                   vouches for a block's K and V, gives its stages back
 // Per 128 keys and row tile: S = Q K^T (operands in shared memory, result in
@@ -24,12 +24,13 @@
 // behind.  The completion of S(j+1) implies that of O(j).
 //
 // The reference m of a row's exponentials need not be its maximum, only near
-// enough for fp32 and bf16 range.  A block's exponentials are taken with the
-// standing m; only where a row's block then sums to more than 1024 (or the row
-// has seen no key before) is the block's maximum found, m raised to it and the
-// block taken again.  The choice is each row's own, so bits do not depend on
-// its neighbours.  Finding every block's maximum first cost a third of the
-// softmax's time.
+// enough for fp32 and bf16 range.  It is the maximum of the first block of
+// which the row sees a key.  Where a later block sums to more than 2^10, m
+// rises after it by that sum's exponent, and the row's sum and output are
+// scaled by the same power of two, exactly; where it sums to more than 2^60,
+// the block's maximum is found and the block taken again.  Each choice is the
+// row's own, so bits do not depend on its neighbours.  Finding every block's
+// maximum first cost a third of the softmax's time.
 #include "dan_device.cuh"
 #include "dan_internal.h"
 #include "dan_attn.cuh"
@@ -57,20 +58,6 @@ struct TileShape {
     static constexpr int O_COL = 256; // O_A, O_B: HD each
 };
 
-// What the roles need to know of an item; warp 9 works it out once.
-struct __align__(16) TileItem {
-    int s, u, split, nsplit; // s < 0: no more items
-    int q0, n, L, rb;        // the sequence; the tile's first row in it
-    int R, b0, b1, pos0;     // rows of the tile, its split's key blocks, first query's position
-    int sink, lo, hi, nsink; // keys that some row sees, blocks of the sinks
-    int first, pad[3];       // first block of the window
-
-    __device__ __forceinline__ int key_of(int j) const
-    {
-        return (j < nsink ? j : j - nsink + first) << 7;
-    }
-};
-
 struct TileBars {
     uint64_t kv_full[10], kv_empty[10];
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
@@ -80,22 +67,6 @@ struct TileBars {
     uint32_t tmem, dead; // dead: a wait ran out
 };
 static_assert(sizeof(TileBars) <= kTileBarBytes, "barrier area");
-
-__device__ __forceinline__ TileItem make_item(const AttnParams &p, const int4 &w)
-{
-    TileItem it;
-    const SeqInfo q = seq_info(p, w.x);
-    const int total = q.n * p.g;
-    const RowRange all = tile_union(p, q, w.y);
-    const KeyBlocks<7> kb(all);
-    const int per = tile_split_blocks(p, (total + kTileRows - 1) / kTileRows, kb.count);
-    it.s = w.x, it.u = w.w, it.split = w.z, it.nsplit = max(1, (kb.count + per - 1) / per);
-    it.q0 = q.q0, it.n = q.n, it.L = q.L, it.rb = w.y * kTileRows;
-    it.R = min(kTileRows, total - it.rb), it.b0 = w.z * per, it.b1 = min(kb.count, it.b0 + per);
-    it.pos0 = q.L - q.n;
-    it.sink = all.sink, it.lo = all.lo, it.hi = all.hi, it.nsink = kb.nsink, it.first = kb.first;
-    return it;
-}
 
 // ------------------------------------------------------- tcgen05 primitives
 
@@ -227,8 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads) window_attention_plan_kernel(con
             if (s < p.S) {
                 const SeqInfo q = seq_info(p, s);
                 if (q.bad && pass == 0) set_status(p.status, kStatusIndex);
-                const int64_t rows = (int64_t)q.n * p.g;
-                tiles = rows > kStepRows ? (int)((rows + 255) / 256) : 0;
+                tiles = q.n * p.g > kStepRows ? seq_tiles(p, q) : 0;
             }
             int x = tiles; // inclusive sum over the chunk
 #pragma unroll
@@ -262,11 +232,12 @@ __global__ void __launch_bounds__(kPlanThreads) window_attention_plan_kernel(con
                 }
                 const int seq = s0 + lo, tile = e - s_first[lo];
                 const SeqInfo q = seq_info(p, seq);
-                const int count = KeyBlocks<7>(tile_union(p, q, tile)).count;
-                const int per = tile_split_blocks(p, (q.n * p.g + 255) / 256, count);
-                const int nsplit = max(1, (count + per - 1) / per);
-                const int rows = min(kTileRows, q.n * p.g - tile * kTileRows);
-                const int cost = min(per, count) * (rows > 128 ? 2 : 1);
+                const RowRange all = tile_union(p, q, tile);
+                const KeyBlocks<7> kb(all);
+                const int per = tile_split_blocks(p, seq_tiles(p, q), kb.count);
+                const int nsplit = max(1, (kb.count + per - 1) / per);
+                const int tok0 = tile * tile_tokens(p.g), ntok = min(tile_tokens(p.g), q.n - tok0);
+                const int cost = min(per, kb.count) * (2 * ntok > tile_tokens(p.g) ? 2 : 1);
                 const int bucket = kPlanBuckets - 1 - min(kPlanBuckets - 1, cost);
                 if (pass == 0) {
                     atomicAdd(&s_hist[bucket], nsplit);
@@ -276,12 +247,19 @@ __global__ void __launch_bounds__(kPlanThreads) window_attention_plan_kernel(con
                     const int at = atomicAdd(&s_hist[bucket], nsplit);
                     const int sp = nsplit > 1 ? atomicAdd(&s_split, 1) : 0;
                     if (at + nsplit <= p.items_cap && (nsplit == 1 || sp < p.split_tiles_cap)) {
-                        for (int k = 0; k < nsplit; ++k) p.items[at + k] = make_int4(seq, tile, k, 0);
+                        TileItem it = {seq, 0, 0, nsplit, q.q0, q.n, q.L, tok0, ntok, 0, 0, q.L - q.n,
+                                       all.sink, all.lo, all.hi, kb.nsink, kb.first, {0, 0, 0}};
+                        for (int k = 0; k < nsplit; ++k) {
+                            it.split = k;
+                            it.b0 = k * per;
+                            it.b1 = min(kb.count, it.b0 + per);
+                            p.items[at + k] = it;
+                        }
                         if (nsplit > 1) p.split_tiles[sp] = make_int2(seq, tile);
                     } else {
                         set_status(p.status, kStatusIndex);
                         for (int k = at; k < min(at + nsplit, p.items_cap); ++k)
-                            p.items[k] = make_int4(-2, 0, 0, 0);
+                            p.items[k].s = -2;
                         if (nsplit > 1 && sp < p.split_tiles_cap) p.split_tiles[sp] = make_int2(-1, 0);
                     }
                 }
@@ -415,24 +393,25 @@ __device__ __forceinline__ void mask_chunk(uint32_t (&x)[32], uint32_t see)
 }
 
 // A row's block: pk = 2^(x * scale - z) of its 128 scores, in pairs rounded to
-// bf16 for the product with V; returns the sum of the unrounded ones.  A chunk
-// of 32 scores is on its way from TMEM while the one before it is worked on.
+// bf16 for the product with V; returns the sum of the unrounded ones.
 __device__ __forceinline__ float block_exp(uint32_t (&pk)[64], uint32_t s_addr, const BlockMask &bm,
                                            bool part, float scale_log2, float z)
 {
     const float2 scale = dup2(scale_log2), minus_z = dup2(-z);
     float2 sum0 = make_float2(0, 0), sum1 = make_float2(0, 0);
-    uint32_t x[2][32];
-    tc_ld32(x[0], s_addr);
+    uint32_t x[4][32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        tc_wait_ld();
-        if (c < 3) tc_ld32(x[(c + 1) & 1], s_addr + 32 * (c + 1));
-        uint32_t(&xc)[32] = x[c & 1];
-        if (part) mask_chunk(xc, bm.bits(c));
+    for (int c = 0; c < 4; ++c) tc_ld32(x[c], s_addr + 32 * c);
+    tc_wait_ld();
+    if (part) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mask_chunk(x[c], bm.bits(c));
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            float2 v = fma2(make_float2(__uint_as_float(xc[2 * e]), __uint_as_float(xc[2 * e + 1])),
+            float2 v = fma2(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])),
                             scale, minus_z);
             v.x = exp2_fast(v.x);
             v.y = exp2_fast(v.y);
@@ -440,7 +419,6 @@ __device__ __forceinline__ float block_exp(uint32_t (&pk)[64], uint32_t s_addr, 
             else sum0 = add2(sum0, v);
             pk[16 * c + e] = pack_bf16(v.x, v.y);
         }
-    }
     sum0 = add2(sum0, sum1);
     return sum0.x + sum0.y;
 }
@@ -464,7 +442,8 @@ __device__ __forceinline__ float block_max(uint32_t s_addr, const BlockMask &bm,
     return fmaxf(m0, m1);
 }
 
-constexpr float kRaiseSum = 1024.0f;
+constexpr float kRiseSum = 1024.0f;        // a block's sum above which m rises after it
+constexpr float kAgainSum = 1.152921504606847e18f; // 2^60: above it the block is taken again
 
 template <int HD>
 __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, uint32_t tmem)
@@ -475,48 +454,56 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t s_addr = tmem + lanes + Sh::S_COL + t * 128;
     const uint32_t o_addr = tmem + lanes + Sh::O_COL + t * HD;
+    const int tq = 128 / p.g, tl = trow / p.g, head = trow - tl * p.g; // the row's token and head
     unsigned s_phase = 0, o_phase = 0;
     TileItem it;
     for (int k = 0; next_item(p, B, k, it); ++k) {
-        if (t == 1 && it.R <= 128) continue; // no rows in tile B
-        const int row = t * 128 + trow, r = it.rb + row;
-        const int tok = r / p.g;
-        const bool live = row < it.R;
+        if (t == 1 && it.ntok <= tq) continue; // no rows in tile B
+        const int tok = it.tok0 + t * tq + tl; // token of the sequence
+        const bool live = tl < tq && t * tq + tl < it.ntok;
         const RowRange rr = live ? row_range(p, it.pos0 + tok, it.L) : RowRange{0, 0, 0};
         float m = -INFINITY, l = 0.0f;
+        int rise = 0; // by which m goes up before the next block
         for (int j = it.b0; j < it.b1; ++j) {
             const int key0 = it.key_of(j);
             const BlockMask bm = {rr.hi - key0, rr.lo - key0, rr.sink - key0};
-            const bool part = !__all_sync(kFull, bm.whole()), some = bm.some();
+            const bool part = __any_sync(kFull, live && !bm.whole()), some = live && bm.some();
             warp_wait(p, B, &B.s_full[t], s_phase);
             s_phase ^= 1;
             tc_fence_after();
+            // O(j-1) is complete (see above)
+            auto scale_output = [&](float f) {
+                l *= f;
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 16) {
+                    uint32_t o[16];
+                    tc_ld16(o, o_addr + c);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tc_st16(o_addr + c, o);
+                }
+            };
+            if (__any_sync(kFull, rise != 0)) {
+                scale_output(__uint_as_float((uint32_t)(127 - rise) << 23));
+                m += (float)rise;
+                rise = 0;
+            }
             uint32_t pk[64];
             float sum = 0.0f;
-            bool raise = m == -INFINITY && some;
-            if (j > it.b0) { // (a first block always finds its maximum)
+            bool again = m == -INFINITY && some;
+            if (j > it.b0) { // (a first block always looks for its maximum)
                 sum = block_exp(pk, s_addr, bm, part, p.scale_log2, m == -INFINITY ? 0.0f : m);
-                raise = raise || sum > kRaiseSum;
+                again = again || (live && sum > kAgainSum);
             }
-            if (j == it.b0 || __any_sync(kFull, raise)) {
+            if (j == it.b0 || __any_sync(kFull, again)) {
                 const float top = block_max(s_addr, bm, part) * p.scale_log2;
-                raise = raise && top > m;
-                const float f = raise ? exp2_fast(m - top) : 1.0f;
-                l *= f;
-                if (j > it.b0) { // O(j-1) is complete (see above)
-#pragma unroll 1
-                    for (int c = 0; c < HD; c += 16) {
-                        uint32_t o[16];
-                        tc_ld16(o, o_addr + c);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc_st16(o_addr + c, o);
-                    }
-                }
-                if (raise) m = top;
+                again = again && top > m;
+                if (j > it.b0) scale_output(again ? exp2_fast(m - top) : 1.0f);
+                if (again) m = top;
                 sum = block_exp(pk, s_addr, bm, part, p.scale_log2, m == -INFINITY ? 0.0f : m);
             }
+            if (live && sum > kRiseSum && sum <= kAgainSum) rise = (int)(__float_as_uint(sum) >> 23) - 127;
             // P over the scores
             tc_st32(s_addr, pk);
             tc_st32(s_addr + 32, pk + 32);
@@ -530,8 +517,9 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
         const bool any = it.b1 > it.b0, part = it.nsplit > 1;
         const float inv = part ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
         const SeqInfo q = {it.q0, it.n, it.L, false};
-        const int64_t orow = live ? (int64_t)(it.q0 + tok) * p.H + it.u * p.g + (r - tok * p.g) : -1;
-        const int64_t prow = live ? part_base(p, it.s, q, it.u) + (int64_t)it.split * it.n * p.g + r : -1;
+        const int64_t orow = live ? (int64_t)(it.q0 + tok) * p.H + it.u * p.g + head : -1;
+        const int64_t prow =
+            live ? part_base(p, it.s, q, it.u) + (int64_t)it.split * it.n * p.g + tok * p.g + head : -1;
         const int64_t base = part ? prow : orow;
         if (live) {
             if (part) p.part_ml[prow] = make_float2(m, l);
@@ -630,7 +618,7 @@ __device__ __forceinline__ void tile_mma(const AttnParams &p, TileBars &B, char 
     };
     TileItem it;
     for (int n = 0; next_item(p, B, n, it); ++n) {
-        const int nt = it.b1 - it.b0, last = it.R > 128 ? 1 : 0; // last active row tile
+        const int nt = it.b1 - it.b0, last = it.ntok > 128 / p.g ? 1 : 0; // last active row tile
         if (elect_one()) {
             if (nt > 0) role_wait(p, B, &B.kv_full[stage], kv_phase);
             unsigned kst = nt > 0 ? advance() : 0; // the key block's stage
@@ -700,7 +688,7 @@ __device__ __forceinline__ void tile_follow(const AttnParams &p, TileBars &B, ch
     };
     TileItem it;
     for (int n = 0; next_item(p, B, n, it); ++n) {
-        const int last = it.R > 128 ? 1 : 0;
+        const int last = it.ntok > 128 / p.g ? 1 : 0;
         if (it.b0 < it.b1) landed(); // K of the first block
         for (int j = it.b0; j < it.b1; ++j) {
             const unsigned vst = landed();
@@ -744,28 +732,32 @@ __device__ __forceinline__ void tile_load(const AttnParams &p, TileBars &B, char
     const int box = min(128, 1 << p.page_shift), per = 128 / box; // pages of a key block
     const int rows_total = (p.num_pages * p.Hkv) << p.page_shift;
     unsigned kv = 0;
-    for (int k = 0; !is_dead(B); ++k) {
-        int4 raw = make_int4(-1, 0, 0, 0);
-        do { // the next item (-2: one that the plan left out)
+    // Take the next item off the list and put it in its slot, one ahead of the
+    // loads, so that the other roles have it when they are done with theirs.
+    auto post = [&](int k) {
+        int4 raw; // lane l < 5: the item's l-th 16 bytes
+        do {      // (-2: one that the plan left out)
             int w = 0;
             if (lane == 0) w = atomicAdd(p.plan_head + 2, 1);
             w = __shfl_sync(kFull, w, 0);
-            raw.x = -1;
-            if (w < total) {
-                raw = p.items[w / p.Hkv];
-                raw.w = w % p.Hkv;
+            raw = make_int4(-1, 0, 0, 0);
+            if (w < total && lane < 5) {
+                raw = reinterpret_cast<const int4 *>(p.items + w / p.Hkv)[lane];
+                if (lane == 0) raw.y = w % p.Hkv;
             }
-        } while (raw.x == -2);
+        } while (__shfl_sync(kFull, raw.x, 0) == -2);
         const int slot = k % kTileItems;
-        TileItem it;
-        it.s = -1;
-        if (raw.x >= 0) it = make_item(p, raw);
         warp_wait(p, B, &B.item_empty[slot], ((k / kTileItems) & 1) ^ 1);
-        if (lane == 0) {
-            B.item[slot] = it;
-            mbar_arrive(&B.item_full[slot]);
-        }
+        if (is_dead(B)) return; // the slot may still be read
+        if (lane < 5) reinterpret_cast<int4 *>(&B.item[slot])[lane] = raw;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.item_full[slot]);
+    };
+    post(0);
+    for (int k = 0; !is_dead(B); ++k) {
+        const TileItem it = B.item[k % kTileItems]; // (this warp wrote it)
         if (it.s < 0) break;
+        post(k + 1);
         const int32_t *trow = p.table + (int64_t)it.s * p.table_stride;
         // Lane l < per: first cache row of page l of key block j (a page that no
         // row sees, or an id out of range: past the end, where the copy gives zeros)
@@ -809,45 +801,39 @@ __device__ __forceinline__ void tile_load(const AttnParams &p, TileBars &B, char
             set_status(p.status, kStatusWaitDrain);
 }
 
-// Query rows into the swizzled tiles, rows past the sequence as zeros.
+// Query rows into the swizzled tiles: whole tokens of the key head's group.
+// Rows of tokens past the tile's own are another sequence's or zeros, and the
+// last 128 % g rows whatever stood there; none of them is looked at.
 template <int HD>
-__device__ __forceinline__ void tile_queries(const AttnParams &p, TileBars &B, char *smem)
+__device__ __forceinline__ void tile_queries(const AttnParams &p, TileBars &B, char *smem,
+                                             const CUtensorMap &qmap)
 {
     using Sh = TileShape<HD>;
-    constexpr int CH = HD / 8, STEP = 32 / CH; // 16-byte chunks of a row, rows of a step
-    const int lane = threadIdx.x & 31;
-    const int dt = STEP / p.g, dh = STEP - dt * p.g; // a step in tokens and heads
+    const int lane = threadIdx.x & 31, tq = 128 / p.g;
     unsigned phase[2] = {1, 1};
     TileItem it;
-    for (int k = 0; next_item(p, B, k, it); ++k) {
-        for (int t = 0; t < (it.R > 128 ? 2 : 1); ++t) {
+    for (int k = 0; next_item(p, B, k, it); ++k)
+        for (int t = 0; t < (it.ntok > tq ? 2 : 1); ++t) {
             warp_wait(p, B, &B.q_empty[t], phase[t]);
             phase[t] ^= 1;
-            const int c = lane % CH, r0 = lane / CH, left = it.R - t * 128;
-            int tok = (it.rb + t * 128 + r0) / p.g, head = it.rb + t * 128 + r0 - tok * p.g;
-            char *dst = smem + Sh::Q_OFF + t * Sh::MAT + (c >> 3) * Sh::HALF;
-            const uint4 *src = p.q + (int64_t)it.q0 * p.q_stride8 + (int64_t)it.u * p.g * CH + c;
-#pragma unroll 4
-            for (int r = r0; r < 128; r += STEP) {
-                char *at = dst + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-                if (r < left) cp_async16(at, src + tok * p.q_stride8 + head * CH);
-                else *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
-                tok += dt;
-                head += dh;
-                if (head >= p.g) head -= p.g, ++tok;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&B.q_full[t], (unsigned)(Sh::HALVES * tq * p.g * 128));
+                for (int h = 0; h < Sh::HALVES; ++h)
+                    tma_load_3d(smem + Sh::Q_OFF + t * Sh::MAT + h * Sh::HALF, &qmap, h * 64, it.u * p.g,
+                                it.q0 + it.tok0 + t * tq, &B.q_full[t]);
             }
-            cp_async_commit();
-            cp_async_wait_all();
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&B.q_full[t]);
         }
-    }
+    // copies still in flight (after a wait that ran out) land before the CTA ends
+    for (int t = 0; t < 2; ++t)
+        if (is_dead(B) && !mbar_wait(&B.q_full[t], phase[t], p.limit_ns))
+            set_status(p.status, kStatusWaitDrain);
 }
 
 template <int HD>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    window_attention_tile_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap,
+    window_attention_tile_kernel(const AttnParams p, const __grid_constant__ CUtensorMap qmap,
+                                 const __grid_constant__ CUtensorMap kmap,
                                  const __grid_constant__ CUtensorMap vmap)
 {
     using Sh = TileShape<HD>;
@@ -888,6 +874,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t tmem = B.tmem;
     grid_dependency_wait(); // the plan, and what came before it
     allow_dependents();
+    // Registers from the third warpgroup to the softmax: 128 * (208 + 208 + 88) =
+    // 384 * 168, what the block was launched with (checked before the launch).
+    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp < 8) {
         tile_softmax<HD>(p, B, tmem);
     } else if (warp == 8) {
@@ -895,7 +885,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     } else if (warp == 9) {
         tile_load<HD>(p, B, smem, kmap, vmap);
     } else if (warp == 10) {
-        tile_queries<HD>(p, B, smem);
+        tile_queries<HD>(p, B, smem, qmap);
     } else {
         tile_follow<HD>(p, B, smem);
     }
@@ -910,26 +900,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 namespace {
 
 template <int HD>
-cudaError_t launch_tile_hd(const AttnParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                           cudaStream_t s)
+cudaError_t launch_tile_hd(const AttnParams &p, const CUtensorMap &qmap, const CUtensorMap &kmap,
+                           const CUtensorMap &vmap, cudaStream_t s)
 {
     auto fn = window_attention_tile_kernel<HD>;
     const int smem = TileShape<HD>::SMEM;
     cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess) return e;
+    static const int regs = [fn] { // the kernel's register split waits for ever if it has fewer
+        cudaFuncAttributes at = {};
+        return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs != 168) return cudaErrorInvalidConfiguration;
     e = launch_overlapped_2d(window_attention_plan_kernel, dim3(1), kPlanThreads, 0, s, p);
     if (e != cudaSuccess) return e;
     const int64_t work = (int64_t)p.items_cap * p.Hkv;
     const int grid = (int)(work < sm_count() ? work : sm_count());
-    return launch_overlapped_2d(fn, dim3((unsigned)grid), kTileThreads, smem, s, p, kmap, vmap);
+    return launch_overlapped_2d(fn, dim3((unsigned)grid), kTileThreads, smem, s, p, qmap, kmap, vmap);
 }
 
 } // namespace
 
-cudaError_t launch_attention_tile(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
-                                  const CUtensorMap &vmap, cudaStream_t s)
+cudaError_t launch_attention_tile(const AttnParams &p, int head_dim, const CUtensorMap &qmap,
+                                  const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t s)
 {
-    return head_dim == 64 ? launch_tile_hd<64>(p, kmap, vmap, s) : launch_tile_hd<128>(p, kmap, vmap, s);
+    return head_dim == 64 ? launch_tile_hd<64>(p, qmap, kmap, vmap, s)
+                          : launch_tile_hd<128>(p, qmap, kmap, vmap, s);
 }
 
 } // namespace dan

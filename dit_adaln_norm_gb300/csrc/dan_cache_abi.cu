@@ -48,6 +48,21 @@ bool cache_map(CUtensorMap *map, const void *cache, int64_t rows, int64_t hd, in
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as [token][head][column], read in boxes of the 128 / g tokens by
+// g heads of a row tile, 64 columns each.
+bool query_map(CUtensorMap *map, const AttnProblem &a, int g)
+{
+    const EncodeTiled enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.heads, (cuuint64_t)a.N};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)(128 / g)};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Most splits that a step sequence over a table of this size can have.
 int step_splits(int64_t max_pages, int64_t page_size)
 {
@@ -81,7 +96,7 @@ Room room_for(int64_t N, int64_t S, int64_t heads, int64_t kv_heads, int64_t hea
         // sequences that the tile kernel takes, and the tiles of one that may be split
         const int64_t long_seqs = S < N * g / kStepRows ? S : N * g / kStepRows;
         const int64_t split_target = kTileSplitTarget / kv_heads;
-        r.items = N * g / kTileRows + long_seqs * (1 + split_target);
+        r.items = N / tile_tokens((int)g) + long_seqs * (1 + split_target);
         r.split_tiles = long_seqs * (1 + split_target / 2);
         cap = cap > split_target * kTileRows ? cap : split_target * kTileRows;
     }
@@ -91,7 +106,7 @@ Room room_for(int64_t N, int64_t S, int64_t heads, int64_t kv_heads, int64_t hea
         r.part_rows = by_seq <= by_row ? by_seq : by_row;
         r.part_bytes = (r.part_rows * (head_dim * 4 + 8) + 15) / 16 * 16;
     }
-    r.bytes = r.part_bytes + (r.tiles ? 16 * (r.items + 1) + 8 * r.split_tiles : 0);
+    r.bytes = r.part_bytes + (r.tiles ? 16 + (int64_t)sizeof(TileItem) * r.items + 8 * r.split_tiles : 0);
     return r;
 }
 
@@ -137,7 +152,7 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
     p.part_cap = room.part_cap;
     p.part_splits = room.splits;
     p.plan_head = reinterpret_cast<int *>(static_cast<char *>(a.workspace) + room.part_bytes);
-    p.items = reinterpret_cast<int4 *>(p.plan_head + 4);
+    p.items = reinterpret_cast<TileItem *>(p.plan_head + 4);
     p.split_tiles = reinterpret_cast<int2 *>(p.items + room.items);
     p.items_cap = (int)room.items;
     p.split_tiles_cap = (int)room.split_tiles;
@@ -150,7 +165,9 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
         const int box = (int)(a.page_size < 128 ? a.page_size : 128);
         if (!cache_map(&kmap, a.k_cache, rows, hd, box) || !cache_map(&vmap, a.v_cache, rows, hd, box))
             return cudaErrorInvalidValue;
-        const cudaError_t e = launch_attention_tile(p, hd, kmap, vmap, s);
+        CUtensorMap qmap;
+        if (!query_map(&qmap, a, p.g)) return cudaErrorInvalidValue;
+        const cudaError_t e = launch_attention_tile(p, hd, qmap, kmap, vmap, s);
         if (e != cudaSuccess) return e;
     }
     if (!cache_map(&kmap, a.k_cache, rows, hd, 1 << kStepShift) ||
@@ -265,6 +282,7 @@ int validate_attention(const dan_bf16 *q, int64_t N, int64_t q_row_stride, const
     if (window < 0 || window > kMaxInt || sinks < 0 || sinks > kMaxInt || chunk < 1 || chunk > kMaxInt)
         return DAN_EINVAL;
     if (!std::isfinite(scale) || scale <= 0.0f) return DAN_EINVAL;
+    if (heads / kv_heads > dan::kMaxGroup || q_row_stride >= (int64_t(1) << 39)) return DAN_EUNSUPPORTED;
     if (N > (int64_t(1) << 30) || S > (int64_t(1) << 20) ||
         N > (int64_t(1) << 30) / heads || max_pages > (int64_t(1) << 30) / page_size)
         return DAN_EUNSUPPORTED;
@@ -348,6 +366,7 @@ int64_t dan_window_attention_workspace(int64_t N, int64_t S, int64_t heads, int6
 {
     if (N < 0 || S < 0 || N > (int64_t(1) << 30) || S > (int64_t(1) << 20) || max_q < 0 ||
         check_cache(heads, kv_heads, head_dim, 1, page_size) != DAN_OK || max_pages < 1 ||
+        heads / kv_heads > dan::kMaxGroup ||
         N > (int64_t(1) << 30) / heads ||
         max_pages > (int64_t(1) << 30) / page_size)
         return 0; // the call itself refuses these sizes

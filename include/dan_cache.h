@@ -122,7 +122,8 @@ int dan_can_use_qk_norm_rope_cache(const dan_bf16 *q, const dan_bf16 *k, const d
  * 16-byte aligned, used by this call alone until it has completed (0 bytes:
  * may be NULL).  Two calls that may run at the same time, or two captured
  * graphs that may, need one each.
- * Limits: S <= 2^20, heads <= 1024, N * heads <= 2^30, max_pages*page_size <= 2^30, window,
+ * Limits: S <= 2^20, heads <= 1024, heads / kv_heads <= 128, q_row_stride < 2^39,
+ * N * heads <= 2^30, max_pages*page_size <= 2^30, window,
  * sinks, chunk in [0, 2^31 - 1] with chunk >= 1; scale finite and > 0. */
 int64_t dan_window_attention_workspace(int64_t N, int64_t S, int64_t heads, int64_t kv_heads,
                                        int64_t head_dim, int64_t max_pages, int64_t page_size,
