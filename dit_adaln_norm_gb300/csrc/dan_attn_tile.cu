@@ -386,60 +386,32 @@ struct BlockMask {
 
 // -infinity in place of the scores that the row does not see: a bit per key
 // and no branch per key (measured: branches took about 9000 cycles a block).
-__device__ __forceinline__ void mask_chunk(uint32_t (&x)[32], uint32_t see)
+__device__ __forceinline__ void mask_chunk(uint32_t *x, uint32_t see)
 {
 #pragma unroll
     for (int e = 0; e < 32; ++e) x[e] = (see >> e) & 1u ? x[e] : 0xFF800000u;
 }
 
-// A row's block: pk = 2^(x * scale - z) of its 128 scores, in pairs rounded to
-// bf16 for the product with V; returns the sum of the unrounded ones.
-__device__ __forceinline__ float block_exp(uint32_t (&pk)[64], uint32_t s_addr, const BlockMask &bm,
-                                           bool part, float scale_log2, float z)
+// Half a row's block: probabilities 2^(x * scale - z) of 64 scores, in pairs
+// rounded to bf16 for the product with V, on their way into TMEM when it
+// returns; the sum of the unrounded ones.
+__device__ __forceinline__ float half_exp(uint32_t p_addr, const uint32_t *x, float scale_log2, float z)
 {
     const float2 scale = dup2(scale_log2), minus_z = dup2(-z);
     float2 sum0 = make_float2(0, 0), sum1 = make_float2(0, 0);
-    uint32_t x[4][32];
+    uint32_t pk[32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tc_ld32(x[c], s_addr + 32 * c);
-    tc_wait_ld();
-    if (part) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mask_chunk(x[c], bm.bits(c));
+    for (int e = 0; e < 32; ++e) {
+        float2 v = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale, minus_z);
+        v.x = exp2_fast(v.x);
+        v.y = exp2_fast(v.y);
+        if (e & 1) sum1 = add2(sum1, v);
+        else sum0 = add2(sum0, v);
+        pk[e] = pack_bf16(v.x, v.y);
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            float2 v = fma2(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])),
-                            scale, minus_z);
-            v.x = exp2_fast(v.x);
-            v.y = exp2_fast(v.y);
-            if (e & 1) sum1 = add2(sum1, v);
-            else sum0 = add2(sum0, v);
-            pk[16 * c + e] = pack_bf16(v.x, v.y);
-        }
+    tc_st32(p_addr, pk);
     sum0 = add2(sum0, sum1);
     return sum0.x + sum0.y;
-}
-
-// The largest of a row's visible scores in a block.
-__device__ __forceinline__ float block_max(uint32_t s_addr, const BlockMask &bm, bool part)
-{
-    float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        tc_ld32(x, s_addr + 32 * c);
-        tc_wait_ld();
-        if (part) mask_chunk(x, bm.bits(c));
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-            m0 = fmaxf(m0, __uint_as_float(x[e]));
-            m1 = fmaxf(m1, __uint_as_float(x[e + 1]));
-        }
-    }
-    return fmaxf(m0, m1);
 }
 
 constexpr float kRiseSum = 1024.0f;        // a block's sum above which m rises after it
@@ -489,24 +461,38 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
                 m += (float)rise;
                 rise = 0;
             }
-            uint32_t pk[64];
+            uint32_t x[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc_ld32(x + 32 * c, s_addr + 32 * c);
+            tc_wait_ld();
+            if (part) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mask_chunk(x + 32 * c, bm.bits(c));
+            }
+            // P goes over the scores, which stay in registers
+            auto block_exp = [&] {
+                const float z = m == -INFINITY ? 0.0f : m;
+                const float a = half_exp(s_addr, x, p.scale_log2, z);
+                return a + half_exp(s_addr + 32, x + 64, p.scale_log2, z);
+            };
             float sum = 0.0f;
             bool again = m == -INFINITY && some;
             if (j > it.b0) { // (a first block always looks for its maximum)
-                sum = block_exp(pk, s_addr, bm, part, p.scale_log2, m == -INFINITY ? 0.0f : m);
+                sum = block_exp();
                 again = again || (live && sum > kAgainSum);
             }
             if (j == it.b0 || __any_sync(kFull, again)) {
-                const float top = block_max(s_addr, bm, part) * p.scale_log2;
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 128; ++c) top = fmaxf(top, __uint_as_float(x[c]));
+                top *= p.scale_log2;
                 again = again && top > m;
+                tc_wait_st();
                 if (j > it.b0) scale_output(again ? exp2_fast(m - top) : 1.0f);
                 if (again) m = top;
-                sum = block_exp(pk, s_addr, bm, part, p.scale_log2, m == -INFINITY ? 0.0f : m);
+                sum = block_exp();
             }
             if (live && sum > kRiseSum && sum <= kAgainSum) rise = (int)(__float_as_uint(sum) >> 23) - 127;
-            // P over the scores
-            tc_st32(s_addr, pk);
-            tc_st32(s_addr + 32, pk + 32);
             l += sum;
             tc_wait_st();
             tc_fence_before();
