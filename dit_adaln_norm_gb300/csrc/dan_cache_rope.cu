@@ -6,11 +6,14 @@
 // column at the token's position; V is copied.  About 8 flops per 4 bytes
 // moved: the bound is memory (and, for a few tokens, latency).
 //
-// A token's heads are one list, Q then K then V.  A warp takes STEPS
+// A token's heads are one list, Q then K then V.  A warp takes kSteps
 // consecutive steps of it, each step 32/LPH heads of LPH = hd/8 lanes with a
-// 16-byte fragment per lane, and has all its loads in flight before the
-// first use.  A head's sum of squares is folded over its own LPH lanes, so
-// its bits do not depend on which warp or step it falls in.
+// 16-byte fragment per lane, and has all its loads in flight before the first
+// use.  The sums of squares of its kSteps heads are folded over their lanes
+// by recursive halving, so that each lane ends with one head's sum and takes
+// one reciprocal square root; a head's fold is the same adjacent-pair tree
+// whatever step it falls in.  For the rotation of halves the lanes of the two
+// halves trade fragments of two heads, so that each has both halves of one.
 #include "dan_device.cuh"
 #include "dan_internal.h"
 #include "dan_attn.cuh"
@@ -33,131 +36,188 @@ struct CacheRopeParams {
 };
 
 constexpr int kCacheRopeWarps = 8;
+constexpr int kSteps = 8; // steps of a warp (two heads each at hd 128, four at 64)
 
-template <int HD, bool NEOX, int STEPS>
+__device__ __forceinline__ uint4 select4(bool c, const uint4 &a, const uint4 &b)
+{
+    return make_uint4(c ? a.x : b.x, c ? a.y : b.y, c ? a.z : b.z, c ? a.w : b.w);
+}
+
+template <int HD, bool NEOX>
 __global__ void __launch_bounds__(32 * kCacheRopeWarps) qk_norm_rope_cache_kernel(const CacheRopeParams p)
 {
-    constexpr int LPH = HD / 8, GPS = 32 / LPH;
+    constexpr int LPH = HD / 8, GPS = 32 / LPH, HALF = LPH / 2;
     const int lane = threadIdx.x & 31, hs = lane / LPH, fl = lane % LPH;
     const int64_t unit = (int64_t)blockIdx.x * kCacheRopeWarps + (threadIdx.x >> 5);
     const int64_t t = unit / p.steps_per_token;
-    const int h0 = (int)(unit - t * p.steps_per_token) * (GPS * STEPS) + hs;
+    const int first = (int)(unit - t * p.steps_per_token) * (GPS * kSteps); // the warp's first head
     grid_dependency_wait();
     allow_dependents();
     if (t >= p.N) return;
 
     const int HQK = p.H + p.Hkv, HT = HQK + p.Hkv;
-    const uint4 *qrow = p.q + t * p.q_stride8 + fl;
-    const uint4 *krow = p.k + t * p.kv_stride8 + fl;
-    const uint4 *vrow = p.v + t * p.kv_stride8 + fl;
+    const uint4 *qrow = p.q + t * p.q_stride8;
+    const uint4 *krow = p.k + t * p.kv_stride8;
+    const uint4 *vrow = p.v + t * p.kv_stride8;
     const int pos = __ldg(p.positions + t), slot = __ldg(p.slots + t);
-    uint4 x[STEPS];
+    uint4 x[kSteps];
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int h = h0 + GPS * i;
-        const uint4 *src = h < p.H ? qrow + h * LPH
-                           : h < HQK ? krow + (h - p.H) * LPH
-                                     : vrow + (h - HQK) * LPH;
-        x[i] = h < HT ? ld_stream(src) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kSteps; ++i) {
+        const int h = first + hs + GPS * i;
+        const uint4 *src = h < p.H ? qrow + h * LPH : h < HQK ? krow + (h - p.H) * LPH : vrow + (h - HQK) * LPH;
+        x[i] = h < HT ? ld_stream(src + fl) : make_uint4(0, 0, 0, 0);
     }
-    const uint4 wq = ld_vec(p.wq + fl), wk = ld_vec(p.wk + fl);
     if (pos < 0 || pos >= p.table_rows) {
         if (lane == 0) set_status(p.status, kStatusIndex);
         return; // the whole warp: one token
     }
     if (slot >= p.slots_total && lane == 0) set_status(p.status, kStatusIndex);
     const bool store = slot >= 0 && slot < p.slots_total;
-    // the lane's columns: pairs 4fl .. 4fl+3, or columns of one half (neox)
-    const float4 *row = p.rope + (int64_t)pos * (HD / 4);
-    float cs[8], sn[8];
-    {
-        constexpr int NV = NEOX ? 2 : 1;
-        const int b = NEOX ? 2 * (fl % (LPH / 2)) : fl;
+    // the slot's first head in the caches, in fragments
+    const int64_t cbase = store ? (((int64_t)(slot >> p.page_shift) * p.Hkv << p.page_shift) +
+                                   (slot & ((1 << p.page_shift) - 1))) * LPH
+                                : 0;
+    // where fragment f of head h goes, or nullptr
+    auto place = [&](int h, int f) -> uint4 * {
+        if (h < p.H) return p.q_out + t * p.qo_stride8 + h * LPH + f;
+        if (!store || h >= HT) return nullptr;
+        const bool key = h < HQK;
+        return (key ? p.k_cache : p.v_cache) + cbase + ((int64_t)(h - (key ? p.H : HQK)) << p.page_shift) * LPH + f;
+    };
+    if (first + GPS * kSteps > HQK) { // values: copied as they are
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const float4 c4 = ld_vec(row + b + i), s4 = ld_vec(row + HD / 8 + b + i);
-            cs[4 * i] = c4.x, cs[4 * i + 1] = c4.y, cs[4 * i + 2] = c4.z, cs[4 * i + 3] = c4.w;
-            sn[4 * i] = s4.x, sn[4 * i + 1] = s4.y, sn[4 * i + 2] = s4.z, sn[4 * i + 3] = s4.w;
+        for (int i = 0; i < kSteps; ++i) {
+            const int h = first + hs + GPS * i;
+            if (h >= HQK) {
+                uint4 *dst = place(h, fl);
+                if (dst) st_stream(dst, x[i]);
+            }
         }
-        if (NEOX && fl < LPH / 2) // first half: own*c - other*s
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
+        if (first >= HQK) return;
     }
-    // fragment offset of the slot's first head in the caches
-    const int64_t cbase =
-        store ? (((int64_t)(slot >> p.page_shift) * p.Hkv << p.page_shift) +
-                 (slot & ((1 << p.page_shift) - 1))) * LPH + fl
-              : 0;
 
+    // Columns of the lane's rotation: pairs 4fl .. 4fl+3, or columns 8 fh ..
+    // 8 fh + 7 of both halves (neox).
+    const int fh = fl % HALF;
+    constexpr int NV = NEOX ? 2 : 1, NC = 4 * NV;
+    const float4 *row = p.rope + (int64_t)pos * (HD / 4) + (NEOX ? 2 * fh : fl);
+    float cs[NC], sn[NC];
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int h = h0 + GPS * i;
-        if (h - hs >= HT) break; // warp-uniform: no head left in any lane
-        const uint4 f = x[i];
-        float acc = 0.0f;
+    for (int i = 0; i < NV; ++i) {
+        const float4 c4 = ld_vec(row + i), s4 = ld_vec(row + HD / 8 + i);
+        cs[4 * i] = c4.x, cs[4 * i + 1] = c4.y, cs[4 * i + 2] = c4.z, cs[4 * i + 3] = c4.w;
+        sn[4 * i] = s4.x, sn[4 * i + 1] = s4.y, sn[4 * i + 2] = s4.z, sn[4 * i + 3] = s4.w;
+    }
+
+    // Sums of squares over the lane's columns in order, two heads at a time.
+    float ps[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; i += 2) {
+        float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float v = elem(f, e);
-            acc = __fadd_rn(acc, __fmul_rn(v, v));
+            const float2 v = make_float2(elem(x[i], e), elem(x[i + 1], e));
+            acc = addmul2(acc, v, v);
         }
+        ps[i] = acc.x;
+        ps[i + 1] = acc.y;
+    }
+    // Fold over the head's lanes at xor offset 1, 2, 4 (, 8); afterwards the
+    // lane holds the sum of step 4 b0 + 2 b1 + b2, bi the bits of its number.
 #pragma unroll
-        for (int off = 1; off < LPH; off <<= 1)
-            acc = __fadd_rn(acc, __shfl_xor_sync(kFull, acc, off));
-        const float r = defined_rsqrt(__fadd_rn(div_by<HD>(acc), p.eps));
-        const uint4 w = h < p.H ? wq : wk;
-        float n[8];
+    for (int lvl = 0, n = kSteps; lvl < 3; ++lvl, n >>= 1) {
+        const bool upper = (fl >> lvl) & 1;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] = __fmul_rn(__fmul_rn(elem(f, e), r), elem(w, e));
-        uint4 out;
-        if (NEOX) {
+        for (int i = 0; i < n / 2; ++i) {
+            const float send = upper ? ps[i] : ps[i + n / 2];
+            const float keep = upper ? ps[i + n / 2] : ps[i];
+            ps[i] = __fadd_rn(keep, __shfl_xor_sync(kFull, send, 1 << lvl));
+        }
+    }
+    if (LPH == 16) ps[0] = __fadd_rn(ps[0], __shfl_xor_sync(kFull, ps[0], 8));
+    const float mine = defined_rsqrt(__fadd_rn(div_by<HD>(ps[0]), p.eps));
+    auto rstd = [&](int i) {
+        return __shfl_sync(kFull, mine, hs * LPH + (((i >> 2) & 1) | (i & 2) | ((i & 1) << 2)));
+    };
+
+    if constexpr (NEOX) {
+        const uint4 wq[2] = {ld_vec(p.wq + fh), ld_vec(p.wq + fh + HALF)};
+        const uint4 wk[2] = {ld_vec(p.wk + fh), ld_vec(p.wk + fh + HALF)};
+        const bool upper = fl >= HALF;
+#pragma unroll
+        for (int i = 0; i < kSteps; i += 2) {
+            if (first + GPS * i >= HQK) break; // warp-uniform: values from here on
+            const float r0 = rstd(i), r1 = rstd(i + 1), r = upper ? r1 : r0;
+            // the lower lanes take both halves of step i's head, the upper of step i+1's
+            const uint4 give = select4(upper, x[i], x[i + 1]);
+            uint4 got;
+            got.x = __shfl_xor_sync(kFull, give.x, HALF);
+            got.y = __shfl_xor_sync(kFull, give.y, HALF);
+            got.z = __shfl_xor_sync(kFull, give.z, HALF);
+            got.w = __shfl_xor_sync(kFull, give.w, HALF);
+            const uint4 a = select4(upper, got, x[i]), b = select4(upper, x[i + 1], got);
+            const int h = first + hs + GPS * (upper ? i + 1 : i);
+            const uint4 wa = select4(h < p.H, wq[0], wk[0]), wb = select4(h < p.H, wq[1], wk[1]);
+            const float2 r2 = dup2(r);
+            uint4 oa, ob;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const float o0 = __shfl_xor_sync(kFull, n[2 * m], LPH / 2);
-                const float o1 = __shfl_xor_sync(kFull, n[2 * m + 1], LPH / 2);
-                // the second half's sum rn(a s) + rn(b c) has its terms the other
-                // way round here, and the sum of two values is the same either way
-                set_word(out, m,
-                         pack_bf16(__fadd_rn(__fmul_rn(n[2 * m], cs[2 * m]), __fmul_rn(o0, sn[2 * m])),
-                                   __fadd_rn(__fmul_rn(n[2 * m + 1], cs[2 * m + 1]),
-                                             __fmul_rn(o1, sn[2 * m + 1]))));
-            }
-        } else {
+                float ra[2], rb[2];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float a = n[2 * m], b = n[2 * m + 1];
-                set_word(out, m,
-                         pack_bf16(__fsub_rn(__fmul_rn(a, cs[m]), __fmul_rn(b, sn[m])),
-                                   __fadd_rn(__fmul_rn(a, sn[m]), __fmul_rn(b, cs[m]))));
+                for (int k = 0; k < 2; ++k) {
+                    const int e = 2 * m + k;
+                    // (first half, second half) of column e
+                    const float2 n = mul2(mul2(make_float2(elem(a, e), elem(b, e)), r2),
+                                          make_float2(elem(wa, e), elem(wb, e)));
+                    const float2 pc = mul2(n, dup2(cs[e])), pn = mul2(n, dup2(sn[e]));
+                    ra[k] = __fsub_rn(pc.x, pn.y);
+                    rb[k] = __fadd_rn(pn.x, pc.y);
+                }
+                set_word(oa, m, pack_bf16(ra[0], ra[1]));
+                set_word(ob, m, pack_bf16(rb[0], rb[1]));
+            }
+            if (h < HQK) {
+                uint4 *dst = place(h, fh);
+                if (dst) {
+                    st_stream(dst, oa);
+                    st_stream(dst + HALF, ob);
+                }
             }
         }
-        if (h < p.H) {
-            st_stream(p.q_out + t * p.qo_stride8 + h * LPH + fl, out);
-        } else if (h < HT && store) {
-            const bool key = h < HQK;
-            const int64_t u = key ? h - p.H : h - HQK;
-            st_stream((key ? p.k_cache : p.v_cache) + cbase + (u << p.page_shift) * LPH,
-                      key ? out : f);
+    } else {
+        const uint4 wq = ld_vec(p.wq + fl), wk = ld_vec(p.wk + fl);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int h = first + hs + GPS * i;
+            if (first + GPS * i >= HQK) break; // warp-uniform: values from here on
+            const uint4 w = select4(h < p.H, wq, wk);
+            const float2 r2 = dup2(rstd(i));
+            uint4 out;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float2 n = mul2(mul2(wide2(word(x[i], m)), r2), wide2(word(w, m)));
+                const float2 pc = mul2(n, dup2(cs[m])), pn = mul2(n, dup2(sn[m]));
+                set_word(out, m, pack_bf16(__fsub_rn(pc.x, pn.y), __fadd_rn(pn.x, pc.y)));
+            }
+            if (h < HQK) {
+                uint4 *dst = place(h, fl);
+                if (dst) st_stream(dst, out);
+            }
         }
     }
 }
 
 namespace {
 
-template <int HD, bool NEOX, int STEPS>
-cudaError_t launch_steps(CacheRopeParams p, cudaStream_t s)
+template <int HD, bool NEOX>
+cudaError_t launch_shape(CacheRopeParams p, cudaStream_t s)
 {
-    constexpr int heads = 32 / (HD / 8) * STEPS;
+    constexpr int heads = 32 / (HD / 8) * kSteps;
     p.steps_per_token = (p.H + 2 * p.Hkv + heads - 1) / heads;
     const int64_t blocks = (p.N * p.steps_per_token + kCacheRopeWarps - 1) / kCacheRopeWarps;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch_overlapped(qk_norm_rope_cache_kernel<HD, NEOX, STEPS>, (int)blocks,
-                             32 * kCacheRopeWarps, 0, s, p);
-}
-
-template <int HD>
-cudaError_t launch_hd(const CacheRopeParams &p, bool neox, cudaStream_t s)
-{
-    return neox ? launch_steps<HD, true, 4>(p, s) : launch_steps<HD, false, 4>(p, s);
+    return launch_overlapped(qk_norm_rope_cache_kernel<HD, NEOX>, (int)blocks, 32 * kCacheRopeWarps, 0, s,
+                             p);
 }
 
 } // namespace
@@ -187,7 +247,8 @@ cudaError_t launch_qk_norm_rope_cache(const CacheRopeProblem &c, cudaStream_t s)
     p.v_cache = static_cast<uint4 *>(c.v_cache);
     p.page_shift = page_shift(c.page_size);
     p.status = device_status();
-    return c.head_dim == 64 ? launch_hd<64>(p, c.neox, s) : launch_hd<128>(p, c.neox, s);
+    if (c.head_dim == 64) return c.neox ? launch_shape<64, true>(p, s) : launch_shape<64, false>(p, s);
+    return c.neox ? launch_shape<128, true>(p, s) : launch_shape<128, false>(p, s);
 }
 
 } // namespace dan
