@@ -12,6 +12,7 @@ The library is loaded on first use.  If it is missing the call raises
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -307,49 +308,80 @@ def qk_norm_rope_epilogue(txt, img, wq_txt, wk_txt, wq_img, wk_img, rope_txt, ro
 
 
 # ------------------------------------------------------ paged-cache operators
+#
+# A decode step calls these for a few microseconds of GPU work, so the checks
+# of a good call are kept short (dtype, device index, shape and strides, each
+# read once); what is wrong with a bad one is worked out only when it is.
 
-def _one_device(named):
-    """The CUDA device that every given tensor lies on."""
-    devs = {}
-    for name, t in named:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name}: expected a CUDA tensor")
-        devs[t.device] = name
-    if len(devs) != 1:
-        raise ValueError(f"tensors lie on several devices: {sorted(map(str, devs))}")
-    return next(iter(devs))
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _is(t, dtype, device: int) -> bool:
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
+
+
+def _want(t, name: str, dtype, device: int):
+    """Raise for a tensor that is not of this dtype on this CUDA device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
+        raise TypeError(f"{name}: expected a CUDA {str(dtype).removeprefix('torch.')} tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: lies on cuda:{t.get_device()}, the caches on cuda:{device}")
 
 
 def _caches(k_cache, v_cache):
-    for c, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _bf16_cuda(c, n)
-        if c.dim() != 4 or not c.is_contiguous():
-            raise ValueError(f"{n}: expected a contiguous [pages, kv_heads, page_size, head_dim] tensor")
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have one shape")
-    return k_cache.shape
+    """([pages, kv_heads, page_size, head_dim], device index) of the caches."""
+    _bf16_cuda(k_cache, "k_cache")
+    device = k_cache.get_device()
+    if not _is(v_cache, _BF16, device):
+        _want(v_cache, "v_cache", _BF16, device)
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape or not k_cache.is_contiguous() or \
+            not v_cache.is_contiguous():
+        raise ValueError("k_cache, v_cache: expected two contiguous [pages, kv_heads, page_size, "
+                         "head_dim] tensors of one shape")
+    if not shape[3]:
+        raise ValueError("k_cache: head_dim is 0")
+    return shape, device
 
 
-def _int32(t, name, shape):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
-        raise TypeError(f"{name}: expected a CUDA int32 tensor")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _ints(t, name: str, shape, device: int):
+    if not _is(t, _I32, device):
+        _want(t, name, _I32, device)
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {list(shape)} tensor")
 
 
-def _token_rows(t, name, N, heads, hd):
-    """A [N, heads, hd] or [N, heads*hd] view whose tokens' rows are dense;
-    returns its row stride."""
-    _bf16_cuda(t, name)
-    dense = (hd, 1) if t.dim() == 3 else (1,)
-    shape = (N, heads, hd) if t.dim() == 3 else (N, heads * hd)
-    strides_ok = all(st == want or n == 1
-                     for n, st, want in zip(t.shape[1:], t.stride()[1:], dense))
-    if tuple(t.shape) != shape or (t.numel() and not strides_ok):
-        raise ValueError(f"{name}: expected [{N}, {heads}, {hd}] (or [{N}, {heads * hd}]) with dense rows")
-    return t.stride(0) if N > 1 else heads * hd
+def _token_rows(t, name: str, N: int, heads: int, hd: int, device: int) -> int:
+    """Row stride of a [N, heads, hd] or [N, heads*hd] view whose rows are dense."""
+    if not _is(t, _BF16, device):
+        _want(t, name, _BF16, device)
+    shape, stride = t.shape, t.stride()
+    width = heads * hd
+    if len(shape) == 2:
+        good = shape == (N, width) and (stride[1] == 1 or width == 1)
+    else:
+        good = shape == (N, heads, hd) and (stride[2] == 1 or hd == 1) and (stride[1] == hd or heads == 1)
+    if not good and not (N == 0 and t.numel() == 0 and shape in ((0, width), (0, heads, hd))):
+        raise ValueError(f"{name}: expected [{N}, {heads}, {hd}] (or [{N}, {width}]) with dense rows")
+    return stride[0] if N > 1 else width
+
+
+def _limit(value, name: str) -> int:
+    value = int(value)
+    if not 0 <= value <= 0x7FFFFFFF:
+        raise ValueError(f"{name}: expected 0 .. 2**31 - 1, got {value}")
+    return value
+
+
+def _on(device: int, name: str, *args):
+    """Call an entry point with the device's current stream, on that device."""
+    if torch.cuda.current_device() == device:
+        status = getattr(load(), name)(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            status = getattr(load(), name)(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status != DAN_OK:
+        raise DanError(status, name)
 
 
 def qk_norm_rope_cache(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache, eps: float,
@@ -357,45 +389,52 @@ def qk_norm_rope_cache(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache
     """RMSNorm per head and RoPE of Q and K at given positions; K and V go to
     the paged cache (include/dan_cache.h).
 
-    q [N, heads*hd], k, v [N, kv_heads*hd]: views with dense rows, k and v with
-    one row stride (e.g. column slices of a packed projection); wq, wk [hd];
-    rope fp32 [rows, hd], row p the cosines then sines of position p; positions,
-    slots int32 [N], a negative slot storing nothing; k_cache, v_cache
-    [pages, kv_heads, page_size, hd], written in place.  Returns the queries
-    [N, heads, hd] (q_out if given; q_out may be q itself)."""
-    pages, Hkv, page, hd = _caches(k_cache, v_cache)
-    _bf16_cuda(q, "q")
-    N = q.shape[0]
-    width = q[0].numel() if N else q.shape[1:].numel()
-    if hd == 0 or width % hd:
-        raise ValueError(f"q: rows of {width} elements are not whole heads of {hd}")
-    H = width // hd
-    qs = _token_rows(q, "q", N, H, hd)
-    ks, vs = _token_rows(k, "k", N, Hkv, hd), _token_rows(v, "v", N, Hkv, hd)
-    if ks != vs:
+    q [N, heads*hd], k, v [N, kv_heads*hd] (or with the heads as a dimension of
+    their own): views with dense rows, k and v with one row stride (e.g. column
+    slices of a packed projection); wq, wk [hd]; rope fp32 [rows, hd], row p the
+    cosines then sines of position p; positions, slots int32 [N], a negative
+    slot storing nothing; k_cache, v_cache [pages, kv_heads, page_size, hd],
+    written in place.  Returns the queries [N, heads, hd] (q_out if given;
+    q_out may be q itself).  All tensors on one device, whose current stream
+    the call runs on."""
+    (pages, Hkv, page, hd), device = _caches(k_cache, v_cache)
+    if not _is(q, _BF16, device):
+        _want(q, "q", _BF16, device)
+    shape = q.shape
+    if len(shape) not in (2, 3) or (len(shape) == 2 and shape[1] % hd):
+        raise ValueError(f"q: expected [N, heads*{hd}] or [N, heads, {hd}]")
+    N = shape[0]
+    H = shape[1] // hd if len(shape) == 2 else shape[1]
+    q_stride = _token_rows(q, "q", N, H, hd, device)
+    kv_stride = _token_rows(k, "k", N, Hkv, hd, device)
+    if _token_rows(v, "v", N, Hkv, hd, device) != kv_stride:
         raise ValueError("k and v must share one row stride")
-    for w, n in ((wq, "wq"), (wk, "wk")):
-        _bf16_cuda(w, n)
-        if tuple(w.shape) != (hd,) or not w.is_contiguous():
-            raise ValueError(f"{n}: expected a contiguous [{hd}] tensor")
-    if not isinstance(rope, torch.Tensor) or not rope.is_cuda or rope.dtype != torch.float32:
-        raise TypeError("rope: expected a CUDA float32 tensor")
+    for w, name in ((wq, "wq"), (wk, "wk")):
+        if not _is(w, _BF16, device):
+            _want(w, name, _BF16, device)
+        if w.shape != (hd,) or not w.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous [{hd}] tensor")
+    if not _is(rope, _F32, device):
+        _want(rope, "rope", _F32, device)
     if rope.dim() != 2 or rope.shape[1] != hd or not rope.is_contiguous():
         raise ValueError(f"rope: expected a contiguous [rows, {hd}] tensor")
-    _int32(positions, "positions", (N,))
-    _int32(slots, "slots", (N,))
-    dev = _one_device([("q", q), ("k", k), ("v", v), ("wq", wq), ("wk", wk), ("rope", rope),
-                       ("positions", positions), ("slots", slots), ("k_cache", k_cache),
-                       ("v_cache", v_cache), ("q_out", q_out)])
-    with torch.cuda.device(dev):
-        if q_out is None:
-            q_out = torch.empty((N, H, hd), dtype=torch.bfloat16, device=dev)
-        os_ = _token_rows(q_out, "q_out", N, H, hd)
-        _check(load().dan_qk_norm_rope_cache(
-            _ptr(q), _ptr(k), _ptr(v), N, qs, ks, H, Hkv, hd, _ptr(wq), _ptr(wk), _ptr(rope),
-            rope.shape[0], _ptr(positions), _ptr(slots), float(eps), int(bool(neox)), _ptr(q_out),
-            os_, _ptr(k_cache), _ptr(v_cache), pages, page, _stream()), "dan_qk_norm_rope_cache")
+    _ints(positions, "positions", (N,), device)
+    _ints(slots, "slots", (N,), device)
+    if q_out is None:
+        q_out = torch.empty((N, H, hd), dtype=_BF16, device=k_cache.device)
+        out_stride = H * hd
+    else:
+        out_stride = _token_rows(q_out, "q_out", N, H, hd, device)
+    _on(device, "dan_qk_norm_rope_cache", q.data_ptr(), k.data_ptr(), v.data_ptr(), N, q_stride,
+        kv_stride, H, Hkv, hd, wq.data_ptr(), wk.data_ptr(), rope.data_ptr(), rope.shape[0],
+        positions.data_ptr(), slots.data_ptr(), eps, 1 if neox else 0, q_out.data_ptr(), out_stride,
+        k_cache.data_ptr(), v_cache.data_ptr(), pages, page)
     return q_out if q_out.dim() == 3 else q_out.unflatten(1, (H, hd))
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(*sizes) -> int:
+    return load().dan_window_attention_workspace(*sizes)
 
 
 def window_attention(q, k_cache, v_cache, page_table, q_start, kv_len, window: int, sinks: int = 0,
@@ -412,46 +451,46 @@ def window_attention(q, k_cache, v_cache, page_table, q_start, kv_len, window: i
     in the cache.  scale defaults to hd**-0.5; max_q is a bound on the rows of
     one sequence.  Returns out [N, heads, hd] (rows outside every sequence are
     not written), or (out, lse) when ``lse`` is a float32 [N, heads] tensor or
-    True."""
-    pages, Hkv, page, hd = _caches(k_cache, v_cache)
-    _bf16_cuda(q, "q")
+    True.  All tensors on one device, whose current stream the call runs on."""
+    (pages, Hkv, page, hd), device = _caches(k_cache, v_cache)
+    if not _is(q, _BF16, device):
+        _want(q, "q", _BF16, device)
     if q.dim() != 3:
         raise ValueError("q: expected a [N, heads, head_dim] tensor")
     N, H, _ = q.shape
-    qs = _token_rows(q, "q", N, H, hd)
-    if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda or page_table.dtype != torch.int32:
-        raise TypeError("page_table: expected a CUDA int32 tensor")
+    q_stride = _token_rows(q, "q", N, H, hd, device)
+    if not _is(page_table, _I32, device):
+        _want(page_table, "page_table", _I32, device)
     if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
         raise ValueError("page_table: expected [S, max_pages] with unit column stride")
     S, M = page_table.shape
-    ts = page_table.stride(0) if S > 1 else M
-    _int32(q_start, "q_start", (S + 1,))
-    _int32(kv_len, "kv_len", (S,))
-    want_lse = lse is not None and lse is not False
-    given_lse = lse if isinstance(lse, torch.Tensor) else None
-    dev = _one_device([("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-                       ("page_table", page_table), ("q_start", q_start), ("kv_len", kv_len),
-                       ("out", out), ("lse", given_lse)])
-    max_q = N if max_q is None else int(max_q)
-    lib = load()
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty((N, H, hd), dtype=torch.bfloat16, device=dev)
-        _bf16_cuda(out, "out")
-        if tuple(out.shape) != (N, H, hd) or not out.is_contiguous():
+    table_stride = page_table.stride(0) if S > 1 else M
+    _ints(q_start, "q_start", (S + 1,), device)
+    _ints(kv_len, "kv_len", (S,), device)
+    window, sinks, chunk = _limit(window, "window"), _limit(sinks, "sinks"), _limit(chunk, "chunk")
+    max_q = N if max_q is None else _limit(max_q, "max_q")
+    if out is None:
+        out = torch.empty((N, H, hd), dtype=_BF16, device=k_cache.device)
+    else:
+        if not _is(out, _BF16, device):
+            _want(out, "out", _BF16, device)
+        if out.shape != (N, H, hd) or not out.is_contiguous():
             raise ValueError("out: expected a contiguous [N, heads, head_dim] tensor")
-        if want_lse:
-            lse = given_lse if given_lse is not None else torch.empty((N, H), dtype=torch.float32, device=dev)
-            if lse.dtype != torch.float32 or tuple(lse.shape) != (N, H) or not lse.is_contiguous():
-                raise ValueError("lse: expected a contiguous float32 [N, heads] tensor")
-        else:
-            lse = None
-        size = lib.dan_window_attention_workspace(N, S, H, Hkv, hd, M, page, max_q)
-        # of this call alone: the allocator hands it on in the stream's order
-        work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-        _check(lib.dan_window_attention(
-            _ptr(q), N, qs, _ptr(k_cache), _ptr(v_cache), pages, page, _ptr(page_table), ts, M,
-            _ptr(q_start), _ptr(kv_len), S, H, Hkv, hd, int(window), int(sinks), int(chunk), max_q,
-            float(hd ** -0.5 if scale is None else scale), _ptr(out), _ptr(lse), _ptr(work), size,
-            _stream()), "dan_window_attention")
-    return (out, lse) if want_lse else out
+    if lse is None or lse is False:
+        lse = None
+    elif lse is True:
+        lse = torch.empty((N, H), dtype=_F32, device=k_cache.device)
+    else:
+        if not _is(lse, _F32, device):
+            _want(lse, "lse", _F32, device)
+        if lse.shape != (N, H) or not lse.is_contiguous():
+            raise ValueError("lse: expected a contiguous float32 [N, heads] tensor")
+    size = _attention_workspace(N, S, H, Hkv, hd, M, page, max_q)
+    # of this call alone: the allocator hands it on in the stream's order
+    work = torch.empty(size, dtype=torch.uint8, device=k_cache.device) if size else None
+    _on(device, "dan_window_attention", q.data_ptr(), N, q_stride, k_cache.data_ptr(),
+        v_cache.data_ptr(), pages, page, page_table.data_ptr(), table_stride, M, q_start.data_ptr(),
+        kv_len.data_ptr(), S, H, Hkv, hd, window, sinks, chunk, max_q,
+        hd ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if work is None else work.data_ptr(), size)
+    return out if lse is None else (out, lse)
