@@ -184,17 +184,21 @@ struct KeyBlocks {
 };
 
 // How a step sequence's keys are split: by its own number of blocks alone, so
-// that a row's bits do not depend on the batch.  Splits of at least 256 keys,
-// at most 32 of them.
+// that a row's bits do not depend on the batch.  Splits of at least 256 keys
+// (head_dim 128) or 512 (64: the same bytes), at most 32 of them.  Measured
+// for 96 sequences of up to 2112 visible keys at head_dim 64: splits of 128
+// keys 137 us, 256 112 us, 512 87 us; one sequence of 1028 keys at head_dim
+// 128 takes the longer the fewer CTAs share it.
 constexpr int kStepRows = 16;     // query rows (tokens x g) that the step kernel takes
 constexpr int kStepShift = 4;     // its key blocks: 16 keys, the smallest page
 constexpr int kMaxSplits = 32;
-constexpr int kStepMinBlocks = 256 >> kStepShift;
+template <int HD>
+constexpr int kStepMinBlocks = (256 * 128 / HD) >> kStepShift;
 
+template <int HD>
 __device__ __forceinline__ int step_split_blocks(int count)
 {
-    const int b = (count + kMaxSplits - 1) / kMaxSplits;
-    return b < kStepMinBlocks ? kStepMinBlocks : b;
+    return max(kStepMinBlocks<HD>, (count + kMaxSplits - 1) / kMaxSplits);
 }
 
 // First partial row of (sequence, key head); its rows are [split][row].  With
@@ -230,7 +234,7 @@ __device__ __forceinline__ int seq_tiles(const AttnParams &p, const SeqInfo &q)
 // Key blocks (128 keys) of a split of a tile that sees `count` of them, in a
 // sequence of `tiles` tiles: split only where the sequence alone has fewer
 // than half of kTileSplitTarget items, and not below 8 blocks.
-constexpr int kTileSplitTarget = 128;
+constexpr int kTileSplitTarget = 64;
 constexpr int kTileMaxSplits = 16;
 constexpr int kTileMinBlocks = 8;
 

@@ -22,7 +22,7 @@
 namespace dan {
 
 constexpr int kStepWarps = 4;
-constexpr int kStepSlots = 3;
+constexpr int kStepSlots = 2; // three: fewer CTAs per SM (96 sequences x 2112 keys, hd 64: 112 us, two 101)
 constexpr int kStepKeys = 1 << kStepShift;
 
 template <int HD>
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(32 * kStepWarps)
     const int pos0 = q.L - q.n;
     const RowRange all = rows_union(p, pos0, q.L - 1, q.L);
     const KeyBlocks<kStepShift> kb(all);
-    const int per = step_split_blocks(kb.count);
+    const int per = step_split_blocks<HD>(kb.count);
     const int nsplit = max(1, (kb.count + per - 1) / per);
     if (split >= nsplit) return;
     const int b0 = split * per, b1 = min(kb.count, b0 + per);
@@ -270,67 +270,69 @@ __global__ void __launch_bounds__(32 * kStepWarps)
     }
 }
 
-// Join one row's split results, in split order: a warp, four columns a lane.
+// Join one row's split results, in split order: HD / 4 threads, four columns
+// each.
 template <int HD>
 __device__ __forceinline__ void join_row(const AttnParams &p, int s, const SeqInfo &q, int u, int r,
-                                         int nsplit)
+                                         int nsplit, int c)
 {
-    const int lane = threadIdx.x & 31, c = lane * 4, R = q.n * p.g;
+    const int R = q.n * p.g;
     const int64_t base = part_base(p, s, q, u) + r;
-    const float2 ml = lane < nsplit ? p.part_ml[base + (int64_t)lane * R] : make_float2(-INFINITY, 0.0f);
-    float m = ml.x;
-#pragma unroll
-    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-    const float f = exp2_fast(ml.x - (m == -INFINITY ? 0.0f : m));
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < nsplit; ++k) m = fmaxf(m, p.part_ml[base + (int64_t)k * R].x);
+    const float z = m == -INFINITY ? 0.0f : m;
     float l = 0.0f;
     float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll 4
     for (int k = 0; k < nsplit; ++k) {
-        const float fk = __shfl_sync(kFull, f, k);
-        l = fmaf(fk, __shfl_sync(kFull, ml.y, k), l);
-        if (c < HD) {
-            const float4 v = *reinterpret_cast<const float4 *>(p.part_o + (base + (int64_t)k * R) * HD + c);
-            a.x = fmaf(fk, v.x, a.x);
-            a.y = fmaf(fk, v.y, a.y);
-            a.z = fmaf(fk, v.z, a.z);
-            a.w = fmaf(fk, v.w, a.w);
-        }
+        const float2 ml = p.part_ml[base + (int64_t)k * R];
+        const float4 v = *reinterpret_cast<const float4 *>(p.part_o + (base + (int64_t)k * R) * HD + c);
+        const float f = exp2_fast(ml.x - z);
+        l = fmaf(f, ml.y, l);
+        a.x = fmaf(f, v.x, a.x);
+        a.y = fmaf(f, v.y, a.y);
+        a.z = fmaf(f, v.z, a.z);
+        a.w = fmaf(f, v.w, a.w);
     }
-    if (c < HD) write_row<HD>(p, q.q0 + r / p.g, u * p.g + r % p.g, c, a, m, l);
+    write_row<HD>(p, q.q0 + r / p.g, u * p.g + r % p.g, c, a, m, l);
 }
 
-// The first step_blocks blocks take four rows each of a (sequence, key head)
-// of the step kernel; the others the split tiles of the tile kernel.
+constexpr int kJoinThreads = 128;
+
+// The first step_blocks blocks take the rows of a (sequence, key head) of the
+// step kernel each; the others the split tiles of the tile kernel.
 template <int HD>
-__global__ void __launch_bounds__(128) window_attention_join_kernel(const AttnParams p, int step_blocks)
+__global__ void __launch_bounds__(kJoinThreads) window_attention_join_kernel(const AttnParams p, int step_blocks)
 {
+    constexpr int CT = HD / 4, RB = kJoinThreads / CT; // threads of a row, rows of a block
     grid_dependency_wait();
     allow_dependents();
-    const int warp = threadIdx.x >> 5;
+    const int br = threadIdx.x / CT, c = threadIdx.x % CT * 4;
     if ((int)blockIdx.x < step_blocks) {
-        constexpr int RB = kStepRows / 4;
-        const int r = (int)(blockIdx.x % RB) * 4 + warp, su = blockIdx.x / RB;
-        const int u = su % p.Hkv, s = su / p.Hkv;
+        const int u = blockIdx.x % p.Hkv, s = blockIdx.x / p.Hkv;
         const SeqInfo q = seq_info(p, s);
         const int R = q.n * p.g;
-        if (r >= R || R > kStepRows) return;
+        if (R > kStepRows) return;
         const KeyBlocks<kStepShift> kb(rows_union(p, q.L - q.n, q.L - 1, q.L));
-        const int per = step_split_blocks(kb.count);
+        const int per = step_split_blocks<HD>(kb.count);
         const int nsplit = (kb.count + per - 1) / per;
-        if (nsplit > 1) join_row<HD>(p, s, q, u, r, nsplit);
+        if (nsplit > 1)
+            for (int r = br; r < R; r += RB) join_row<HD>(p, s, q, u, r, nsplit, c);
         return;
     }
-    constexpr int RB = kTileRows / 4;
-    const int64_t work = (int64_t)p.plan_head[1] * p.Hkv * RB;
+    constexpr int TB = kTileRows / RB; // blocks of a tile's rows
+    const int64_t work = (int64_t)p.plan_head[1] * p.Hkv * TB;
     for (int64_t w = blockIdx.x - step_blocks; w < work; w += gridDim.x - step_blocks) {
-        const int2 st = p.split_tiles[w / RB / p.Hkv];
+        const int2 st = p.split_tiles[w / TB / p.Hkv];
         if (st.x < 0) continue;
-        const int u = (int)(w / RB % p.Hkv);
+        const int u = (int)(w / TB % p.Hkv);
         const SeqInfo q = seq_info(p, st.x);
-        const int rows = tile_tokens(p.g) * p.g, rt = (int)(w % RB) * 4 + warp, r = st.y * rows + rt;
+        const int rows = tile_tokens(p.g) * p.g, rt = (int)(w % TB) * RB + br, r = st.y * rows + rt;
         if (rt >= rows || r >= q.n * p.g) continue;
         const int count = KeyBlocks<7>(tile_union(p, q, st.y)).count;
         const int per = tile_split_blocks(p, seq_tiles(p, q), count);
-        join_row<HD>(p, st.x, q, u, r, (count + per - 1) / per);
+        join_row<HD>(p, st.x, q, u, r, (count + per - 1) / per, c);
     }
 }
 
@@ -351,10 +353,10 @@ cudaError_t launch_step_hd(const AttnParams &p, const CUtensorMap &kmap, const C
 template <int HD>
 cudaError_t launch_join_hd(const AttnParams &p, bool tiles, cudaStream_t s)
 {
-    const int64_t step = (int64_t)p.S * p.Hkv * (kStepRows / 4);
-    const int64_t grid = step + (tiles ? 4 * sm_count() : 0);
+    const int64_t step = (int64_t)p.S * p.Hkv;
+    const int64_t grid = step + (tiles ? 12 * sm_count() : 0);
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch_overlapped_2d(window_attention_join_kernel<HD>, dim3((unsigned)grid), 128, 0, s, p,
+    return launch_overlapped_2d(window_attention_join_kernel<HD>, dim3((unsigned)grid), kJoinThreads, 0, s, p,
                                 (int)step);
 }
 

@@ -64,11 +64,12 @@ bool query_map(CUtensorMap *map, const AttnProblem &a, int g)
 }
 
 // Most splits that a step sequence over a table of this size can have.
-int step_splits(int64_t max_pages, int64_t page_size)
+int step_splits(int64_t max_pages, int64_t page_size, int64_t head_dim)
 {
     // the sinks' last block and the window's first may both be partly used
     const int64_t blocks = ((max_pages * page_size) >> kStepShift) + 1;
-    const int64_t n = (blocks + kStepMinBlocks - 1) / kStepMinBlocks;
+    const int64_t least = head_dim == 64 ? kStepMinBlocks<64> : kStepMinBlocks<128>;
+    const int64_t n = (blocks + least - 1) / least;
     return (int)(n < kMaxSplits ? n : kMaxSplits);
 }
 
@@ -89,7 +90,7 @@ Room room_for(int64_t N, int64_t S, int64_t heads, int64_t kv_heads, int64_t hea
     if (N == 0 || S == 0) return r;
     const int64_t g = heads / kv_heads;
     max_q = max_q < N ? max_q : N;
-    r.splits = step_splits(max_pages, page_size);
+    r.splits = step_splits(max_pages, page_size, head_dim);
     r.tiles = max_q * g > kStepRows;
     int64_t cap = (int64_t)kStepRows * r.splits;
     if (r.tiles) {
