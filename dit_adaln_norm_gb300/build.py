@@ -22,7 +22,7 @@ SOURCES = ["dan_rows_rms.cu", "dan_rows_gated.cu", "dan_rows_ln.cu", "dan_rows_l
            "dan_cache_rope.cu", "dan_attn_step.cu", "dan_attn_tile.cu",
            "dan_cache_abi.cu"]
 HEADERS = ["dan_device.cuh", "dan_internal.h", "dan_ring.cuh", "dan_rows.cuh",
-           "dan_attn.cuh", "dan_attn_tma.cuh"]
+           "dan_attn.cuh", "dan_attn_plan.cuh", "dan_attn_tma.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NUMERICS = ["-fmad=false", "-prec-div=true", "-prec-sqrt=true", "-ftz=false"]

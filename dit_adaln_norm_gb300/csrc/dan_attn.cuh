@@ -247,9 +247,9 @@ __device__ __forceinline__ int tile_split_blocks(const AttnParams &p, int tiles,
 }
 
 // Launch one kernel each: sequences of at most kStepRows rows, split at most
-// `splits` ways; the others (with the plan before it); the join of splits.
+// `splits` ways (and the plan of the others); the others; the join of splits.
 cudaError_t launch_attention_step(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
-                                  const CUtensorMap &vmap, int splits, cudaStream_t s);
+                                  const CUtensorMap &vmap, int splits, bool plan, cudaStream_t s);
 cudaError_t launch_attention_tile(const AttnParams &p, int head_dim, const CUtensorMap &qmap,
                                   const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t s);
 cudaError_t launch_attention_join(const AttnParams &p, int head_dim, bool tiles, cudaStream_t s);

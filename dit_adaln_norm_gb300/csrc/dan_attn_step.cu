@@ -8,7 +8,8 @@
 // keys.  Every key and value is read once for all query heads that share it;
 // at 16 rows the arithmetic per byte is small and the bound is memory.
 //
-// One CTA has one (sequence, key head, split).  Its four warps take blocks of
+// One CTA has one (sequence, key head, split); where the tile kernel follows,
+// one more plans its work.  Its four warps take blocks of
 // 16 keys in turn, each with its own ring of TMA-filled slots, its own running
 // maximum, sum and output; nothing but the end joins them.  The 16 query rows
 // are the rows of m16n8k16 products.  TMA brings a block's K and V with the
@@ -16,6 +17,7 @@
 #include "dan_device.cuh"
 #include "dan_internal.h"
 #include "dan_attn.cuh"
+#include "dan_attn_plan.cuh"
 #include "dan_attn_tma.cuh"
 #include "dan_ring.cuh"
 
@@ -37,7 +39,7 @@ struct StepShape {
 
 template <int HD>
 __global__ void __launch_bounds__(32 * kStepWarps)
-    window_attention_step_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap,
+    window_attention_step_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                                  const __grid_constant__ CUtensorMap vmap)
 {
     using Sh = StepShape<HD>;
@@ -59,6 +61,10 @@ __global__ void __launch_bounds__(32 * kStepWarps)
 
     const int u = blockIdx.x % p.Hkv;
     const int s = blockIdx.x / p.Hkv, split = blockIdx.y;
+    if (s == p.S) { // the block past the sequences: the tile kernel's plan
+        if (u == 0 && split == 0) plan_tiles(p, *reinterpret_cast<PlanShared *>(ring));
+        return;
+    }
     const SeqInfo q = seq_info(p, s);
     if (q.bad && split == 0 && u == 0 && threadIdx.x == 0) set_status(p.status, kStatusIndex);
     const int R = q.n * p.g;
@@ -340,14 +346,15 @@ namespace {
 
 template <int HD>
 cudaError_t launch_step_hd(const AttnParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                           int splits, cudaStream_t s)
+                           int splits, bool plan, cudaStream_t s)
 {
+    static_assert(32 * kStepWarps == kPlanThreads && sizeof(PlanShared) <= StepShape<HD>::RING, "plan");
     auto fn = window_attention_step_kernel<HD>;
     const int smem = StepShape<HD>::SMEM;
     const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess) return e;
-    return launch_overlapped_2d(fn, dim3((unsigned)(p.S * p.Hkv), (unsigned)splits), 32 * kStepWarps,
-                                smem, s, p, kmap, vmap);
+    return launch_overlapped_2d(fn, dim3((unsigned)(p.S * p.Hkv + (plan ? 1 : 0)), (unsigned)splits),
+                                32 * kStepWarps, smem, s, p, kmap, vmap);
 }
 
 template <int HD>
@@ -363,10 +370,10 @@ cudaError_t launch_join_hd(const AttnParams &p, bool tiles, cudaStream_t s)
 } // namespace
 
 cudaError_t launch_attention_step(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
-                                  const CUtensorMap &vmap, int splits, cudaStream_t s)
+                                  const CUtensorMap &vmap, int splits, bool plan, cudaStream_t s)
 {
-    return head_dim == 64 ? launch_step_hd<64>(p, kmap, vmap, splits, s)
-                          : launch_step_hd<128>(p, kmap, vmap, splits, s);
+    return head_dim == 64 ? launch_step_hd<64>(p, kmap, vmap, splits, plan, s)
+                          : launch_step_hd<128>(p, kmap, vmap, splits, plan, s);
 }
 
 cudaError_t launch_attention_join(const AttnParams &p, int head_dim, bool tiles, cudaStream_t s)

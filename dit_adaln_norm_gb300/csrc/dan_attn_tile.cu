@@ -173,131 +173,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
     return upk2(r);
 }
 
-// ------------------------------------------------------------------- plan
-
-// Work lists: items (sequence, tile, split, -) longest first, and the tiles
-// that are split.  head: [0] items, [1] split tiles, [2] next item * Hkv + u.
-constexpr int kPlanThreads = 1024;
-
-__global__ void __launch_bounds__(kPlanThreads) window_attention_plan_kernel(const AttnParams p)
-{
-    __shared__ int s_first[kPlanThreads + 1]; // first tile of each sequence of the chunk
-    __shared__ int s_warp[32];
-    __shared__ int s_hist[kPlanBuckets];
-    __shared__ int s_split;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < kPlanBuckets; i += kPlanThreads) s_hist[i] = 0;
-    if (tid == 0) s_split = 0;
-    grid_dependency_wait();
-    allow_dependents();
-    __syncthreads();
-    for (int pass = 0; pass < 2; ++pass) { // count by length, then place
-        for (int s0 = 0; s0 < p.S; s0 += kPlanThreads) {
-            const int s = s0 + tid;
-            int tiles = 0;
-            if (s < p.S) {
-                const SeqInfo q = seq_info(p, s);
-                if (q.bad && pass == 0) set_status(p.status, kStatusIndex);
-                tiles = q.n * p.g > kStepRows ? seq_tiles(p, q) : 0;
-            }
-            int x = tiles; // inclusive sum over the chunk
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFull, x, o);
-                if (lane >= o) x += y;
-            }
-            if (lane == 31) s_warp[warp] = x;
-            __syncthreads();
-            if (warp == 0) {
-                int w = s_warp[lane];
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(kFull, w, o);
-                    if (lane >= o) w += y;
-                }
-                s_warp[lane] = w;
-            }
-            __syncthreads();
-            x += warp ? s_warp[warp - 1] : 0;
-            s_first[tid + 1] = x;
-            if (tid == 0) s_first[0] = 0;
-            __syncthreads();
-            const int total = s_first[kPlanThreads];
-            for (int e = tid; e < total; e += kPlanThreads) {
-                int lo = 0, hi = kPlanThreads; // the sequence whose tiles hold e
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (s_first[mid] <= e) lo = mid;
-                    else hi = mid;
-                }
-                const int seq = s0 + lo, tile = e - s_first[lo];
-                const SeqInfo q = seq_info(p, seq);
-                const RowRange all = tile_union(p, q, tile);
-                const KeyBlocks<7> kb(all);
-                const int per = tile_split_blocks(p, seq_tiles(p, q), kb.count);
-                const int nsplit = max(1, (kb.count + per - 1) / per);
-                const int tok0 = tile * tile_tokens(p.g), ntok = min(tile_tokens(p.g), q.n - tok0);
-                const int cost = min(per, kb.count) * (2 * ntok > tile_tokens(p.g) ? 2 : 1);
-                const int bucket = kPlanBuckets - 1 - min(kPlanBuckets - 1, cost);
-                if (pass == 0) {
-                    atomicAdd(&s_hist[bucket], nsplit);
-                } else {
-                    // query starts that let sequences overlap may ask for more items
-                    // than N rows can have: what is past the lists is left out
-                    const int at = atomicAdd(&s_hist[bucket], nsplit);
-                    const int sp = nsplit > 1 ? atomicAdd(&s_split, 1) : 0;
-                    if (at + nsplit <= p.items_cap && (nsplit == 1 || sp < p.split_tiles_cap)) {
-                        TileItem it = {seq, 0, 0, nsplit, q.q0, q.n, q.L, tok0, ntok, 0, 0, q.L - q.n,
-                                       all.sink, all.lo, all.hi, kb.nsink, kb.first, {0, 0, 0}};
-                        for (int k = 0; k < nsplit; ++k) {
-                            it.split = k;
-                            it.b0 = k * per;
-                            it.b1 = min(kb.count, it.b0 + per);
-                            p.items[at + k] = it;
-                        }
-                        if (nsplit > 1) p.split_tiles[sp] = make_int2(seq, tile);
-                    } else {
-                        set_status(p.status, kStatusIndex);
-                        for (int k = at; k < min(at + nsplit, p.items_cap); ++k)
-                            p.items[k].s = -2;
-                        if (nsplit > 1 && sp < p.split_tiles_cap) p.split_tiles[sp] = make_int2(-1, 0);
-                    }
-                }
-            }
-            __syncthreads();
-        }
-        if (pass == 0) { // first place of each bucket
-            int v[kPlanBuckets / kPlanThreads], sum = 0;
-#pragma unroll
-            for (int i = 0; i < kPlanBuckets / kPlanThreads; ++i) {
-                v[i] = s_hist[tid * (kPlanBuckets / kPlanThreads) + i];
-                sum += v[i];
-            }
-            int x = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFull, x, o);
-                if (lane >= o) x += y;
-            }
-            if (lane == 31) s_warp[warp] = x;
-            __syncthreads();
-            int before = x - sum;
-            for (int w = 0; w < warp; ++w) before += s_warp[w];
-#pragma unroll
-            for (int i = 0; i < kPlanBuckets / kPlanThreads; ++i) {
-                s_hist[tid * (kPlanBuckets / kPlanThreads) + i] = before;
-                before += v[i];
-            }
-            if (tid == kPlanThreads - 1) p.plan_head[0] = min(before, p.items_cap);
-            __syncthreads();
-        }
-    }
-    if (tid == 0) {
-        p.plan_head[1] = min(s_split, p.split_tiles_cap);
-        p.plan_head[2] = 0;
-    }
-}
-
 // ------------------------------------------------------------------- main
 
 // A wait of a role, each lane by itself.  One that runs out marks the CTA dead;
@@ -891,15 +766,13 @@ cudaError_t launch_tile_hd(const AttnParams &p, const CUtensorMap &qmap, const C
 {
     auto fn = window_attention_tile_kernel<HD>;
     const int smem = TileShape<HD>::SMEM;
-    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
+    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess) return e;
     static const int regs = [fn] { // the kernel's register split waits for ever if it has fewer
         cudaFuncAttributes at = {};
         return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs != 168) return cudaErrorInvalidConfiguration;
-    e = launch_overlapped_2d(window_attention_plan_kernel, dim3(1), kPlanThreads, 0, s, p);
-    if (e != cudaSuccess) return e;
     const int64_t work = (int64_t)p.items_cap * p.Hkv;
     const int grid = (int)(work < sm_count() ? work : sm_count());
     return launch_overlapped_2d(fn, dim3((unsigned)grid), kTileThreads, smem, s, p, qmap, kmap, vmap);

@@ -162,19 +162,18 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
     const int64_t rows = a.num_pages * a.kv_heads * a.page_size;
     CUtensorMap kmap, vmap;
     const int hd = (int)a.head_dim;
-    if (room.tiles) {
-        const int box = (int)(a.page_size < 128 ? a.page_size : 128);
-        if (!cache_map(&kmap, a.k_cache, rows, hd, box) || !cache_map(&vmap, a.v_cache, rows, hd, box))
-            return cudaErrorInvalidValue;
-        CUtensorMap qmap;
-        if (!query_map(&qmap, a, p.g)) return cudaErrorInvalidValue;
-        const cudaError_t e = launch_attention_tile(p, hd, qmap, kmap, vmap, s);
-        if (e != cudaSuccess) return e;
-    }
     if (!cache_map(&kmap, a.k_cache, rows, hd, 1 << kStepShift) ||
         !cache_map(&vmap, a.v_cache, rows, hd, 1 << kStepShift))
         return cudaErrorInvalidValue;
-    const cudaError_t e = launch_attention_step(p, hd, kmap, vmap, room.splits, s);
+    cudaError_t e = launch_attention_step(p, hd, kmap, vmap, room.splits, room.tiles, s);
+    if (e == cudaSuccess && room.tiles) {
+        const int box = (int)(a.page_size < 128 ? a.page_size : 128);
+        CUtensorMap qmap;
+        if (!query_map(&qmap, a, p.g) || !cache_map(&kmap, a.k_cache, rows, hd, box) ||
+            !cache_map(&vmap, a.v_cache, rows, hd, box))
+            return cudaErrorInvalidValue;
+        e = launch_attention_tile(p, hd, qmap, kmap, vmap, s);
+    }
     if (e != cudaSuccess || room.splits == 1) return e;
     return launch_attention_join(p, hd, room.tiles, s);
 }

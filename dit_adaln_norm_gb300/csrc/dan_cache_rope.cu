@@ -35,7 +35,7 @@ struct CacheRopeParams {
     unsigned *status;
 };
 
-constexpr int kCacheRopeWarps = 8;
+constexpr int kCacheRopeWarps = 2; // small blocks: an SM is refilled by the warp pair
 constexpr int kSteps = 8; // steps of a warp (two heads each at hd 128, four at 64)
 
 __device__ __forceinline__ uint4 select4(bool c, const uint4 &a, const uint4 &b)
@@ -44,7 +44,7 @@ __device__ __forceinline__ uint4 select4(bool c, const uint4 &a, const uint4 &b)
 }
 
 template <int HD, bool NEOX>
-__global__ void __launch_bounds__(32 * kCacheRopeWarps) qk_norm_rope_cache_kernel(const CacheRopeParams p)
+__global__ void __launch_bounds__(32 * kCacheRopeWarps, 12) qk_norm_rope_cache_kernel(const CacheRopeParams p)
 {
     constexpr int LPH = HD / 8, GPS = 32 / LPH, HALF = LPH / 2;
     const int lane = threadIdx.x & 31, hs = lane / LPH, fl = lane % LPH;
