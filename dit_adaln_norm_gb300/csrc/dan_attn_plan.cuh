@@ -67,7 +67,7 @@ __device__ __noinline__ void plan_tiles(const AttnParams &p, PlanShared &S)
                 const int per = tile_split_blocks(p, seq_tiles(p, q), kb.count);
                 const int nsplit = max(1, (kb.count + per - 1) / per);
                 const int tok0 = tile * tile_tokens(p.g), ntok = min(tile_tokens(p.g), q.n - tok0);
-                const int cost = min(per, kb.count) * (2 * ntok > tile_tokens(p.g) ? 2 : 1);
+                const int cost = min(per, kb.count); // a block takes as long with one row tile as with two
                 const int bucket = kPlanBuckets - 1 - min(kPlanBuckets - 1, cost);
                 if (pass == 0) {
                     atomicAdd(&S.hist[bucket], nsplit);

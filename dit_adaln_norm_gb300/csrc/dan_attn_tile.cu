@@ -27,7 +27,7 @@
 // enough for fp32 and bf16 range.  It is the maximum of the first block of
 // which the row sees a key.  Where a later block sums to more than 2^10, m
 // rises after it by that sum's exponent, and the row's sum and output are
-// scaled by the same power of two, exactly; where it sums to more than 2^60,
+// scaled by the same power of two, exactly; where it sums to more than 2^24,
 // the block's maximum is found and the block taken again.  Each choice is the
 // row's own, so bits do not depend on its neighbours.  Finding every block's
 // maximum first cost a third of the softmax's time.
@@ -290,7 +290,8 @@ __device__ __forceinline__ float half_exp(uint32_t p_addr, const uint32_t *x, fl
 }
 
 constexpr float kRiseSum = 1024.0f;        // a block's sum above which m rises after it
-constexpr float kAgainSum = 1.152921504606847e18f; // 2^60: above it the block is taken again
+constexpr float kAgainSum = 16777216.0f; // 2^24: above it the block is taken again, so that
+                                         // outputs of values up to 2^96 stay in range
 
 template <int HD>
 __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, uint32_t tmem)

@@ -94,7 +94,7 @@ const char *dan_status_string(int status);
  * current device's status word and return, leaving its outputs incomplete:
  *   1 = a warp gave up waiting for a row (or head group) it had requested,
  *   4 = after that, it also gave up waiting for its other copies in flight.
- * (Bit 2 is not used.)
+ * (Bit 2 is not used; bit 8 is described in dan_cache.h.)
  * dan_get_device_status reads the word of the current device into *status
  * and clears it.  It is synchronous: call it after synchronising the streams
  * the kernels ran on.  Returns DAN_OK, DAN_EINVAL (status NULL) or DAN_ECUDA.

@@ -94,7 +94,8 @@ int dan_can_use_qk_norm_rope_cache(const dan_bf16 *q, const dan_bf16 *k, const d
  *   lse_i = ln sum_j exp(scale * q_i . k_j)           fp32 [N, heads]
  * query head h reads key head h / (heads / kv_heads).  lse may be NULL.  A row
  * that sees no key (also one with p < 0) gives out 0 and lse -infinity.  Rows
- * of q outside every sequence are not read, and out and lse keep theirs.
+ * of q outside every sequence are not looked at, and out and lse keep theirs.
+ * A row whose scores are all -infinity counts as one that sees no key.
  * Key slots that no query of their sequence sees are not used: they may hold
  * anything (NaN included), and page-table entries that cover only such slots
  * may be anything (e.g. -1).  A value row that some query of the call sees

@@ -204,6 +204,18 @@ def test_prefill_masks(window, sinks, chunk, H, Hkv, hd, page):
                 seed=window + chunk + hd))
 
 
+@pytest.mark.parametrize("H,Hkv", [(128, 1), (100, 1), (24, 1), (17, 1), (66, 2)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_wide_groups(H, Hkv, hd):
+    """Groups of query heads that fill a row tile, or leave rows of it over."""
+    run(Problem([1, 5, 33], [300, 5, 200], H, Hkv, hd, 32, 150, 3, seed=H + hd))
+
+
+def test_most_heads():
+    run(Problem([1, 3], [40, 60], 1024, 8, 64, 16, seed=30))
+    run(Problem([1, 3], [40, 60], 1024, 1024, 64, 16, seed=31))
+
+
 def test_mixed_batch_with_empty_sequences_and_rows_behind():
     run(Problem([0, 1, 300, 0, 2, 70, 1, 0], [0, 1, 500, 40, 900, 70, 1300, 0], 8, 2, 128, 32, 250, 5,
                 seed=3, pad=9))
@@ -223,6 +235,31 @@ def test_max_q_bound_is_only_a_hint(max_q):
 def test_large_scores_and_values(q):
     run(Problem([q, q], [400, 257], 4, 2, 128, 16, seed=6, q_std=30.0, v_mean=1000.0))
     run(Problem([q, q], [400, 257], 4, 2, 128, 16, seed=7, q_std=1e-3, scale=3.0))
+
+
+@pytest.mark.parametrize("q", [1, 40])
+def test_huge_values(q):
+    """Value rows near the type's largest: sums of probabilities stay small enough."""
+    p = Problem([q], [600], 4, 2, 64, 16, seed=32, q_std=3.0, v_mean=1e30)
+    run(p)
+
+
+@pytest.mark.parametrize("first", [0.0, 2.0, 200.0])
+@pytest.mark.parametrize("q", [1, 40])
+def test_jump_after_the_first_block(q, first):
+    """Scores of the first keys are `first` lower than the others': the reference
+    they set has to rise, a little, by a power of two, or far at once."""
+    p = Problem([q], [640], 2, 1, 64, 16, seed=33)
+    u = torch.ones(64, device="cuda") / 8
+    base = p.q.float() * 0.3
+    p.q.copy_((base + u * 8).bfloat16())
+    p.K[0] = (p.K[0].float() * 0.3).bfloat16()
+    p.K[0][:, 200:] += (u * first).bfloat16()
+    for b in range(40):
+        pid = int(p.table[0, b])
+        if 0 <= pid < p.k_cache.shape[0]:
+            p.k_cache[pid] = p.K[0][:, 16 * b:16 * b + 16]
+    run(p)
 
 
 @pytest.mark.parametrize("q", [1, 50])
@@ -306,6 +343,35 @@ def test_bad_lengths_and_max_q():
     assert (out[0] == 0).all() and (lse[0] == float("-inf")).all()   # no keys
     assert (out[2:] == SENTINEL).all()                               # more than max_q rows
     assert not (out[1] == SENTINEL).any()
+
+
+def test_sequences_that_overlap_are_safe():
+    """Query starts that go back and forth name more rows than there are: what
+    does not fit the work lists is left out, and nothing else is touched."""
+    p = Problem([300], [300], 8, 1, 64, 16, seed=21, poison=False)
+    S = 4001
+    starts = torch.tensor([0 if i % 2 == 0 else 300 for i in range(S + 1)], dtype=torch.int32, device="cuda")
+    guard = torch.full((300 + 64, 8, 64), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    ops.window_attention(p.q, p.k_cache, p.v_cache, p.table.expand(S, -1).contiguous(), starts,
+                         p.kv_len.expand(S).contiguous(), 1 << 20, scale=p.scale, out=guard[32:-32])
+    torch.cuda.synchronize()
+    assert ops.device_status() == 8
+    assert (guard[:32] == SENTINEL).all() and (guard[-32:] == SENTINEL).all()
+
+
+def test_two_streams_at_once():
+    ps = [Problem([1, 300, 3], [700, 900, 64], 8, 2, 128, 32, 400, 4, seed=22 + i) for i in range(2)]
+    want = [[t.clone() for t in p.call(ops)] for p in ps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    for _ in range(5):
+        got = []
+        for p, s in zip(ps, streams):
+            with torch.cuda.stream(s):
+                got.append(p.call(ops))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
 
 
 def same(a, b):
