@@ -110,9 +110,42 @@ def test_rope_cache(N, H, Hkv, page, hd, neox):
     rope_check(p, rope_call(p, neox), neox)
 
 
+@pytest.mark.parametrize("hd,neox", [(128, False), (128, True), (64, False), (64, True)])
+@pytest.mark.parametrize("N,H,Hkv,page", [(5003, 1, 1, 16), (1751, 32, 8, 64), (2600, 9, 3, 128)])
+def test_rope_cache_many_tokens(N, H, Hkv, page, hd, neox):
+    """Enough units of work for the persistent form, several a warp."""
+    p = rope_problem(N, H, Hkv, hd, page, N + H + hd, pad=N // 7)
+    p["pos"][17] = 499
+    rope_check(p, rope_call(p, neox), neox)
+
+
+def test_rope_cache_many_tokens_in_place_and_bad_indices():
+    p = rope_problem(6000, 4, 2, 128, 64, 40)
+    q_in, out_of = p["q"].clone(), [5, 4999, 5999]
+    p["pos"][out_of] = [-1, 500, 1 << 30]
+    p["slots"][11] = p["caches"][0].shape[0] * 64
+    got = rope_call(p, True, q_out=p["q"])
+    torch.cuda.synchronize()
+    assert ops.device_status() == 8
+    assert torch.equal(p["q"][out_of].view(torch.int16), q_in[out_of].view(torch.int16))
+    keep = np.ones(6000, bool)
+    keep[out_of] = False
+    pos = np.where(keep, p["pos"], 0).astype(np.int32)
+    want = rotate_steps(q_in.float().cpu().numpy().reshape(6000, -1, 128), p["w"][0].float().cpu().numpy(),
+                        p["table"], pos, EPS, True)
+    assert (bits(got)[keep] == want[keep]).all()
+    slots = p["slots"].copy()
+    slots[out_of + [11]] = -1
+    full = bits(got).copy()
+    full[~keep] = want[~keep]
+    rope_check(dict(p, pos=pos, slots=slots), torch.from_numpy(full.view(np.int16)).view(torch.bfloat16).cuda(),
+               True, q_in=q_in)
+
+
+@pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("neox", [False, True])
-def test_rope_cache_extreme_values(neox):
-    p = rope_problem(64, 4, 2, 128, 16, 5)
+def test_rope_cache_extreme_values(neox, many):
+    p = rope_problem(5000 if many else 64, 4, 2, 128, 16, 5)
     p["q"][0], p["k"][0] = 0.0, 0.0
     p["q"][1], p["k"][1] = 1e-38, -1e-38
     p["q"][2], p["k"][2] = 3e38, 3e38            # squares overflow
