@@ -184,21 +184,24 @@ struct KeyBlocks {
 };
 
 // How a step sequence's keys are split: by its own number of blocks alone, so
-// that a row's bits do not depend on the batch.  Splits of at least 256 keys
-// (head_dim 128) or 512 (64: the same bytes), at most 32 of them.  Measured
-// for 96 sequences of up to 2112 visible keys at head_dim 64: splits of 128
-// keys 137 us, 256 112 us, 512 87 us; one sequence of 1028 keys at head_dim
-// 128 takes the longer the fewer CTAs share it.
+// that a row's bits do not depend on the batch.  Splits of 512 keys, at
+// head_dim 128 down to 256 where that makes at most eight of them, and never
+// more than 32 in all.  Measured: 96 sequences of up to 2112 visible keys at
+// head_dim 64, splits of 256 keys 103 us, 512 84 us, 1024 73 us, but one such
+// sequence of 1028 keys 8.3, 10.7 and 16.1 us; at head_dim 128 one sequence of
+// 1028 keys takes 9.2 us with 256 and 11.9 with 512, eight of up to 4216 take
+// 23.2 and 17.8.
 constexpr int kStepRows = 16;     // query rows (tokens x g) that the step kernel takes
 constexpr int kStepShift = 4;     // its key blocks: 16 keys, the smallest page
 constexpr int kMaxSplits = 32;
+constexpr int kStepBlocks = 512 >> kStepShift;
 template <int HD>
-constexpr int kStepMinBlocks = (256 * 128 / HD) >> kStepShift;
+constexpr int kStepMinBlocks = HD == 64 ? kStepBlocks : kStepBlocks / 2;
 
 template <int HD>
 __device__ __forceinline__ int step_split_blocks(int count)
 {
-    return max(kStepMinBlocks<HD>, (count + kMaxSplits - 1) / kMaxSplits);
+    return max(max(kStepMinBlocks<HD>, min(count / 8, kStepBlocks)), (count + kMaxSplits - 1) / kMaxSplits);
 }
 
 // First partial row of (sequence, key head); its rows are [split][row].  With
