@@ -141,14 +141,6 @@ __device__ __forceinline__ void tc_ld32(uint32_t *r, uint32_t addr)
                  : DAN_R8(r, 0), DAN_R8(r, 8), DAN_R8(r, 16), DAN_R8(r, 24)
                  : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-                 DAN_I8(r, 0), DAN_I8(r, 8), DAN_I8(r, 16), DAN_I8(r, 24)
-                 : "memory");
-}
 __device__ __forceinline__ void tc_ld16(uint32_t *r, uint32_t addr)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -284,7 +276,8 @@ __device__ __forceinline__ float half_exp(uint32_t p_addr, const uint32_t *x, fl
         else sum0 = add2(sum0, v);
         pk[e] = pack_bf16(v.x, v.y);
     }
-    tc_st32(p_addr, pk);
+    tc_st16(p_addr, pk);
+    tc_st16(p_addr + 16, pk + 16);
     sum0 = add2(sum0, sum1);
     return sum0.x + sum0.y;
 }
