@@ -697,6 +697,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     TileBars &B = *reinterpret_cast<TileBars *>(smem + Sh::BAR_OFF);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
+        prefetch_map(&qmap);
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
         for (int i = 0; i < Sh::STAGES; ++i) {
             mbar_init(&B.kv_full[i], 1);
             mbar_init(&B.kv_empty[i], 1);

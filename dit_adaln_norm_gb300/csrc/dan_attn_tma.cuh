@@ -20,6 +20,13 @@ __device__ __forceinline__ void tma_load_2d(void *smem_dst, const CUtensorMap *m
                  : "memory");
 }
 
+// Fetch a tensor map before its first use (it is a kernel argument: it does
+// not depend on the kernel before).
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // Box at (column x, y, z) of a 3-D tensor map, likewise.
 __device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, int x, int y, int z,
                                             uint64_t *bar)
