@@ -11,6 +11,8 @@ namespace dan {
 
 constexpr unsigned kStatusIndex = 8u; // an index in a caller's array was out of its range
 
+constexpr int kSmallestPage = 16;
+
 inline int page_shift(int64_t page_size)
 {
     int s = 0;
@@ -184,24 +186,26 @@ struct KeyBlocks {
 };
 
 // How a step sequence's keys are split: by its own number of blocks alone, so
-// that a row's bits do not depend on the batch.  Splits of 512 keys, at
-// head_dim 128 down to 256 where that makes at most eight of them, and never
-// more than 32 in all.  Measured: 96 sequences of up to 2112 visible keys at
-// head_dim 64, splits of 256 keys 103 us, 512 84 us, 1024 73 us, but one such
-// sequence of 1028 keys 8.3, 10.7 and 16.1 us; at head_dim 128 one sequence of
-// 1028 keys takes 9.2 us with 256 and 11.9 with 512, eight of up to 4216 take
-// 23.2 and 17.8.
+// that a row's bits do not depend on the batch, and never more than 32 ways.
+// At head_dim 64 splits have 768 keys at least, at 128 they have 512, or down
+// to 256 where that makes at most eight.  Measured: 96 sequences of up to 2112
+// visible keys at head_dim 64, splits of 512 keys 94 us, 768 81, 1024 80; one
+// such sequence of 1028 keys 9.6, 11.3 and 13.1 us.  At head_dim 128 one
+// sequence of 1028 keys takes 9.2 us with 256 and 11.9 with 512, eight of up to
+// 4216 take 23.2 and 17.8.
 constexpr int kStepRows = 16;     // query rows (tokens x g) that the step kernel takes
-constexpr int kStepShift = 4;     // its key blocks: 16 keys, the smallest page
 constexpr int kMaxSplits = 32;
-constexpr int kStepBlocks = 512 >> kStepShift;
 template <int HD>
-constexpr int kStepMinBlocks = HD == 64 ? kStepBlocks : kStepBlocks / 2;
+constexpr int kStepShift = HD == 64 ? 5 : 4; // its key blocks: 32 or 16 keys, 4 KB of each cache
+template <int HD>
+constexpr int kStepBlocks = 512 >> kStepShift<HD>;
+template <int HD>
+constexpr int kStepMinBlocks = HD == 64 ? kStepBlocks<HD> * 3 / 2 : kStepBlocks<HD> / 2;
 
 template <int HD>
 __device__ __forceinline__ int step_split_blocks(int count)
 {
-    return max(max(kStepMinBlocks<HD>, min(count / 8, kStepBlocks)), (count + kMaxSplits - 1) / kMaxSplits);
+    return max(max(kStepMinBlocks<HD>, min(count / 8, kStepBlocks<HD>)), (count + kMaxSplits - 1) / kMaxSplits);
 }
 
 // First partial row of (sequence, key head); its rows are [split][row].  With

@@ -9,11 +9,12 @@
 // at 16 rows the arithmetic per byte is small and the bound is memory.
 //
 // One CTA has one (sequence, key head, split); where the tile kernel follows,
-// one more plans its work.  Its four warps take blocks of
-// 16 keys in turn, each with its own ring of TMA-filled slots, its own running
-// maximum, sum and output; nothing but the end joins them.  The 16 query rows
-// are the rows of m16n8k16 products.  TMA brings a block's K and V with the
-// 128-byte swizzle, so that the matrix loads are free of bank conflicts.
+// one more plans its work.  Its four warps take blocks of 16 keys (32 at
+// head_dim 64) in turn, each with its own ring of TMA-filled slots, its own
+// running maximum, sum and output; nothing but the end joins them.  The 16
+// query rows are the rows of m16n8k16 products.  TMA brings a block's K and V
+// with the 128-byte swizzle, so that the matrix loads are free of bank
+// conflicts.
 #include "dan_device.cuh"
 #include "dan_internal.h"
 #include "dan_attn.cuh"
@@ -24,13 +25,14 @@
 namespace dan {
 
 constexpr int kStepWarps = 4;
-constexpr int kStepSlots = 2; // three: fewer CTAs per SM (96 sequences x 2112 keys, hd 64: 112 us, two 101)
-constexpr int kStepKeys = 1 << kStepShift;
-
+constexpr int kStepSlots = 2; // three leave fewer CTAs per SM (96 sequences x 2112 keys: 112 us, two 101)
 template <int HD>
 struct StepShape {
     static constexpr int HALVES = HD / 64;               // 128-byte columns of a row
-    static constexpr int HALF = kStepKeys * 128;         // bytes of one box
+    static constexpr int KEYS = 1 << kStepShift<HD>;     // of a block
+    static constexpr int BOXES = KEYS / kSmallestPage;   // a box lies in one page
+    static constexpr int BOX = kSmallestPage * 128;      // bytes of one box
+    static constexpr int HALF = BOXES * BOX;
     static constexpr int TILE = HALVES * HALF;           // K or V of a block
     static constexpr int SLOT = 2 * TILE;
     static constexpr int RING = kStepWarps * kStepSlots * SLOT;
@@ -71,7 +73,7 @@ __global__ void __launch_bounds__(32 * kStepWarps)
     if (R == 0 || R > kStepRows) return;
     const int pos0 = q.L - q.n;
     const RowRange all = rows_union(p, pos0, q.L - 1, q.L);
-    const KeyBlocks<kStepShift> kb(all);
+    const KeyBlocks<kStepShift<HD>> kb(all);
     const int per = step_split_blocks<HD>(kb.count);
     const int nsplit = max(1, (kb.count + per - 1) / per);
     if (split >= nsplit) return;
@@ -104,11 +106,16 @@ __global__ void __launch_bounds__(32 * kStepWarps)
     const int32_t *trow = p.table + (int64_t)s * p.table_stride;
     const int rows_total = (p.num_pages * p.Hkv) << p.page_shift; // < 2^31 (host)
     auto my_block = [&](int i) { return kb.block(b0 + warp + i * kStepWarps); };
-    // First cache row of the warp's i-th block, or rows_total (filled with
-    // zeros by the copy) for a page id that is out of range.
-    auto cache_row = [&](int i) {
-        if (i >= nblk) return 0;
-        const int key = my_block(i) << kStepShift;
+    constexpr int ROUND = 32 / Sh::BOXES; // blocks whose rows the lanes hold
+    // Lane l: first cache row of box l % BOXES of the warp's block i + l / BOXES;
+    // rows_total (filled with zeros by the copy) where no query sees the box or
+    // its page id is out of range.
+    auto cache_rows = [&](int i) {
+        i += lane / Sh::BOXES;
+        if (i >= nblk) return rows_total;
+        const int key = (my_block(i) << kStepShift<HD>) + lane % Sh::BOXES * kSmallestPage;
+        const bool see = (all.lo < all.hi && key < all.hi && key + kSmallestPage > all.lo) || key < all.sink;
+        if (!see) return rows_total;
         const int page = __ldg(trow + (key >> p.page_shift));
         if (page < 0 || page >= p.num_pages) {
             set_status(p.status, kStatusIndex);
@@ -116,22 +123,23 @@ __global__ void __launch_bounds__(32 * kStepWarps)
         }
         return ((page * p.Hkv + u) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
     };
-    auto request = [&](int i, int row) { // lane 0 only
+    int rows = cache_rows(0);
+    auto request = [&](int i) { // the whole warp
         uint64_t *b = bar + Pipe::slot(i);
         char *dst = slots + Pipe::slot(i) * Sh::SLOT;
-        mbar_arrive_expect_tx(b, Sh::SLOT);
+        if (lane == 0 && i < nblk) mbar_arrive_expect_tx(b, Sh::SLOT);
 #pragma unroll
-        for (int hf = 0; hf < Sh::HALVES; ++hf) {
-            tma_load_2d(dst + hf * Sh::HALF, &kmap, hf * 64, row, b);
-            tma_load_2d(dst + Sh::TILE + hf * Sh::HALF, &vmap, hf * 64, row, b);
+        for (int x = 0; x < Sh::BOXES; ++x) {
+            const int row = __shfl_sync(kFull, rows, i % ROUND * Sh::BOXES + x);
+            if (lane == 0 && i < nblk)
+#pragma unroll
+                for (int hf = 0; hf < Sh::HALVES; ++hf) {
+                    tma_load_2d(dst + hf * Sh::HALF + x * Sh::BOX, &kmap, hf * 64, row, b);
+                    tma_load_2d(dst + Sh::TILE + hf * Sh::HALF + x * Sh::BOX, &vmap, hf * 64, row, b);
+                }
         }
     };
-    int rows = cache_row(lane); // lane l holds the row of block (32 * round + l)
-#pragma unroll
-    for (int i = 0; i < kStepSlots; ++i) {
-        const int row = __shfl_sync(kFull, rows, i);
-        if (lane == 0 && i < nblk) request(i, row);
-    }
+    for (int i = 0; i < kStepSlots; ++i) request(i);
 
     float o[NT][4];
 #pragma unroll
@@ -143,10 +151,10 @@ __global__ void __launch_bounds__(32 * kStepWarps)
             break;
         }
         char *kt = slots + Pipe::slot(i) * Sh::SLOT, *vt = kt + Sh::TILE;
-        const int key0 = my_block(i) << kStepShift;
+        const int key0 = my_block(i) << kStepShift<HD>;
         // value rows that no query of the sequence sees may hold anything: zeros
-        if (key0 + kStepKeys > all.hi || (key0 < all.lo && key0 + kStepKeys > all.sink)) {
-            for (int r = lane; r < kStepKeys; r += 32) {
+        if (key0 + Sh::KEYS > all.hi || (key0 < all.lo && key0 + Sh::KEYS > all.sink)) {
+            for (int r = lane; r < Sh::KEYS; r += 32) {
                 const int key = key0 + r;
                 if (key >= all.hi || (key >= all.sink && key < all.lo))
                     for (int c = 0; c < Sh::HALVES * 8; ++c)
@@ -155,19 +163,24 @@ __global__ void __launch_bounds__(32 * kStepWarps)
             }
             __syncwarp();
         }
-        float x[2][4]; // scores: keys 8t + c2, +1 of rows r0 and r1
-        x[0][0] = x[0][1] = x[0][2] = x[0][3] = x[1][0] = x[1][1] = x[1][2] = x[1][3] = 0.0f;
+        constexpr int KT = Sh::KEYS / 8; // score tiles of 8 keys
+        float x[KT][4];                  // keys 8t + c2, +1 of rows r0 and r1
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            // matrices: keys 0-7 and 8-15, columns 16k..+7 and +8..+15
-            const int key = (lane & 7) + ((lane >> 4) << 3), chunk = (2 * k + ((lane >> 3) & 1)) & 7;
-            uint32_t b[4];
-            ldmatrix4(b, kt + (k >> 2) * Sh::HALF + key * 128 + ((chunk ^ (key & 7)) << 4));
-            mma_bf16(x[0], qf[k], b[0], b[1]);
-            mma_bf16(x[1], qf[k], b[2], b[3]);
-        }
+        for (int t = 0; t < KT; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.0f;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int t = 0; t < KT; t += 2) {
+                // matrices: keys 8t..+7 and 8t+8..+15, columns 16k..+7 and +8..+15
+                const int key = 8 * t + (lane & 7) + ((lane >> 4) << 3);
+                const int chunk = (2 * k + ((lane >> 3) & 1)) & 7;
+                uint32_t b[4];
+                ldmatrix4(b, kt + (k >> 2) * Sh::HALF + key * 128 + ((chunk ^ (key & 7)) << 4));
+                mma_bf16(x[t], qf[k], b[0], b[1]);
+                mma_bf16(x[t + 1], qf[k], b[2], b[3]);
+            }
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int key = key0 + 8 * t + c2 + (e & 1);
@@ -175,8 +188,12 @@ __global__ void __launch_bounds__(32 * kStepWarps)
                 const bool see = key < r.hi && (key < r.sink || key >= r.lo);
                 x[t][e] = see ? __fmul_rn(x[t][e], p.scale_log2) : -INFINITY;
             }
-        float a0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-        float a1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+        float a0 = fmaxf(x[0][0], x[0][1]), a1 = fmaxf(x[0][2], x[0][3]);
+#pragma unroll
+        for (int t = 1; t < KT; ++t) {
+            a0 = fmaxf(fmaxf(a0, x[t][0]), x[t][1]);
+            a1 = fmaxf(fmaxf(a1, x[t][2]), x[t][3]);
+        }
         a0 = fmaxf(a0, __shfl_xor_sync(kFull, a0, 1));
         a1 = fmaxf(a1, __shfl_xor_sync(kFull, a1, 1));
         a0 = fmaxf(a0, __shfl_xor_sync(kFull, a0, 2));
@@ -198,34 +215,37 @@ __global__ void __launch_bounds__(32 * kStepWarps)
             m0 = n0;
             m1 = n1;
         }
-        float e0[4], e1[4]; // keys c2, c2+1, 8+c2, 8+c2+1
+        // Probabilities, rounded to bf16 for the product with V (relative 2^-9
+        // each, of either sign); the sums are of the unrounded ones, of this
+        // lane's keys (the quad's are added at the end).
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < KT; t += 2) {
+            float e0[4], e1[4]; // keys 8t + c2, +1 and 8t + 8 + c2, +1
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                e0[2 * t + e] = exp2_fast(x[t][e] - z0);
-                e1[2 * t + e] = exp2_fast(x[t][2 + e] - z1);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    e0[2 * i + e] = exp2_fast(x[t + i][e] - z0);
+                    e1[2 * i + e] = exp2_fast(x[t + i][2 + e] - z1);
+                }
+            l0 += (e0[0] + e0[1]) + (e0[2] + e0[3]);
+            l1 += (e1[0] + e1[1]) + (e1[2] + e1[3]);
+            const uint32_t pf[4] = {pack_bf16(e0[0], e0[1]), pack_bf16(e1[0], e1[1]),
+                                    pack_bf16(e0[2], e0[3]), pack_bf16(e1[2], e1[3])};
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                // matrices: keys 8t..+7 and 8t+8..+15 of columns 8n..+7, then of 8n+8..+15
+                const int key = 8 * t + (lane & 15), chunk = (n + (lane >> 4)) & 7;
+                uint32_t b[4];
+                ldmatrix4_trans(b, vt + (n >> 3) * Sh::HALF + key * 128 + ((chunk ^ (key & 7)) << 4));
+                mma_bf16(o[n], pf, b[0], b[1]);
+                mma_bf16(o[n + 1], pf, b[2], b[3]);
             }
-        l0 += (e0[0] + e0[1]) + (e0[2] + e0[3]); // this lane's keys; the quad's at the end
-        l1 += (e1[0] + e1[1]) + (e1[2] + e1[3]);
-        // rounded to bf16 for the product with V (relative 2^-9 each, of either
-        // sign); the sum above is of the unrounded ones
-        const uint32_t pf[4] = {pack_bf16(e0[0], e0[1]), pack_bf16(e1[0], e1[1]),
-                                pack_bf16(e0[2], e0[3]), pack_bf16(e1[2], e1[3])};
-#pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-            // matrices: keys 0-7 and 8-15 of columns 8n..+7, then of 8n+8..+15
-            const int key = lane & 15, chunk = (n + (lane >> 4)) & 7;
-            uint32_t b[4];
-            ldmatrix4_trans(b, vt + (n >> 3) * Sh::HALF + key * 128 + ((chunk ^ (key & 7)) << 4));
-            mma_bf16(o[n], pf, b[0], b[1]);
-            mma_bf16(o[n + 1], pf, b[2], b[3]);
         }
         slot_reads_done();
         const int nx = i + kStepSlots;
-        if ((nx & 31) == 0) rows = cache_row(nx + lane);
-        const int row = __shfl_sync(kFull, rows, nx & 31);
-        if (lane == 0 && nx < nblk) request(nx, row);
+        if (nx % ROUND == 0) rows = cache_rows(nx);
+        request(nx);
     }
     l0 += __shfl_xor_sync(kFull, l0, 1);
     l1 += __shfl_xor_sync(kFull, l1, 1);
@@ -320,7 +340,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_attention_join_kernel(con
         const SeqInfo q = seq_info(p, s);
         const int R = q.n * p.g;
         if (R > kStepRows) return;
-        const KeyBlocks<kStepShift> kb(rows_union(p, q.L - q.n, q.L - 1, q.L));
+        const KeyBlocks<kStepShift<HD>> kb(rows_union(p, q.L - q.n, q.L - 1, q.L));
         const int per = step_split_blocks<HD>(kb.count);
         const int nsplit = (kb.count + per - 1) / per;
         if (nsplit > 1)

@@ -67,7 +67,7 @@ bool query_map(CUtensorMap *map, const AttnProblem &a, int g)
 int step_splits(int64_t max_pages, int64_t page_size, int64_t head_dim)
 {
     // the sinks' last block and the window's first may both be partly used
-    const int64_t blocks = ((max_pages * page_size) >> kStepShift) + 1;
+    const int64_t blocks = ((max_pages * page_size) >> (head_dim == 64 ? kStepShift<64> : kStepShift<128>)) + 2;
     const int64_t least = head_dim == 64 ? kStepMinBlocks<64> : kStepMinBlocks<128>;
     const int64_t n = (blocks + least - 1) / least;
     return (int)(n < kMaxSplits ? n : kMaxSplits);
@@ -162,8 +162,8 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
     const int64_t rows = a.num_pages * a.kv_heads * a.page_size;
     CUtensorMap kmap, vmap;
     const int hd = (int)a.head_dim;
-    if (!cache_map(&kmap, a.k_cache, rows, hd, 1 << kStepShift) ||
-        !cache_map(&vmap, a.v_cache, rows, hd, 1 << kStepShift))
+    if (!cache_map(&kmap, a.k_cache, rows, hd, kSmallestPage) ||
+        !cache_map(&vmap, a.v_cache, rows, hd, kSmallestPage))
         return cudaErrorInvalidValue;
     cudaError_t e = launch_attention_step(p, hd, kmap, vmap, room.splits, room.tiles, s);
     if (e == cudaSuccess && room.tiles) {
