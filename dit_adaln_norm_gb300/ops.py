@@ -317,7 +317,10 @@ _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _is(t, dtype, device: int) -> bool:
-    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
+    try:
+        return t.dtype is dtype and t.get_device() == device
+    except AttributeError:  # not a tensor
+        return False
 
 
 def _want(t, name: str, dtype, device: int):
@@ -330,11 +333,11 @@ def _want(t, name: str, dtype, device: int):
 
 def _caches(k_cache, v_cache):
     """([pages, kv_heads, page_size, head_dim], device index) of the caches."""
-    _bf16_cuda(k_cache, "k_cache")
-    device = k_cache.get_device()
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype is not _BF16 or not k_cache.is_cuda:
+        raise TypeError("k_cache: expected a CUDA bfloat16 tensor")
+    device, shape = k_cache.get_device(), k_cache.shape
     if not _is(v_cache, _BF16, device):
         _want(v_cache, "v_cache", _BF16, device)
-    shape = k_cache.shape
     if len(shape) != 4 or shape != v_cache.shape or not k_cache.is_contiguous() or \
             not v_cache.is_contiguous():
         raise ValueError("k_cache, v_cache: expected two contiguous [pages, kv_heads, page_size, "
@@ -375,11 +378,12 @@ def _limit(value, name: str) -> int:
 
 def _on(device: int, name: str, *args):
     """Call an entry point with the device's current stream, on that device."""
-    if torch.cuda.current_device() == device:
-        status = getattr(load(), name)(*args, torch._C._cuda_getCurrentRawStream(device))
+    fn = getattr(_lib or load(), name)
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
-            status = getattr(load(), name)(*args, torch._C._cuda_getCurrentRawStream(device))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     if status != DAN_OK:
         raise DanError(status, name)
 
