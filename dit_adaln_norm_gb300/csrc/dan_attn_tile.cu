@@ -5,7 +5,10 @@
 // (token, query head of the group) pairs, tokens outermost, so that a tile
 // of rows shares its keys; 4 * hd flops per (row, key) against 2 * 2 * hd
 // bytes per key for 256 rows: the bound is the tensor cores, and beside them
-// one exponential per (row, key).
+// one exponential per (row, key).  Measured on one GB300: a prompt of 4216
+// tokens, 32 query and 8 key heads of 128, 113 us, 1.28 PFLOP/s, 0.65 of a
+// large library product's rate; the tensor pipe is busy 79% of the time in the
+// middle of an item.
 //
 // One persistent CTA per SM, work items (sequence, 256-row tile, split, key
 // head) from a list that a planning kernel wrote, longest first, taken in
