@@ -10,9 +10,9 @@
 // large library product's rate; the tensor pipe is busy 79% of the time in the
 // middle of an item.
 //
-// One persistent CTA per SM, work items (sequence, 256-row tile, split, key
-// head) from a list that a planning kernel wrote, longest first, taken in
-// turn from a counter.  Roles:
+// One persistent CTA per SM, work items (sequence, tile, split, key head) from
+// a list that a block of the step kernel wrote, longest first, taken in turn
+// from a counter.  Roles:
 //   warps 0-3, 4-7  softmax of row tiles A and B (128 rows each, a row per
 //                   thread): scores out of TMEM, probabilities back into it
 //   warp 8          issues every tcgen05 product

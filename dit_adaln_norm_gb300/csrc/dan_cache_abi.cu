@@ -158,7 +158,9 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
     p.items_cap = (int)room.items;
     p.split_tiles_cap = (int)room.split_tiles;
     p.status = device_status();
-    p.limit_ns = 1000000000ull;
+    // a second, and what an item with every key of the table takes: some waits are
+    // for a whole item (a block of 128 keys takes about 1.4 us)
+    p.limit_ns = 1000000000ull + 30ull * (unsigned long long)(a.max_pages * a.page_size);
     const int64_t rows = a.num_pages * a.kv_heads * a.page_size;
     CUtensorMap kmap, vmap;
     const int hd = (int)a.head_dim;
