@@ -9,8 +9,8 @@
 // at 16 rows the arithmetic per byte is small and the bound is memory.  Measured
 // on one GB300: 64 tokens over up to 32768 keys, 32 query and 8 key heads of
 // 128, 618 us, 7.0 TB/s (a copy reaches 6.7); 96 sequences of one to three
-// tokens over 2112 keys of 8 heads of 64, 81 us, 4.7 TB/s; one token over 1028
-// keys 9.3 us, launches and dependent loads.
+// tokens over 2112 keys of 8 heads of 64, 76 us, 5.0 TB/s; one token over 1028
+// keys 9.2 us, launches and dependent loads.
 //
 // One CTA has one (sequence, key head, split); where the tile kernel follows,
 // one more plans its work.  Its four warps take blocks of 16 keys (32 at

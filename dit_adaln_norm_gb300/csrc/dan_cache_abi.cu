@@ -63,11 +63,11 @@ bool query_map(CUtensorMap *map, const AttnProblem &a, int g)
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Most splits that a step sequence over a table of this size can have.
-int step_splits(int64_t max_pages, int64_t page_size, int64_t head_dim)
+// Most splits that a step sequence that sees at most `keys` keys can have.
+int step_splits(int64_t keys, int64_t head_dim)
 {
-    // the sinks' last block and the window's first may both be partly used
-    const int64_t blocks = ((max_pages * page_size) >> (head_dim == 64 ? kStepShift<64> : kStepShift<128>)) + 2;
+    // the first tokens' last block and the window's first and last may be partly seen
+    const int64_t blocks = (keys >> (head_dim == 64 ? kStepShift<64> : kStepShift<128>)) + 3;
     const int64_t least = head_dim == 64 ? kStepMinBlocks<64> : kStepMinBlocks<128>;
     const int64_t n = (blocks + least - 1) / least;
     return (int)(n < kMaxSplits ? n : kMaxSplits);
@@ -90,7 +90,7 @@ Room room_for(int64_t N, int64_t S, int64_t heads, int64_t kv_heads, int64_t hea
     if (N == 0 || S == 0) return r;
     const int64_t g = heads / kv_heads;
     max_q = max_q < N ? max_q : N;
-    r.splits = step_splits(max_pages, page_size, head_dim);
+    r.splits = step_splits(max_pages * page_size, head_dim);
     r.tiles = max_q * g > kStepRows;
     int64_t cap = (int64_t)kStepRows * r.splits;
     if (r.tiles) {
@@ -167,7 +167,12 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
     if (!cache_map(&kmap, a.k_cache, rows, hd, kSmallestPage) ||
         !cache_map(&vmap, a.v_cache, rows, hd, kSmallestPage))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch_attention_step(p, hd, kmap, vmap, room.splits, room.tiles, s);
+    // a step sequence's at most 16 tokens see the first ones and no more than
+    // their windows and chunks: the grid need not cover what no call reaches
+    const int64_t seen = a.sinks + (a.window ? a.window + 2 * a.chunk + kStepRows : 0);
+    const int64_t cap = a.max_pages * a.page_size;
+    const int splits = step_splits(seen < cap ? seen : cap, a.head_dim);
+    cudaError_t e = launch_attention_step(p, hd, kmap, vmap, splits, room.tiles, s);
     if (e == cudaSuccess && room.tiles) {
         const int box = (int)(a.page_size < 128 ? a.page_size : 128);
         CUtensorMap qmap;
@@ -176,7 +181,7 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
             return cudaErrorInvalidValue;
         e = launch_attention_tile(p, hd, qmap, kmap, vmap, s);
     }
-    if (e != cudaSuccess || room.splits == 1) return e;
+    if (e != cudaSuccess || (room.tiles ? room.splits : splits) == 1) return e;
     return launch_attention_join(p, hd, room.tiles, s);
 }
 

@@ -332,6 +332,14 @@ def test_long_context_split():
     run(Problem([48, 20], [9000, 5000], 4, 1, 128, 64, seed=11))
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("window,sinks,chunk", [(3000, 700, 1), (1, 6000, 1), (2500, 0, 900), (16, 1, 5000),
+                                                (769, 0, 1), (1, 0, 800)])
+def test_windows_in_long_tables(window, sinks, chunk, hd):
+    """Few of a long table's keys are seen: the launch covers those."""
+    run(Problem([1, 3, 2, 4], [20000, 15001, 2, 9999], 4, 1, hd, 16, window, sinks, chunk, seed=hd + window))
+
+
 def test_lse_is_optional_and_out_is_made():
     p = Problem([3, 20], [50, 60], 4, 2, 64, 16, seed=12)
     out = ops.window_attention(p.q, p.k_cache, p.v_cache, p.table, p.q_start, p.kv_len, p.window)
