@@ -415,6 +415,64 @@ def test_two_streams_at_once():
             assert all(torch.equal(a, b) for a, b in zip(g, w))
 
 
+@pytest.mark.parametrize("S", [127, 128, 129, 300])
+def test_many_sequences(S):
+    """More sequences than the plan's block looks at together, of every length."""
+    rng = random.Random(S)
+    q = [rng.choice([0, 1, 1, 3, 9, 20, 70]) for _ in range(S)]
+    run(Problem(q, [n + rng.randint(0, 300) for n in q], 6, 2, 64, 16, 90, 3, seed=S))
+
+
+def test_most_heads_rotated():
+    p = rope_problem(5, 1024, 1024, 64, 16, 41)
+    rope_check(p, rope_call(p, True), True)
+
+
+def test_sequences_share_pages():
+    """A prefix's pages in two sequences' tables, as after a fork."""
+    p = Problem([1, 40, 1], [200, 240, 200], 8, 2, 128, 32, seed=42)
+    p.table[2, :7] = p.table[0, :7]
+    p.K[2], p.V[2] = p.K[0], p.V[0]
+    run(p)
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_decode_step_in_a_graph(many):
+    """Both operators captured once and replayed as the sequences grow, lengths,
+    positions, slots and inputs rewritten in place between replays."""
+    H, Hkv, hd, page, S, M = 8, 2, 128, 16, 3, 12
+    add = 25 if many else 1
+    g = torch.Generator(device="cuda").manual_seed(43)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.randperm(S * M, generator=g, device="cuda").int().view(S, M)
+    kc, vc = (torch.zeros((S * M, Hkv, page, hd), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rope = torch.from_numpy(synth.rope_table(256, hd)).cuda()
+    w = torch.ones(hd, dtype=torch.bfloat16, device="cuda")
+    qkv = torch.zeros(S * add, (H + 2 * Hkv) * hd, dtype=torch.bfloat16, device="cuda")
+    pos, slots, lens = i32([0] * S * add), i32([-1] * S * add), i32([add] * S)
+    starts = i32([add * s for s in range(S + 1)])
+
+    def step(kc, vc):
+        q = ops.qk_norm_rope_cache(qkv[:, :H * hd], qkv[:, H * hd:(H + Hkv) * hd], qkv[:, (H + Hkv) * hd:],
+                                   w, w, rope, pos, slots, kc, vc, EPS)
+        return ops.window_attention(q, kc, vc, table, starts, lens, 60, sinks=2, max_q=add)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(kc, vc)
+    kc2, vc2 = kc.clone(), vc.clone()
+    for t in range(6):
+        qkv.copy_(torch.randn(qkv.shape, generator=g, device="cuda"))
+        at = [(s, t * add + i) for s in range(S) for i in range(add)]
+        pos.copy_(i32([p for _, p in at]))
+        slots.copy_(i32([int(table[s, p // page]) * page + p % page for s, p in at]))
+        lens.fill_((t + 1) * add)
+        graph.replay()
+        want = step(kc2, vc2)
+        torch.cuda.synchronize()
+        assert same(out, want) and same(kc, kc2) and same(vc, vc2), t
+
+
 def same(a, b):
     return torch.equal(a.view(torch.int16), b.view(torch.int16))
 
