@@ -52,9 +52,7 @@ struct AttnProblem {
 
 cudaError_t launch_qk_norm_rope_cache(const CacheRopeProblem &p, cudaStream_t s);
 cudaError_t launch_window_attention(const AttnProblem &p, cudaStream_t s);
-int64_t window_attention_workspace(int64_t N, int64_t S, int64_t heads, int64_t kv_heads,
-                                   int64_t head_dim, int64_t max_pages, int64_t page_size,
-                                   int64_t max_q);
+int64_t window_attention_workspace(const AttnProblem &p); // its sizes alone
 
 // Launch with programmatic stream serialization (see launch_overlapped) on a
 // two-dimensional grid.

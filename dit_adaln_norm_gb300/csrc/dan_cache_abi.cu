@@ -73,39 +73,57 @@ int step_splits(int64_t keys, int64_t head_dim)
     return (int)(n < kMaxSplits ? n : kMaxSplits);
 }
 
+// Keys that `tokens` successive tokens of a sequence can see together: the
+// first ones, and their windows and chunks.
+int64_t keys_seen(const AttnProblem &a, int64_t tokens)
+{
+    const int64_t seen = a.sinks + (a.window ? a.window + 2 * a.chunk + tokens : 0);
+    const int64_t cap = a.max_pages * a.page_size;
+    return seen < cap ? seen : cap;
+}
+
+// Most splits that a tile of the tile kernel can have.
+int tile_splits(int64_t keys, int64_t kv_heads)
+{
+    const int64_t n = kTileSplitTarget / kv_heads, blocks = keys / 128 + 3;
+    const int64_t most = blocks / kTileMinBlocks < kTileMaxSplits ? blocks / kTileMinBlocks : kTileMaxSplits;
+    return (int)(n < most ? (n < 1 ? 1 : n) : most < 1 ? 1 : most);
+}
+
 // What a call needs of the workspace: partial results of splits, with room
 // by (sequence, key head) (cap rows each) or by query row, whichever is less
 // in all, and the tile kernel's work lists.
 struct Room {
-    int splits = 1;     // most splits of a step sequence
-    bool tiles = false; // a sequence may have more rows than the step kernel takes
+    int step_splits = 1; // most splits of a step sequence
+    int splits = 1;      // and of any sequence
+    bool tiles = false;  // a sequence may have more rows than the step kernel takes
     int64_t part_rows = 0, part_cap = 0, items = 0, split_tiles = 0;
     int64_t part_bytes = 0, bytes = 0;
 };
 
-Room room_for(int64_t N, int64_t S, int64_t heads, int64_t kv_heads, int64_t head_dim,
-              int64_t max_pages, int64_t page_size, int64_t max_q)
+Room room_for(const AttnProblem &a)
 {
     Room r;
-    if (N == 0 || S == 0) return r;
-    const int64_t g = heads / kv_heads;
-    max_q = max_q < N ? max_q : N;
-    r.splits = step_splits(max_pages * page_size, head_dim);
+    if (a.N == 0 || a.S == 0) return r;
+    const int64_t g = a.heads / a.kv_heads, max_q = a.max_q < a.N ? a.max_q : a.N;
+    r.step_splits = r.splits = step_splits(keys_seen(a, kStepRows), a.head_dim);
     r.tiles = max_q * g > kStepRows;
     int64_t cap = (int64_t)kStepRows * r.splits;
     if (r.tiles) {
         // sequences that the tile kernel takes, and the tiles of one that may be split
-        const int64_t long_seqs = S < N * g / kStepRows ? S : N * g / kStepRows;
-        const int64_t split_target = kTileSplitTarget / kv_heads;
-        r.items = N / tile_tokens((int)g) + long_seqs * (1 + split_target);
+        const int64_t long_seqs = a.S < a.N * g / kStepRows ? a.S : a.N * g / kStepRows;
+        const int64_t split_target = kTileSplitTarget / a.kv_heads;
+        r.items = a.N / tile_tokens((int)g) + long_seqs * (1 + split_target);
         r.split_tiles = long_seqs * (1 + split_target / 2);
-        cap = cap > split_target * kTileRows ? cap : split_target * kTileRows;
+        const int splits = tile_splits(keys_seen(a, kTileRows), a.kv_heads);
+        if (splits > 1 && cap < split_target * kTileRows) cap = split_target * kTileRows;
+        if (splits > r.splits) r.splits = splits;
     }
     if (r.splits > 1) {
-        const int64_t by_seq = S * kv_heads * cap, by_row = N * heads * r.splits;
+        const int64_t by_seq = a.S * a.kv_heads * cap, by_row = a.N * a.heads * r.splits;
         r.part_cap = by_seq <= by_row ? cap : 0;
         r.part_rows = by_seq <= by_row ? by_seq : by_row;
-        r.part_bytes = (r.part_rows * (head_dim * 4 + 8) + 15) / 16 * 16;
+        r.part_bytes = (r.part_rows * (a.head_dim * 4 + 8) + 15) / 16 * 16;
     }
     r.bytes = r.part_bytes + (r.tiles ? 16 + (int64_t)sizeof(TileItem) * r.items + 8 * r.split_tiles : 0);
     return r;
@@ -113,12 +131,7 @@ Room room_for(int64_t N, int64_t S, int64_t heads, int64_t kv_heads, int64_t hea
 
 } // namespace
 
-int64_t window_attention_workspace(int64_t N, int64_t S, int64_t heads, int64_t kv_heads,
-                                   int64_t head_dim, int64_t max_pages, int64_t page_size,
-                                   int64_t max_q)
-{
-    return room_for(N, S, heads, kv_heads, head_dim, max_pages, page_size, max_q).bytes;
-}
+int64_t window_attention_workspace(const AttnProblem &a) { return room_for(a).bytes; }
 
 cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
 {
@@ -145,8 +158,7 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
     p.out = static_cast<uint4 *>(a.out);
     p.lse = a.lse;
-    const Room room = room_for(a.N, a.S, a.heads, a.kv_heads, a.head_dim, a.max_pages, a.page_size,
-                               a.max_q);
+    const Room room = room_for(a);
     if (room.items > 0x7FFFFFFF || room.split_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.part_o = static_cast<float *>(a.workspace);
     p.part_ml = reinterpret_cast<float2 *>(p.part_o + room.part_rows * a.head_dim);
@@ -167,12 +179,7 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
     if (!cache_map(&kmap, a.k_cache, rows, hd, kSmallestPage) ||
         !cache_map(&vmap, a.v_cache, rows, hd, kSmallestPage))
         return cudaErrorInvalidValue;
-    // a step sequence's at most 16 tokens see the first ones and no more than
-    // their windows and chunks: the grid need not cover what no call reaches
-    const int64_t seen = a.sinks + (a.window ? a.window + 2 * a.chunk + kStepRows : 0);
-    const int64_t cap = a.max_pages * a.page_size;
-    const int splits = step_splits(seen < cap ? seen : cap, a.head_dim);
-    cudaError_t e = launch_attention_step(p, hd, kmap, vmap, splits, room.tiles, s);
+    cudaError_t e = launch_attention_step(p, hd, kmap, vmap, room.step_splits, room.tiles, s);
     if (e == cudaSuccess && room.tiles) {
         const int box = (int)(a.page_size < 128 ? a.page_size : 128);
         CUtensorMap qmap;
@@ -181,7 +188,7 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
             return cudaErrorInvalidValue;
         e = launch_attention_tile(p, hd, qmap, kmap, vmap, s);
     }
-    if (e != cudaSuccess || (room.tiles ? room.splits : splits) == 1) return e;
+    if (e != cudaSuccess || room.splits == 1) return e;
     return launch_attention_join(p, hd, room.tiles, s);
 }
 
@@ -298,8 +305,8 @@ int validate_attention(const dan_bf16 *q, int64_t N, int64_t q_row_stride, const
     const int64_t qb = rows_bytes(N, heads * hd, q_row_stride);
     if (qb < 0) return DAN_EINVAL;
     if (!q || !k_cache || !v_cache || !page_table || !q_start || !kv_len || !out) return DAN_EINVAL;
-    const int64_t need = dan::window_attention_workspace(N, S, heads, kv_heads, hd, max_pages,
-                                                         page_size, max_q);
+    const int64_t need = dan_window_attention_workspace(N, S, heads, kv_heads, hd, max_pages, page_size,
+                                                        window, sinks, chunk, max_q);
     if (workspace_bytes < need || (need > 0 && !workspace)) return DAN_EINVAL;
     const void *p16[] = {q, k_cache, v_cache, out, workspace};
     for (const void *p : p16)
@@ -369,15 +376,19 @@ int dan_qk_norm_rope_cache(const dan_bf16 *q, const dan_bf16 *k, const dan_bf16 
 
 int64_t dan_window_attention_workspace(int64_t N, int64_t S, int64_t heads, int64_t kv_heads,
                                        int64_t head_dim, int64_t max_pages, int64_t page_size,
-                                       int64_t max_q)
+                                       int64_t window, int64_t sinks, int64_t chunk, int64_t max_q)
 {
-    if (N < 0 || S < 0 || N > (int64_t(1) << 30) || S > (int64_t(1) << 20) || max_q < 0 ||
+    if (N < 0 || S < 0 || N > (int64_t(1) << 30) || S > (int64_t(1) << 20) || max_q < 0 || window < 0 ||
+        window > kMaxInt || sinks < 0 || sinks > kMaxInt || chunk < 1 || chunk > kMaxInt ||
         check_cache(heads, kv_heads, head_dim, 1, page_size) != DAN_OK || max_pages < 1 ||
-        heads / kv_heads > dan::kMaxGroup ||
-        N > (int64_t(1) << 30) / heads ||
+        heads / kv_heads > dan::kMaxGroup || N > (int64_t(1) << 30) / heads ||
         max_pages > (int64_t(1) << 30) / page_size)
         return 0; // the call itself refuses these sizes
-    return dan::window_attention_workspace(N, S, heads, kv_heads, head_dim, max_pages, page_size, max_q);
+    dan::AttnProblem a = {};
+    a.N = N, a.S = S, a.heads = heads, a.kv_heads = kv_heads, a.head_dim = head_dim;
+    a.max_pages = max_pages, a.page_size = page_size, a.max_q = max_q;
+    a.window = window, a.sinks = sinks, a.chunk = chunk;
+    return dan::window_attention_workspace(a);
 }
 
 int dan_can_use_window_attention(const dan_bf16 *q, int64_t N, int64_t q_row_stride,

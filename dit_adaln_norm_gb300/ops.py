@@ -59,7 +59,7 @@ _SIGS = {
                             + [_F, _P, _P, _P, _I, _P],
     "dan_can_use_window_attention": [_P, _I, _I, _P, _P, _I, _I, _P, _I, _I, _P, _P] + [_I] * 8
                                     + [_F, _P, _P, _P, _I],
-    "dan_window_attention_workspace": [_I] * 8,
+    "dan_window_attention_workspace": [_I] * 11,
 }
 
 _lib = None
@@ -489,7 +489,7 @@ def window_attention(q, k_cache, v_cache, page_table, q_start, kv_len, window: i
             _want(lse, "lse", _F32, device)
         if lse.shape != (N, H) or not lse.is_contiguous():
             raise ValueError("lse: expected a contiguous float32 [N, heads] tensor")
-    size = _attention_workspace(N, S, H, Hkv, hd, M, page, max_q)
+    size = _attention_workspace(N, S, H, Hkv, hd, M, page, window, sinks, chunk, max_q)
     # of this call alone: the allocator hands it on in the stream's order
     work = torch.empty(size, dtype=torch.uint8, device=k_cache.device) if size else None
     _on(device, "dan_window_attention", q.data_ptr(), N, q_stride, k_cache.data_ptr(),

@@ -121,14 +121,16 @@ int dan_can_use_qk_norm_rope_cache(const dan_bf16 *q, const dan_bf16 *k, const d
  *
  * workspace: dan_window_attention_workspace(...) bytes of device memory,
  * 16-byte aligned, used by this call alone until it has completed (0 bytes:
- * may be NULL).  Two calls that may run at the same time, or two captured
- * graphs that may, need one each.
+ * may be NULL).  The count follows from its arguments alone: a call passes the
+ * same ones.  A window that lets a query see little of a long table asks for
+ * less, and for none where no sequence can be split.  Two calls that may run
+ * at the same time, or two captured graphs that may, need one each.
  * Limits: S <= 2^20, heads <= 1024, heads / kv_heads <= 128, q_row_stride < 2^39,
  * N * heads <= 2^30, max_pages*page_size <= 2^30, window,
  * sinks, chunk in [0, 2^31 - 1] with chunk >= 1; scale finite and > 0. */
 int64_t dan_window_attention_workspace(int64_t N, int64_t S, int64_t heads, int64_t kv_heads,
                                        int64_t head_dim, int64_t max_pages, int64_t page_size,
-                                       int64_t max_q);
+                                       int64_t window, int64_t sinks, int64_t chunk, int64_t max_q);
 int dan_window_attention(const dan_bf16 *q, int64_t N, int64_t q_row_stride,
                          const dan_bf16 *k_cache, const dan_bf16 *v_cache, int64_t num_pages,
                          int64_t page_size, const int32_t *page_table, int64_t table_stride,

@@ -499,6 +499,29 @@ def test_batch_invariance(hd):
         t0 += n
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (16, 2), (6, 1)])
+@pytest.mark.parametrize("window,sinks,chunk", [(0, 1500, 1), (200, 4, 1), (700, 100, 33), (1600, 40, 128),
+                                                (1 << 20, 0, 1)])
+def test_workspace_is_as_large_as_is_used(hd, H, Hkv, window, sinks, chunk):
+    """With exactly the bytes asked for, between guards that stay as they were."""
+    p = Problem([1, 2, 130, 300, 1], [2600, 2000, 2500, 2111, 40], H, Hkv, hd, 32, window, sinks, chunk,
+                seed=window + hd + H)
+    want = p.call(ops)
+    lib, (S, M) = ops.load(), p.table.shape
+    need = lib.dan_window_attention_workspace(p.N, S, H, Hkv, hd, M, 32, window, sinks, chunk, 300)
+    buf = torch.full((256 + need + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = torch.full_like(want[0], SENTINEL), torch.full((p.N, H), SENTINEL, device="cuda")
+    st = lib.dan_window_attention(
+        p.q.data_ptr(), p.N, p.q.stride(0), p.k_cache.data_ptr(), p.v_cache.data_ptr(), p.k_cache.shape[0], 32,
+        p.table.data_ptr(), p.table.stride(0), M, p.q_start.data_ptr(), p.kv_len.data_ptr(), S, H, Hkv, hd,
+        window, sinks, chunk, 300, p.scale, out.data_ptr(), lse.data_ptr(), buf.data_ptr() + 256, need,
+        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and same(out, want[0]) and torch.equal(lse, want[1])
+    assert (buf[:256] == 0xA5).all() and (buf[256 + need:] == 0xA5).all()
+
+
 @pytest.mark.parametrize("q,kv", [([1] * 5, [700, 1, 64, 5000, 333]), ([1, 200, 30], [900, 300, 4000])])
 def test_graph_replay_and_other_stream(q, kv):
     p = Problem(q, kv, 8, 2, 128, 32, 800, 4, seed=17)

@@ -80,7 +80,7 @@ def attn(lib, q=Q, N=100, qs=4096, kc=KC, vc=VC, pages=50, page=64, tab=TAB, ts=
          kl=KL, S=8, H=32, Hkv=8, hd=128, window=1000, sinks=4, chunk=1, max_q=100, scale=0.1, out=OUT,
          lse=LSE, work=WORK, size=None):
     if size is None:
-        size = lib.dan_window_attention_workspace(N, S, H, Hkv, hd, M, page, max_q)
+        size = lib.dan_window_attention_workspace(N, S, H, Hkv, hd, M, page, window, sinks, chunk, max_q)
     return lib.dan_can_use_window_attention(q, N, qs, kc, vc, pages, page, tab, ts, M, q_start, kl, S,
                                             H, Hkv, hd, window, sinks, chunk, max_q, scale, out, lse,
                                             work, size)
@@ -115,14 +115,22 @@ def test_attention_validation(lib):
 
 
 def test_workspace(lib):
-    size = lambda N=64, S=64, H=32, Hkv=8, hd=128, M=512, page=64, max_q=1: \
-        lib.dan_window_attention_workspace(N, S, H, Hkv, hd, M, page, max_q)  # noqa: E731
+    size = lambda N=64, S=64, H=32, Hkv=8, hd=128, M=512, page=64, window=1000, sinks=4, chunk=1, \
+        max_q=1: lib.dan_window_attention_workspace(N, S, H, Hkv, hd, M, page, window, sinks, chunk, max_q)  # noqa: E731
     need = size()
     assert need > 0 and attn(lib, N=64, S=64, M=512, ts=512, max_q=1, size=need) == OK
     assert attn(lib, N=64, S=64, M=512, ts=512, max_q=1, size=need - 1) == EINVAL
     assert attn(lib, N=64, S=64, M=512, ts=512, max_q=1, work=None) == EINVAL
     assert size(N=0) == 0 and size(S=0) == 0
     assert size(hd=80) == 0 and size(M=0) == 0 and size(N=-1) == 0  # refused by the call
+    assert size(window=-1) == 0 and size(sinks=1 << 31) == 0 and size(chunk=0) == 0
+    # what a wider window needs is no less, up to the whole table
+    grows = [size(window=w) for w in (0, 1, 200, 1000, 5000, 40000, 0x7FFFFFFF)]
+    assert grows == sorted(grows) and grows[-1] == grows[-2]
+    assert size(window=100, sinks=4) == 0 and attn(lib, N=64, S=64, M=512, ts=512, max_q=1, window=100,
+                                                   work=None) == OK
+    # a prompt always has its work list
+    assert size(N=500, S=1, max_q=500, window=100) > 0
     # a table that holds fewer keys than two splits needs none, and none may be passed
     assert size(M=1) == 0 and attn(lib, N=64, S=64, M=1, ts=1, max_q=1, work=None) == OK
 
