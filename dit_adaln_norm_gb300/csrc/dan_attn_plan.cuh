@@ -35,6 +35,34 @@ __device__ __forceinline__ int plan_scan(int x, int *s_warp)
     return x;
 }
 
+// Largest x of the block's threads before this one (0 for the first); all: of
+// every thread.  Only for x >= 0.
+__device__ __forceinline__ int plan_max_before(int x, int *s_warp, int &all)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x = max(x, y);
+    }
+    if (lane == 31) s_warp[warp] = x;
+    int before = __shfl_up_sync(kFull, x, 1);
+    if (lane == 0) before = 0;
+    __syncthreads();
+    all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before = max(before, s_warp[w]);
+        all = max(all, s_warp[w]);
+    }
+    __syncthreads();
+    return before;
+}
+
+// A sequence that begins before an earlier one's end is left out.  So the
+// planned sequences share no row, and their tiles are at most N / tile_tokens
+// and one for each: the counts below fit 32 bits and the lists the places
+// that the host gave them, whatever the query starts are, and the block's
+// work is bounded by N and S.
 __device__ __noinline__ void plan_tiles(const AttnParams &p, PlanShared &S)
 {
     const int tid = threadIdx.x;
@@ -42,11 +70,20 @@ __device__ __noinline__ void plan_tiles(const AttnParams &p, PlanShared &S)
     if (tid == 0) S.split = 0;
     __syncthreads();
     for (int pass = 0; pass < 2; ++pass) { // count by length, then place
+        int reach = 0; // where the furthest of the sequences before s0 ends
         for (int s0 = 0; s0 < p.S; s0 += kPlanThreads) {
-            int tiles = 0;
+            int tiles = 0, first = 0, end = 0;
             if (s0 + tid < p.S) {
                 const SeqInfo q = seq_info(p, s0 + tid);
                 tiles = q.n * p.g > kStepRows ? seq_tiles(p, q) : 0;
+                if (q.n > 0) first = q.q0, end = q.q0 + q.n;
+            }
+            int furthest;
+            const int before = max(reach, plan_max_before(end, S.warp, furthest));
+            reach = max(reach, furthest);
+            if (tiles && first < before) {
+                tiles = 0;
+                set_status(p.status, kStatusIndex);
             }
             const int upto = plan_scan(tiles, S.warp);
             S.first[tid + 1] = upto;
@@ -72,8 +109,7 @@ __device__ __noinline__ void plan_tiles(const AttnParams &p, PlanShared &S)
                 if (pass == 0) {
                     atomicAdd(&S.hist[bucket], nsplit);
                 } else {
-                    // query starts that let sequences overlap may ask for more items
-                    // than N rows can have: what is past the lists is left out
+                    // (past the lists only where a caller changes the arrays meanwhile)
                     const int at = atomicAdd(&S.hist[bucket], nsplit);
                     const int sp = nsplit > 1 ? atomicAdd(&S.split, 1) : 0;
                     if (at + nsplit <= p.items_cap && (nsplit == 1 || sp < p.split_tiles_cap)) {

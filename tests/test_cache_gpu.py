@@ -400,6 +400,67 @@ def test_sequences_that_overlap_are_safe():
     assert (guard[:32] == SENTINEL).all() and (guard[-32:] == SENTINEL).all()
 
 
+def guarded_call(p, table, starts, kv_len, max_q, window=1 << 20, sinks=0, chunk=1):
+    """A call through the C entry with a workspace of exactly the bytes asked for, which, like
+    out and lse, lies between guards that have to stay as they were."""
+    lib, (S, M), H, hd = ops.load(), table.shape, p.H, p.hd
+    need = lib.dan_window_attention_workspace(p.N, S, H, p.Hkv, hd, M, p.page, window, sinks, chunk, max_q)
+    buf = torch.full((256 + need + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((p.N + 64, H, hd), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((p.N + 64, H), SENTINEL, device="cuda")
+    st = lib.dan_window_attention(
+        p.q.data_ptr(), p.N, p.q.stride(0), p.k_cache.data_ptr(), p.v_cache.data_ptr(), p.k_cache.shape[0], p.page,
+        table.data_ptr(), table.stride(0), M, starts.data_ptr(), kv_len.data_ptr(), S, H, p.Hkv, hd, window, sinks,
+        chunk, max_q, p.scale, out[32:].data_ptr(), lse[32:].data_ptr(), buf.data_ptr() + 256, need,
+        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0
+    assert (buf[:256] == 0xA5).all() and (buf[256 + need:] == 0xA5).all()
+    for t in (out, lse):
+        assert (t[:32] == SENTINEL).all() and (t[-32:] == SENTINEL).all()
+    return out[32:-32], lse[32:-32]
+
+
+def test_sequences_that_share_rows_are_left_out():
+    """The first sequence's rows are its own, whatever later ones name the same rows."""
+    p = Problem([300], [300], 8, 1, 64, 16, seed=21, poison=False)
+    S = 4001
+    starts = torch.tensor([0 if i % 2 == 0 else 300 for i in range(S + 1)], dtype=torch.int32, device="cuda")
+    kv_len = torch.full((S,), 150, dtype=torch.int32, device="cuda")
+    kv_len[0] = 300
+    got = guarded_call(p, p.table.expand(S, -1).contiguous(), starts, kv_len, 300)
+    assert ops.device_status() == 8
+    p.check(got)
+
+
+def test_more_shared_rows_than_32_bits_count():
+    """2^19 sequences name the same 8192 rows of 128 heads, 4096 tiles each: 2^31 tiles in all."""
+    p = Problem([8192], [16], 128, 1, 64, 16, seed=23, poison=False)
+    S = 1 << 20
+    starts = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    starts[1::2] = 8192
+    kv_len = torch.full((S,), 5, dtype=torch.int32, device="cuda")
+    kv_len[0] = 16
+    out, lse = guarded_call(p, p.table.expand(S, -1).contiguous(), starts, kv_len, 8192)
+    assert ops.device_status() == 8
+    assert (out[:8176] == 0).all() and (lse[:8176] == float("-inf")).all()  # before the first key
+    tail = Problem([16], [16], 128, 1, 64, 16, seed=23, poison=False)
+    tail.q, tail.K, tail.V = p.q[8176:], p.K, p.V
+    tail.check((out[8176:], lse[8176:]))
+
+
+@pytest.mark.parametrize("behind", [False, True])
+def test_a_sequence_after_a_bad_one_keeps_its_rows(behind):
+    """A sequence that is left out (its start lies past its end, or its rows past N) takes no rows."""
+    p = Problem([40, 0, 50, 30], [40, 10, 90, 30], 4, 2, 64, 16, seed=24, poison=False)
+    want = [t.clone() for t in p.call(ops)]
+    p.q_start.copy_(torch.tensor([0, 1 << 30 if behind else 40, 40, 90, 120], dtype=torch.int32))
+    got = p.call(ops)
+    torch.cuda.synchronize()
+    assert ops.device_status() == (8 if behind else 0)
+    assert same(got[0][40:], want[0][40:]) and torch.equal(got[1][40:], want[1][40:])
+
+
 def test_two_streams_at_once():
     ps = [Problem([1, 300, 3], [700, 900, 64], 8, 2, 128, 32, 400, 4, seed=22 + i) for i in range(2)]
     want = [[t.clone() for t in p.call(ops)] for p in ps]
