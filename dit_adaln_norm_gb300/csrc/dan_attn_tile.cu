@@ -285,9 +285,15 @@ __device__ __forceinline__ float half_exp(uint32_t p_addr, const uint32_t *x, fl
     return sum0.x + sum0.y;
 }
 
-constexpr float kRiseSum = 1024.0f;        // a block's sum above which m rises after it
-constexpr float kAgainSum = 16777216.0f; // 2^24: above it the block is taken again, so that
-                                         // outputs of values up to 2^96 stay in range
+// A block's sum above which m rises after it, and above which the block is taken
+// again.  They bound the row's sum: at most 2^10 from each block that leaves m
+// where it is, 2^24 from one after which it rises (which then divides what is
+// there by 2^10 or more), so 2^24 + 8 kv_len in all and 16 times 2^24 over joined
+// splits.  Outputs are that times the largest value before the division, bf16's
+// rounding of the probabilities included: with values up to 2^99 at most
+// 2^99 * (2^28 + 2^27) * 1.004 < 2^128 for 2^24 keys, and with 2^94 likewise for 2^30.
+constexpr float kRiseSum = 1024.0f;
+constexpr float kAgainSum = 16777216.0f;
 
 template <int HD>
 __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, uint32_t tmem)

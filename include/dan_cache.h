@@ -99,8 +99,10 @@ int dan_can_use_qk_norm_rope_cache(const dan_bf16 *q, const dan_bf16 *k, const d
  * Key slots that no query of their sequence sees are not used: they may hold
  * anything (NaN included), and page-table entries that cover only such slots
  * may be anything (e.g. -1).  A value row that some query of the call sees
- * must be finite; keys may hold anything (a query that sees a NaN key gives
- * NaN).
+ * must be finite, of magnitude at most 2^99 (2^94 where kv_len > 2^24): the
+ * sums are divided after they are taken, and larger values may take them past
+ * fp32's range.  Keys may hold anything (a query that sees a NaN key, or one
+ * whose score is +infinity, gives NaN).
  *
  * Arithmetic: products of bf16 values summed in fp32; the softmax statistics
  * in fp32; each probability rounded to bf16 for its product with V, the sum

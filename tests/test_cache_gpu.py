@@ -295,6 +295,36 @@ def test_jump_after_the_first_block(q, first):
     run(p)
 
 
+def jump(p, first, V=None):
+    """Make the scores of keys 0..199 of the one sequence `first` lower than the others',
+    and its values V, in the problem and in its cache."""
+    u = torch.ones(p.hd, device="cuda") / 8
+    p.q.copy_((p.q.float() * 0.3 + u * 8 * 64 / p.hd).bfloat16())
+    p.K[0] = (p.K[0].float() * 0.3).bfloat16()
+    p.K[0][:, 200:] += (u * first).bfloat16()
+    if V is not None:
+        p.V[0] = V.bfloat16()
+    L = p.kv_lens[0]
+    for b in range(-(-L // p.page)):
+        pid, a, e = int(p.table[0, b]), p.page * b, min(L, p.page * b + p.page)
+        if 0 <= pid < p.k_cache.shape[0]:
+            p.k_cache[pid, :, :e - a] = p.K[0][:, a:e]
+            p.v_cache[pid, :, :e - a] = p.V[0][:, a:e]
+
+
+@pytest.mark.parametrize("first", [0.0, 4.0, 9.0, 11.0, 12.0, 13.0, 16.0, 200.0])
+@pytest.mark.parametrize("q,kv,hd", [(1, 640, 64), (40, 640, 64), (40, 640, 128), (48, 9000, 128)])
+def test_values_up_to_the_documented_largest(q, kv, hd, first):
+    """All of one sign and within a factor of two below 2^99, under scores that rise after the
+    first block by what moves its reference late (a block's sum just below 2^24), or far."""
+    p = Problem([q], [kv], 4, 1, hd, 16, seed=34, poison=False)
+    g = torch.Generator(device="cuda").manual_seed(35)
+    V = (torch.rand(p.V[0].shape, generator=g, device="cuda") * 0.49 + 0.5) * 2.0 ** 99
+    jump(p, first, V)
+    assert p.V[0].isfinite().all() and p.V[0].max() <= 2.0 ** 99
+    run(p)
+
+
 @pytest.mark.parametrize("q", [1, 50])
 def test_rising_scores_rescale(q):
     """Keys that grow along the sequence: the running maximum moves at every block."""
