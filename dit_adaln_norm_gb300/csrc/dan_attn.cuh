@@ -251,6 +251,12 @@ __device__ __forceinline__ int tile_split_blocks(const AttnParams &p, int tiles,
     return n <= 1 ? max(1, count) : (count + n - 1) / n;
 }
 
+// What the step and the tile kernel need before their first launch on the
+// current device.  A call asks for all that it will launch before its first
+// launch: one that cannot run whole writes nothing.
+cudaError_t ready_attention_step(int head_dim);
+cudaError_t ready_attention_tile(int head_dim);
+
 // Launch one kernel each: sequences of at most kStepRows rows, split at most
 // `splits` ways (and the plan of the others); the others; the join of splits.
 cudaError_t launch_attention_step(const AttnParams &p, int head_dim, const CUtensorMap &kmap,

@@ -373,12 +373,9 @@ cudaError_t launch_step_hd(const AttnParams &p, const CUtensorMap &kmap, const C
                            int splits, bool plan, cudaStream_t s)
 {
     static_assert(32 * kStepWarps == kPlanThreads && sizeof(PlanShared) <= StepShape<HD>::RING, "plan");
-    auto fn = window_attention_step_kernel<HD>;
-    const int smem = StepShape<HD>::SMEM;
-    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
-    if (e != cudaSuccess) return e;
-    return launch_overlapped_2d(fn, dim3((unsigned)(p.S * p.Hkv + (plan ? 1 : 0)), (unsigned)splits),
-                                32 * kStepWarps, smem, s, p, kmap, vmap);
+    return launch_overlapped_2d(window_attention_step_kernel<HD>,
+                                dim3((unsigned)(p.S * p.Hkv + (plan ? 1 : 0)), (unsigned)splits),
+                                32 * kStepWarps, StepShape<HD>::SMEM, s, p, kmap, vmap);
 }
 
 template <int HD>
@@ -392,6 +389,14 @@ cudaError_t launch_join_hd(const AttnParams &p, bool tiles, cudaStream_t s)
 }
 
 } // namespace
+
+cudaError_t ready_attention_step(int head_dim)
+{
+    return head_dim == 64 ? allow_dynamic_smem(reinterpret_cast<const void *>(window_attention_step_kernel<64>),
+                                               StepShape<64>::SMEM)
+                          : allow_dynamic_smem(reinterpret_cast<const void *>(window_attention_step_kernel<128>),
+                                               StepShape<128>::SMEM);
+}
 
 cudaError_t launch_attention_step(const AttnParams &p, int head_dim, const CUtensorMap &kmap,
                                   const CUtensorMap &vmap, int splits, bool plan, cudaStream_t s)

@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     grid_dependency_wait(); // the plan, and what came before it
     allow_dependents();
     // Registers from the third warpgroup to the softmax: 128 * (208 + 208 + 88) =
-    // 384 * 168, what the block was launched with (checked before the launch).
+    // 384 * 168, what the block was launched with (kTileRegs, checked before the launch).
     if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp < 8) {
@@ -766,25 +766,45 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 namespace {
 
+// The registers that the kernel's split takes from and gives to its warps: with
+// fewer at launch the split would wait for ever.  The count is asked for until
+// it is known (a failed query is not kept).
+constexpr int kTileRegs = 168;
+
+template <int HD>
+cudaError_t ready_tile_hd()
+{
+    const void *fn = reinterpret_cast<const void *>(window_attention_tile_kernel<HD>);
+    static DeviceCache<int> regs;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const int n = cached_per_device(regs, dev, [&] {
+        cudaFuncAttributes at = {};
+        e = cudaFuncGetAttributes(&at, fn);
+        return e == cudaSuccess ? at.numRegs : 0;
+    });
+    if (e != cudaSuccess) return e;
+    if (n != kTileRegs) return cudaErrorInvalidConfiguration;
+    return allow_dynamic_smem(fn, TileShape<HD>::SMEM);
+}
+
 template <int HD>
 cudaError_t launch_tile_hd(const AttnParams &p, const CUtensorMap &qmap, const CUtensorMap &kmap,
                            const CUtensorMap &vmap, cudaStream_t s)
 {
-    auto fn = window_attention_tile_kernel<HD>;
-    const int smem = TileShape<HD>::SMEM;
-    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
-    if (e != cudaSuccess) return e;
-    static const int regs = [fn] { // the kernel's register split waits for ever if it has fewer
-        cudaFuncAttributes at = {};
-        return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (regs != 168) return cudaErrorInvalidConfiguration;
     const int64_t work = (int64_t)p.items_cap * p.Hkv;
     const int grid = (int)(work < sm_count() ? work : sm_count());
-    return launch_overlapped_2d(fn, dim3((unsigned)grid), kTileThreads, smem, s, p, qmap, kmap, vmap);
+    return launch_overlapped_2d(window_attention_tile_kernel<HD>, dim3((unsigned)grid), kTileThreads,
+                                TileShape<HD>::SMEM, s, p, qmap, kmap, vmap);
 }
 
 } // namespace
+
+cudaError_t ready_attention_tile(int head_dim)
+{
+    return head_dim == 64 ? ready_tile_hd<64>() : ready_tile_hd<128>();
+}
 
 cudaError_t launch_attention_tile(const AttnParams &p, int head_dim, const CUtensorMap &qmap,
                                   const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t s)

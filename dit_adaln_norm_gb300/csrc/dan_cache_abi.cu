@@ -174,20 +174,18 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
     // for a whole item (a block of 128 keys takes about 1.4 us)
     p.limit_ns = 1000000000ull + 30ull * (unsigned long long)(a.max_pages * a.page_size);
     const int64_t rows = a.num_pages * a.kv_heads * a.page_size;
-    CUtensorMap kmap, vmap;
-    const int hd = (int)a.head_dim;
+    const int hd = (int)a.head_dim, box = (int)(a.page_size < 128 ? a.page_size : 128);
+    CUtensorMap kmap, vmap, tile_q, tile_k, tile_v;
+    cudaError_t e = ready_attention_step(hd);
+    if (e == cudaSuccess && room.tiles) e = ready_attention_tile(hd);
+    if (e != cudaSuccess) return e;
     if (!cache_map(&kmap, a.k_cache, rows, hd, kSmallestPage) ||
-        !cache_map(&vmap, a.v_cache, rows, hd, kSmallestPage))
+        !cache_map(&vmap, a.v_cache, rows, hd, kSmallestPage) ||
+        (room.tiles && (!query_map(&tile_q, a, p.g) || !cache_map(&tile_k, a.k_cache, rows, hd, box) ||
+                        !cache_map(&tile_v, a.v_cache, rows, hd, box))))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch_attention_step(p, hd, kmap, vmap, room.step_splits, room.tiles, s);
-    if (e == cudaSuccess && room.tiles) {
-        const int box = (int)(a.page_size < 128 ? a.page_size : 128);
-        CUtensorMap qmap;
-        if (!query_map(&qmap, a, p.g) || !cache_map(&kmap, a.k_cache, rows, hd, box) ||
-            !cache_map(&vmap, a.v_cache, rows, hd, box))
-            return cudaErrorInvalidValue;
-        e = launch_attention_tile(p, hd, qmap, kmap, vmap, s);
-    }
+    e = launch_attention_step(p, hd, kmap, vmap, room.step_splits, room.tiles, s);
+    if (e == cudaSuccess && room.tiles) e = launch_attention_tile(p, hd, tile_q, tile_k, tile_v, s);
     if (e != cudaSuccess || room.splits == 1) return e;
     return launch_attention_join(p, hd, room.tiles, s);
 }
