@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import fcntl
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -23,6 +24,11 @@ SOURCES = ["dan_rows_rms.cu", "dan_rows_gated.cu", "dan_rows_ln.cu", "dan_rows_l
            "dan_cache_abi.cu"]
 HEADERS = ["dan_device.cuh", "dan_internal.h", "dan_ring.cuh", "dan_rows.cuh",
            "dan_attn.cuh", "dan_attn_plan.cuh", "dan_attn_tma.cuh"]
+
+# Registers a thread that the kernels of a source must have: the attention's
+# tile kernel moves registers between its warps, and with fewer at launch than
+# its split adds up to (128 * (208 + 208 + 88) = 384 * 168) it would wait for ever.
+REGISTERS = {"dan_attn_tile.cu": 168}
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NUMERICS = ["-fmad=false", "-prec-div=true", "-prec-sqrt=true", "-ftz=false"]
@@ -60,13 +66,26 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         return _compile(verbose, extra)
 
 
+def check_registers(src: str, report: str):
+    """Raise unless ptxas's report (-Xptxas -v) gives every kernel of `src` the
+    registers that REGISTERS asks for."""
+    used = re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", report, flags=re.S)
+    if not used:
+        raise RuntimeError(f"{src}: no register counts in the compiler's report:\n{report}")
+    for kernel, count in used:
+        if int(count) != REGISTERS[src]:
+            raise RuntimeError(f"{src}: {kernel} was given {count} registers a thread, its split of "
+                               f"them needs {REGISTERS[src]}")
+
+
 def _compile(verbose: bool, extra: list[str] | None) -> str:
     cc = nvcc()
     extra = list(extra or [])
     procs = []
     for src in SOURCES:
         obj = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
-        cmd = [cc, *ARCH, *NUMERICS, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+        report = ["-Xptxas", "-v"] if src in REGISTERS else []
+        cmd = [cc, *ARCH, *NUMERICS, *COMMON, *extra, *report, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE,
@@ -78,9 +97,14 @@ def _compile(verbose: bool, extra: list[str] | None) -> str:
             print(out, flush=True)
         if p.returncode != 0:
             errors.append(f"--- {src}\n{out}")
+        elif src in REGISTERS:
+            try:
+                check_registers(src, out)
+            except RuntimeError as e:
+                errors.append(str(e))
         objs.append(obj)
     if errors:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
+        raise RuntimeError("the build failed:\n" + "\n".join(errors))
     tmp = LIB + ".tmp%d" % os.getpid()
     link = [cc, *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp,
             "-Xlinker", "-rpath=/usr/local/cuda/lib64"]

@@ -132,3 +132,39 @@ def test_other_register_counts_launch_nothing(fake, registers):
                        "print(json.dumps([attention(), attention(max_q=4)]))")
     assert prompt == [ECUDA, []]
     assert few[0] == OK and threads(few[1]) == [128, 128]
+
+
+REPORT = """ptxas info    : 0 bytes gmem
+ptxas info    : Compiling entry function '_kernel_a' for 'sm_103a'
+ptxas info    : Function properties for _kernel_a
+    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads
+ptxas info    : Used {} registers, used 1 barriers
+ptxas info    : Compiling entry function '_kernel_b' for 'sm_103a'
+ptxas info    : Function properties for _kernel_b
+    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads
+ptxas info    : Used {} registers, used 1 barriers
+"""
+
+
+def test_the_build_refuses_other_register_counts():
+    src = "dan_attn_tile.cu"
+    dan_build.check_registers(src, REPORT.format(168, 168))
+    for a, b in ((160, 168), (168, 176)):
+        with pytest.raises(RuntimeError, match="registers"):
+            dan_build.check_registers(src, REPORT.format(a, b))
+    with pytest.raises(RuntimeError, match="no register counts"):
+        dan_build.check_registers(src, "")
+
+
+def test_the_build_asks_for_the_register_counts(monkeypatch, tmp_path):
+    """The compile itself: its own source passes, and with another count asked for the
+    library is not made."""
+    monkeypatch.setattr(dan_build, "OUT_DIR", str(tmp_path))
+    monkeypatch.setattr(dan_build, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(dan_build, "SOURCES", ["dan_attn_tile.cu"])
+    dan_build._compile(False, None)
+    os.remove(dan_build.LIB)
+    monkeypatch.setattr(dan_build, "REGISTERS", {"dan_attn_tile.cu": 160})
+    with pytest.raises(RuntimeError, match="168 registers"):
+        dan_build._compile(False, None)
+    assert not os.path.exists(dan_build.LIB)
