@@ -88,6 +88,14 @@ struct __align__(16) TileItem {
     __host__ __device__ int key_of(int j) const { return (j < nsink ? j : j - nsink + first) << 7; }
 };
 
+// Where the partial results of a kernel's split sequences lie in the workspace,
+// in rows from `first`: `cap` rows for each (sequence, key head) or, with cap 0,
+// `splits` rows for each row of a query head.
+struct PartRoom {
+    int64_t first, cap;
+    int splits;
+};
+
 struct AttnParams {
     const uint4 *q;
     int64_t N, q_stride8; // query row stride in 16-byte fragments
@@ -101,11 +109,10 @@ struct AttnParams {
     float scale_log2; // scale * log2(e): the softmax is taken in base 2
     uint4 *out;
     float *lse;
-    // partial results (see PartLayout)
+    // partial results: rows of outputs, and of (maximum, sum)
     float *part_o;
     float2 *part_ml;
-    int64_t part_cap; // rows of a (sequence, key head), or 0: room by query row,
-    int part_splits;  // that many for each
+    PartRoom step_part, tile_part;
     // work of the tile kernel (see its plan)
     TileItem *items;
     int2 *split_tiles;
@@ -206,13 +213,12 @@ __device__ __forceinline__ int step_split_blocks(int count)
     return max(max(kStepMinBlocks<HD>, min(count / 8, kStepBlocks<HD>)), (count + kMaxSplits - 1) / kMaxSplits);
 }
 
-// First partial row of (sequence, key head); its rows are [split][row].  With
-// part_cap each has room for part_cap rows; otherwise room goes by the query
-// rows, H * kMaxSplits for each.
-__device__ __forceinline__ int64_t part_base(const AttnParams &p, int s, const SeqInfo &q, int u)
+// First partial row of (sequence, key head); its rows are [split][row].
+__device__ __forceinline__ int64_t part_base(const AttnParams &p, const PartRoom &room, int s,
+                                             const SeqInfo &q, int u)
 {
-    if (p.part_cap) return ((int64_t)s * p.Hkv + u) * p.part_cap;
-    return ((int64_t)q.q0 * p.H + (int64_t)u * q.n * p.g) * p.part_splits;
+    if (room.cap) return room.first + ((int64_t)s * p.Hkv + u) * room.cap;
+    return room.first + ((int64_t)q.q0 * p.H + (int64_t)u * q.n * p.g) * room.splits;
 }
 
 // The tile kernel's rows: two row tiles of 128 / g whole tokens each, at most

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(32 * kStepWarps)
     }
     __syncthreads();
     constexpr int CT = HD / 4; // threads of a row, four columns each
-    const int64_t base = part_base(p, s, q, u) + (int64_t)split * R;
+    const int64_t base = part_base(p, p.step_part, s, q, u) + (int64_t)split * R;
     for (int r = threadIdx.x / CT; r < R; r += 32 * kStepWarps / CT) {
         const int c = (threadIdx.x % CT) * 4;
         float m = -INFINITY, l = 0.0f;
@@ -303,11 +303,11 @@ __global__ void __launch_bounds__(32 * kStepWarps)
 // Join one row's split results, in split order: HD / 4 threads, four columns
 // each.
 template <int HD>
-__device__ __forceinline__ void join_row(const AttnParams &p, int s, const SeqInfo &q, int u, int r,
-                                         int nsplit, int c)
+__device__ __forceinline__ void join_row(const AttnParams &p, const PartRoom &room, int s, const SeqInfo &q,
+                                         int u, int r, int nsplit, int c)
 {
     const int R = q.n * p.g;
-    const int64_t base = part_base(p, s, q, u) + r;
+    const int64_t base = part_base(p, room, s, q, u) + r;
     float m = -INFINITY;
 #pragma unroll 4
     for (int k = 0; k < nsplit; ++k) m = fmaxf(m, p.part_ml[base + (int64_t)k * R].x);
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_attention_join_kernel(con
         const int per = step_split_blocks<HD>(kb.count);
         const int nsplit = (kb.count + per - 1) / per;
         if (nsplit > 1)
-            for (int r = br; r < R; r += RB) join_row<HD>(p, s, q, u, r, nsplit, c);
+            for (int r = br; r < R; r += RB) join_row<HD>(p, p.step_part, s, q, u, r, nsplit, c);
         return;
     }
     constexpr int TB = kTileRows / RB; // blocks of a tile's rows
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_attention_join_kernel(con
         if (rt >= rows || r >= q.n * p.g) continue;
         const int count = KeyBlocks<7>(tile_union(p, q, st.y)).count;
         const int per = tile_split_blocks(p, seq_tiles(p, q), count);
-        join_row<HD>(p, st.x, q, u, r, (count + per - 1) / per, c);
+        join_row<HD>(p, p.tile_part, st.x, q, u, r, (count + per - 1) / per, c);
     }
 }
 

@@ -383,7 +383,7 @@ __device__ __forceinline__ void tile_softmax(const AttnParams &p, TileBars &B, u
         const SeqInfo q = {it.q0, it.n, it.L, false};
         const int64_t orow = live ? (int64_t)(it.q0 + tok) * p.H + it.u * p.g + head : -1;
         const int64_t prow =
-            live ? part_base(p, it.s, q, it.u) + (int64_t)it.split * it.n * p.g + tok * p.g + head : -1;
+            live ? part_base(p, p.tile_part, it.s, q, it.u) + (int64_t)it.split * it.n * p.g + tok * p.g + head : -1;
         const int64_t base = part ? prow : orow;
         if (live) {
             if (part) p.part_ml[prow] = make_float2(m, l);

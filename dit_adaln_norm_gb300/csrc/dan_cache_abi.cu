@@ -90,14 +90,27 @@ int tile_splits(int64_t keys, int64_t kv_heads)
     return (int)(n < most ? (n < 1 ? 1 : n) : most < 1 ? 1 : most);
 }
 
-// What a call needs of the workspace: partial results of splits, with room
-// by (sequence, key head) (cap rows each) or by query row, whichever is less
-// in all, and the tile kernel's work lists.
+// Most partial rows of a (sequence, key head) that the tile kernel splits, whose
+// sequence has `tiles` tiles: a tile's splits are as many as the items allow.
+int64_t tile_part_rows(int64_t tiles, int64_t g, int64_t kv_heads, int64_t max_q, int most)
+{
+    const int64_t n = kTileSplitTarget / (tiles * kv_heads), splits = n < most ? n : most;
+    const int64_t tokens = tiles * tile_tokens((int)g);
+    return splits > 1 ? (tokens < max_q ? tokens : max_q) * g * splits : 0;
+}
+
+// What a call needs of the workspace: partial results of splits, and the tile
+// kernel's work lists.  Partial results have room by (sequence, key head) or
+// by query row, whichever is least: the same for both kernels, as a sequence
+// is one kernel's alone, or the step kernel's by sequence (it takes 16 rows of
+// one at most) and after it the tile kernel's by row (it splits less).  At 32
+// query and 8 key heads of 128 over a table of 32768 keys, 256 sequences with
+// 4096 rows: 1040 MiB, one room for both 2080; 64 single tokens: 32 MiB.
 struct Room {
-    int step_splits = 1; // most splits of a step sequence
-    int splits = 1;      // and of any sequence
-    bool tiles = false;  // a sequence may have more rows than the step kernel takes
-    int64_t part_rows = 0, part_cap = 0, items = 0, split_tiles = 0;
+    int step_splits = 1, tile_splits = 1; // most splits of a sequence of either kernel
+    bool tiles = false; // a sequence may have more rows than the step kernel takes
+    PartRoom step = {}, tile = {};
+    int64_t part_rows = 0, items = 0, split_tiles = 0;
     int64_t part_bytes = 0, bytes = 0;
 };
 
@@ -106,25 +119,39 @@ Room room_for(const AttnProblem &a)
     Room r;
     if (a.N == 0 || a.S == 0) return r;
     const int64_t g = a.heads / a.kv_heads, max_q = a.max_q < a.N ? a.max_q : a.N;
-    r.step_splits = r.splits = step_splits(keys_seen(a, kStepRows), a.head_dim);
+    // rows of a step sequence's key head
+    const int64_t step_rows = kStepRows / g < max_q ? kStepRows / g * g : max_q * g;
+    if (step_rows) r.step_splits = step_splits(keys_seen(a, kStepRows), a.head_dim);
+    const int64_t step_cap = r.step_splits > 1 ? step_rows * r.step_splits : 0;
     r.tiles = max_q * g > kStepRows;
-    int64_t cap = (int64_t)kStepRows * r.splits;
+    int64_t tile_cap = 0;
     if (r.tiles) {
         // sequences that the tile kernel takes, and the tiles of one that may be split
         const int64_t long_seqs = a.S < a.N * g / kStepRows ? a.S : a.N * g / kStepRows;
         const int64_t split_target = kTileSplitTarget / a.kv_heads;
         r.items = a.N / tile_tokens((int)g) + long_seqs * (1 + split_target);
         r.split_tiles = long_seqs * (1 + split_target / 2);
-        const int splits = tile_splits(keys_seen(a, kTileRows), a.kv_heads);
-        if (splits > 1 && cap < split_target * kTileRows) cap = split_target * kTileRows;
-        if (splits > r.splits) r.splits = splits;
+        r.tile_splits = tile_splits(keys_seen(a, kTileRows), a.kv_heads);
+        for (int64_t t = 1; t <= split_target / 2 && (t - 1) * tile_tokens((int)g) < max_q; ++t) {
+            const int64_t rows = tile_part_rows(t, g, a.kv_heads, max_q, r.tile_splits);
+            if (rows > tile_cap) tile_cap = rows;
+        }
+        if (!tile_cap) r.tile_splits = 1;
     }
-    if (r.splits > 1) {
-        const int64_t by_seq = a.S * a.kv_heads * cap, by_row = a.N * a.heads * r.splits;
-        r.part_cap = by_seq <= by_row ? cap : 0;
-        r.part_rows = by_seq <= by_row ? by_seq : by_row;
-        r.part_bytes = (r.part_rows * (a.head_dim * 4 + 8) + 15) / 16 * 16;
+    const int64_t seqs = a.S * a.kv_heads, rows = a.N * a.heads;
+    const int64_t cap = step_cap > tile_cap ? step_cap : tile_cap;
+    const int splits = r.step_splits > r.tile_splits ? r.step_splits : r.tile_splits;
+    const int64_t by_seq = seqs * cap, by_row = splits > 1 ? rows * splits : 0;
+    const int64_t apart = seqs * step_cap + rows * r.tile_splits;
+    r.part_rows = by_seq < by_row ? by_seq : by_row;
+    if (step_cap && tile_cap && apart < r.part_rows) {
+        r.step = {0, step_cap, r.step_splits};
+        r.tile = {seqs * step_cap, 0, r.tile_splits};
+        r.part_rows = apart;
+    } else {
+        r.step = r.tile = {0, by_seq < by_row ? cap : 0, splits};
     }
+    r.part_bytes = (r.part_rows * (a.head_dim * 4 + 8) + 15) / 16 * 16;
     r.bytes = r.part_bytes + (r.tiles ? 16 + (int64_t)sizeof(TileItem) * r.items + 8 * r.split_tiles : 0);
     return r;
 }
@@ -162,8 +189,8 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
     if (room.items > 0x7FFFFFFF || room.split_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.part_o = static_cast<float *>(a.workspace);
     p.part_ml = reinterpret_cast<float2 *>(p.part_o + room.part_rows * a.head_dim);
-    p.part_cap = room.part_cap;
-    p.part_splits = room.splits;
+    p.step_part = room.step;
+    p.tile_part = room.tile;
     p.plan_head = reinterpret_cast<int *>(static_cast<char *>(a.workspace) + room.part_bytes);
     p.items = reinterpret_cast<TileItem *>(p.plan_head + 4);
     p.split_tiles = reinterpret_cast<int2 *>(p.items + room.items);
@@ -186,7 +213,7 @@ cudaError_t launch_window_attention(const AttnProblem &a, cudaStream_t s)
         return cudaErrorInvalidValue;
     e = launch_attention_step(p, hd, kmap, vmap, room.step_splits, room.tiles, s);
     if (e == cudaSuccess && room.tiles) e = launch_attention_tile(p, hd, tile_q, tile_k, tile_v, s);
-    if (e != cudaSuccess || room.splits == 1) return e;
+    if (e != cudaSuccess || room.part_rows == 0) return e;
     return launch_attention_join(p, hd, room.tiles, s);
 }
 

@@ -463,6 +463,32 @@ def test_sequences_that_share_rows_are_left_out():
     p.check(got)
 
 
+@pytest.mark.parametrize("H,Hkv,hd", [(32, 8, 128), (16, 4, 64), (8, 1, 128)])
+def test_split_sequences_of_both_kernels_in_a_large_batch(H, Hkv, hd):
+    """256 sequences over one long cache, half of them a few rows and half a tile, all split:
+    each row has the bits of a call of its sequence alone, and the workspace, which keeps the
+    two kernels' partial results apart, is exactly what is asked for."""
+    g, few = H // Hkv, 16 * Hkv // H
+    q_lens = [few if s % 2 else 32 - few for s in range(256)]
+    p = Problem([sum(q_lens)], [16384], H, Hkv, hd, 64, seed=25, poison=False)
+    starts = torch.tensor([sum(q_lens[:s]) for s in range(257)], dtype=torch.int32, device="cuda")
+    kv = [16384 - 61 * (s % 7) for s in range(256)]
+    kv_len = torch.tensor(kv, dtype=torch.int32, device="cuda")
+    out, lse = guarded_call(p, p.table.expand(256, -1).contiguous(), starts, kv_len, 32)
+    assert (lse != SENTINEL).all()
+    for s in [*range(0, 256, 37), 1, 254, 255]:
+        a, b = int(starts[s]), int(starts[s + 1])
+        o1, l1 = torch.empty_like(out[a:b]), torch.empty_like(lse[a:b])
+        ops.window_attention(p.q[a:b], p.k_cache, p.v_cache, p.table, torch.tensor(
+            [0, b - a], dtype=torch.int32, device="cuda"), kv_len[s:s + 1], 1 << 20, scale=p.scale, out=o1, lse=l1)
+        assert same(o1, out[a:b]) and torch.equal(l1, lse[a:b]), s
+    for s in (0, 1):  # and those of the formula
+        one = Problem([q_lens[s]], [kv[s]], H, Hkv, hd, 64, seed=25, poison=False)
+        a, b = int(starts[s]), int(starts[s + 1])
+        one.q, one.K, one.V = p.q[a:b], [p.K[0][:, :kv[s]]], [p.V[0][:, :kv[s]]]
+        one.check((out[a:b], lse[a:b]), str(s))
+
+
 def test_more_shared_rows_than_32_bits_count():
     """2^19 sequences name the same 8192 rows of 128 heads, 4096 tiles each: 2^31 tiles in all."""
     p = Problem([8192], [16], 128, 1, 64, 16, seed=23, poison=False)

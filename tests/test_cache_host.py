@@ -135,6 +135,25 @@ def test_workspace(lib):
     assert size(M=1) == 0 and attn(lib, N=64, S=64, M=1, ts=1, max_q=1, work=None) == OK
 
 
+def test_workspace_is_bounded_by_each_kernel(lib):
+    """A sequence is split by one kernel or the other, each with rows and splits of its own: a
+    large batch over long caches asks for what both can use, not for the larger of each."""
+    size = lambda N, S, H=32, Hkv=8, hd=128, M=512, page=64, window=1 << 30, sinks=0, chunk=1, max_q=None: \
+        lib.dan_window_attention_workspace(N, S, H, Hkv, hd, M, page, window, sinks, chunk,
+                                           N if max_q is None else max_q)  # noqa: E731
+    MiB = 1 << 20
+    # 256 sequences of up to 16 rows and 32 splits, 4096 rows of up to 8 splits, 520 bytes each
+    assert size(4096, 256) < 1100 * MiB
+    assert size(8192, 1024) < 3200 * MiB
+    assert size(4096, 256, max_q=28) < 1000 * MiB
+    # a group of more than 16 query heads leaves the step kernel no sequence: no room for it
+    assert size(64, 64, H=32, Hkv=1, max_q=1) <= 64 * 32 * 16 * 520 + (8 + 64 * 65) * 80 + 64 * 33 * 8 + 16
+    # tokens that the step kernel alone takes: their own rows, 32 splits each
+    assert size(64, 64, max_q=1) == 64 * 32 * 32 * 520
+    # prompts too long to be split have work lists alone, where the bound says so
+    assert size(65536, 64, H=8, Hkv=8, hd=64, M=4, max_q=1024) < MiB
+
+
 def test_binding_refuses_without_cuda_tensors():
     z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
     with pytest.raises(TypeError):
