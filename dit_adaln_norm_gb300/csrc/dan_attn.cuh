@@ -126,7 +126,8 @@ struct AttnParams {
 // where nothing is to be done.
 struct SeqInfo {
     int q0, n, L;
-    bool bad; // an entry was out of its range
+    bool bad;  // an entry was out of its range
+    bool down; // its start lies past the next one's
 };
 
 __device__ __forceinline__ SeqInfo seq_info(const AttnParams &p, int s)
@@ -139,6 +140,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams &p, int s)
     q.L = L < 0 ? 0 : L > cap ? cap : L;
     q.q0 = a;
     q.n = b - a;
+    q.down = b < a;
     if (a < 0 || b < a || b > p.N || q.n > p.max_q) {
         q.bad = true;
         q.n = 0;

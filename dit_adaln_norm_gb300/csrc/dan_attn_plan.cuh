@@ -19,8 +19,9 @@ struct PlanShared {
     int split;
 };
 
-// Sum over the block's threads up to and with this one.
-__device__ __forceinline__ int plan_scan(int x, int *s_warp)
+// Sum over the block's threads up to and with this one; any: whether one of
+// them has the flag.
+__device__ __forceinline__ int plan_scan(int x, int *s_warp, bool flag, bool &any)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -29,33 +30,36 @@ __device__ __forceinline__ int plan_scan(int x, int *s_warp)
         if (lane >= o) x += y;
     }
     if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
+    any = __syncthreads_or(flag);
     for (int w = 0; w < warp; ++w) x += s_warp[w];
     __syncthreads();
     return x;
 }
 
-// Largest x of the block's threads before this one (0 for the first); all: of
-// every thread.  Only for x >= 0.
-__device__ __forceinline__ int plan_max_before(int x, int *s_warp, int &all)
+// Whether the sequence of this thread, rows first .. end-1, begins before the
+// end of one before it: of an earlier thread's, or of what any thread has seen
+// in earlier turns (`reach`).  Apart from the plan, which seldom needs it.
+__device__ __noinline__ bool plan_overlaps(int first, int end, int reach, int *s_warp)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kFull, x, o);
-        if (lane >= o) x = max(x, y);
+        reach = max(reach, __shfl_xor_sync(kFull, reach, o));
+        const int y = __shfl_up_sync(kFull, end, o);
+        if (lane >= o) end = max(end, y);
     }
-    if (lane == 31) s_warp[warp] = x;
-    int before = __shfl_up_sync(kFull, x, 1);
-    if (lane == 0) before = 0;
+    // ends >= 0 up to and with this thread's; the warp's own, and of earlier turns
+    const int before = __shfl_up_sync(kFull, end, 1);
+    if (lane == 0) s_warp[warp] = reach;
     __syncthreads();
-    all = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < warp) before = max(before, s_warp[w]);
-        all = max(all, s_warp[w]);
-    }
+    for (int w = 0; w < kPlanThreads / 32; ++w) reach = max(reach, s_warp[w]);
     __syncthreads();
-    return before;
+    if (lane == 31) s_warp[warp] = end;
+    __syncthreads();
+    if (lane > 0) reach = max(reach, before);
+    for (int w = 0; w < warp; ++w) reach = max(reach, s_warp[w]);
+    __syncthreads();
+    return first < reach;
 }
 
 // A sequence that begins before an earlier one's end is left out.  So the
@@ -70,22 +74,30 @@ __device__ __noinline__ void plan_tiles(const AttnParams &p, PlanShared &S)
     if (tid == 0) S.split = 0;
     __syncthreads();
     for (int pass = 0; pass < 2; ++pass) { // count by length, then place
-        int reach = 0; // where the furthest of the sequences before s0 ends
+        // An earlier end lies past a later start only where a start lies past the
+        // next one: until one does, no sequence is compared with the others
+        // (always comparing cost the call of a prompt 0.8 us, this 0.3).
+        bool descended = false, any;
+        int reach = 0; // furthest end that this thread has seen in earlier turns
         for (int s0 = 0; s0 < p.S; s0 += kPlanThreads) {
             int tiles = 0, first = 0, end = 0;
+            bool down = false;
             if (s0 + tid < p.S) {
                 const SeqInfo q = seq_info(p, s0 + tid);
                 tiles = q.n * p.g > kStepRows ? seq_tiles(p, q) : 0;
                 if (q.n > 0) first = q.q0, end = q.q0 + q.n;
+                down = q.down;
             }
-            int furthest;
-            const int before = max(reach, plan_max_before(end, S.warp, furthest));
-            reach = max(reach, furthest);
-            if (tiles && first < before) {
-                tiles = 0;
-                set_status(p.status, kStatusIndex);
+            int upto = plan_scan(tiles, S.warp, down, any);
+            descended = descended || any;
+            if (descended) { // the whole block
+                if (plan_overlaps(first, end, reach, S.warp) && tiles) {
+                    tiles = 0;
+                    set_status(p.status, kStatusIndex);
+                }
+                upto = plan_scan(tiles, S.warp, false, any);
             }
-            const int upto = plan_scan(tiles, S.warp);
+            reach = max(reach, end);
             S.first[tid + 1] = upto;
             if (tid == 0) S.first[0] = 0;
             __syncthreads();
@@ -140,7 +152,7 @@ __device__ __noinline__ void plan_tiles(const AttnParams &p, PlanShared &S)
                 v[i] = S.hist[tid * NB + i];
                 sum += v[i];
             }
-            int before = plan_scan(sum, S.warp) - sum;
+            int before = plan_scan(sum, S.warp, false, any) - sum;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 S.hist[tid * NB + i] = before;

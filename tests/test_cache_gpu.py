@@ -463,6 +463,23 @@ def test_sequences_that_share_rows_are_left_out():
     p.check(got)
 
 
+@pytest.mark.parametrize("at", [3, 127, 128, 150])
+def test_a_start_that_goes_back_far_behind(at):
+    """Sequence `at` + 1 and the next lie on the rows of the first; the last has its own."""
+    p = Problem([300, 30], [300, 77], 8, 1, 64, 16, seed=26, poison=False)
+    S = 200
+    starts = [0] + [300] * at + [100, 180] + [300] * (S - at - 3) + [330]
+    kv_len = torch.full((S,), 150, dtype=torch.int32, device="cuda")
+    kv_len[0], kv_len[-1] = 300, 77
+    table = p.table[:1].expand(S, -1).contiguous()
+    table[-1] = p.table[1]
+    starts = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    assert starts.shape == (S + 1,) and starts[at + 1] == 100
+    got = guarded_call(p, table, starts, kv_len, 330)
+    assert ops.device_status() == 8
+    p.check(got)
+
+
 @pytest.mark.parametrize("H,Hkv,hd", [(32, 8, 128), (16, 4, 64), (8, 1, 128)])
 def test_split_sequences_of_both_kernels_in_a_large_batch(H, Hkv, hd):
     """256 sequences over one long cache, half of them a few rows and half a tile, all split:
