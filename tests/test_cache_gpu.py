@@ -119,6 +119,34 @@ def test_rope_cache_many_tokens(N, H, Hkv, page, hd, neox):
     rope_check(p, rope_call(p, neox), neox)
 
 
+def ring_tokens(units, H, Hkv, hd):
+    """Tokens that give each of the persistent form's warps (16 an SM) `units` units of work."""
+    per_token = -(-(H + 2 * Hkv) // (2048 // hd))
+    return -(-units * 16 * torch.cuda.get_device_properties(0).multi_processor_count // per_token)
+
+
+@pytest.mark.parametrize("hd,neox", [(128, False), (128, True), (64, False), (64, True)])
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_rope_cache_where_the_persistent_form_begins(hd, neox, more):
+    N = ring_tokens(2, 1, 1, hd) + more
+    p = rope_problem(N, 1, 1, hd, 16, N + hd, pad=N // 9)
+    rope_check(p, rope_call(p, neox), neox)
+
+
+@pytest.mark.parametrize("hd,neox", [(128, False), (128, True), (64, False), (64, True)])
+@pytest.mark.parametrize("one,in_place", [(True, False), (True, True), (False, False), (False, True)])
+def test_rope_cache_slots_are_refilled(hd, neox, one, in_place):
+    """36 units a warp: its three slots are filled again and again, their barriers' phases
+    come round, and the positions and slots of its units are looked up twice (32 at a time);
+    with one unit a token, and with two (the second one of values too)."""
+    H, Hkv = (1, 1) if one else (2048 // hd - 4, 4)
+    N = ring_tokens(36, H, Hkv, hd) + 5
+    p = rope_problem(N, H, Hkv, hd, 64, N + hd, pad=N // 7)
+    q_in = p["q"].clone()
+    got = rope_call(p, neox, q_out=p["q"] if in_place else None)
+    rope_check(p, got, neox, q_in=q_in)
+
+
 def test_rope_cache_many_tokens_in_place_and_bad_indices():
     p = rope_problem(6000, 4, 2, 128, 64, 40)
     q_in, out_of = p["q"].clone(), [5, 4999, 5999]
