@@ -385,6 +385,31 @@ def test_visible_nan_and_infinite_keys_reach_only_their_rows(q):
             assert torch.equal(got[0][i], base[0][i]) and torch.equal(got[1][i], base[1][i])
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("q", [1, 40])
+@pytest.mark.parametrize("at", [3, 150, 190])
+def test_infinite_keys(q, at, value):
+    """A key with an infinite element has a score of +infinity, and its row NaN, where the
+    query's element is of its sign, and a score of -infinity, and no weight, where it is not."""
+    p = Problem([q], [200], 2, 1, 64, 16, seed=9, poison=False)
+    pid = int(p.table[0, at // 16])
+    p.k_cache[pid, 0, at % 16, 3] = value
+    p.K[0][0, at, 3] = value
+    out, lse = p.call(ops)
+    sign = p.q[..., 3].float() * (1.0 if value > 0 else -1.0)   # [rows, heads]
+    sees = (torch.arange(200 - q, 200, device="cuda") >= at)[:, None]
+    gone = sees & (sign > 0)
+    assert (sign != 0).all() and (q == 1 or (gone.any() and (sees & ~gone).any()))
+    assert out[gone].isnan().all() and lse[gone].isnan().all()
+    want, wlse, otol, ltol = p.reference()   # NaN where the formula's is; weights of 0 elsewhere
+    err, lerr = (out.double() - want).abs(), (lse.double() - wlse).abs()
+    # a score's tolerance goes by its largest seen product, which is infinite here: the same
+    # problem's without that key's element
+    p.K[0][0, at, 3] = 0.0
+    _, _, otol, ltol = p.reference()
+    assert (err[~gone] <= otol[~gone]).all() and (lerr[~gone] <= ltol[~gone]).all()
+
+
 def test_long_context_split():
     run(Problem([1, 1, 2], [20000, 9000, 12345], 4, 1, 128, 64, seed=10), max_q=2)
     run(Problem([48, 20], [9000, 5000], 4, 1, 128, 64, seed=11))
