@@ -291,13 +291,15 @@ int validate_rope(const dan_bf16 *q, const dan_bf16 *k, const dan_bf16 *v, int64
     for (int o = 0; o < 3; ++o) {
         for (int i = 0; i < 8; ++i) {
             if (o == 0 && i == 0 && in_place) continue;
-            // the columns of one packed buffer: in-place q rows lie beside k and v rows
-            if (o == 0 && in_place && (i == 1 || i == 2)) {
+            // the columns of one packed buffer, in any order: in-place q rows lie beside
+            // k and v rows of the same stride
+            if (o == 0 && in_place && (i == 1 || i == 2) && q_row_stride == kv_row_stride) {
                 const uintptr_t row = (uintptr_t)(heads * hd * 2), krow = (uintptr_t)(kv_heads * hd * 2);
                 const uintptr_t step = (uintptr_t)q_row_stride * 2;
-                if (q_row_stride == kv_row_stride && ins[i].lo > outs[0].lo &&
-                    ins[i].lo - outs[0].lo >= row && ins[i].lo - outs[0].lo + krow <= step)
-                    continue;
+                const uintptr_t at = ins[i].lo >= outs[0].lo // where k's rows begin behind q's, below step
+                                         ? (ins[i].lo - outs[0].lo) % step
+                                         : (step - (outs[0].lo - ins[i].lo) % step) % step;
+                if (at >= row && at + krow <= step) continue;
             }
             if (overlap(outs[o], ins[i])) return DAN_EALIAS;
         }

@@ -59,7 +59,8 @@ extern "C" {
  * Slots that no token names keep their contents.  positions[t] outside
  * [0, table_rows): the token is left out (q row and slot unchanged), bit 8.
  * slots[t] >= num_pages*page_size: K and V are not stored, bit 8.
- * In place: q_out == q with qo_row_stride == q_row_stride. */
+ * In place: q_out == q with qo_row_stride == q_row_stride; q, k and v may then
+ * still be the columns of one packed projection, in any order. */
 int dan_qk_norm_rope_cache(const dan_bf16 *q, const dan_bf16 *k, const dan_bf16 *v, int64_t N,
                            int64_t q_row_stride, int64_t kv_row_stride, int64_t heads,
                            int64_t kv_heads, int64_t head_dim, const dan_bf16 *wq,

@@ -191,6 +191,21 @@ def test_rope_cache_in_place_beside_k_and_v(neox):
     rope_check(p, got, neox, q_in=q_in)
 
 
+@pytest.mark.parametrize("order", ["kvq", "kqv"])
+@pytest.mark.parametrize("N", [70, 5000])
+def test_rope_cache_in_place_behind_k_and_v(N, order):
+    p = rope_problem(N, 6, 2, 128, 32, 6)
+    parts = {n: p[n] for n in "qkv"}
+    packed = torch.cat([parts[n] for n in order], 1)
+    at = 0
+    for n in order:
+        p[n] = packed[:, at:at + parts[n].shape[1]]
+        at += parts[n].shape[1]
+    got = rope_call(p, True, q_out=p["q"])
+    assert got.data_ptr() == p["q"].data_ptr()
+    rope_check(p, got, True, q_in=parts["q"].clone())
+
+
 def test_rope_cache_bad_indices_are_left_out():
     p = rope_problem(40, 4, 2, 64, 16, 8)
     total = p["caches"][0].shape[0] * 16

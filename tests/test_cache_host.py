@@ -76,6 +76,18 @@ def test_rope_cache_aliases(lib):
     assert f(kc=Q) == EALIAS and f(vc=V) == EALIAS and f(kc=ROPE) == EALIAS and f(vc=SLOT) == EALIAS
 
 
+def test_rope_cache_in_place_in_a_packed_projection(lib):
+    """q, k and v as the columns of one buffer in any order; rows that cross are refused."""
+    f = lambda q, k, v, **kw: rope(lib, q=Q + q * 2, qo=Q + q * 2, os=6144, k=Q + k * 2, v=Q + v * 2, **kw)  # noqa: E731
+    assert f(0, 4096, 5120) == f(1024, 0, 5120) == f(2048, 0, 1024) == f(2048, 1024, 0) == OK
+    # the same columns some rows further on or back, which share no element either
+    assert f(2048, 6144 * 3, 1024) == f(6144 * 50, 6144 * 3 + 4096, 5120) == OK
+    assert f(2048, 1032, 0) == EALIAS      # k's rows run into q's
+    assert f(2048, 6144 - 8, 0) == EALIAS  # k's rows begin inside q's
+    assert f(1024, 1024, 0) == EALIAS and f(1024, 2048, 0) == EALIAS
+    assert rope(lib, q=Q + 4096, qo=Q + 4096, os=6144, k=Q, v=Q + 2048, ks=6152) == EALIAS  # other strides
+
+
 def attn(lib, q=Q, N=100, qs=4096, kc=KC, vc=VC, pages=50, page=64, tab=TAB, ts=70, M=66, q_start=QS,
          kl=KL, S=8, H=32, Hkv=8, hd=128, window=1000, sinks=4, chunk=1, max_q=100, scale=0.1, out=OUT,
          lse=LSE, work=WORK, size=None):
