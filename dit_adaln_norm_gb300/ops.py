@@ -431,7 +431,7 @@ def qk_norm_rope_cache(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache
         out_stride = _token_rows(q_out, "q_out", N, H, hd, device)
     _on(device, "dan_qk_norm_rope_cache", q.data_ptr(), k.data_ptr(), v.data_ptr(), N, q_stride,
         kv_stride, H, Hkv, hd, wq.data_ptr(), wk.data_ptr(), rope.data_ptr(), rope.shape[0],
-        positions.data_ptr(), slots.data_ptr(), eps, 1 if neox else 0, q_out.data_ptr(), out_stride,
+        positions.data_ptr(), slots.data_ptr(), float(eps), 1 if neox else 0, q_out.data_ptr(), out_stride,
         k_cache.data_ptr(), v_cache.data_ptr(), pages, page)
     return q_out if q_out.dim() == 3 else q_out.unflatten(1, (H, hd))
 
@@ -495,6 +495,6 @@ def window_attention(q, k_cache, v_cache, page_table, q_start, kv_len, window: i
     _on(device, "dan_window_attention", q.data_ptr(), N, q_stride, k_cache.data_ptr(),
         v_cache.data_ptr(), pages, page, page_table.data_ptr(), table_stride, M, q_start.data_ptr(),
         kv_len.data_ptr(), S, H, Hkv, hd, window, sinks, chunk, max_q,
-        hd ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        hd ** -0.5 if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
         None if work is None else work.data_ptr(), size)
     return out if lse is None else (out, lse)

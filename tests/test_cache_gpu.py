@@ -227,6 +227,20 @@ def test_rope_cache_bad_indices_are_left_out():
     rope_check(p2, torch.from_numpy(want.view(np.int16)).view(torch.bfloat16).cuda(), True)
 
 
+@pytest.mark.parametrize("number", [np.float32, np.float64, torch.tensor, float])
+def test_numbers_of_any_kind(number):
+    """eps and scale as the other entry points take theirs: what float() takes."""
+    p = rope_problem(9, 2, 1, 64, 16, 10)
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    args = (p["q"], p["k"], p["v"], p["w"][0], p["w"][1], dev(p["table"]), dev(p["pos"]), dev(p["slots"]))
+    want = ops.qk_norm_rope_cache(*args, *p["caches"], 0.25)
+    assert same(ops.qk_norm_rope_cache(*args, *p["caches"], number(0.25)), want)
+    a = Problem([1, 20], [30, 40], 2, 1, 64, 16, seed=44, scale=0.25)
+    want = [t.clone() for t in a.call(ops)]
+    a.scale = number(0.25)
+    assert all(torch.equal(x, y) for x, y in zip(a.call(ops), want))
+
+
 def test_rope_cache_empty_call():
     p = rope_problem(0, 4, 2, 64, 16, 9)
     assert rope_call(p, True).shape == (0, 4, 64)
