@@ -361,7 +361,17 @@ int validate_attention(const dan_bf16 *q, int64_t N, int64_t q_row_stride, const
     return DAN_OK;
 }
 
-int status_of(cudaError_t e) { return e == cudaSuccess ? DAN_OK : DAN_ECUDA; }
+// A launch's status.  What it keeps on the host (a map, a lock) may throw, and
+// no exception may pass the C boundary.
+template <typename F>
+int status_of(F launch)
+{
+    try {
+        return launch() == cudaSuccess ? DAN_OK : DAN_ECUDA;
+    } catch (...) {
+        return DAN_ECUDA;
+    }
+}
 
 } // namespace
 
@@ -398,7 +408,7 @@ int dan_qk_norm_rope_cache(const dan_bf16 *q, const dan_bf16 *k, const dan_bf16 
     const dan::CacheRopeProblem c{q, k, v, N, q_row_stride, kv_row_stride, heads, kv_heads, head_dim,
                                   wq, wk, rope, table_rows, positions, slots, eps, neox != 0, q_out,
                                   qo_row_stride, k_cache, v_cache, num_pages, page_size};
-    return status_of(dan::launch_qk_norm_rope_cache(c, static_cast<cudaStream_t>(stream)));
+    return status_of([&] { return dan::launch_qk_norm_rope_cache(c, static_cast<cudaStream_t>(stream)); });
 }
 
 int64_t dan_window_attention_workspace(int64_t N, int64_t S, int64_t heads, int64_t kv_heads,
@@ -450,7 +460,7 @@ int dan_window_attention(const dan_bf16 *q, int64_t N, int64_t q_row_stride,
     const dan::AttnProblem a{q, N, q_row_stride, k_cache, v_cache, num_pages, page_size, page_table,
                              table_stride, max_pages, q_start, kv_len, S, heads, kv_heads, head_dim,
                              window, sinks, chunk, max_q, scale, out, lse, workspace};
-    return status_of(dan::launch_window_attention(a, static_cast<cudaStream_t>(stream)));
+    return status_of([&] { return dan::launch_window_attention(a, static_cast<cudaStream_t>(stream)); });
 }
 
 } // extern "C"

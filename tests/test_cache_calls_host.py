@@ -28,8 +28,6 @@ static int encode(void) { return failing(ENCODE) ? 1 : 0; }
 int cudaGetDevice(int *d) { return *d = 0; }
 int cudaDeviceGetAttribute(int *v, int which, int d) { *v = which == 16 ? 152 : 232448; return 0; }
 int cudaGetSymbolAddress(void **p, const void *s) { static unsigned word; *p = &word; return 0; }
-int cudaFuncSetAttribute(const void *f, int a, int v) { return failing(SET) ? 1 : 0; }
-int cudaFuncGetAttributes(void *out, const void *f);
 int cudaGetDriverEntryPointByVersion(const char *n, void **p, unsigned v, unsigned long long fl, int *found)
 {
     if (failing(ENTRY)) return 1;
@@ -45,10 +43,18 @@ int cudaLaunchKernelExC(const struct config *c, const void *f, void **args)
     return 0;
 }
 """
-# the one struct whose layout the fake needs comes from the toolkit's header
+# what needs a struct of the toolkit's header, or C++
 ATTR = r"""
 #include <cuda_runtime_api.h>
+#include <new>
 extern "C" int registers, count[], fail_at[];
+extern "C" int throws = 0;
+extern "C" cudaError_t cudaFuncSetAttribute(const void *, cudaFuncAttribute, int)
+{
+    if (++count[3] != fail_at[3]) return cudaSuccess;
+    if (throws) throw std::bad_alloc();
+    return cudaErrorUnknown;
+}
 extern "C" cudaError_t cudaFuncGetAttributes(struct cudaFuncAttributes *out, const void *)
 {
     *out = cudaFuncAttributes();
@@ -122,6 +128,14 @@ def test_a_call_that_cannot_run_whole_launches_nothing(fake, kind, calls):
                                      f"print(json.dumps([a, count[{kind}], attention()]))")
         assert first == [ECUDA, []] and counted == n, n
         assert again[0] == OK and threads(again[1]) == [128, 384, 128], n
+
+
+def test_no_exception_leaves_a_call(fake):
+    """Memory that runs out on the host inside a call: a status, and the next call is as good."""
+    first, again = fake("fail_at[SET] = 2\nctypes.c_int.in_dll(fake, 'throws').value = 1\n"
+                        "print(json.dumps([attention(), attention()]))")
+    assert first == [ECUDA, []]
+    assert again[0] == OK and threads(again[1]) == [128, 384, 128]
 
 
 @pytest.mark.parametrize("registers", [128, 160, 176])
