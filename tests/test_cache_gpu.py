@@ -639,6 +639,14 @@ def test_many_sequences(S):
     run(Problem(q, [n + rng.randint(0, 300) for n in q], 6, 2, 64, 16, 90, 3, seed=S))
 
 
+@pytest.mark.parametrize("H,Hkv,hd", [(8, 2, 64), (24, 1, 128)])
+def test_very_many_sequences(H, Hkv, hd):
+    """Twelve turns of the plan's block, with sequences of no rows, a few, one tile and two."""
+    rng = random.Random(50)
+    q = [rng.choice([0, 1, 1, 2, 4, 5, 17, 40, 70]) for _ in range(1500)]
+    run(Problem(q, [max(0, n + rng.randint(-3, 60)) for n in q], H, Hkv, hd, 16, 33, 2, seed=51, pad=7))
+
+
 def test_most_heads_rotated():
     p = rope_problem(5, 1024, 1024, 64, 16, 41)
     rope_check(p, rope_call(p, True), True)
