@@ -830,3 +830,38 @@ def test_offsets_past_32_bits():
     first = dict(r, caches=[kc, vc], slots=(r["slots"] + (pages - small) * page).astype(np.int32))
     got = rope_call(first, True)
     rope_check(dict(r, caches=[kc[-small:].clone(), vc[-small:].clone()]), got, True)
+
+
+def test_row_offsets_past_32_bits():
+    """Queries, outputs and rotated rows more than 2^31 elements into their buffers."""
+    H, Hkv, hd = 64, 8, 128
+    N = (1 << 31) // (H * hd) + 400
+    p = Problem([300, 1, 40], [300, 900, 6000], H, Hkv, hd, 64, seed=45)
+    q = torch.zeros((N, H, hd), dtype=torch.bfloat16, device="cuda")
+    q[-p.N:] = p.q
+    out = torch.full_like(q, SENTINEL)
+    lse = torch.full((N, H), SENTINEL, device="cuda")
+    ops.window_attention(q, p.k_cache, p.v_cache, p.table, p.q_start + (N - p.N), p.kv_len, p.window,
+                         scale=p.scale, max_q=300, out=out, lse=lse)
+    p.check((out[-p.N:], lse[-p.N:]))
+    assert (out[:-p.N] == SENTINEL).all() and (lse[:-p.N] == SENTINEL).all()
+    del out, lse
+
+    # the last 50 tokens of as many, all padding but those
+    r = rope_problem(50, H, 1, hd, 64, 46)
+    kv = torch.zeros((N, 2 * hd), dtype=torch.bfloat16, device="cuda")
+    q[-50:], kv[-50:, :hd], kv[-50:, hd:] = r["q"].reshape(50, H, hd), r["k"], r["v"]
+    pos, slots = np.zeros(N, np.int32), np.full(N, -1, np.int32)
+    pos[-50:], slots[-50:] = r["pos"], r["slots"]
+    got = rope_call(dict(r, q=q, k=kv[:, :hd], v=kv[:, hd:], pos=pos, slots=slots), True, q_out=q)
+    rope_check(r, got[-50:], True)
+    assert (q[:-50 - p.N] == 0).all()
+
+
+def test_no_rows_allowed():
+    """max_q = 0: every sequence that has rows is left out."""
+    p = Problem([1, 0, 30], [9, 5, 30], 2, 1, 64, 16, seed=47)
+    out, lse = p.call(ops, max_q=0)
+    torch.cuda.synchronize()
+    assert ops.device_status() == 8
+    assert (out == SENTINEL).all() and (lse == SENTINEL).all()
