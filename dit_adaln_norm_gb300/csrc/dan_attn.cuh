@@ -195,11 +195,11 @@ struct KeyBlocks {
 // How a step sequence's keys are split: by its own number of blocks alone, so
 // that a row's bits do not depend on the batch, and never more than 32 ways.
 // At head_dim 64 splits have 768 keys at least, at 128 they have 512, or down
-// to 256 where that makes at most eight.  Measured: 96 sequences of up to 2112
-// visible keys at head_dim 64, splits of 512 keys 94 us, 768 81, 1024 80; one
-// such sequence of 1028 keys 9.6, 11.3 and 13.1 us.  At head_dim 128 one
-// sequence of 1028 keys takes 9.2 us with 256 and 11.9 with 512, eight of up to
-// 4216 take 23.2 and 17.8.
+// to 256 where that makes at most nine.  Measured (replayed, keys not in L2): at
+// head_dim 64, 96 sequences of up to 2112 visible keys take 81 us with splits of
+// 512 keys at least, 75 with 768 and 74 with 1024, one sequence of 1028 keys
+// 9.5, 10.9 and 12.9.  At head_dim 128 one sequence of 1028 keys takes 10.2 us
+// with 256 and 12.1 with 512, eight of up to 4216 take 23.5 and 22.8.
 constexpr int kStepRows = 16;     // query rows (tokens x g) that the step kernel takes
 constexpr int kMaxSplits = 32;
 template <int HD>

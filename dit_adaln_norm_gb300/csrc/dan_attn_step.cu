@@ -1,7 +1,6 @@
 // dan_attn_step.cu -- attention over the paged cache for sequences with few
 // query rows (n_s * heads/kv_heads <= 16): a decoded token, or a few drafted
-// ones; and the join of split
-// results of both kernels.
+// ones; and the join of split results of both kernels.
 //
 // Mathematics: o = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m) with
 // x_j = scale * log2(e) * q.k_j and a running maximum m, one pass over the
@@ -10,7 +9,7 @@
 // on one GB300: 64 tokens over up to 32768 keys, 32 query and 8 key heads of
 // 128, 618 us, 7.0 TB/s (a copy reaches 6.7); 96 sequences of one to three
 // tokens over 2112 keys of 8 heads of 64, 76 us, 5.0 TB/s; one token over 1028
-// keys 9.2 us, launches and dependent loads.
+// keys 10 us, launches and dependent loads.
 //
 // One CTA has one (sequence, key head, split); where the tile kernel follows,
 // one more plans its work.  Its four warps take blocks of 16 keys (32 at
@@ -29,7 +28,9 @@
 namespace dan {
 
 constexpr int kStepWarps = 4;
-constexpr int kStepSlots = 2; // three leave fewer CTAs per SM (96 sequences x 2112 keys: 112 us, two 101)
+// Three slots leave fewer CTAs per SM: 96 sequences of 2112 keys of 8 heads of 64
+// take 84 us with them and 76 with two, 64 over up to 32768 keys 627 and 619.
+constexpr int kStepSlots = 2;
 template <int HD>
 struct StepShape {
     static constexpr int HALVES = HD / 64;               // 128-byte columns of a row
@@ -219,9 +220,11 @@ __global__ void __launch_bounds__(32 * kStepWarps)
             m0 = n0;
             m1 = n1;
         }
-        // Probabilities, rounded to bf16 for the product with V (relative 2^-9
-        // each, of either sign); the sums are of the unrounded ones, of this
-        // lane's keys (the quad's are added at the end).
+        // Probabilities, rounded to bf16 for the product with V, whose operands
+        // are of one type (relative 2^-8 at most each, of either sign: against 64
+        // bits outputs are off by 0.0020 to 0.0023 of their size, 0.0017 of it their
+        // own rounding); the sums are of the unrounded ones, of this lane's keys
+        // (the quad's are added at the end).
 #pragma unroll
         for (int t = 0; t < KT; t += 2) {
             float e0[4], e1[4]; // keys 8t + c2, +1 and 8t + 8 + c2, +1

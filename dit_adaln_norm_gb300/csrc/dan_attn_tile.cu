@@ -6,7 +6,7 @@
 // of rows shares its keys; 4 * hd flops per (row, key) against 2 * 2 * hd
 // bytes per key for 256 rows: the bound is the tensor cores, and beside them
 // one exponential per (row, key).  Measured on one GB300: a prompt of 4216
-// tokens, 32 query and 8 key heads of 128, 113 us, 1.28 PFLOP/s, 0.65 of a
+// tokens, 32 query and 8 key heads of 128, 114 us, 1.27 PFLOP/s, 0.65 of a
 // large library product's rate; the tensor pipe is busy 79% of the time in the
 // middle of an item.
 //
@@ -264,7 +264,8 @@ __device__ __forceinline__ void mask_chunk(uint32_t *x, uint32_t see)
 
 // Half a row's block: probabilities 2^(x * scale - z) of 64 scores, in pairs
 // rounded to bf16 for the product with V, on their way into TMEM when it
-// returns; the sum of the unrounded ones.
+// returns; the sum of the unrounded ones.  (The product takes two operands of
+// one type, and V is bf16: relative 2^-8 at most each, as in the step kernel.)
 __device__ __forceinline__ float half_exp(uint32_t p_addr, const uint32_t *x, float scale_log2, float z)
 {
     const float2 scale = dup2(scale_log2), minus_z = dup2(-z);

@@ -10,10 +10,11 @@
 //
 // A token's heads are one list, Q then K then V.  A unit of work is kSteps
 // consecutive steps of it, each step 32/LPH heads of LPH = hd/8 lanes with a
-// 16-byte fragment per lane; a warp has a unit's loads in flight together.  The sums of squares of its kSteps heads are folded over their lanes
-// by recursive halving, so that each lane ends with one head's sum and takes
-// one reciprocal square root; a head's fold is the same adjacent-pair tree
-// whatever step it falls in.  For the rotation of halves the lanes of the two
+// 16-byte fragment per lane; a warp has a unit's loads in flight together.  The
+// sums of squares of its kSteps heads are folded over their lanes by recursive
+// halving, so that each lane ends with one head's sum and takes one reciprocal
+// square root; a head's fold is the same adjacent-pair tree whatever step it
+// falls in.  For the rotation of halves the lanes of the two
 // halves trade fragments of two heads, so that each has both halves of one.
 #include "dan_device.cuh"
 #include "dan_internal.h"
@@ -25,7 +26,7 @@ namespace dan {
 struct CacheRopeParams {
     const uint4 *q, *k, *v;
     int64_t N, q_stride8, kv_stride8, qo_stride8; // strides in 16-byte fragments
-    int H, Hkv, steps_per_token;                  // warps per token
+    int H, Hkv, steps_per_token;                  // units of work of a token
     const uint4 *wq, *wk;
     const float4 *rope;
     int64_t table_rows, slots_total;
