@@ -121,8 +121,9 @@ int dan_can_use_qk_norm_rope_cache(const dan_bf16 *q, const dan_bf16 *k, const d
  * nearest bound, bit 8.  A page id outside [0, num_pages) for a visible key:
  * zeros in place of the page's keys and values, bit 8.  Sequences may share
  * pages and q rows must not be shared: a sequence with n_s * heads / kv_heads
- * > 16 that begins before an earlier one's end is left out, bit 8; where
- * shorter ones overlap, the shared rows of out and lse hold either's results.
+ * > 16 that begins before an earlier one's end is left out, bit 8; where a
+ * shorter one overlaps another, the rows of both are not defined in out and
+ * lse (other rows are not touched).
  *
  * workspace: dan_window_attention_workspace(...) bytes of device memory,
  * 16-byte aligned, used by this call alone until it has completed (0 bytes:
