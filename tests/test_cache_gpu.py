@@ -865,3 +865,97 @@ def test_no_rows_allowed():
     torch.cuda.synchronize()
     assert ops.device_status() == 8
     assert (out == SENTINEL).all() and (lse == SENTINEL).all()
+
+
+def test_a_page_twice_in_one_sequence():
+    """Repeated tokens: two entries of a table row name one page."""
+    p = Problem([1, 40], [200, 240], 8, 2, 128, 32, seed=48)
+    for s in (0, 1):
+        p.table[s, 4] = p.table[s, 1]
+        p.K[s][:, 128:160], p.V[s][:, 128:160] = p.K[s][:, 32:64].clone(), p.V[s][:, 32:64].clone()
+    run(p)
+
+
+def refuses(error, call, **changed):
+    with pytest.raises(error) as e:
+        call(**changed)
+    if error is ops.DanError:
+        assert e.value.status in (ops.DAN_EINVAL, ops.DAN_EALIGN, ops.DAN_EALIAS, ops.DAN_EUNSUPPORTED)
+
+
+def test_rope_cache_refusals():
+    """Each by its type, before anything is written."""
+    p = rope_problem(6, 4, 2, 64, 16, 49)
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    good = dict(q=p["q"], k=p["k"], v=p["v"], wq=p["w"][0], wk=p["w"][1], rope=dev(p["table"]),
+                positions=dev(p["pos"]), slots=dev(p["slots"]), k_cache=p["caches"][0], v_cache=p["caches"][1])
+    before = [c.clone() for c in p["caches"]]
+    call = lambda **kw: ops.qk_norm_rope_cache(**{**good, "eps": EPS, **kw})  # noqa: E731
+    for name in good:
+        refuses(TypeError, call, **{name: good[name].cpu()})
+        refuses(TypeError, call, **{name: good[name].double()})
+        refuses(TypeError, call, **{name: None})
+    for name in ("positions", "slots"):
+        refuses(TypeError, call, **{name: good[name].long()})
+        refuses(ValueError, call, **{name: good[name][:5]})
+        refuses(ValueError, call, **{name: torch.stack([good[name]] * 2, 1)[:, 0]})
+    refuses(ValueError, call, q=good["q"][:, :-1])
+    refuses(ValueError, call, k=good["k"][:, :64])
+    refuses(ValueError, call, v=good["v"].clone())            # another row stride than k's
+    refuses(ValueError, call, q=good["q"].t().contiguous().t())
+    refuses(ValueError, call, wq=good["wq"][:32])
+    refuses(ValueError, call, rope=good["rope"][:, :32])
+    refuses(ValueError, call, k_cache=good["k_cache"][:, :1])
+    refuses(ValueError, call, k_cache=good["k_cache"].transpose(1, 2))
+    refuses(ValueError, call, q_out=torch.empty((6, 4, 32), dtype=torch.bfloat16, device="cuda"))
+    refuses(ops.DanError, call, eps=-1.0)
+    refuses(ops.DanError, call, eps=float("nan"))
+    refuses(ops.DanError, call, q=torch.zeros(6, 4 * 64 + 4, dtype=torch.bfloat16, device="cuda")[:, 4:])
+    refuses(ops.DanError, call, q_out=good["q"].as_strided((6, 4, 64), (good["q"].stride(0), 64, 1),
+                                                           good["q"].storage_offset() + 64))
+    refuses(ops.DanError, call, v_cache=good["k_cache"])
+    refuses(ops.DanError, call, q=good["q"][:, :3 * 64])       # 3 heads on 2 key heads
+    small = [torch.zeros((9, 2, 8, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    refuses(ops.DanError, call, k_cache=small[0], v_cache=small[1])
+    torch.cuda.synchronize()
+    assert all(same(a, b) for a, b in zip(p["caches"], before))
+    call()
+
+
+def test_attention_refusals():
+    p = Problem([1, 20], [30, 40], 4, 2, 64, 16, seed=50, poison=False)
+    good = dict(q=p.q, k_cache=p.k_cache, v_cache=p.v_cache, page_table=p.table, q_start=p.q_start, kv_len=p.kv_len)
+    out = torch.full((21, 4, 64), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((21, 4), SENTINEL, device="cuda")
+    call = lambda **kw: ops.window_attention(**{**good, "window": 9, "out": out, "lse": lse, **kw})  # noqa: E731
+    for name in good:
+        refuses(TypeError, call, **{name: good[name].cpu()})
+        refuses(TypeError, call, **{name: good[name].double()})
+        refuses(TypeError, call, **{name: None})
+    for name in ("page_table", "q_start", "kv_len"):
+        refuses(TypeError, call, **{name: good[name].long()})
+    refuses(ValueError, call, q=p.q.flatten(1))
+    refuses(ValueError, call, q=p.q[..., :32])
+    refuses(ValueError, call, q=p.q.transpose(1, 2).contiguous().transpose(1, 2))
+    refuses(ValueError, call, page_table=p.table.t().contiguous().t())
+    refuses(ValueError, call, page_table=p.table[0])
+    refuses(ValueError, call, q_start=p.q_start[:2])
+    refuses(ValueError, call, kv_len=p.kv_len[:1])
+    refuses(ValueError, call, out=out[:20])
+    refuses(ValueError, call, lse=lse[:, :3])
+    refuses(TypeError, call, out=out.float())
+    refuses(TypeError, call, lse=lse.bfloat16())
+    for name in ("window", "sinks", "chunk", "max_q"):
+        refuses(ValueError, call, **{name: -1})
+        refuses(ValueError, call, **{name: 1 << 31})
+    refuses(ops.DanError, call, chunk=0)
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        refuses(ops.DanError, call, scale=scale)
+    refuses(ops.DanError, call, q=torch.zeros((21, 3, 64), dtype=torch.bfloat16, device="cuda"),
+            out=torch.empty((21, 3, 64), dtype=torch.bfloat16, device="cuda"), lse=None)
+    refuses(ops.DanError, call, page_table=p.table[:1].expand(2, -1))   # rows on one another
+    both = p.q.contiguous()
+    refuses(ops.DanError, call, q=both, out=both)
+    torch.cuda.synchronize()
+    assert (out == SENTINEL).all() and (lse == SENTINEL).all()
+    call()
