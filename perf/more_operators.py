@@ -126,8 +126,9 @@ def _checkpoint(x):
     """(E4M3 codes, E8M0 codes) of x [..., C] in blocks of 32 channels, as bytes; exact up to the codes' rounding."""
     C, tail = x.shape[-1], -x.shape[-1] % 32
     blocks = torch.nn.functional.pad(x.float(), (0, tail)).unflatten(-1, (-1, 32))
-    m, e = torch.frexp(blocks.abs().amax(-1))  # m in [0.5, 1): 448 is 0.875 * 2^9
-    e = (e - 9 + (m > 0.875)).clamp(min=-126)
+    top = blocks.abs().amax(-1)
+    m, e = torch.frexp(top)  # m in [0.5, 1): 448 is 0.875 * 2^9
+    e = torch.where(top > 0, e - 9 + (m > 0.875), -126).clamp(min=-126)
     power = ((127 - e) << 23).to(torch.int32).view(torch.float32)  # 2^-e
     codes = (blocks * power[..., None]).to(torch.float8_e4m3fn).view(torch.uint8)
     return codes.flatten(-2)[..., :C].contiguous(), (e + 127).to(torch.uint8)
