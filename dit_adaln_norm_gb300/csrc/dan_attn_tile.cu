@@ -161,13 +161,6 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r)
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk2(a)), "l"(pk2(b)), "l"(pk2(c)));
-    return upk2(r);
-}
-
 // ------------------------------------------------------------------- main
 
 // A wait of a role, each lane by itself.  One that runs out marks the CTA dead;

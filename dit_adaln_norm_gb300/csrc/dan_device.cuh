@@ -8,6 +8,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -170,9 +171,57 @@ __device__ __forceinline__ float2 addmul2(float2 acc, float2 a, float2 b)
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk2(acc)), "l"(t));
     return upk2(r);
 }
+// a * b + c per lane, rounded once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk2(a)), "l"(pk2(b)), "l"(pk2(c)));
+    return upk2(r);
+}
 __device__ __forceinline__ float2 dup2(float a) { return make_float2(a, a); }
 // Both elements of a bf16 word as a float2 (low column first).
 __device__ __forceinline__ float2 wide2(uint32_t w) { return make_float2(lo_f(w), hi_f(w)); }
+
+// ------------------------------------------------------ 8-bit checkpoints
+// A block of 32 values has the scale 2^k, the least with k >= -126 at which its
+// largest magnitude is at most 448 * 2^k (448 = 1.75 * 2^8, the largest E4M3
+// value): with |v| = 1.m * 2^e that is k = e - 8, or e - 7 where 1.m > 1.75.
+
+// The largest magnitude of eight values; a NaN counts as nothing.
+__device__ __forceinline__ float top8(const float (&v)[8])
+{
+    float a = fmaxf(fabsf(v[0]), fabsf(v[1])), b = fmaxf(fabsf(v[2]), fabsf(v[3]));
+    float c = fmaxf(fabsf(v[4]), fabsf(v[5])), d = fmaxf(fabsf(v[6]), fabsf(v[7]));
+    return fmaxf(fmaxf(fmaxf(a, b), fmaxf(c, d)), 0.0f);
+}
+
+// E8M0 code (k + 127, in 1 .. 247) of a block whose largest magnitude is `top`:
+// the sum carries into the exponent exactly where the fraction is past 0.75.
+__device__ __forceinline__ unsigned block_scale_code(float top)
+{
+    const unsigned e = (__float_as_uint(top) + 0x1FFFFFu) >> 23;
+    return e > 9u ? e - 8u : 1u;
+}
+
+// 2^-k and 2^k of a code k + 127 in 1 .. 247 (both are normal numbers).
+__device__ __forceinline__ float block_scale_inverse(unsigned code) { return __uint_as_float((254u - code) << 23); }
+__device__ __forceinline__ float block_scale_value(unsigned code) { return __uint_as_float(code << 23); }
+
+// Eight values times `inv` (a power of two) as E4M3 codes, nearest even.
+__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float inv)
+{
+    uint32_t c[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) c[w] = fp8x2_e4m3(mul2(make_float2(v[2 * w], v[2 * w + 1]), dup2(inv)));
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// The two values (without their block's scale) of the codes in the low half.
+__device__ __forceinline__ float2 e4m3_pair(uint32_t codes)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
 
 // ------------------------------------------------------- bf16x2 arithmetic
 // For bf16 operands these equal the fp32-then-round chain bit for bit:

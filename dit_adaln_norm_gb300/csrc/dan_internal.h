@@ -45,8 +45,10 @@ struct RowProblem {
     void *r_out; // gated residual output, or nullptr
     int64_t B, T, D;
     float eps;
-    void *q = nullptr;  // E4M3 output (LayerNorm + FP8), or nullptr
+    void *q = nullptr;  // E4M3 output (LayerNorm + FP8), the checkpoint's codes (+ save), or nullptr
     float qinv = 0.0f;  // rn(1 / qscale) (LayerNorm + FP8)
+    void *stats = nullptr;        // mean and rstd of each row (LayerNorm + save)
+    void *block_scales = nullptr; // the checkpoint's E8M0 scales (LayerNorm + save), or nullptr
 };
 
 struct QkProblem {
@@ -97,6 +99,7 @@ cudaError_t launch_rms_modulate(const RowProblem &p, cudaStream_t s);
 cudaError_t launch_gated_rms_modulate(const RowProblem &p, cudaStream_t s);
 cudaError_t launch_ln_modulate(const RowProblem &p, cudaStream_t s);
 cudaError_t launch_ln_modulate_fp8(const RowProblem &p, cudaStream_t s);
+cudaError_t launch_ln_modulate_save(const RowProblem &p, cudaStream_t s);
 cudaError_t launch_gated_ln_modulate(const RowProblem &p, cudaStream_t s);
 // neox: rotate the halves' pairs (i, i + head_dim/2) instead of (2i, 2i+1).
 cudaError_t launch_qk_norm_rope(const QkProblem &p, bool neox, cudaStream_t s);

@@ -1,7 +1,7 @@
 // dan_rows.cuh -- fused norm + adaLN modulate row kernels for sm_103a
 // (included by dan_rows_rms.cu, dan_rows_gated.cu, dan_rows_ln.cu,
-// dan_rows_lnfp8.cu, dan_rows_gatedln.cu and dan_noalloc.cu, which
-// instantiate and launch them).
+// dan_rows_lnfp8.cu, dan_rows_lnsave.cu, dan_rows_gatedln.cu and
+// dan_noalloc.cu, which instantiate and launch them).
 //
 // RMSNorm ("SGLang diffusion fused-op package guide", section "Norm +
 // scale/shift (adaLN)"; "PR #33854 report", key source excerpt) and
@@ -9,7 +9,9 @@
 // section), each followed by the aten modulate chain
 // y = bf16(bf16(n * bf16(1 + scale)) + shift).  The gated forms first
 // form r' = bf16(r + bf16(gate * h)) and store it; the FP8 form quantises
-// y to E4M3 with a static scale.
+// y to E4M3 with a static scale.  The training form of LayerNorm rounds
+// y = n * (1 + scale) + shift once and also stores the row's mean and rstd and
+// the row itself as an 8-bit checkpoint (blocks of 32 columns).
 //
 // Design (HBM-bound row work, no tensor cores):
 //  - One CTA per SM (two for one shape) takes a contiguous block of rows or
@@ -63,6 +65,8 @@ struct RowParams {
     uint4 *r_out;
     uint2 *q8;   // E4M3 output, 8 codes per 16-byte input fragment (LN + FP8 only)
     float qinv;  // rn(1 / qscale) (LN + FP8 only)
+    float2 *stats;         // mean and rstd of each row (LN + save only)
+    uint8_t *block_scales; // E8M0 scales of the checkpoint whose codes are q8 (LN + save only)
     int64_t rows;
     int64_t T;
     int64_t vs8; // batch stride of the vectors in 16-byte fragments
@@ -79,15 +83,16 @@ struct RowParams {
     int l2_pre_skip;             // > 1: teams t with t % l2_pre_skip == l2_pre_skip - 1 skip it
 };
 
-// Per-batch vector fragment f: which = 0 -> bf16(1 + scale), 1 -> shift,
-// 2 -> gate.  Staged copy when available, else computed from global.
-template <int NV, bool STAGED>
+// Per-batch vector fragment f: which = 0 -> bf16(1 + scale) (RAW: scale
+// itself), 1 -> shift, 2 -> gate.  Staged copy when available, else computed
+// from global.
+template <int NV, bool STAGED, bool RAW = false>
 __device__ __forceinline__ uint4 vec_frag(const RowParams &p, const uint4 *s_vec, int64_t b, int f,
                                           int which)
 {
     if (STAGED) return s_vec[(b * NV + which) * p.F + f];
     const int64_t off = b * p.vs8 + f;
-    if (which == 0) return one_plus_fragment(ld_vec(p.scale + off));
+    if (which == 0) return RAW ? ld_vec(p.scale + off) : one_plus_fragment(ld_vec(p.scale + off));
     return ld_vec((which == 1 ? p.shift : p.gate) + off);
 }
 
@@ -95,7 +100,7 @@ __device__ __forceinline__ uint4 vec_frag(const RowParams &p, const uint4 *s_vec
 // shared memory, in two halves around the first row loads: stage_begin
 // issues asynchronous copies (they enter the memory system ahead of the row
 // loads and hold no registers); stage_end waits for them, then rewrites
-// each scale fragment in place as bf16(1 + scale).
+// each scale fragment in place as bf16(1 + scale) (not with RAW).
 template <int NV, bool HAS_W>
 __device__ __forceinline__ void stage_begin(const RowParams &p, uint4 *s_w, uint4 *s_vec)
 {
@@ -113,12 +118,13 @@ __device__ __forceinline__ void stage_begin(const RowParams &p, uint4 *s_w, uint
     cp_async_commit();
 }
 
-template <int NV>
+template <int NV, bool RAW = false>
 __device__ __forceinline__ void stage_end(const RowParams &p, uint4 *s_vec)
 {
     const int F = p.F;
     cp_async_wait_all();
     __syncthreads();
+    if (RAW) return;
     for (int i = threadIdx.x; i < p.Bs * F; i += blockDim.x) {
         const int b = i / F, f = i - b * F;
         uint4 *dst = s_vec + (int64_t)b * NV * F + f;
@@ -490,9 +496,37 @@ __device__ __forceinline__ void ln_final(const Welford (&W)[4], float &mean, flo
     }
 }
 
-// Normalise, modulate and store (FP8: quantise and store) the logical warps
-// r + TW*m of a row.
-template <int FPT, int J, int TW, bool RAGGED, bool STAGED, bool FP8, int NV>
+// The training form of one fragment: y = bf16(n * (1 + scale) + shift), rounded
+// once, stored, and with codes the checkpoint of the fragment's inputs x.  A
+// block of 32 columns is the fragments of four neighbouring lanes; all 32 lanes
+// call this (`here`: the lane has a fragment; others only take part in the
+// exchange).
+__device__ __forceinline__ void save_store(uint4 *y, uint2 *q8, uint8_t *block_scale, int f, bool here,
+                                           const float (&x)[8], const float (&n)[8], const uint4 &sc,
+                                           const uint4 &sh, int lane)
+{
+    uint4 out;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float2 o = add2(dup2(1.0f), wide2(word(sc, w)));
+        const float2 z = fma2(make_float2(n[2 * w], n[2 * w + 1]), o, wide2(word(sh, w)));
+        set_word(out, w, pack_bf16(z.x, z.y));
+    }
+    if (here) st_stream(y + f, out);
+    if (q8 == nullptr) return;
+    float top = 0.0f;
+    if (here) top = top8(x);
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+    const unsigned code = block_scale_code(top);
+    if (!here) return;
+    st_stream8(q8 + f, e4m3x8(x, block_scale_inverse(code)));
+    if ((lane & 3) == 0) block_scale[f >> 2] = (uint8_t)code;
+}
+
+// Normalise, modulate and store (FP8: quantise and store; SAVE: the training
+// form) the logical warps r + TW*m of a row.
+template <int FPT, int J, int TW, bool RAGGED, bool STAGED, bool FP8, bool SAVE, int NV>
 __device__ __forceinline__ void ln_store(const float (&x)[J][FPT][8], int r, float mean, float m2,
                                          const RowParams &p, int64_t row, int64_t bidx,
                                          const uint4 *s_vec, int lane)
@@ -501,11 +535,37 @@ __device__ __forceinline__ void ln_store(const float (&x)[J][FPT][8], int r, flo
     // rn(m2 / D): a multiply by the exact reciprocal when D is a power of
     // two (the same bits as the division), else the IEEE division
     const float var = p.inv_d != 0.0f ? __fmul_rn(m2, p.inv_d) : __fdiv_rn(m2, (float)(8 * F));
-    const float2 rstd2 = dup2(defined_rsqrt(__fadd_rn(var, p.eps)));
+    const float rstd = defined_rsqrt(__fadd_rn(var, p.eps));
+    const float2 rstd2 = dup2(rstd);
     const float2 mean2 = dup2(mean);
     uint4 *y = FP8 ? nullptr : p.y + row * F;
-    uint2 *q8 = FP8 ? p.q8 + row * F : nullptr;
+    uint2 *q8 = FP8 || (SAVE && p.q8) ? p.q8 + row * F : nullptr;
     const float2 qinv2 = dup2(p.qinv);
+    if (SAVE && r == 0 && lane == 0) p.stats[row] = make_float2(mean, rstd);
+    if constexpr (SAVE) {
+        uint8_t *block_scale = p.block_scales + row * ((F + 3) >> 2);
+#pragma unroll
+        for (int m = 0; m < J; ++m)
+#pragma unroll
+            for (int k = 0; k < FPT; ++k) {
+                const int f = ln_frag(r + TW * m, lane, k);
+                const bool here = !RAGGED || f < F;
+                float t[8];
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 t2 = mul2(sub2(make_float2(x[m][k][e], x[m][k][e + 1]), mean2), rstd2);
+                    t[e] = t2.x;
+                    t[e + 1] = t2.y;
+                }
+                uint4 sc = make_uint4(0, 0, 0, 0), sh = sc;
+                if (here) {
+                    sc = vec_frag<NV, STAGED, true>(p, s_vec, bidx, f, 0);
+                    sh = vec_frag<NV, STAGED, true>(p, s_vec, bidx, f, 1);
+                }
+                save_store(y, q8, block_scale, f, here, x[m][k], t, sc, sh, lane);
+            }
+        return;
+    }
     auto out = [&](int f, const float (&t)[8]) {
         const uint4 o = vec_frag<NV, STAGED>(p, s_vec, bidx, f, 0);
         const uint4 sh = vec_frag<NV, STAGED>(p, s_vec, bidx, f, 1);
@@ -551,7 +611,7 @@ __device__ __forceinline__ void ln_store(const float (&x)[J][FPT][8], int r, flo
 
 // ------------------------------------------------------- the row kernel
 
-enum RowKind { kRms = 0, kGated = 1, kLn = 2, kLnFp8 = 3, kGatedLn = 4 };
+enum RowKind { kRms = 0, kGated = 1, kLn = 2, kLnFp8 = 3, kGatedLn = 4, kLnSave = 5 };
 
 template <int KIND>
 struct RowShape {
@@ -598,7 +658,7 @@ __global__ void __launch_bounds__(32 * NW, CPS)
     using Pipe = WarpPipe<SPC>;
     using Lay = RowLayout<KIND, NW, TW, SPC>;
     constexpr int NIN = Shape::NIN, NV = Shape::NV, NT = Lay::NT;
-    constexpr bool LN = KIND == kLn || KIND == kLnFp8 || KIND == kGatedLn;
+    constexpr bool LN = KIND == kLn || KIND == kLnFp8 || KIND == kGatedLn || KIND == kLnSave;
     constexpr int LWW = LN ? 1 : LW / TW; // RMS logical warps per warp
     constexpr int J = LN ? 4 / TW : 1;     // LayerNorm logical warps per warp
     static_assert(NW % TW == 0, "teams of TW warps");
@@ -686,7 +746,7 @@ __global__ void __launch_bounds__(32 * NW, CPS)
     // The first SPC rows go out before waiting for the staged vectors.
     if (leader)
         for (int i = 0; i < SPC && i < units; ++i) request(i);
-    stage_end<NV>(p, s_vec);
+    stage_end<NV, KIND == kLnSave>(p, s_vec);
 
     // Batch of the team's current row, kept incrementally (rows step by
     // rstep = q_step * T + r_step).
@@ -787,8 +847,8 @@ __global__ void __launch_bounds__(32 * NW, CPS)
                 for (int m = 0; m < 4; ++m) all[m] = Welford{xch[3 * m], xch[3 * m + 1], xch[3 * m + 2]};
             float mean, m2;
             ln_final<RAGGED>(all, mean, m2);
-            ln_store<FPT, J, TW, RAGGED, STAGED, KIND == kLnFp8, NV>(x, r, mean, m2, p, row, bidx,
-                                                                     s_vec, lane);
+            ln_store<FPT, J, TW, RAGGED, STAGED, KIND == kLnFp8, KIND == kLnSave, NV>(
+                x, r, mean, m2, p, row, bidx, s_vec, lane);
         } else {
             float x[LWW][8][8];
             const int j0 = r * LWW;
@@ -862,6 +922,8 @@ RowParams make_params(const RowProblem &q)
     p.r_out = static_cast<uint4 *>(q.r_out);
     p.q8 = static_cast<uint2 *>(q.q);
     p.qinv = q.qinv;
+    p.stats = static_cast<float2 *>(q.stats);
+    p.block_scales = static_cast<uint8_t *>(q.block_scales);
     p.rows = q.B * q.T;
     p.T = q.T;
     p.vs8 = q.vs / 8;

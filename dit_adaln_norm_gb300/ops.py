@@ -1,7 +1,8 @@
-"""Thin ctypes binding of libdan.so (include/dan.h and include/dan_cache.h):
-argument marshalling only.
+"""Thin ctypes binding of libdan.so (include/dan.h, include/dan_cache.h and
+include/dan_train.h): argument marshalling only.
 
-Every function takes CUDA bf16 torch tensors, checks the layout the C ABI
+Every function takes CUDA torch tensors (bf16; the group norm also fp16 and
+fp32), checks the layout the C ABI
 expects, passes raw pointers, strides and the current CUDA stream, and turns
 a non-zero status into an exception.  All arithmetic runs in the CUDA
 kernels; there is no CPU or eager fallback.  PyTorch only allocates outputs.
@@ -13,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import re
 
@@ -22,12 +24,14 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdan.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "dan.h")
 CACHE_HEADER = os.path.join(os.path.dirname(HERE), "include", "dan_cache.h")
+TRAIN_HEADER = os.path.join(os.path.dirname(HERE), "include", "dan_train.h")
 
 DAN_OK, DAN_EINVAL, DAN_EUNSUPPORTED, DAN_EALIGN, DAN_EALIAS, DAN_ECUDA = range(6)
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int64
 _F = ctypes.c_float
+_N = ctypes.c_int
 _SIGS = {
     "dan_rms_modulate": [_P, _P, _P, _P, _I, _P, _I, _I, _I, _F, _P],
     "dan_rms_modulate_noalloc": [_P, _P, _P, _P, _I, _P, _I, _I, _I, _F, _P],
@@ -60,6 +64,21 @@ _SIGS = {
     "dan_can_use_window_attention": [_P, _I, _I, _P, _P, _I, _I, _P, _I, _I, _P, _P] + [_I] * 8
                                     + [_F, _P, _P, _P, _I],
     "dan_window_attention_workspace": [_I] * 11,
+    "dan_ln_modulate_save": [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _F, _P],
+    "dan_can_use_ln_modulate_save": [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _F],
+    "dan_ln_modulate_backward_workspace": [_I, _I, _I],
+    "dan_ln_modulate_backward": [_P] * 6 + [_I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P],
+    "dan_can_use_ln_modulate_backward": [_P] * 6 + [_I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I],
+    "dan_group_norm_workspace": [_I, _I, _I, _I, _N, _N],
+    "dan_group_norm": [_P, _N, _P, _P, _N, _P, _P, _I, _N, _P, _P, _P, _P, _I, _I, _I, _I, _F, _P, _I,
+                       _P],
+    "dan_can_use_group_norm": [_P, _N, _P, _P, _N, _P, _P, _I, _N, _P, _P, _P, _P, _I, _I, _I, _I, _F,
+                               _P, _I],
+    "dan_group_norm_backward_workspace": [_I, _I, _I, _I, _N, _N],
+    "dan_group_norm_backward": [_P, _P, _N, _P, _P, _P, _P, _P, _N, _P, _P, _I, _N] + [_P] * 5
+                               + [_I] * 5 + [_P, _I, _P],
+    "dan_can_use_group_norm_backward": [_P, _P, _N, _P, _P, _P, _P, _P, _N, _P, _P, _I, _N] + [_P] * 5
+                                       + [_I] * 5 + [_P, _I],
 }
 
 _lib = None
@@ -82,7 +101,9 @@ def load():
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
-        lib.dan_window_attention_workspace.restype = ctypes.c_int64
+        for name in _SIGS:
+            if name.endswith("_workspace"):
+                getattr(lib, name).restype = ctypes.c_int64
         lib.dan_status_string.argtypes = [ctypes.c_int]
         lib.dan_status_string.restype = ctypes.c_char_p
         lib.dan_get_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -323,12 +344,12 @@ def _is(t, dtype, device: int) -> bool:
         return False
 
 
-def _want(t, name: str, dtype, device: int):
-    """Raise for a tensor that is not of this dtype on this CUDA device."""
+def _want(t, name: str, dtype, device: int, first: str = "the caches"):
+    """Raise for a tensor that is not of this dtype on this CUDA device (that of `first`)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
         raise TypeError(f"{name}: expected a CUDA {str(dtype).removeprefix('torch.')} tensor")
     if t.get_device() != device:
-        raise ValueError(f"{name}: lies on cuda:{t.get_device()}, the caches on cuda:{device}")
+        raise ValueError(f"{name}: lies on cuda:{t.get_device()}, {first} on cuda:{device}")
 
 
 def _caches(k_cache, v_cache):
@@ -498,3 +519,288 @@ def window_attention(q, k_cache, v_cache, page_table, q_start, kv_len, window: i
         hd ** -0.5 if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
         None if work is None else work.data_ptr(), size)
     return out if lse is None else (out, lse)
+
+
+# ---------------------------------------------------------- training operators
+#
+# What a forward pass keeps is a tuple (stats, codes, scales): the rows' or
+# groups' mean and 1/std, and the input's 8-bit checkpoint (or None twice).
+
+_U8 = torch.uint8
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes(name: str, device: int, *sizes) -> int:
+    with torch.cuda.device(device):  # the count may follow from the device's SMs
+        return getattr(load(), name)(*sizes)
+
+
+def _dense(t, name: str, dtype, shape, device: int, first: str):
+    """A contiguous tensor of this dtype and shape on the device of `first`."""
+    if not _is(t, dtype, device):
+        _want(t, name, dtype, device, first)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {list(shape)} tensor")
+
+
+def _batch_rows(t, name: str, dtype, B: int, D: int, device: int, first: str) -> int:
+    """Batch stride of a [B, D] view (or [D] when B == 1) with unit column stride."""
+    if not _is(t, dtype, device):
+        _want(t, name, dtype, device, first)
+    shape = t.shape
+    if shape == (B, D):
+        if t.stride(1) != 1 and B > 0:
+            raise ValueError(f"{name}: expected unit column stride")
+        return t.stride(0) if B > 1 else D
+    if B != 1 or shape != (D,) or t.stride(0) != 1:
+        raise ValueError(f"{name}: expected a [{B}, {D}] view with unit column stride")
+    return D
+
+
+def _pair(a, b, names, dtype, B: int, D: int, device: int, first: str) -> int:
+    """The one batch stride of two [B, D] views."""
+    stride = _batch_rows(a, names[0], dtype, B, D, device, first)
+    if _batch_rows(b, names[1], dtype, B, D, device, first) != stride:
+        raise ValueError(f"{names[0]} and {names[1]} must share one batch stride")
+    return stride
+
+
+def _kept(saved):
+    try:
+        stats, codes, scales = saved
+    except (TypeError, ValueError):
+        raise TypeError("saved: expected the (stats, codes, scales) of the forward pass") from None
+    return stats, codes, scales
+
+
+def ln_modulate_save(x, scale, shift, eps: float, checkpoint: bool = True, out=None):
+    """y = LayerNorm(x) * (1 + scale) + shift for training (include/dan_train.h):
+    rounded to bf16 once, and what the gradient needs.
+
+    x [B, T, D] contiguous; scale, shift [B, D] (or [D] when B == 1) views that
+    share one batch stride; out may be x itself.  Returns (y, saved) with saved
+    = (stats, codes, scales): stats float32 [B, T, 2], the rows' mean and 1/std;
+    codes uint8 [B, T, D] and scales uint8 [B, T, ceil(D / 32)], x in 8 bits
+    (E4M3 codes, an E8M0 power of two for each 32 columns), or None without
+    ``checkpoint``."""
+    B, T, D = _rows(x, "x")
+    device = x.get_device()
+    vs = _pair(scale, shift, ("scale", "shift"), _BF16, B, D, device, "x")
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _dense(out, "out", _BF16, x.shape, device, "x")
+    stats = torch.empty((B, T, 2), dtype=_F32, device=x.device)
+    codes = scales = None
+    if checkpoint:
+        codes = torch.empty((B, T, D), dtype=_U8, device=x.device)
+        scales = torch.empty((B, T, (D + 31) // 32), dtype=_U8, device=x.device)
+    _on(device, "dan_ln_modulate_save", x.data_ptr(), scale.data_ptr(), shift.data_ptr(), vs, out.data_ptr(),
+        stats.data_ptr(), _ptr(codes), _ptr(scales), B, T, D, float(eps))
+    return out, (stats, codes, scales)
+
+
+def ln_modulate_backward(dy, x, scale, saved, dres=None, dx=None, dscale=None, dshift=None):
+    """The gradients of ``ln_modulate_save`` (include/dan_train.h).
+
+    dy [B, T, D]; x the forward pass's input, or None to take it from the
+    checkpoint in ``saved``; scale as there; dres [B, T, D]: a gradient of x from
+    elsewhere, added to dx before its rounding.  dx may be dy or dres itself;
+    dscale, dshift [B, D] (or [D] when B == 1): views that share one batch stride,
+    e.g. of the embedding's gradient.  Returns (dx, dscale, dshift), bf16."""
+    B, T, D = _rows(dy, "dy")
+    device, shape = dy.get_device(), dy.shape
+    stats, codes, scales = _kept(saved)
+    _dense(stats, "stats", _F32, (B, T, 2), device, "dy")
+    if x is not None:
+        _dense(x, "x", _BF16, shape, device, "dy")
+        at = x.data_ptr(), None, None
+    elif codes is None or scales is None:
+        raise ValueError("x: None, but nothing in saved holds it")
+    else:
+        _dense(codes, "codes", _U8, shape, device, "dy")
+        _dense(scales, "scales", _U8, (B, T, (D + 31) // 32), device, "dy")
+        at = None, codes.data_ptr(), scales.data_ptr()
+    vs = _batch_rows(scale, "scale", _BF16, B, D, device, "dy")
+    if dres is not None:
+        _dense(dres, "dres", _BF16, shape, device, "dy")
+    if dx is None:
+        dx = torch.empty_like(dy)
+    else:
+        _dense(dx, "dx", _BF16, shape, device, "dy")
+    if dscale is None and dshift is None:
+        dscale, dshift = torch.empty((2, B, D), dtype=_BF16, device=dy.device).unbind(0)
+        gs = D
+    elif dscale is None or dshift is None:
+        raise ValueError("dscale and dshift: expected both or neither")
+    else:
+        gs = _pair(dscale, dshift, ("dscale", "dshift"), _BF16, B, D, device, "dy")
+    size = _bytes("dan_ln_modulate_backward_workspace", device, B, T, D)
+    # of this call alone: the allocator hands it on in the stream's order
+    work = torch.empty(size, dtype=_U8, device=dy.device) if size else None
+    _on(device, "dan_ln_modulate_backward", dy.data_ptr(), *at, stats.data_ptr(), scale.data_ptr(), vs,
+        _ptr(dres), dx.data_ptr(), dscale.data_ptr(), dshift.data_ptr(), gs, B, T, D, _ptr(work), size)
+    return dx, dscale, dshift
+
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_ACTS = {None: 0, "silu": 1}
+
+
+def _last(t) -> bool:
+    """Whether a tensor's memory is dense with its channels last."""
+    if t.dim() == 3:
+        return t.is_contiguous()
+    return t.is_contiguous(memory_format=torch.channels_last if t.dim() == 4 else torch.channels_last_3d)
+
+
+def _images(t, name: str):
+    """(N, S, C) of a channels-last image tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _TYPES:
+        raise TypeError(f"{name}: expected a CUDA bfloat16, float16 or float32 tensor")
+    shape = t.shape
+    if len(shape) not in (3, 4, 5) or not _last(t):
+        raise ValueError(f"{name}: expected [N, C, H, W] (or [N, C, D, H, W]) in channels_last memory, or "
+                         "a contiguous [N, S, C] tensor")
+    if len(shape) == 3:
+        return tuple(shape)
+    return shape[0], math.prod(shape[2:]), shape[1]
+
+
+def _like(t, name: str, dtype, shape, device: int, first: str):
+    """A channels-last image tensor of this dtype and shape on the device of `first`."""
+    if not _is(t, dtype, device):
+        _want(t, name, dtype, device, first)
+    if t.shape != shape or not _last(t):
+        raise ValueError(f"{name}: expected a {list(shape)} tensor, channels last in memory")
+
+
+def _scale_shape(shape):
+    """The shape of the checkpoint's scales for images of a shape."""
+    if len(shape) == 3:
+        return shape[0], shape[1], shape[2] // 32
+    return shape[0], shape[1] // 32, *shape[2:]
+
+
+def _gains(weight, bias, scale, shift, dtype, N: int, C: int, device: int, first: str):
+    """(type of weight and bias, image stride of scale and shift)."""
+    ptype, vs = _TYPES[dtype], C
+    if weight is not None or bias is not None:
+        if weight is None or bias is None:
+            raise ValueError("weight and bias: expected both or neither")
+        wtype = weight.dtype if isinstance(weight, torch.Tensor) and weight.dtype is _F32 else dtype
+        ptype = _TYPES[wtype]
+        for t, name in ((weight, "weight"), (bias, "bias")):
+            _dense(t, name, wtype, (C,), device, first)
+    if scale is not None or shift is not None:
+        if scale is None or shift is None:
+            raise ValueError("scale and shift: expected both or neither")
+        vs = _pair(scale, shift, ("scale", "shift"), dtype, N, C, device, first)
+    return ptype, vs
+
+
+def _act(act) -> int:
+    try:
+        return _ACTS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"act: expected None or 'silu', got {act!r}") from None
+
+
+def _group_norm(x, groups, weight, bias, eps, act, scale, shift, out, save: bool, checkpoint: bool):
+    N, S, C = _images(x, "x")
+    device, dtype, shape = x.get_device(), x.dtype, x.shape
+    groups, act = int(groups), _act(act)
+    ptype, vs = _gains(weight, bias, scale, shift, dtype, N, C, device, "x")
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _like(out, "out", dtype, shape, device, "x")
+    stats = codes = scales = None
+    if save:
+        stats = torch.empty((N, max(groups, 0), 2), dtype=_F32, device=x.device)
+        if checkpoint:
+            if C % 32:
+                raise ValueError(f"checkpoint: expected channels in blocks of 32, got {C}")
+            codes = torch.empty_like(x, dtype=_U8)
+            scales = torch.empty_strided(*_scale_layout(shape), dtype=_U8, device=x.device)
+    size = _bytes("dan_group_norm_workspace", device, N, S, C, groups, _TYPES[dtype], 1 if codes is not None else 0)
+    work = torch.empty(size, dtype=_U8, device=x.device) if size else None
+    _on(device, "dan_group_norm", x.data_ptr(), _TYPES[dtype], _ptr(weight), _ptr(bias), ptype, _ptr(scale),
+        _ptr(shift), vs, act, out.data_ptr(), _ptr(stats), _ptr(codes), _ptr(scales), N, S, C, groups, float(eps),
+        _ptr(work), size)
+    return out, (stats, codes, scales)
+
+
+def _scale_layout(shape):
+    """Shape and (channels-last) strides of the checkpoint's scales."""
+    shape = _scale_shape(shape)
+    if len(shape) == 3:
+        return shape, (shape[1] * shape[2], shape[2], 1)
+    strides, step = [1] * len(shape), shape[1]
+    for i in range(len(shape) - 1, 1, -1):
+        strides[i], step = step, step * shape[i]
+    strides[0] = step
+    return shape, tuple(strides)
+
+
+def group_norm(x, groups: int, weight, bias, eps: float, act=None, scale=None, shift=None, out=None):
+    """Group norm of channels-last images (include/dan_train.h):
+    z = (n * weight + bias) * (1 + scale) + shift, y = z, or silu(z) with
+    ``act="silu"``.
+
+    x [N, C, H, W] (or [N, C, D, H, W]) in torch's channels_last memory, or
+    [N, S, C] contiguous, in bf16, fp16 or fp32; weight, bias [C] in x's type or
+    fp32 (or None); scale, shift [N, C] (or [C] when N == 1) in x's type, views
+    that share one image stride (or None).  out may be x itself.  Returns y like
+    x."""
+    return _group_norm(x, groups, weight, bias, eps, act, scale, shift, out, False, False)[0]
+
+
+def group_norm_save(x, groups: int, weight, bias, eps: float, act=None, scale=None, shift=None,
+                    checkpoint: bool = True, out=None):
+    """``group_norm`` for training.  Returns (y, saved) with saved = (stats,
+    codes, scales): stats float32 [N, groups, 2], the groups' mean and 1/std;
+    codes uint8 like x and scales uint8 like x with C / 32 channels, x in 8 bits
+    (for C % 32 == 0), or None without ``checkpoint``."""
+    return _group_norm(x, groups, weight, bias, eps, act, scale, shift, out, True, checkpoint)
+
+
+def group_norm_backward(dy, x, groups: int, weight, bias, saved, act=None, scale=None, shift=None, dx=None):
+    """The gradients of ``group_norm_save`` (include/dan_train.h).
+
+    dy like the forward pass's x; x that input, or None to take it from the
+    checkpoint in ``saved``; the others as there.  dx may be dy itself.  Returns
+    (dx, dweight, dbias, dscale, dshift), each in the type of what it is the
+    gradient of, None where that is."""
+    N, S, C = _images(dy, "dy")
+    device, dtype, shape = dy.get_device(), dy.dtype, dy.shape
+    groups, act = int(groups), _act(act)
+    stats, codes, scales = _kept(saved)
+    _dense(stats, "stats", _F32, (N, groups, 2), device, "dy")
+    if x is not None:
+        _like(x, "x", dtype, shape, device, "dy")
+        at = x.data_ptr() or 16, None, None  # (no memory is looked at where there is none)
+    elif codes is None or scales is None:
+        raise ValueError("x: None, but nothing in saved holds it")
+    else:
+        if C % 32:
+            raise ValueError(f"saved: a checkpoint has channels in blocks of 32, dy has {C}")
+        _like(codes, "codes", _U8, shape, device, "dy")
+        _like(scales, "scales", _U8, _scale_shape(shape), device, "dy")
+        at = None, codes.data_ptr(), scales.data_ptr()
+    ptype, vs = _gains(weight, bias, scale, shift, dtype, N, C, device, "dy")
+    if dx is None:
+        dx = torch.empty_like(dy)
+    else:
+        _like(dx, "dx", dtype, shape, device, "dy")
+    dweight = dbias = dscale = dshift = None
+    if weight is not None:
+        dweight, dbias = torch.empty((2, C), dtype=weight.dtype, device=dy.device).unbind(0)
+    if scale is not None:
+        dscale, dshift = torch.empty((2, N, C), dtype=dtype, device=dy.device).unbind(0)
+    size = _bytes("dan_group_norm_backward_workspace", device, N, S, C, groups, _TYPES[dtype], 1 if x is None else 0)
+    work = torch.empty(size, dtype=_U8, device=dy.device) if size else None
+    _on(device, "dan_group_norm_backward", dy.data_ptr(), at[0], _TYPES[dtype], at[1], at[2], stats.data_ptr(),
+        _ptr(weight), _ptr(bias), ptype, _ptr(scale), _ptr(shift), vs, act, dx.data_ptr(), _ptr(dweight),
+        _ptr(dbias), _ptr(dscale), _ptr(dshift), C, N, S, C, groups, _ptr(work), size)
+    return dx, dweight, dbias, dscale, dshift
