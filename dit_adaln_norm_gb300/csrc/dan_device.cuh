@@ -212,7 +212,8 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float inv)
 {
     uint32_t c[4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) c[w] = fp8x2_e4m3(mul2(make_float2(v[2 * w], v[2 * w + 1]), dup2(inv)));
+    for (int w = 0; w < 4; ++w)
+        c[w] = fp8x2_e4m3(make_float2(__fmul_rn(v[2 * w], inv), __fmul_rn(v[2 * w + 1], inv)));
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 

@@ -3,19 +3,25 @@
 //
 // With the forward pass's mean and rstd at hand, everything that dx needs of
 // the rest of its group, and all the parameters' gradients, follow from two
-// sums per image and channel, s0 = sum dz and s1 = sum dz * n.  So: a kernel
-// that reads dy and x (or its checkpoint) once and stores the sums of each chunk
-// of rows; one that joins the chunks, per group; one that reads both again (the
-// chunks in the opposite order, the last ones still in the L2) and writes dx;
-// and for several images one that adds their shares of dweight and dbias.
+// sums per image and channel, s0 = sum dz and s1 = sum dz * n.  Where a cluster of
+// CTAs can hold a slab of whole groups of dy and x in shared memory, one launch
+// reads both once.  Else: a kernel that reads dy and x (or its checkpoint) once
+// and stores the sums of each chunk of rows; one that joins the chunks, per group;
+// and one that reads both again, in the opposite order (the last rows still lie in
+// the L2), and writes dx.  For several images one more adds their shares of
+// dweight and dbias.
+//
+// In the loops n = (x - mean) * rstd appears as t = x - mean, with rstd in the
+// factors of a channel: z = t * (a * rstd) + b, s1 = rstd * sum dz * t.
 #include "dan_gn.cuh"
 
 namespace dan {
 namespace {
 
 struct GnBackParams {
+    GnGrid g;
     const char *dy, *x;
-    const uint2 *codes;
+    const char *codes;
     const uint8_t *block_scales;
     const float2 *stats;
     char *dx;
@@ -25,265 +31,329 @@ struct GnBackParams {
     void *dweight, *dbias, *dscale, *dshift;
     Gains gains;
     int64_t gs;
-    int64_t S, R, P;
-    int F, Ft, tiles, RL;
-    int per, groups;
     int act;
+    bool last;     // the call's only image
+    float count;   // values of a group
+    int log_cs, M; // slabs: CTAs of a cluster, rows of a thread at most
 };
 
-// A row's fragment of x: its own values, or its checkpoint's.
-template <int TYPE, bool CKPT>
-struct Input {
-    Fragment<TYPE> f;
-    __device__ __forceinline__ void load(const GnBackParams &p, int64_t at)
-    {
-        f.load(p.x + at * Fragment<TYPE>::kBytes);
-    }
-    __device__ __forceinline__ void values(float2 (&v)[4]) const { f.values(v); }
-};
-template <int TYPE>
-struct Input<TYPE, true> {
-    uint2 c;
-    unsigned scale;
-    __device__ __forceinline__ void load(const GnBackParams &p, int64_t at)
-    {
-        c = __ldg(p.codes + at);
-        scale = __ldg(p.block_scales + (at >> 2));
-    }
-    __device__ __forceinline__ void values(float2 (&v)[4]) const { decode8(c, block_scale_value(scale), v); }
-};
-
-// A thread's eight channels: n = (x - mean) * rstd, z = n * a + b.  UNI: they lie
-// in one group.
-template <bool UNI>
+// A thread's P pairs of channels.  UNI: they lie in one group.
+template <int P, bool UNI>
 struct Channels {
-    static constexpr int K = UNI ? 1 : 4;
-    float2 mean[K], rstd[K], a[4], b[4];
-    __device__ __forceinline__ void get(const GnBackParams &p, int64_t n, int f)
+    static constexpr int K = UNI ? 1 : P;
+    float2 minus[K], a[P], b[P]; // minus the mean, the gain times rstd, the offset
+    // stats: of the groups from the tile's channel 0 on; c: the thread's first channel of it
+    template <int TYPE>
+    __device__ __forceinline__ void get(const GnBackParams &p, int64_t n, int f, const float2 *stats, int c)
     {
+        GroupOf group(p.g, c);
+        p.gains.get<TYPE>(n, f, a, b);
+        float2 rstd[K];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = 8 * f + e;
-            float g, h;
-            p.gains.get(n, c, g, h);
-            if (e & 1) a[e / 2].y = g, b[e / 2].y = h;
-            else a[e / 2].x = g, b[e / 2].x = h;
-            if (UNI && e > 0) continue;
-            const float2 st = p.stats[n * p.groups + c / p.per];
-            if (UNI) mean[0] = dup2(st.x), rstd[0] = dup2(st.y);
-            else if (e & 1) mean[e / 2 % K].y = st.x, rstd[e / 2 % K].y = st.y;
-            else mean[e / 2 % K].x = st.x, rstd[e / 2 % K].x = st.y;
+        for (int k = 0; k < K; ++k) {
+            const float2 s = stats[group.next()];
+            const float2 t = UNI ? s : stats[group.next()];
+            minus[k] = make_float2(-s.x, -t.x);
+            rstd[k] = make_float2(s.y, t.y);
+        }
+#pragma unroll
+        for (int w = 0; w < P; ++w) a[w] = mul2(a[w], rstd[w % K]);
+    }
+    // rstd alone (it would only take registers in the loops).
+    __device__ __forceinline__ static void rstds(const GnGrid &q, const float2 *stats, int c, float2 (&rstd)[K])
+    {
+        GroupOf group(q, c);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            rstd[k].x = stats[group.next()].y;
+            rstd[k].y = UNI ? rstd[k].x : stats[group.next()].y;
         }
     }
-    // n of pair w, and dz of dy.
-    __device__ __forceinline__ void pair(int w, int act, float2 x, float2 dy, float2 &n, float2 &dz) const
+    // dz of dy.
+    __device__ __forceinline__ float2 dz(int w, int act, float2 t, float2 dy) const
     {
-        n = mul2(sub2(x, mean[w % K]), rstd[w % K]);
-        dz = dy;
-        if (act) {
-            const float2 z = fma2(n, a[w], b[w]);
-            const float2 p = make_float2(sigmoid(z.x), sigmoid(z.y));
-            // the derivative, p * (1 + z * (1 - p))
-            dz = mul2(dy, fma2(mul2(z, p), sub2(dup2(1.0f), p), p));
+        if (!act) return dy;
+        const float2 z = fma2(t, a[w], b[w]);
+        const float2 p = sigmoid2(z);
+        // the derivative, p * (1 + z * (1 - p))
+        return mul2(dy, fma2(mul2(z, p), sub2(dup2(1.0f), p), p));
+    }
+    // Minus the means of a * dz (times rstd) and of a * dz * n (times rstd^2).
+    __device__ __forceinline__ static void means(const GnGrid &q, const float2 *means, const float2 *stats, int c,
+                                                 float2 (&m1)[K], float2 (&m2)[K])
+    {
+        float2 rstd[K];
+        rstds(q, stats, c, rstd);
+        GroupOf group(q, c);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float2 u = means[group.next()];
+            const float2 v = UNI ? u : means[group.next()];
+            m1[k] = mul2(make_float2(-u.x, -v.x), rstd[k]);
+            m2[k] = mul2(mul2(make_float2(-u.y, -v.y), rstd[k]), rstd[k]);
         }
+    }
+    // dx of pair w.
+    __device__ __forceinline__ float2 dx(int w, float2 t, float2 dz, const float2 (&m1)[K], const float2 (&m2)[K]) const
+    {
+        return fma2(t, m2[w % K], fma2(dz, a[w], m1[w % K]));
     }
 };
 
-struct Where {
-    int64_t n, chunk;
-    int tile;
-    __device__ __forceinline__ Where(int64_t id, int tiles, int64_t P)
+// Rows of dy and x (or its checkpoint) in flight of a thread, through shared
+// memory that it alone uses: as many as 48 KB of 256 threads hold.  Their number A
+// and the CTA's threads are known to the compiler, so that a row's slots and what
+// is left are constants of an unrolled round of A rows.
+template <int TYPE, bool CKPT, bool UNI, int NT>
+struct Ring {
+    using Frag = Fragment<TYPE>;
+    using XWord = typename std::conditional<CKPT, typename Frag::Codes, uint4>::type;
+    static constexpr int kBytes = 16 + (int)sizeof(XWord);
+    static constexpr int A = 48 * 1024 / 256 / kBytes;
+    const char *dy, *x;   // this thread's first row of the round
+    const uint8_t *scale; // and its block's scale
+    int step;             // fragments from a row to the next
+    int left;             // rows from the round's first on
+    uint4 *s_dy;          // [A][NT]
+    XWord *s_x;           // [A][NT]
+    unsigned next_scale;
+
+    // `rows` rows from fragment `at` on, `step` fragments apart.
+    __device__ __forceinline__ Ring(const GnBackParams &p, uint4 *smem, int64_t at, int step_, int rows)
     {
-        chunk = id % P;
-        const int64_t rest = id / P;
-        tile = (int)(rest % tiles);
-        n = rest / tiles;
+        s_dy = smem + threadIdx.x;
+        s_x = reinterpret_cast<XWord *>(smem + A * NT) + threadIdx.x;
+        step = step_;
+        left = rows;
+        dy = p.dy + at * 16;
+        x = (CKPT ? p.codes : p.x) + at * (int64_t)sizeof(XWord);
+        scale = p.block_scales + at / Frag::kBlock;
+        next_scale = 127;
+#pragma unroll
+        for (int j = 0; j < A; ++j) ask(j, j);
+        if (CKPT && left > 0) next_scale = __ldg(scale);
+    }
+    // Row `ahead` of the round into slot j.
+    __device__ __forceinline__ void ask(int j, int ahead)
+    {
+        if (left > ahead) {
+            cp_async16(s_dy + j * NT, dy + ahead * (int64_t)(step * 16));
+            cp_async_word(s_x + j * NT, x + ahead * (int64_t)(step * (int)sizeof(XWord)));
+        }
+        cp_async_commit();
+    }
+    // Row j of the round, x - mean and dy; the slot is filled again.
+    __device__ __forceinline__ void take(int j, const Channels<Frag::kP, UNI> &ch, float2 (&t)[Frag::kP], float2 (&d)[Frag::kP])
+    {
+        cp_async_wait<A - 1>();
+        const uint4 a = s_dy[j * NT];
+        const XWord c = s_x[j * NT];
+        if constexpr (CKPT) {
+            const float2 s = dup2(block_scale_value(next_scale));
+            if (left > j + 1) // (a row's fragments, and so the step, are whole blocks)
+                next_scale = __ldg(scale + (j + 1) * (int64_t)(step / Frag::kBlock));
+            Frag::codes(c, t);
+#pragma unroll
+            for (int w = 0; w < Frag::kP; ++w) t[w] = fma2(t[w], s, ch.minus[w % ch.K]);
+        } else {
+            Frag::values(c, t);
+#pragma unroll
+            for (int w = 0; w < Frag::kP; ++w) t[w] = add2(t[w], ch.minus[w % ch.K]);
+        }
+        ask(j, j + A);
+        Frag::values(a, d);
+    }
+    // On to the next round.
+    __device__ __forceinline__ void round()
+    {
+        dy += A * (int64_t)(step * 16);
+        x += A * (int64_t)(step * (int)sizeof(XWord));
+        scale += A * (int64_t)(step / Frag::kBlock);
+        left -= A;
     }
 };
 
-template <int TYPE, bool CKPT, bool UNI>
-__global__ void __launch_bounds__(kGnMost, 1) gn_sums_kernel(const GnBackParams p)
+// CTAs of 256 threads that share an SM (three, of 80 registers, spill and took
+// 128 us for the gradient of [1, 512 x 512, 256] images against 109).
+constexpr int kBackBlocks = 2;
+
+template <int TYPE, bool CKPT, bool UNI, int NT>
+__global__ void __launch_bounds__(NT, NT > 256 ? 1 : kBackBlocks) gn_sums_kernel(const GnBackParams p)
 {
     using Frag = Fragment<TYPE>;
-    extern __shared__ float2 s_sums[]; // [RL][8 channels of the fragments]
-    const int tid = threadIdx.x;
-    const Where at(blockIdx.x, p.tiles, p.P);
-    const int f0 = at.tile * p.Ft, Ft = min(p.Ft, p.F - f0);
-    const int r = tid / p.Ft, f = tid - r * p.Ft;
-    const bool here = r < p.RL && f < Ft;
-    const int64_t row0 = at.chunk * p.R;
-    const int rows = (int)min(p.R, p.S - row0);
+    using R = Ring<TYPE, CKPT, UNI, NT>;
+    constexpr int P = Frag::kP;
+    extern __shared__ __align__(16) uint4 s_ring[];
+    const int64_t n = blockIdx.x;
+    const GnPlace at(p.g, blockIdx.z, blockIdx.y);
     grid_dependency_wait();
     allow_dependents();
-    if (here) {
-        Channels<UNI> ch;
-        ch.get(p, at.n, f0 + f);
-        float2 s0[4], s1[4];
+    float2 s0[P], s1[P];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) s0[w] = s1[w] = make_float2(0.0f, 0.0f);
-        const int64_t base = (at.n * p.S + row0) * p.F + f0 + f;
-        constexpr int U = 4;
-        for (int i = r; i < rows; i += U * p.RL) {
-            Frag dy[U];
-            Input<TYPE, CKPT> x[U];
+    for (int w = 0; w < P; ++w) s0[w] = s1[w] = make_float2(0.0f, 0.0f);
+    if (at.mine > 0) {
+        R ring(p, s_ring, at.first(p.g, n), p.g.RL * p.g.F, at.mine);
+        Channels<P, UNI> ch;
+        ch.template get<TYPE>(p, n, at.f0 + at.f, p.stats + n * p.g.groups + at.g0, at.f * Frag::kE);
+        for (; ring.left > 0; ring.round()) {
 #pragma unroll
-            for (int j = 0; j < U; ++j)
-                if (i + j * p.RL < rows) {
-                    const int64_t k = base + (int64_t)(i + j * p.RL) * p.F;
-                    dy[j].load(p.dy + k * Frag::kBytes);
-                    x[j].load(p, k);
-                }
+            for (int j = 0; j < R::A; ++j) {
+                if (ring.left <= j) break;
+                float2 t[P], d[P];
+                ring.take(j, ch, t, d);
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                if (i + j * p.RL >= rows) break;
-                float2 v[4], d[4];
-                dy[j].values(d);
-                x[j].values(v);
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    float2 n, dz;
-                    ch.pair(w, p.act, v[w], d[w], n, dz);
+                for (int w = 0; w < P; ++w) {
+                    const float2 dz = ch.dz(w, p.act, t[w], d[w]);
                     s0[w] = add2(s0[w], dz);
-                    s1[w] = fma2(dz, n, s1[w]);
+                    s1[w] = fma2(dz, t[w], s1[w]);
                 }
             }
         }
-        float4 *to = reinterpret_cast<float4 *>(s_sums + (r * Ft + f) * 8);
+        float2 rstd[ch.K];
+        ch.rstds(p.g, p.stats + n * p.g.groups + at.g0, at.f * Frag::kE, rstd);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) to[w] = make_float4(s0[w].x, s1[w].x, s0[w].y, s1[w].y);
+        for (int w = 0; w < P; ++w) s1[w] = mul2(s1[w], rstd[w % ch.K]);
+    }
+    cp_async_wait_all();
+    __syncthreads(); // every thread has read its slots
+    float2 *s_sums = reinterpret_cast<float2 *>(s_ring); // [RL][channels]
+    const int channels = at.Ft * Frag::kE;
+    if (at.r < p.g.RL && at.f < at.Ft) {
+        float4 *to = reinterpret_cast<float4 *>(s_sums + at.r * channels + at.f * Frag::kE);
+#pragma unroll
+        for (int w = 0; w < P; ++w) to[w] = make_float4(s0[w].x, s1[w].x, s0[w].y, s1[w].y);
     }
     __syncthreads();
-    for (int c = tid; c < Ft * 8; c += blockDim.x) {
+    float2 *to = p.part + (n * p.g.P + blockIdx.y) * ((int64_t)p.g.F * Frag::kE) + at.f0 * Frag::kE;
+    for (int c = threadIdx.x; c < channels; c += NT) {
         float2 t = s_sums[c];
-        for (int k = 1; k < p.RL; ++k) t = add2(t, s_sums[k * Ft * 8 + c]);
-        p.part[(at.n * p.P + at.chunk) * (8 * (int64_t)p.F) + 8 * f0 + c] = t;
+        for (int k = 1; k < p.g.RL; ++k) t = add2(t, s_sums[k * channels + c]);
+        to[c] = t;
+    }
+}
+
+// What follows from an image's sums t = (s0, s1) of channel c with the gains g.
+template <int TYPE>
+__device__ __forceinline__ void store_sums(const GnBackParams &p, int64_t n, int64_t c, const Gains::One &g, float2 t)
+{
+    if (p.dscale) {
+        store_as(p.dscale, TYPE, n * p.gs + c, __fmaf_rn(g.w, t.y, __fmul_rn(g.b, t.x)));
+        store_as(p.dshift, TYPE, n * p.gs + c, t.x);
+    }
+    if (!p.dweight) return;
+    if (p.last) {
+        store_as(p.dweight, p.gains.param_type, c, __fmul_rn(g.o, t.y));
+        store_as(p.dbias, p.gains.param_type, c, __fmul_rn(g.o, t.x));
+    } else {
+        p.sums[n * ((int64_t)p.g.F * Fragment<TYPE>::kE) + c] = t;
     }
 }
 
 // Joins the chunks of a group's channels; then what follows from the sums.
 constexpr int kJoin = 256;
-__global__ void __launch_bounds__(kJoin) gn_back_join_kernel(const GnBackParams p, bool last)
+template <int TYPE>
+__global__ void __launch_bounds__(kJoin) gn_back_join_kernel(const GnBackParams p)
 {
     __shared__ float2 s_part[kJoin];
     const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t n = blockIdx.x / p.groups;
-    const int g = (int)(blockIdx.x - n * p.groups);
-    const int64_t C = 8 * (int64_t)p.F;
-    const int cols = min(p.per, kJoin), shares = kJoin / cols;
-    const int col = tid % cols, share = tid / cols;
-    grid_dependency_wait();
-    allow_dependents();
+    const int64_t n = blockIdx.x / (unsigned)p.g.groups;
+    const int g = blockIdx.x - (unsigned)n * p.g.groups;
+    const int64_t C = (int64_t)p.g.F * Fragment<TYPE>::kE;
+    const int cols = min(p.g.per, kJoin), shares = kJoin / cols;
+    const int share = tid / cols, col = tid - share * cols;
     float2 all = make_float2(0.0f, 0.0f); // sums of a * s0 and a * s1 over this thread's channels
-    for (int j0 = 0; j0 < p.per; j0 += cols) {
-        const int64_t c = g * (int64_t)p.per + j0 + col;
-        const bool here = share < shares && j0 + col < p.per;
+    for (int j0 = 0; j0 < p.g.per; j0 += cols) {
+        const int64_t c = g * (int64_t)p.g.per + j0 + col;
+        const bool here = share < shares && j0 + col < p.g.per;
         float2 t = make_float2(0.0f, 0.0f);
-        if (here)
-#pragma unroll 8
-            for (int64_t k = share; k < p.P; k += shares) t = add2(t, __ldcg(p.part + (n * p.P + k) * C + c));
+        Gains::One gain = {};
+        if (here && share == 0) gain = p.gains.one<TYPE>(n, c); // (an input: complete before the sums began)
+        if (j0 == 0) {
+            grid_dependency_wait();
+            allow_dependents();
+        }
+        if (here) {
+            const float2 *from = p.part + n * p.g.P * C + c;
+            constexpr int U = 16; // loads under way at once
+            for (int k = share; k < p.g.P; k += U * shares) {
+                float2 u[U];
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    u[j] = k + j * shares < p.g.P ? __ldcg(from + (k + j * shares) * C) : make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int j = 0; j < U; ++j) t = add2(t, u[j]);
+            }
+        }
         s_part[tid] = t;
         __syncthreads();
         if (here && share == 0) {
             for (int k = 1; k < shares; ++k) t = add2(t, s_part[k * cols + col]);
-            float a, b;
-            p.gains.get(n, c, a, b);
-            all = fma2(dup2(a), t, all);
-            p.sums[n * C + c] = t;
-            if (p.dscale) {
-                const float w = p.gains.weight ? load_as(p.gains.weight, p.gains.param_type, c) : 1.0f;
-                const float v = p.gains.bias ? load_as(p.gains.bias, p.gains.param_type, c) : 0.0f;
-                store_as(p.dscale, p.gains.type, n * p.gs + c, __fmaf_rn(w, t.y, __fmul_rn(v, t.x)));
-                store_as(p.dshift, p.gains.type, n * p.gs + c, t.x);
-            }
-            if (last && p.dweight) { // the call's only image
-                const float o = p.gains.scale ? __fadd_rn(1.0f, load_as(p.gains.scale, p.gains.type, c)) : 1.0f;
-                store_as(p.dweight, p.gains.param_type, c, __fmul_rn(o, t.y));
-                store_as(p.dbias, p.gains.param_type, c, __fmul_rn(o, t.x));
-            }
+            all = fma2(dup2(gain.gain()), t, all);
+            store_sums<TYPE>(p, n, c, gain, t);
         }
         __syncthreads();
     }
     // the group's means
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-        all.x = __fadd_rn(all.x, __shfl_xor_sync(kFull, all.x, off));
-        all.y = __fadd_rn(all.y, __shfl_xor_sync(kFull, all.y, off));
-    }
+    all.x = lane_sum(all.x, 32);
+    all.y = lane_sum(all.y, 32);
     if (lane == 0) s_part[tid >> 5] = all;
     __syncthreads();
     if (tid != 0) return;
     for (int k = 1; k < kJoin / 32; ++k) all = add2(all, s_part[k]);
-    const float count = (float)(p.S * p.per);
-    p.mean[n * p.groups + g] = make_float2(__fdiv_rn(all.x, count), __fdiv_rn(all.y, count));
+    p.mean[n * p.g.groups + g] = make_float2(__fdiv_rn(all.x, p.count), __fdiv_rn(all.y, p.count));
 }
 
-template <int TYPE, bool CKPT, bool UNI>
-__global__ void __launch_bounds__(kGnMost, 1) gn_dx_kernel(const GnBackParams p)
+template <int TYPE, bool CKPT, bool UNI, int NT>
+__global__ void __launch_bounds__(NT, NT > 256 ? 1 : kBackBlocks) gn_dx_kernel(const GnBackParams p)
 {
     using Frag = Fragment<TYPE>;
-    const int tid = threadIdx.x;
-    const Where at(gridDim.x - 1 - blockIdx.x, p.tiles, p.P); // the last chunk first
-    const int f0 = at.tile * p.Ft, Ft = min(p.Ft, p.F - f0);
-    const int r = tid / p.Ft, f = f0 + tid - r * p.Ft;
-    const int64_t row0 = at.chunk * p.R;
-    const int rows = (int)min(p.R, p.S - row0);
+    using R = Ring<TYPE, CKPT, UNI, NT>;
+    constexpr int P = Frag::kP;
+    extern __shared__ __align__(16) uint4 s_ring[];
+    // the last chunk first, and of it the last rows
+    const int64_t n = gridDim.x - 1 - blockIdx.x;
+    const GnPlace at(p.g, gridDim.z - 1 - blockIdx.z, gridDim.y - 1 - blockIdx.y);
+    const int step = -p.g.RL * p.g.F;
+    const int64_t to = at.first(p.g, n) - (at.mine - 1) * (int64_t)step;
+    char *dx = p.dx + to * 16;
+    // dy, x, the statistics and the gains were complete before the kernel whose
+    // results are waited for below let this one start
+    R ring(p, s_ring, to, step, at.mine);
+    Channels<P, UNI> ch = {};
+    if (at.mine > 0) ch.template get<TYPE>(p, n, at.f0 + at.f, p.stats + n * p.g.groups + at.g0, at.f * Frag::kE);
     grid_dependency_wait();
     allow_dependents();
-    if (r >= p.RL || f - f0 >= Ft) return;
-    Channels<UNI> ch;
-    ch.get(p, at.n, f);
-    constexpr int K = Channels<UNI>::K;
-    float2 m1[K], m2[K]; // minus the means, times rstd
+    if (at.mine == 0) return;
+    float2 m1[ch.K], m2[ch.K];
+    ch.means(p.g, p.mean + n * p.g.groups + at.g0, p.stats + n * p.g.groups + at.g0, at.f * Frag::kE, m1, m2);
+    for (; ring.left > 0; ring.round(), dx += R::A * (int64_t)(step * 16)) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = 8 * f + 2 * k;
-        const float2 u = p.mean[at.n * p.groups + c / p.per];
-        const float2 v = UNI ? u : p.mean[at.n * p.groups + (c + 1) / p.per];
-        m1[k] = mul2(make_float2(-u.x, -v.x), ch.rstd[k]);
-        m2[k] = mul2(make_float2(-u.y, -v.y), ch.rstd[k]);
-    }
-    const int64_t base = (at.n * p.S + row0) * p.F + f;
-    constexpr int U = 4;
-    for (int i = r; i < rows; i += U * p.RL) {
-        Frag dy[U];
-        Input<TYPE, CKPT> x[U];
+        for (int j = 0; j < R::A; ++j) {
+            if (ring.left <= j) break;
+            float2 t[P], d[P];
+            ring.take(j, ch, t, d);
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (i + j * p.RL < rows) {
-                const int64_t k = base + (int64_t)(i + j * p.RL) * p.F;
-                dy[j].load(p.dy + k * Frag::kBytes);
-                x[j].load(p, k);
-            }
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (i + j * p.RL >= rows) break;
-            float2 v[4], d[4];
-            dy[j].values(d);
-            x[j].values(v);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                float2 n, dz;
-                ch.pair(w, p.act, v[w], d[w], n, dz);
-                d[w] = fma2(n, m2[w % K], fma2(mul2(dz, ch.a[w]), ch.rstd[w % K], m1[w % K]));
-            }
-            Frag::store(p.dx + (base + (int64_t)(i + j * p.RL) * p.F) * Frag::kBytes, d);
+            for (int w = 0; w < P; ++w) d[w] = ch.dx(w, t[w], ch.dz(w, p.act, t[w], d[w]), m1, m2);
+            Frag::store(dx + j * (int64_t)(step * 16), d);
         }
     }
 }
 
 // dweight and dbias from the images' sums, in order; eight threads a channel.
+template <int TYPE>
 __global__ void __launch_bounds__(256) gn_params_kernel(const GnBackParams p, int64_t N)
 {
     __shared__ float2 s_sum[8][32];
     const int share = threadIdx.x >> 5;
-    const int64_t C = 8 * (int64_t)p.F, c = blockIdx.x * (int64_t)32 + (threadIdx.x & 31);
+    const int64_t C = (int64_t)p.g.F * Fragment<TYPE>::kE, c = blockIdx.x * (int64_t)32 + (threadIdx.x & 31);
     grid_dependency_wait();
     allow_dependents();
     float2 t = make_float2(0.0f, 0.0f);
     if (c < C)
+#pragma unroll 4
         for (int64_t n = share; n < N; n += 8) {
-            const float o = p.gains.scale ? __fadd_rn(1.0f, load_as(p.gains.scale, p.gains.type, n * p.gains.vs + c)) : 1.0f;
-            t = fma2(dup2(o), __ldcg(p.sums + n * C + c), t);
+            const float s = p.gains.scale ? Gains::value<TYPE>(p.gains.scale, n * p.gains.vs + c) : 0.0f;
+            t = fma2(dup2(__fadd_rn(1.0f, s)), __ldcg(p.sums + n * C + c), t);
         }
     s_sum[share][threadIdx.x & 31] = t;
     __syncthreads();
@@ -293,87 +363,257 @@ __global__ void __launch_bounds__(256) gn_params_kernel(const GnBackParams p, in
     store_as(p.dbias, p.gains.param_type, c, t.x);
 }
 
-GnCut backward_cut(int64_t S, int64_t C, int64_t groups, int type, bool checkpoint)
+// ------------------------------------------------------------------- slabs
+
+// One launch, one read of dy and x: a cluster holds a slab (whole groups of an
+// image) of both in its CTAs' shared memory.  Each thread copies its own
+// fragments there and nobody else reads them; the channels' sums are joined in
+// the CTA, then over the cluster, each CTA for itself in the same order.
+template <int TYPE, bool CKPT, bool UNI>
+__global__ void __launch_bounds__(512, 1) gn_back_slab_kernel(const GnBackParams p)
 {
-    return gn_cut(S, C, groups, type, checkpoint, 65536, 1024);
+    using Frag = Fragment<TYPE>;
+    constexpr int P = Frag::kP, E = Frag::kE;
+    using XWord = typename std::conditional<CKPT, typename Frag::Codes, uint4>::type;
+    extern __shared__ __align__(16) uint4 s_dy[]; // [M][threads]
+    const int tid = threadIdx.x, lane = tid & 31, NT = blockDim.x, cs = 1 << p.log_cs;
+    float2 *s_sums = reinterpret_cast<float2 *>(s_dy + p.M * NT); // [RL][channels]
+    XWord *s_x = reinterpret_cast<XWord *>(s_sums + NT * E);      // [M][threads]
+    float2 *s_ch = reinterpret_cast<float2 *>(s_x + p.M * NT);    // [channels] this CTA's sums
+    float2 *s_all = s_ch + E * p.g.Ft;                            // [channels] the slab's, times the gain
+    float2 *s_mean = s_all + E * p.g.Ft;                          // [groups]
+    uint8_t *s_scale = reinterpret_cast<uint8_t *>(s_mean + E * p.g.Ft); // [M][threads] (CKPT)
+
+    const int rank = blockIdx.x & (cs - 1); // (clusters lie along x)
+    const int64_t n = blockIdx.x >> p.log_cs;
+    const GnPlace at(p.g, blockIdx.y, rank);
+    const int64_t base = at.first(p.g, n), step = (int64_t)p.g.RL * p.g.F;
+
+    grid_dependency_wait();
+    allow_dependents();
+    constexpr int kParts = 4; // the rows arrive in parts, the first is summed while the others are under way
+    const int part = (p.M + kParts - 1) / kParts;
+    {
+        const char *dy = p.dy + base * 16, *x = (CKPT ? p.codes : p.x) + base * (int64_t)sizeof(XWord);
+        int i = 0;
+#pragma unroll
+        for (int k = 1; k <= kParts; ++k) {
+            for (const int end = min(at.mine, k * part); i < end; ++i) {
+                cp_async16(s_dy + i * NT + tid, dy);
+                cp_async_word(s_x + i * NT + tid, x);
+                dy += step * 16;
+                x += step * (int64_t)sizeof(XWord);
+            }
+            cp_async_commit();
+        }
+    }
+    if (CKPT) {
+        const uint8_t *scale = p.block_scales + base / Frag::kBlock;
+#pragma unroll 4
+        for (int i = 0; i < at.mine; ++i) s_scale[i * NT + tid] = __ldg(scale + i * (step / Frag::kBlock));
+    }
+    const int channels = at.Ft * E, c0 = at.f0 * E;
+    Channels<P, UNI> ch = {};
+    if (at.mine > 0) ch.template get<TYPE>(p, n, at.f0 + at.f, p.stats + n * p.g.groups + at.g0, at.f * E);
+    Gains::One gain = {}; // of this thread's channel of the slab (the first, where it has several)
+    if (tid < channels) gain = p.gains.one<TYPE>(n, c0 + tid);
+    auto get = [&](int i, float2 (&t)[P], float2 (&d)[P]) {
+        Frag::values(s_dy[i * NT + tid], d);
+        if constexpr (CKPT) {
+            const float2 s = dup2(block_scale_value(s_scale[i * NT + tid]));
+            Frag::codes(s_x[i * NT + tid], t);
+#pragma unroll
+            for (int w = 0; w < P; ++w) t[w] = fma2(t[w], s, ch.minus[w % ch.K]);
+        } else {
+            Frag::values(s_x[i * NT + tid], t);
+#pragma unroll
+            for (int w = 0; w < P; ++w) t[w] = add2(t[w], ch.minus[w % ch.K]);
+        }
+    };
+    float2 s0[P], s1[P];
+#pragma unroll
+    for (int w = 0; w < P; ++w) s0[w] = s1[w] = make_float2(0.0f, 0.0f);
+    int i = 0;
+#pragma unroll
+    for (int k = 1; k <= kParts; ++k) {
+        if (k == 1) cp_async_wait<3>();
+        if (k == 2) cp_async_wait<2>();
+        if (k == 3) cp_async_wait<1>();
+        if (k == 4) cp_async_wait<0>();
+        for (const int end = min(at.mine, k * part); i < end; ++i) {
+            float2 t[P], d[P];
+            get(i, t, d);
+#pragma unroll
+            for (int w = 0; w < P; ++w) {
+                const float2 dz = ch.dz(w, p.act, t[w], d[w]);
+                s0[w] = add2(s0[w], dz);
+                s1[w] = fma2(dz, t[w], s1[w]);
+            }
+        }
+    }
+    // the CTA's sums: of every `shares`-th row lane, then those
+    if (at.r < p.g.RL && at.f < at.Ft) {
+        float4 *to = reinterpret_cast<float4 *>(s_sums + at.r * channels + at.f * E);
+        float2 rstd[ch.K];
+        ch.rstds(p.g, p.stats + n * p.g.groups + at.g0, at.f * E, rstd);
+#pragma unroll
+        for (int w = 0; w < P; ++w) {
+            s1[w] = mul2(s1[w], rstd[w % ch.K]);
+            to[w] = make_float4(s0[w].x, s1[w].x, s0[w].y, s1[w].y);
+        }
+    }
+    __syncthreads();
+    const int shares = min(p.g.RL, max(1, NT / channels));
+    for (int c = tid; c < channels * shares; c += NT) {
+        const int share = c / channels;
+        float2 t = make_float2(0.0f, 0.0f);
+        for (int k = share; k < p.g.RL; k += shares) t = add2(t, s_sums[k * channels + c - share * channels]);
+        s_sums[c] = t; // (an entry that nobody else reads)
+    }
+    __syncthreads();
+    for (int c = tid; c < channels; c += NT) {
+        float2 t = s_sums[c];
+        for (int k = 1; k < shares; ++k) t = add2(t, s_sums[k * channels + c]);
+        s_ch[c] = t;
+    }
+    if (cs > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } // else each thread goes on with the channels that it has just summed
+    for (int c = tid; c < channels; c += NT) {
+        float2 t = s_ch[c];
+        if (cs > 1) {
+            t = make_float2(0.0f, 0.0f);
+            for (int k = 0; k < cs; ++k) t = add2(t, ld_cluster(s_ch + c, k));
+        }
+        if (c != tid) gain = p.gains.one<TYPE>(n, c0 + c);
+        s_all[c] = mul2(dup2(gain.gain()), t);
+        if (rank == 0) store_sums<TYPE>(p, n, c0 + c, gain, t);
+    }
+    if (cs > 1) cluster_arrive(); // nobody reads this CTA's sums after the wait below
+    __syncthreads();
+    for (int g = tid >> 5; g < at.groups; g += NT >> 5) {
+        float2 t = make_float2(0.0f, 0.0f);
+        for (int c = lane; c < p.g.per; c += 32) t = add2(t, s_all[g * p.g.per + c]);
+        t.x = lane_sum(t.x, 32);
+        t.y = lane_sum(t.y, 32);
+        if (lane == 0) s_mean[g] = make_float2(__fdiv_rn(t.x, p.count), __fdiv_rn(t.y, p.count));
+    }
+    __syncthreads();
+    if (at.mine > 0) {
+        float2 m1[ch.K], m2[ch.K];
+        ch.means(p.g, s_mean, p.stats + n * p.g.groups + at.g0, at.f * E, m1, m2);
+        char *dx = p.dx + base * 16;
+        for (int k = 0; k < at.mine; ++k, dx += step * 16) {
+            float2 t[P], d[P];
+            get(k, t, d);
+#pragma unroll
+            for (int w = 0; w < P; ++w) d[w] = ch.dx(w, t[w], ch.dz(w, p.act, t[w], d[w]), m1, m2);
+            Frag::store(dx, d);
+        }
+    }
+    if (cs > 1) cluster_wait();
+}
+
+GnSlab backward_slab(int64_t S, int64_t C, int64_t groups, int type, bool checkpoint)
+{
+    const int E = (int)type_channels(type);
+    // (a slab need not hold whole blocks: their scales are read only)
+    return gn_slab(S, C, groups, type, false, checkpoint ? 16 + E + 1 : 32, E * (int)sizeof(float2));
+}
+
+GnCut backward_cut(int64_t S, int64_t C, int64_t groups, int type)
+{
+    return gn_cut(S, C, groups, type, false, 65536, 304);
 }
 
 template <int TYPE, bool CKPT, bool UNI>
-cudaError_t launch_passes(const GnBackParams &p, const GnProblem &q, const GnCut &c, int64_t grid, bool last,
-                          cudaStream_t s)
+cudaError_t launch_slab(GnBackParams p, const GnProblem &q, const GnSlab &c, cudaStream_t s)
 {
-    const int smem = c.RL * c.Ft * 8 * (int)sizeof(float2);
-    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(gn_sums_kernel<TYPE, CKPT, UNI>), smem);
-    if (e != cudaSuccess) return e;
-    e = launch_overlapped(gn_sums_kernel<TYPE, CKPT, UNI>, (int)grid, c.threads, smem, s, p);
-    if (e != cudaSuccess) return e;
-    e = launch_overlapped(gn_back_join_kernel, (int)(q.N * q.groups), kJoin, 0, s, p, last);
-    if (e != cudaSuccess) return e;
-    return launch_overlapped(gn_dx_kernel<TYPE, CKPT, UNI>, (int)grid, c.threads, 0, s, p);
+    p.g = gn_grid(q.S, q.C, q.groups, TYPE, c.Ft, c.R, 1 << c.log_cs, c.RL);
+    p.log_cs = c.log_cs;
+    p.M = c.M;
+    p.sums = static_cast<float2 *>(q.workspace);
+    return launch_grid(gn_back_slab_kernel<TYPE, CKPT, UNI>, dim3((unsigned)(q.N << c.log_cs), c.slabs), 1 << c.log_cs,
+                       c.threads, c.smem, s, p);
 }
 
-template <int TYPE>
-cudaError_t launch_type(const GnBackParams &p, const GnProblem &q, const GnCut &c, int64_t grid, bool last,
-                        cudaStream_t s)
+// The workspace of the passes: the chunks' sums, the images', the means.
+void set_passes(GnBackParams &p, const GnProblem &q, const GnCut &c)
 {
-    const bool uni = p.per % 8 == 0;
-    if (q.x == nullptr)
-        return uni ? launch_passes<TYPE, true, true>(p, q, c, grid, last, s)
-                   : launch_passes<TYPE, true, false>(p, q, c, grid, last, s);
-    return uni ? launch_passes<TYPE, false, true>(p, q, c, grid, last, s)
-               : launch_passes<TYPE, false, false>(p, q, c, grid, last, s);
+    p.g = gn_grid(q.S, q.C, q.groups, q.type, c.Ft, c.R, c.P, c.RL);
+    p.part = static_cast<float2 *>(q.workspace);
+    p.sums = p.part + q.N * c.P * q.C;
+    p.mean = p.sums + q.N * q.C;
+}
+
+template <int TYPE, bool CKPT, bool UNI>
+cudaError_t launch_passes(const GnBackParams &p, const GnProblem &q, const GnCut &c, cudaStream_t s)
+{
+    using R = Ring<TYPE, CKPT, UNI, 256>;
+    const dim3 grid((unsigned)q.N, (unsigned)c.P, c.tiles), joins((unsigned)(q.N * q.groups));
+    const int ring = R::A * R::kBytes * c.threads, sums = c.RL * c.Ft * Fragment<TYPE>::kE * (int)sizeof(float2);
+    const auto go = [&](auto threads) {
+        constexpr int NT = decltype(threads)::value;
+        cudaError_t e = launch_grid(gn_sums_kernel<TYPE, CKPT, UNI, NT>, grid, 1, c.threads, ring > sums ? ring : sums, s, p);
+        if (e == cudaSuccess) e = launch_grid(gn_back_join_kernel<TYPE>, joins, 1, kJoin, 0, s, p);
+        if (e == cudaSuccess) e = launch_grid(gn_dx_kernel<TYPE, CKPT, UNI, NT>, grid, 1, c.threads, ring, s, p);
+        return e;
+    };
+    if (c.threads <= 256) return go(std::integral_constant<int, 256>());
+    return go(std::integral_constant<int, gn_threads(TYPE)>());
 }
 
 } // namespace
 
 int64_t group_norm_backward_workspace(int64_t N, int64_t S, int64_t C, int64_t groups, int type, bool checkpoint)
 {
-    const GnCut c = backward_cut(S, C, groups, type, checkpoint);
+    if (S > 0 && backward_slab(S, C, groups, type, checkpoint).Ft) // the images' sums, to be added
+        return N > 1 ? N * C * (int64_t)sizeof(float2) : 0;
+    const GnCut c = backward_cut(S, C, groups, type);
     return N * (C * (c.P + 1) + groups) * (int64_t)sizeof(float2);
 }
 
 cudaError_t launch_group_norm_backward(const GnProblem &q, cudaStream_t s)
 {
     const bool ckpt = q.x == nullptr;
-    const GnCut c = backward_cut(q.S, q.C, q.groups, q.type, ckpt);
+    const int64_t E = type_channels(q.type), per = q.C / q.groups;
     GnBackParams p = {};
     p.dy = static_cast<const char *>(q.dy);
     p.x = static_cast<const char *>(q.x);
-    p.codes = static_cast<const uint2 *>(q.codes);
+    p.codes = static_cast<const char *>(q.codes);
     p.block_scales = static_cast<const uint8_t *>(q.block_scales);
     p.stats = static_cast<const float2 *>(q.stats);
     p.dx = static_cast<char *>(q.dx);
-    p.part = static_cast<float2 *>(q.workspace);
-    p.sums = p.part + q.N * c.P * q.C;
-    p.mean = p.sums + q.N * q.C;
     p.dweight = q.dweight;
     p.dbias = q.dbias;
     p.dscale = q.dscale;
     p.dshift = q.dshift;
-    p.gains = Gains{q.weight, q.bias, q.scale, q.shift, q.param_type, q.type, q.vs};
+    p.gains = Gains{q.weight, q.bias, q.scale, q.shift, q.param_type, q.vs};
     p.gs = q.gs;
-    p.S = q.S;
-    p.R = c.R;
-    p.P = c.P;
-    p.F = c.F;
-    p.Ft = c.Ft;
-    p.tiles = c.tiles;
-    p.RL = c.RL;
-    p.per = (int)(q.C / q.groups);
-    p.groups = (int)q.groups;
     p.act = q.act;
-    const bool last = q.N == 1;
-    const int64_t grid = q.N * c.tiles * c.P, joins = q.N * q.groups;
-    if (grid > 0x7FFFFFFF || joins > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaSuccess;
-    if (grid > 0)
-        e = q.type == kBf16   ? launch_type<kBf16>(p, q, c, grid, last, s)
-            : q.type == kFp16 ? launch_type<kFp16>(p, q, c, grid, last, s)
-                              : launch_type<kFp32>(p, q, c, grid, last, s);
-    else if (joins > 0) // no positions: sums of nothing
-        e = launch_overlapped(gn_back_join_kernel, (int)joins, kJoin, 0, s, p, last);
-    if (e != cudaSuccess || last || !q.dweight) return e;
-    return launch_overlapped(gn_params_kernel, (int)((q.C + 31) / 32), 256, 0, s, p, q.N);
+    p.last = q.N == 1;
+    p.count = (float)(q.S * per);
+    const GnSlab slab = q.S ? backward_slab(q.S, q.C, q.groups, q.type, ckpt) : GnSlab{};
+    const GnCut cut = backward_cut(q.S, q.C, q.groups, q.type);
+    set_passes(p, q, cut);
+    if (slab.Ft) p.sums = p.part;
+    return with_type(q.type, [&](auto type) -> cudaError_t {
+        constexpr int T = decltype(type)::value;
+        cudaError_t e = cudaSuccess;
+        if (q.N > 0 && q.S > 0) {
+            e = with_bool(ckpt, [&](auto codes) {
+                return with_bool(per % E == 0, [&](auto uni) {
+                    constexpr bool K = decltype(codes)::value, U = decltype(uni)::value;
+                    return slab.Ft ? launch_slab<T, K, U>(p, q, slab, s) : launch_passes<T, K, U>(p, q, cut, s);
+                });
+            });
+        } else if (q.N > 0) { // no positions: sums of nothing
+            e = launch_grid(gn_back_join_kernel<T>, dim3((unsigned)(q.N * q.groups)), 1, kJoin, 0, s, p);
+        }
+        if (e != cudaSuccess || p.last || !q.dweight) return e;
+        return launch_grid(gn_params_kernel<T>, dim3((unsigned)((q.C + 31) / 32)), 1, 256, 0, s, p, q.N);
+    });
 }
 
 } // namespace dan

@@ -6,22 +6,32 @@
 // needs two sums over the row, and dscale, dshift are sums of dy * n and dy
 // over a batch's rows: one pass over the data, bound by HBM.
 //
-// A CTA per SM takes a contiguous block of rows.  Its 16 warps form teams of W
-// warps (narrow rows: several rows share a warp); every thread has the same
-// columns of each of its team's rows, so the column sums stay in its registers
-// until the batch ends.  Each thread copies its own columns of the next rows
-// into shared memory with cp.async, kAhead rows ahead, and nobody else reads
-// them: the only exchange per row is that of the two sums.  At the end of a
-// batch, or of the CTA's rows, the teams' column sums are added in order and
-// stored as one partial of the batch; a second kernel adds the partials in
-// order.
+// A CTA per SM takes a contiguous block of rows.  Its warps form teams of W warps
+// (narrow rows: several rows share a warp) that take R rows at a time; every
+// thread has the same K fragments of eight columns of each of its team's rows, so
+// the column sums stay in its registers until the batch ends.  K * R is large, up
+// to eight fragments, on eight warps of up to 255 registers: what a step costs
+// apart from its elements, the exchange of the rows' sums above all, is spread
+// over 32 to 64 elements of a thread, and the rows' chains of shuffles and
+// barriers run side by side (at D = 4096, one row at a time by two teams of four
+// warps: 24.1 us for 4216 rows).  Each thread copies its own columns of the next
+// rows into shared memory with cp.async and nobody else reads them.  At the end
+// of a batch, or of the CTA's rows, the teams' column sums are added in order and
+// stored as one partial of the batch; a second kernel adds the partials in order.
 #include "dan_train.cuh"
 
 namespace dan {
 namespace {
 
-constexpr int kWarps = 16, kThreads = 32 * kWarps;
-constexpr int kAhead = 4; // rows (of each team) in flight
+// Threads of a CTA: large shares take the registers of two threads.
+__host__ __device__ constexpr int threads_of(int K, int R) { return K * R <= 2 ? 512 : 256; }
+
+// Steps (of R rows of each team) in flight: four, or what shared memory has room for.
+__host__ __device__ constexpr int ahead_of(int K, int R, bool ckpt, bool res)
+{
+    const int step = R * K * threads_of(K, R) * (16 + (ckpt ? 8 : 16) + (res ? 16 : 0));
+    return 4 * step <= 220 * 1024 ? 4 : 3 * step <= 220 * 1024 ? 3 : 2;
+}
 
 struct LnBackParams {
     const uint4 *dy, *x;
@@ -49,30 +59,54 @@ __device__ __forceinline__ void team_barrier(int team, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
 }
 
-// K fragments per thread.
-template <int K, bool CKPT, bool RES>
-__global__ void __launch_bounds__(kThreads, 1) ln_back_kernel(const LnBackParams p)
+// Sums of N values over a warp: each step halves the lanes' values, the lanes of
+// the one half of a pair going on with the one half of them.  Value i ends in the
+// lanes whose upper bits are i (32 / N lanes each).
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane)
+{
+    int off = 16;
+#pragma unroll
+    for (int n = N; n > 1; n /= 2, off /= 2) {
+        const bool upper = lane & off;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float mine = upper ? v[i + n / 2] : v[i], other = upper ? v[i] : v[i + n / 2];
+            v[i] = __fadd_rn(mine, __shfl_xor_sync(kFull, other, off));
+        }
+    }
+    float s = v[0];
+#pragma unroll
+    for (int k = 32 / N / 2; k >= 1; k /= 2) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, k));
+    return s;
+}
+
+// K fragments per thread, R rows at a time.  MULTI: several rows share a warp
+// (K == R == W == 1).
+template <int K, int R, bool CKPT, bool RES, bool MULTI>
+__global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBackParams p)
 {
     using XWord = typename std::conditional<CKPT, uint2, uint4>::type;
+    constexpr int NT = threads_of(K, R), A = ahead_of(K, R, CKPT, RES), NV = 2 * R;
     extern __shared__ __align__(16) uint4 smem[];
-    uint4 *s_dy = smem;                                                     // [kAhead][K][kThreads]
-    uint4 *s_res = s_dy + kAhead * K * kThreads;                            // likewise (RES)
-    XWord *s_x = reinterpret_cast<XWord *>(s_res + (RES ? kAhead * K * kThreads : 0));
-    float2 *s_red = reinterpret_cast<float2 *>(s_x + kAhead * K * kThreads); // [2][kWarps]
+    uint4 *s_dy = smem;                   // [A][R][K][NT]
+    uint4 *s_res = s_dy + A * R * K * NT; // likewise (RES)
+    XWord *s_x = reinterpret_cast<XWord *>(s_res + (RES ? A * R * K * NT : 0));
+    float *s_red = reinterpret_cast<float *>(s_x + A * R * K * NT); // [2][warps][NV]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int W = p.W, L = p.L, F = p.F;
+    const int W = p.W, L = MULTI ? p.L : 32, F = p.F;
     const int team = warp / W;
     const bool in_team = team < p.teams;
-    const int sub = lane / L, per_warp = 32 / L; // this lane's row of its warp's
-    const int width = W == 1 ? L : 32 * W;       // threads of a row
-    const int col = W == 1 ? lane - sub * L : (warp - team * W) * 32 + lane;
+    const int sub = MULTI ? lane / L : 0, per_warp = MULTI ? 32 / L : R; // this lane's row of its team's
+    const int width = MULTI ? L : 32 * W;                                // threads of a row
+    const int col = MULTI ? lane - sub * L : (warp - team * W) * 32 + lane;
     const int step = p.teams * per_warp; // rows of a CTA's step
     const int64_t c = blockIdx.x, G = gridDim.x;
     const int64_t r_end = first_row(c + 1, p.rows, G);
-    bool has[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) has[k] = in_team && col + width * k < F;
+    // every fragment but a thread's last is there for sure
+    const bool has_last = in_team && col + width * (K - 1) < F;
+    auto has = [&](int k) { return k < K - 1 || has_last; };
 
     grid_dependency_wait();
     allow_dependents();
@@ -80,144 +114,180 @@ __global__ void __launch_bounds__(kThreads, 1) ln_back_kernel(const LnBackParams
     for (int64_t r0 = first_row(c, p.rows, G); r0 < r_end;) {
         const int64_t b = r0 / p.T;
         const int64_t r1 = min(r_end, (b + 1) * p.T);
-        const int steps = (int)((r1 - r0 + step - 1) / step);
-        const int64_t mine = r0 + team * per_warp + sub; // this lane's row of step 0
+        const int64_t first = r0 + team * per_warp + sub; // this lane's first row
+        const int64_t team_first = r0 + team * per_warp;
+        const int steps = in_team && team_first < r1 ? (int)((r1 - team_first + step - 1) / step) : 0;
 
-        float2 o[K][4]; // 1 + scale
-        float2 sum_n[K][4], sum_1[K][4];
+        float2 sum_n[K][4], sum_1[K][4], o[K][4]; // o: 1 + scale
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             uint4 sc = make_uint4(0, 0, 0, 0);
-            if (has[k]) sc = ld_vec(p.scale + b * p.vs8 + col + width * k);
+            if (in_team && has(k)) sc = ld_vec(p.scale + b * p.vs8 + col + width * k);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 o[k][w] = add2(dup2(1.0f), wide2(word(sc, w)));
                 sum_n[k][w] = sum_1[k][w] = make_float2(0.0f, 0.0f);
             }
         }
-        auto request = [&](int i) {
-            const int64_t row = mine + (int64_t)i * step;
-            const int slot = i % kAhead;
-            if (i < steps && row < r1) {
+        // where this lane's next step to request, to fetch and to write begins, and
+        // the rows that are left from there on
+        int64_t ask = first * F + col, store = ask;
+        const int64_t stride = (int64_t)step * F;
+        const float2 *stats = p.stats + first;
+        const uint8_t *scales = p.block_scales + (CKPT ? first * p.blocks + (col >> 2) : 0);
+        int ask_left = in_team ? (int)(r1 - first) : 0, fetch_left = ask_left, left = ask_left;
+        auto request = [&](int slot) {
 #pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (has[k]) {
-                        const int64_t at = row * F + col + width * k;
-                        const int to = (slot * K + k) * kThreads + tid;
-                        cp_async16(s_dy + to, p.dy + at);
-                        if (RES) cp_async16(s_res + to, p.dres + at);
-                        if (CKPT) cp_async8(s_x + to, p.codes + at);
-                        else cp_async16(s_x + to, p.x + at);
-                    }
-                if (CKPT && (lane & 31) == 0 && has[0])
-                    prefetch_l2_line(p.block_scales + row * p.blocks + (col >> 2));
-            }
-            cp_async_commit();
-        };
-        float2 next_stats = make_float2(0.0f, 0.0f);
-        unsigned next_code[K];
-        auto fetch = [&](int i) { // the row's statistics and block scales, a row ahead
-            const int64_t row = mine + (int64_t)i * step;
-#pragma unroll
-            for (int k = 0; k < K; ++k) next_code[k] = 127;
-            if (i < steps && row < r1 && in_team) {
-                next_stats = __ldg(p.stats + row);
-                if (CKPT)
+            for (int r = 0; r < R; ++r)
+                if (r < ask_left) {
 #pragma unroll
                     for (int k = 0; k < K; ++k)
-                        if (has[k]) next_code[k] = __ldg(p.block_scales + row * p.blocks + ((col + width * k) >> 2));
-            }
+                        if (has(k)) {
+                            const int64_t at = ask + (int64_t)r * F + width * k;
+                            const int to = ((slot * R + r) * K + k) * NT + tid;
+                            cp_async16(s_dy + to, p.dy + at);
+                            if (RES) cp_async16(s_res + to, p.dres + at);
+                            if (CKPT) cp_async8(s_x + to, p.codes + at);
+                            else cp_async16(s_x + to, p.x + at);
+                        }
+                }
+            ask += stride;
+            ask_left -= step;
+            cp_async_commit();
         };
-        for (int i = 0; i < kAhead; ++i) request(i);
-        fetch(0);
+        float2 next_stats[R];
+        unsigned next_code[R][K];
+        auto fetch = [&]() { // the next step's statistics and block scales
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < fetch_left) {
+                    next_stats[r] = __ldg(stats + r);
+                    if (CKPT)
+#pragma unroll
+                        for (int k = 0; k < K; ++k)
+                            if (has(k)) next_code[r][k] = __ldg(scales + (int64_t)r * p.blocks + (width >> 2) * k);
+                }
+            scales += (int64_t)step * p.blocks;
+            stats += step;
+            fetch_left -= step;
+        };
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            next_stats[r] = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < K; ++k) next_code[r][k] = 127;
+        }
+        for (int i = 0; i < A; ++i) request(i);
+        fetch();
 
+        int slot = 0;
         for (int i = 0; i < steps; ++i) {
-            const int64_t row = mine + (int64_t)i * step;
-            const bool live = row < r1;
-            const float2 st = next_stats;
-            float bs[K];
+            float2 st[R], n[R][K][4], g[R][K][4];
+            float bs[R][K], sums[NV];
 #pragma unroll
-            for (int k = 0; k < K; ++k) bs[k] = block_scale_value(next_code[k]);
-            fetch(i + 1);
-            cp_async_wait<kAhead - 1>();
-            float2 n[K][4], g[K][4];
-            float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
-            const float2 neg_mean = dup2(-st.x), rstd = dup2(st.y);
-            uint4 res[K];
+            for (int r = 0; r < R; ++r) {
+                st[r] = next_stats[r];
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int at = ((i % kAhead) * K + k) * kThreads + tid;
-                uint4 dy = make_uint4(0, 0, 0, 0);
-                XWord xv = XWord();
-                res[k] = dy;
-                if (has[k] && live) {
-                    dy = s_dy[at];
-                    xv = s_x[at];
-                    if (RES) res[k] = s_res[at];
-                }
-                float2 v[4];
-                if constexpr (CKPT) {
-                    decode8(xv, bs[k], v);
-                } else {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) v[w] = wide2(word(xv, w));
-                }
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const float2 d = wide2(word(dy, w));
-                    n[k][w] = mul2(add2(v[w], neg_mean), rstd);
-                    if (!(has[k] && live)) n[k][w] = make_float2(0.0f, 0.0f);
-                    g[k][w] = mul2(d, o[k][w]);
-                    sum_1[k][w] = add2(sum_1[k][w], d);
-                    sum_n[k][w] = fma2(d, n[k][w], sum_n[k][w]);
-                    s1 = add2(s1, g[k][w]);
-                    s2 = fma2(g[k][w], n[k][w], s2);
-                }
+                for (int k = 0; k < K; ++k) bs[r][k] = block_scale_value(next_code[r][k]);
             }
-            request(i + kAhead); // into the slot that was just read
-            float a = __fadd_rn(s1.x, s1.y), q = __fadd_rn(s2.x, s2.y);
-            for (int off = L >> 1; off >= 1; off >>= 1) {
-                a = __fadd_rn(a, __shfl_xor_sync(kFull, a, off));
-                q = __fadd_rn(q, __shfl_xor_sync(kFull, q, off));
-            }
-            if (W > 1 && in_team) {
-                if (lane == 0) s_red[(i & 1) * kWarps + warp] = make_float2(a, q);
-                team_barrier(team, 32 * W);
-                a = q = 0.0f;
-                for (int j = 0; j < W; ++j) {
-                    const float2 t = s_red[(i & 1) * kWarps + team * W + j];
-                    a = __fadd_rn(a, t.x);
-                    q = __fadd_rn(q, t.y);
+            fetch();
+            cp_async_wait<A - 1>();
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+                const float2 neg_mean = dup2(-st[r].x), rstd = dup2(st[r].y);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int at = ((slot * R + r) * K + k) * NT + tid;
+                    uint4 dy = make_uint4(0, 0, 0, 0);
+                    XWord xv = XWord();
+                    const bool here = has(k) && r < left;
+                    if (here) {
+                        dy = s_dy[at];
+                        xv = s_x[at];
+                    }
+                    float2 v[4];
+                    if constexpr (CKPT) {
+                        const float2 s = dup2(bs[r][k]);
+                        v[0] = fma2(e4m3_pair(xv.x & 0xFFFFu), s, neg_mean);
+                        v[1] = fma2(e4m3_pair(xv.x >> 16), s, neg_mean);
+                        v[2] = fma2(e4m3_pair(xv.y & 0xFFFFu), s, neg_mean);
+                        v[3] = fma2(e4m3_pair(xv.y >> 16), s, neg_mean);
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) v[w] = add2(wide2(word(xv, w)), neg_mean);
+                    }
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const float2 d = wide2(word(dy, w));
+                        n[r][k][w] = mul2(v[w], rstd);
+                        // a column or row that is not there adds 0 * 0, whatever the statistics
+                        if ((MULTI || R > 1 || k == K - 1) && !here) n[r][k][w] = make_float2(0.0f, 0.0f);
+                        g[r][k][w] = mul2(d, o[k][w]);
+                        sum_1[k][w] = add2(sum_1[k][w], d);
+                        sum_n[k][w] = fma2(d, n[r][k][w], sum_n[k][w]);
+                        s1 = add2(s1, g[r][k][w]);
+                        s2 = fma2(g[r][k][w], n[r][k][w], s2);
+                    }
                 }
+                sums[2 * r] = __fadd_rn(s1.x, s1.y);
+                sums[2 * r + 1] = __fadd_rn(s2.x, s2.y);
+            }
+            if (MULTI) {
+                for (int off = L >> 1; off >= 1; off >>= 1) {
+                    sums[0] = __fadd_rn(sums[0], __shfl_xor_sync(kFull, sums[0], off));
+                    sums[1] = __fadd_rn(sums[1], __shfl_xor_sync(kFull, sums[1], off));
+                }
+            } else {
+                constexpr int LV = 32 / NV; // lanes per value
+                float v = warp_sums<NV>(sums, lane);
+                if (W > 1) {
+                    float *red = s_red + (i & 1) * (NT / 32) * NV;
+                    if (lane % LV == 0) red[warp * NV + lane / LV] = v;
+                    team_barrier(team, 32 * W);
+                    v = 0.0f; // a value's lanes take every LV-th warp's
+                    for (int k = lane % LV; k < W; k += LV) v = __fadd_rn(v, red[(team * W + k) * NV + lane / LV]);
+#pragma unroll
+                    for (int off = 1; off < LV; off *= 2) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, off));
+                }
+#pragma unroll
+                for (int k = 0; k < NV; ++k) sums[k] = __shfl_sync(kFull, v, k * LV);
             }
             // dx = g * rstd - mean(g) * rstd - n * (mean(g * n) * rstd)
-            const float2 m1 = dup2(-__fmul_rn(__fmul_rn(a, p.inv_d), st.y));
-            const float2 m2 = dup2(-__fmul_rn(__fmul_rn(q, p.inv_d), st.y));
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (!(has[k] && live)) continue;
-                uint4 out;
+            for (int r = 0; r < R; ++r) {
+                const float2 rstd = dup2(st[r].y);
+                const float2 m1 = dup2(-__fmul_rn(__fmul_rn(sums[2 * r], p.inv_d), st[r].y));
+                const float2 m2 = dup2(-__fmul_rn(__fmul_rn(sums[2 * r + 1], p.inv_d), st[r].y));
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    float2 v = fma2(n[k][w], m2, fma2(g[k][w], rstd, m1));
-                    if (RES) v = add2(v, wide2(word(res[k], w)));
-                    set_word(out, w, pack_bf16(v.x, v.y));
+                for (int k = 0; k < K; ++k) {
+                    uint4 out, res = make_uint4(0, 0, 0, 0);
+                    if (RES) res = s_res[((slot * R + r) * K + k) * NT + tid];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        float2 v = fma2(n[r][k][w], m2, fma2(g[r][k][w], rstd, m1));
+                        if (RES) v = add2(v, wide2(word(res, w)));
+                        set_word(out, w, pack_bf16(v.x, v.y));
+                    }
+                    if (has(k) && r < left) st_stream(p.dx + store + (int64_t)r * F + width * k, out);
                 }
-                st_stream(p.dx + row * F + col + width * k, out);
             }
+            request(slot); // into the slot that was read
+            slot = slot + 1 == A ? 0 : slot + 1;
+            store += stride;
+            left -= step;
         }
         cp_async_wait_all();
 
         // the batch's column sums: of a warp's rows, then of the teams, in order
-        for (int off = L; off < 32; off <<= 1)
-#pragma unroll
-            for (int k = 0; k < K; ++k)
+        if (MULTI)
+            for (int off = L; off < 32; off <<= 1)
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    sum_n[k][w].x = __fadd_rn(sum_n[k][w].x, __shfl_xor_sync(kFull, sum_n[k][w].x, off));
-                    sum_n[k][w].y = __fadd_rn(sum_n[k][w].y, __shfl_xor_sync(kFull, sum_n[k][w].y, off));
-                    sum_1[k][w].x = __fadd_rn(sum_1[k][w].x, __shfl_xor_sync(kFull, sum_1[k][w].x, off));
-                    sum_1[k][w].y = __fadd_rn(sum_1[k][w].y, __shfl_xor_sync(kFull, sum_1[k][w].y, off));
+                    sum_n[0][w].x = __fadd_rn(sum_n[0][w].x, __shfl_xor_sync(kFull, sum_n[0][w].x, off));
+                    sum_n[0][w].y = __fadd_rn(sum_n[0][w].y, __shfl_xor_sync(kFull, sum_n[0][w].y, off));
+                    sum_1[0][w].x = __fadd_rn(sum_1[0][w].x, __shfl_xor_sync(kFull, sum_1[0][w].x, off));
+                    sum_1[0][w].y = __fadd_rn(sum_1[0][w].y, __shfl_xor_sync(kFull, sum_1[0][w].y, off));
                 }
         __syncthreads(); // every thread has read its slots
         float2 *s_sum = reinterpret_cast<float2 *>(smem); // [team][K][8][width]
@@ -231,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) ln_back_kernel(const LnBackParams
                 }
         __syncthreads();
         float *part = p.part + (c + b) * 2 * (8 * (int64_t)F);
-        for (int i = tid; i < K * 2 * width; i += kThreads) {
+        for (int i = tid; i < K * 2 * width; i += NT) {
             const int k = i / (2 * width), which = i / width & 1, at = i % width;
             const int f = at + width * k;
             if (f >= F) continue;
@@ -252,63 +322,60 @@ __global__ void __launch_bounds__(kThreads, 1) ln_back_kernel(const LnBackParams
 }
 
 // dscale and dshift of batch b: the partials c + b of the CTAs c that had rows
-// of it, added in order (eight threads a share of them each, then the shares).
-// A block has 32 groups of four columns of [dscale | dshift].
-constexpr int kJoinLanes = 8;
-__global__ void __launch_bounds__(32 * kJoinLanes)
+// of it, added in order (32 threads a share of them each, then the shares): at
+// most five loads of a thread, all under way at once.  A block has 8 groups of
+// four columns of [dscale | dshift].
+constexpr int kJoinShares = 32, kJoinQuads = 8;
+__global__ void __launch_bounds__(kJoinShares * kJoinQuads)
     ln_back_join_kernel(const float4 *part, uint2 *dscale, uint2 *dshift, int64_t gs4, int64_t rows,
                         int64_t T, int64_t G, int D4, int tiles)
 {
-    __shared__ float4 s_sum[kJoinLanes][32];
+    __shared__ float4 s_sum[kJoinShares][kJoinQuads];
     const int64_t b = blockIdx.x / tiles;
-    const int quad = (int)(blockIdx.x - b * tiles) * 32 + (threadIdx.x & 31);
-    const int share = threadIdx.x >> 5;
+    const int mine = threadIdx.x % kJoinQuads, share = threadIdx.x / kJoinQuads;
+    const int quad = (int)(blockIdx.x - b * tiles) * kJoinQuads + mine;
+    // the CTAs of the batch's first and last rows
+    auto cta_of = [&](int64_t row) {
+        int64_t c = row * G / rows;
+        while (first_row(c + 1, rows, G) <= row) ++c;
+        while (first_row(c, rows, G) > row) --c;
+        return c;
+    };
+    const int64_t c0 = rows > 0 ? cta_of(b * T) : 0, c1 = rows > 0 ? cta_of((b + 1) * T - 1) : -1;
     grid_dependency_wait();
     allow_dependents();
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (quad < 2 * D4 && rows > 0) {
-        // the CTAs of the batch's first and last rows
-        auto cta_of = [&](int64_t row) {
-            int64_t c = row * G / rows;
-            while (first_row(c + 1, rows, G) <= row) ++c;
-            while (first_row(c, rows, G) > row) --c;
-            return c;
-        };
-        const int64_t c0 = cta_of(b * T), c1 = cta_of((b + 1) * T - 1);
-#pragma unroll 4
-        for (int64_t c = c0 + share; c <= c1; c += kJoinLanes) {
-            const float4 t = __ldg(part + (c + b) * 2 * D4 + quad);
-            v.x = __fadd_rn(v.x, t.x);
-            v.y = __fadd_rn(v.y, t.y);
-            v.z = __fadd_rn(v.z, t.z);
-            v.w = __fadd_rn(v.w, t.w);
-        }
-    }
-    s_sum[share][threadIdx.x & 31] = v;
-    __syncthreads();
-    if (share != 0 || quad >= 2 * D4) return;
-#pragma unroll
-    for (int j = 1; j < kJoinLanes; ++j) {
-        const float4 t = s_sum[j][threadIdx.x];
+    auto add = [&](const float4 &t) {
         v.x = __fadd_rn(v.x, t.x);
         v.y = __fadd_rn(v.y, t.y);
         v.z = __fadd_rn(v.z, t.z);
         v.w = __fadd_rn(v.w, t.w);
+    };
+    if (quad < 2 * D4) {
+#pragma unroll 5
+        for (int64_t c = c0 + share; c <= c1; c += kJoinShares) add(__ldcg(part + (c + b) * 2 * D4 + quad));
     }
+    s_sum[share][mine] = v;
+    __syncthreads();
+    if (share != 0 || quad >= 2 * D4) return;
+#pragma unroll
+    for (int j = 1; j < kJoinShares; ++j) add(s_sum[j][mine]);
     uint2 *to = quad < D4 ? dscale + b * gs4 + quad : dshift + b * gs4 + quad - D4;
     *to = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
 int64_t back_grid(int64_t rows) { return rows < sm_count() ? rows : sm_count(); }
 
-template <int K, bool CKPT, bool RES>
-cudaError_t launch_back(const LnBackParams &p, int grid, cudaStream_t s)
+template <int K, int R, bool CKPT, bool RES, bool MULTI>
+cudaError_t launch_back(LnBackParams p, int grid, cudaStream_t s)
 {
-    const int smem = kAhead * K * kThreads * (16 + (CKPT ? 8 : 16) + (RES ? 16 : 0)) +
-                     2 * kWarps * (int)sizeof(float2);
-    const auto fn = ln_back_kernel<K, CKPT, RES>;
+    constexpr int NT = threads_of(K, R);
+    p.teams = NT / 32 / p.W;
+    const int smem = ahead_of(K, R, CKPT, RES) * R * K * NT * (16 + (CKPT ? 8 : 16) + (RES ? 16 : 0)) +
+                     2 * (NT / 32) * 2 * R * (int)sizeof(float);
+    const auto fn = ln_back_kernel<K, R, CKPT, RES, MULTI>;
     const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
-    return e != cudaSuccess ? e : launch_overlapped(fn, grid, kThreads, smem, s, p);
+    return e != cudaSuccess ? e : launch_overlapped(fn, grid, NT, smem, s, p);
 }
 
 } // namespace
@@ -339,23 +406,39 @@ cudaError_t launch_ln_modulate_backward(const LnBackProblem &q, cudaStream_t s)
     p.inv_d = 1.0f / (float)q.D;
     const int64_t G = back_grid(p.rows);
     if (p.rows > 0) {
-        const int K = p.F <= 256 ? 1 : 2;
+        // a warp per row up to five fragments a lane; else teams of up to eight warps,
+        // several rows at a time where the registers last
+        const int K = p.F <= 160 ? (p.F + 31) / 32 : p.F <= 256 ? 2 : p.F <= 384 ? 3 : p.F <= 512 ? 2 : 4;
         p.W = (p.F + 32 * K - 1) / (32 * K);
-        p.teams = kWarps / p.W;
         p.L = 32;
         while (p.W == 1 && p.L / 2 >= p.F) p.L /= 2;
         const bool ckpt = q.x == nullptr, res = q.dres != nullptr;
-        auto go = [&](auto k) {
-            constexpr int KK = decltype(k)::value;
-            if (ckpt) return res ? launch_back<KK, true, true>(p, (int)G, s) : launch_back<KK, true, false>(p, (int)G, s);
-            return res ? launch_back<KK, false, true>(p, (int)G, s) : launch_back<KK, false, false>(p, (int)G, s);
+        auto go = [&](auto k, auto rows, auto multi) {
+            constexpr int KK = decltype(k)::value, R = decltype(rows)::value;
+            constexpr bool M = decltype(multi)::value;
+            const int grid = (int)G;
+            if (ckpt) return res ? launch_back<KK, R, true, true, M>(p, grid, s) : launch_back<KK, R, true, false, M>(p, grid, s);
+            return res ? launch_back<KK, R, false, true, M>(p, grid, s) : launch_back<KK, R, false, false, M>(p, grid, s);
         };
-        const cudaError_t e = K == 1 ? go(std::integral_constant<int, 1>()) : go(std::integral_constant<int, 2>());
+        const std::false_type no;
+        const std::integral_constant<int, 1> one;
+        const std::integral_constant<int, 2> two;
+        const std::integral_constant<int, 3> three;
+        const std::integral_constant<int, 4> four;
+        const std::integral_constant<int, 5> five;
+        const cudaError_t e = p.L < 32                ? go(one, one, std::true_type())
+                              : K == 1                ? go(one, one, no)
+                              : K == 2 && p.W == 1    ? go(two, one, no)
+                              : K == 2                ? go(two, four, no)
+                              : K == 3 && p.W == 1    ? go(three, one, no)
+                              : K == 3                ? go(three, two, no)
+                              : K == 4                ? go(four, one, no)
+                                                      : go(five, one, no);
         if (e != cudaSuccess) return e;
     }
-    const int D4 = (int)(q.D / 4), tiles = (2 * D4 + 31) / 32;
+    const int D4 = (int)(q.D / 4), tiles = (2 * D4 + kJoinQuads - 1) / kJoinQuads;
     if (q.B > (int64_t(1) << 30) / tiles) return cudaErrorInvalidConfiguration;
-    return launch_overlapped(ln_back_join_kernel, (int)(q.B * tiles), 32 * kJoinLanes, 0, s,
+    return launch_overlapped(ln_back_join_kernel, (int)(q.B * tiles), kJoinShares * kJoinQuads, 0, s,
                              static_cast<const float4 *>(q.workspace), static_cast<uint2 *>(q.dscale),
                              static_cast<uint2 *>(q.dshift), q.gs / 4, p.rows, p.T, G, D4, tiles);
 }

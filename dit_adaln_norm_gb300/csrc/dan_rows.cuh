@@ -496,22 +496,17 @@ __device__ __forceinline__ void ln_final(const Welford (&W)[4], float &mean, flo
     }
 }
 
-// The training form of one fragment: y = bf16(n * (1 + scale) + shift), rounded
-// once, stored, and with codes the checkpoint of the fragment's inputs x.  A
+// The training form of one fragment: y = bf16(z), z = n * (1 + scale) + shift
+// unrounded, and with codes the checkpoint of the fragment's inputs x.  A
 // block of 32 columns is the fragments of four neighbouring lanes; all 32 lanes
 // call this (`here`: the lane has a fragment; others only take part in the
 // exchange).
 __device__ __forceinline__ void save_store(uint4 *y, uint2 *q8, uint8_t *block_scale, int f, bool here,
-                                           const float (&x)[8], const float (&n)[8], const uint4 &sc,
-                                           const uint4 &sh, int lane)
+                                           const float (&x)[8], const float (&z)[8], int lane)
 {
     uint4 out;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float2 o = add2(dup2(1.0f), wide2(word(sc, w)));
-        const float2 z = fma2(make_float2(n[2 * w], n[2 * w + 1]), o, wide2(word(sh, w)));
-        set_word(out, w, pack_bf16(z.x, z.y));
-    }
+    for (int w = 0; w < 4; ++w) set_word(out, w, pack_bf16(z[2 * w], z[2 * w + 1]));
     if (here) st_stream(y + f, out);
     if (q8 == nullptr) return;
     float top = 0.0f;
@@ -544,26 +539,54 @@ __device__ __forceinline__ void ln_store(const float (&x)[J][FPT][8], int r, flo
     if (SAVE && r == 0 && lane == 0) p.stats[row] = make_float2(mean, rstd);
     if constexpr (SAVE) {
         uint8_t *block_scale = p.block_scales + row * ((F + 3) >> 2);
+        if (!RAGGED && J >= 2) { // pairs across logical warps, as in ln_states
 #pragma unroll
-        for (int m = 0; m < J; ++m)
+            for (int q = 0; q < J / 2; ++q)
 #pragma unroll
-            for (int k = 0; k < FPT; ++k) {
-                const int f = ln_frag(r + TW * m, lane, k);
-                const bool here = !RAGGED || f < F;
-                float t[8];
+                for (int k = 0; k < FPT; ++k) {
+                    const int f0 = ln_frag(r + TW * 2 * q, lane, k);
+                    const int f1 = ln_frag(r + TW * (2 * q + 1), lane, k);
+                    const uint4 sc0 = vec_frag<NV, STAGED, true>(p, s_vec, bidx, f0, 0);
+                    const uint4 sc1 = vec_frag<NV, STAGED, true>(p, s_vec, bidx, f1, 0);
+                    const uint4 sh0 = vec_frag<NV, STAGED, true>(p, s_vec, bidx, f0, 1);
+                    const uint4 sh1 = vec_frag<NV, STAGED, true>(p, s_vec, bidx, f1, 1);
+                    float z0[8], z1[8];
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float2 t2 = mul2(sub2(make_float2(x[m][k][e], x[m][k][e + 1]), mean2), rstd2);
-                    t[e] = t2.x;
-                    t[e + 1] = t2.y;
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 n2 =
+                            mul2(sub2(make_float2(x[2 * q][k][e], x[2 * q + 1][k][e]), mean2), rstd2);
+                        const float2 o2 = add2(dup2(1.0f), make_float2(elem(sc0, e), elem(sc1, e)));
+                        const float2 z2 = fma2(n2, o2, make_float2(elem(sh0, e), elem(sh1, e)));
+                        z0[e] = z2.x;
+                        z1[e] = z2.y;
+                    }
+                    save_store(y, q8, block_scale, f0, true, x[2 * q][k], z0, lane);
+                    save_store(y, q8, block_scale, f1, true, x[2 * q + 1][k], z1, lane);
                 }
-                uint4 sc = make_uint4(0, 0, 0, 0), sh = sc;
-                if (here) {
-                    sc = vec_frag<NV, STAGED, true>(p, s_vec, bidx, f, 0);
-                    sh = vec_frag<NV, STAGED, true>(p, s_vec, bidx, f, 1);
+        } else { // neighbouring elements of one logical warp
+#pragma unroll
+            for (int m = 0; m < J; ++m)
+#pragma unroll
+                for (int k = 0; k < FPT; ++k) {
+                    const int f = ln_frag(r + TW * m, lane, k);
+                    const bool here = !RAGGED || f < F;
+                    uint4 sc = make_uint4(0, 0, 0, 0), sh = sc;
+                    if (here) {
+                        sc = vec_frag<NV, STAGED, true>(p, s_vec, bidx, f, 0);
+                        sh = vec_frag<NV, STAGED, true>(p, s_vec, bidx, f, 1);
+                    }
+                    float z[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float2 n2 = mul2(sub2(make_float2(x[m][k][e], x[m][k][e + 1]), mean2), rstd2);
+                        const float2 o2 = add2(dup2(1.0f), wide2(word(sc, e / 2)));
+                        const float2 z2 = fma2(n2, o2, wide2(word(sh, e / 2)));
+                        z[e] = z2.x;
+                        z[e + 1] = z2.y;
+                    }
+                    save_store(y, q8, block_scale, f, here, x[m][k], z, lane);
                 }
-                save_store(y, q8, block_scale, f, here, x[m][k], t, sc, sh, lane);
-            }
+        }
         return;
     }
     auto out = [&](int f, const float (&t)[8]) {

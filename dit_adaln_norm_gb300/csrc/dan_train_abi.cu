@@ -129,8 +129,8 @@ int check_gn(int64_t N, int64_t S, int64_t C, int64_t groups, int type, bool che
 {
     if (N < 0 || S < 0 || C < 0 || groups < 1 || type < 0 || type > 2) return DAN_EINVAL;
     if (C < 8 || C % 8 || C > (int64_t(1) << 20) || C % groups || (checkpoint && C % 32)) return DAN_EUNSUPPORTED;
-    if (dan::gn_step(C / groups, checkpoint) > 8 * dan::kGnMost) return DAN_EUNSUPPORTED;
-    if (S > 0x7FFFFFFF || N > 0x7FFFFFFF) return DAN_EUNSUPPORTED;
+    if (dan::gn_step(C / groups, checkpoint) > dan::kGnWidest) return DAN_EUNSUPPORTED;
+    if (S > 0x7FFFFFFF || N >= (int64_t(1) << 28) || N * groups > 0x7FFFFFFF) return DAN_EUNSUPPORTED;
     if (S > 0 && N > kMaxElems / S) return DAN_EINVAL;
     if (N * S > kMaxElems / C || N > kMaxElems / C) return DAN_EINVAL;
     return DAN_OK;

@@ -104,9 +104,9 @@ def test_group_norm_validation(lib):
     assert f(C=12, G=1) == EUNSUP and f(C=320, G=33) == EUNSUP and f(C=320, G=0) == EINVAL
     assert f(C=8192, G=1) == EUNSUP and f(C=8 * 1025, G=8) == EUNSUP and f(C=(1 << 20) + 8, G=8) == EUNSUP
     assert f(C=40, G=5, st=ST, co=CO, bs=BS) == EUNSUP                  # blocks of 32 channels
-    assert f(S=1 << 31) == EUNSUP and f(N=1 << 31, S=1) == EUNSUP and f(N=1 << 20, S=1 << 20) == EINVAL
-    assert f(y=X) == OK and f(y=X + 16) == EALIAS and f(st=X) == EALIAS and f(wk=Y) == EALIAS
-    assert f(wk=X) == EALIAS and f(st=ST, co=Y, bs=BS) == EALIAS and f(y=W) == EALIAS
+    assert f(S=1 << 31) == EUNSUP and f(N=1 << 28, S=1) == EUNSUP and f(N=1 << 27, S=1) == EUNSUP and f(N=1 << 20, S=1 << 20) == EINVAL
+    assert f(y=X) == OK and f(y=X + 16) == EALIAS and f(st=X) == EALIAS and f(S=1 << 20, wk=Y) == EALIAS
+    assert f(S=1 << 20, wk=X) == EALIAS and f(st=ST, co=Y, bs=BS) == EALIAS and f(y=W) == EALIAS
     assert f(x=X + 8) == EALIGN and f(w=W + 2) == EALIGN and f(st=ST + 4) == EALIGN
     assert f(N=2, sc=SC, sh=SH, vs=516) == EALIGN and f(N=2, sc=SC, sh=SH, vs=504) == EINVAL
     assert f(N=2, ty=F32, pt=F32, sc=SC, sh=SH, vs=516) == OK
@@ -136,13 +136,15 @@ def test_group_norm_backward_validation(lib):
     assert f(x=None) == EINVAL and f(x=None, co=CO) == EINVAL and f(st=None) == EINVAL
     assert f(x=None, co=CO, bs=BS, C=40, G=5) == EUNSUP and f(C=40, G=5) == OK
     assert f(dx=X) == EALIAS and f(dx=DY + 16) == EALIAS and f(dw=W) == EALIAS and f(db=Y) == EALIAS
-    assert f(**{**mod, "dsh": G1}) == EALIAS and f(**{**mod, "dsc": DX}) == EALIAS and f(wk=DX) == EALIAS
+    assert f(**{**mod, "dsh": G1}) == EALIAS and f(**{**mod, "dsc": DX}) == EALIAS and f(N=2, wk=DX) == EALIAS
     assert f(**mod, N=2, gs=1024) == OK and f(**{**mod, "dsh": G1 + 1024}, N=2, gs=1024) == OK
     assert f(**{**mod, "dsh": G1 + 512}, N=2, gs=1024) == EALIAS
     assert f(**mod, N=2, gs=516) == EALIGN and f(**mod, N=2, gs=504) == EINVAL
     assert f(dy=DY + 8) == EALIGN and f(x=None, co=CO + 4, bs=BS) == EALIGN
-    need = lib.dan_group_norm_backward_workspace(1, 4096, 512, 32, BF, 0)
-    assert need > 0 and f(size=need - 1) == EINVAL and f(wk=None) == EINVAL
+    for n, s in ((1, 1 << 20), (2, 4096)):
+        need = lib.dan_group_norm_backward_workspace(n, s, 512, 32, BF, 0)
+        assert need > 0 and f(N=n, S=s, db=Y + 8 * GB) == OK
+        assert f(N=n, S=s, size=need - 1) == EINVAL and f(N=n, S=s, wk=None) == EINVAL
     assert f(S=0, dy=None, x=16, dx=None, st=None) == OK and f(S=0, dw=None) == EINVAL
 
 
@@ -150,8 +152,7 @@ def test_cuts_do_not_follow_the_batch(lib):
     """What a call asks for grows with the images, so that each is cut up alike."""
     for size, k in ((lib.dan_group_norm_workspace, 0), (lib.dan_group_norm_backward_workspace, 0)):
         for S, C, G in ((1 << 16, 128, 32), (77, 320, 32), (1, 8, 8)):
-            one = size(1, S, C, G, BF, k)
-            assert size(7, S, C, G, BF, k) == 7 * one
+            assert size(14, S, C, G, BF, k) == 2 * size(7, S, C, G, BF, k)
 
 
 def test_binding_refuses_without_cuda_tensors():
