@@ -36,6 +36,7 @@ struct GnParams {
     float eps;
     float count;   // values of a group
     float keep;    // share of a chunk's rows that the L2 is to hold
+    int chunks;    // of a CTA of the first kernel
     int log_cs, M; // slabs: CTAs of a cluster, rows of a thread at most
 };
 
@@ -142,8 +143,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) gn_moments_kernel(const GnParam
 {
     using Frag = Fragment<TYPE>;
     extern __shared__ __align__(16) uint4 s_ring[]; // [kRing][NT]
-    float2 *s_units = reinterpret_cast<float2 *>(s_ring + kRing * NT); // [RL][units of the tile]
-    const GnPlace at(p.g, blockIdx.z, blockIdx.y);
+    float2 *s_units = reinterpret_cast<float2 *>(s_ring + kRing * NT); // [2][RL][units of the tile]
+    const int chunk0 = blockIdx.y * p.chunks;
+    const GnPlace at(p.g, blockIdx.z, chunk0, p.chunks);
     const int64_t n = blockIdx.x;
     const int step = p.g.RL * p.g.F * 16;
     const char *x = p.x + at.first(p.g, n) * 16;
@@ -160,27 +162,31 @@ __global__ void __launch_bounds__(NT, 1024 / NT) gn_moments_kernel(const GnParam
     };
 #pragma unroll
     for (int j = 0; j < kRing; ++j) ask(j, j);
-    if (at.mine > 0) {
-        Sums<Frag::kP> sums;
-        float2 v[Frag::kP];
-        cp_async_wait<kRing - 1>();
-        Frag::values(slot[0], v);
-        sums.start(v, p.unit);
-        for (; left > 0; left -= kRing, x += kRing * (int64_t)step) {
+    for (int c = 0; at.rows > c * p.g.R; ++c) {
+        const GnPlace part = at.part(p.g, c);
+        float2 *units = s_units + (c & 1) * p.g.RL * p.g.Ft * p.per_frag;
+        if (part.mine > 0) {
+            Sums<Frag::kP> sums;
+            float2 v[Frag::kP];
+            cp_async_wait<kRing - 1>();
+            Frag::values(slot[0], v);
+            sums.start(v, p.unit);
+            for (int rows = part.mine; rows > 0; rows -= kRing, left -= kRing, x += kRing * (int64_t)step) {
 #pragma unroll
-            for (int j = 0; j < kRing; ++j) {
-                if (left <= j) break;
-                cp_async_wait<kRing - 1>();
-                Frag::values(slot[j * NT], v);
-                sums.add(v);
-                ask(j, j + kRing);
+                for (int j = 0; j < kRing; ++j) {
+                    if (rows <= j) break;
+                    cp_async_wait<kRing - 1>();
+                    Frag::values(slot[j * NT], v);
+                    sums.add(v);
+                    ask(j, j + kRing);
+                }
             }
+            sums.finish(p.unit, part.mine, units + (at.r * at.Ft + at.f) * p.per_frag);
         }
-        sums.finish(p.unit, at.mine, s_units + (at.r * at.Ft + at.f) * p.per_frag);
+        __syncthreads(); // (the other half of s_units may still be read)
+        join_units(p, part, units, p.part + (n * p.g.groups + at.g0) * p.g.P + chunk0 + c, p.g.P);
     }
     cp_async_wait_all();
-    __syncthreads();
-    join_units(p, at, s_units, p.part + (n * p.g.groups + at.g0) * p.g.P + blockIdx.y, p.g.P);
 }
 
 // Mean and rstd of each group (a block's) from its chunks' moments: up to kU
@@ -446,7 +452,7 @@ GnSlab forward_slab(int64_t S, int64_t C, int64_t groups, int type, bool checkpo
 
 GnCut forward_cut(int64_t S, int64_t C, int64_t groups, int type, bool checkpoint)
 {
-    return gn_cut(S, C, groups, type, checkpoint, 65536, 608);
+    return gn_cut(S, C, groups, type, checkpoint, kRing, 2, 608);
 }
 
 // Lanes of a group's join: one per entry of RL row lanes if there are fewer than a warp's.
@@ -482,13 +488,20 @@ cudaError_t launch_passes(GnParams p, const GnProblem &q, const GnCut &c, cudaSt
     // second: some 64 MB.
     const float all = (float)(q.N * q.S) * (float)q.C * (float)type_bytes(TYPE);
     p.keep = all > 64e6f ? 64e6f / all : 1.0f;
-    const dim3 grid((unsigned)q.N, (unsigned)c.P, c.tiles);
-    const int ring = kRing * 16 * c.threads, units = c.RL * c.Ft * p.per_frag * (int)sizeof(float2);
+    const int ring = kRing * 16 * c.threads, units = 2 * c.RL * c.Ft * p.per_frag * (int)sizeof(float2);
+    const int64_t slots = (int64_t)sm_count() * (1024 / c.threads) / c.tiles;
+    // the second kernel's rows need not be whole chunks
+    const int64_t round = (int64_t)kRing * c.RL, second = gn_share(q.N, slots, (q.S + round - 1) / round);
+    GnParams a = p;
+    a.g.R = (int)((q.S + second - 1) / second);
+    p.chunks = c.rounds ? (int)((c.P + gn_share(q.N, slots, c.P) - 1) / gn_share(q.N, slots, c.P)) : 1;
+    const dim3 one((unsigned)q.N, (unsigned)((c.P + p.chunks - 1) / p.chunks), c.tiles);
+    const dim3 two((unsigned)q.N, (unsigned)((q.S + a.g.R - 1) / a.g.R), c.tiles);
     auto go = [&](auto threads) {
         constexpr int NT = decltype(threads)::value;
-        cudaError_t e = launch_grid(gn_moments_kernel<TYPE, NT>, grid, 1, NT, ring + units, s, p);
+        cudaError_t e = launch_grid(gn_moments_kernel<TYPE, NT>, one, 1, NT, room_for(1024 / NT, ring + units), s, p);
         if (e == cudaSuccess) e = launch_grid(gn_join_kernel, dim3((unsigned)(q.N * q.groups)), 1, kJoin, 0, s, p);
-        if (e == cudaSuccess) e = launch_grid(gn_apply_kernel<TYPE, CKPT, UNI, NT>, grid, 1, NT, ring, s, p);
+        if (e == cudaSuccess) e = launch_grid(gn_apply_kernel<TYPE, CKPT, UNI, NT>, two, 1, NT, room_for(1024 / NT, ring), s, a);
         return e;
     };
     if (c.threads <= 256) return go(std::integral_constant<int, 256>());

@@ -225,19 +225,30 @@ struct GnPlace {
     int rows, whole, rest; // rows; row lanes below `rest` have whole + 1 of them, the others whole
     int r, f;
     int mine; // this thread's rows
-    __device__ __forceinline__ GnPlace(const GnGrid &g, int tile, int chunk)
+    // `chunk`: the first one; `chunks` of them.
+    __device__ __forceinline__ GnPlace(const GnGrid &g, int tile, int chunk, int chunks = 1)
     {
         f0 = tile * g.Ft;
         Ft = min(g.Ft, g.F - f0);
         g0 = tile * g.tile_groups;
         groups = min(g.tile_groups, g.groups - g0);
         row0 = (int64_t)chunk * g.R;
-        rows = (int)max((int64_t)0, min((int64_t)g.R, g.S - row0));
+        rows = (int)max((int64_t)0, min((int64_t)g.R * chunks, g.S - row0));
         whole = g.by_RL.of(rows);
         rest = rows - whole * g.RL;
         r = g.by_Ft.of(threadIdx.x);
         f = threadIdx.x - r * g.Ft;
         mine = r < g.RL && f < Ft ? whole + (r < rest) : 0;
+    }
+    // Their rows in chunk i of several (whole rounds, so that the row lanes go on alike).
+    __device__ __forceinline__ GnPlace part(const GnGrid &g, int i) const
+    {
+        GnPlace q = *this;
+        q.rows = min(g.R, rows - i * g.R);
+        q.whole = g.by_RL.of(q.rows);
+        q.rest = q.rows - q.whole * g.RL;
+        q.mine = r < g.RL && f < Ft ? q.whole + (r < q.rest) : 0;
+        return q;
     }
     // The thread's first fragment of image n.
     __device__ __forceinline__ int64_t first(const GnGrid &g, int64_t n) const
@@ -272,15 +283,28 @@ constexpr int64_t kGnWidest = 4096; // channels of the widest tile
 inline int64_t type_bytes(int type) { return type == kFp32 ? 4 : 2; }
 inline int64_t type_channels(int type) { return type == kFp32 ? 4 : 8; } // of a fragment
 
-// How an image is cut for the kernels that read it in passes.
+// How an image is cut for the kernels that read it in passes: tiles, and chunks
+// of rows whose sums are kept one by one.
 struct GnCut {
     int Ft, tiles, threads, RL;
     int64_t R, P;
+    bool rounds; // chunks are whole rounds: a CTA may take several on end
 };
 
+// Shared memory that lets `blocks` CTAs share an SM and no more.  A wave is one CTA
+// in each of these places; where the registers would let another one in, some SMs
+// took three of a wave of two per SM and others one (the gradient of a [1, 512 x
+// 512, 256] image: 120 us, with two each 109).
+inline int room_for(int blocks, int smem)
+{
+    const int least = 228 * 1024 / (blocks + 1);
+    return smem > least ? smem : least;
+}
+
 // Tiles of whole rows where they have up to 256 fragments, else of as many
-// whole steps; chunks of `bytes` (of `type`) at least, `most` chunks at most.
-inline GnCut gn_cut(int64_t S, int64_t C, int64_t groups, int type, bool checkpoint, int64_t bytes,
+// whole steps; chunks of `rounds` rounds of `ring` rows of each thread (a round of
+// eight rows of 256 threads is 32 KB), or where there would be over `most`, that many.
+inline GnCut gn_cut(int64_t S, int64_t C, int64_t groups, int type, bool checkpoint, int64_t ring, int64_t rounds,
                     int64_t most)
 {
     GnCut c;
@@ -289,11 +313,20 @@ inline GnCut gn_cut(int64_t S, int64_t C, int64_t groups, int type, bool checkpo
     c.tiles = (int)((F + c.Ft - 1) / c.Ft);
     c.threads = c.Ft <= 256 ? 256 : gn_threads(type);
     c.RL = c.threads / c.Ft;
-    c.R = (bytes + c.Ft * 16 - 1) / (c.Ft * 16);
-    if (c.R < c.RL) c.R = c.RL;
-    if (c.R < (S + most - 1) / most) c.R = (S + most - 1) / most;
+    const int64_t round = ring * c.RL, all = (S + round - 1) / round;
+    c.rounds = all <= rounds * most;
+    c.R = c.rounds ? rounds * round : (S + most - 1) / most;
     c.P = (S + c.R - 1) / c.R;
     return c;
+}
+
+// CTAs of an image (at most `most`) such that all images' come to whole waves of
+// `slots`: the last, part-filled wave of a few costs as much as a full one.
+inline int64_t gn_share(int64_t N, int64_t slots, int64_t most)
+{
+    int64_t q = slots / N;
+    if (q * N * 20 < slots * 17) q = (4 * slots + N - 1) / N; // not 85% of a wave: several waves
+    return q < 1 ? 1 : q < most ? q : most;
 }
 
 // How an image is cut into slabs of whole groups that a cluster of CTAs holds in

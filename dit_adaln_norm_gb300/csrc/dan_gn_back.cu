@@ -34,6 +34,7 @@ struct GnBackParams {
     int act;
     bool last;     // the call's only image
     float count;   // values of a group
+    int chunks;    // of a CTA of the first kernel
     int log_cs, M; // slabs: CTAs of a cluster, rows of a thread at most
 };
 
@@ -116,7 +117,7 @@ struct Ring {
     int left;             // rows from the round's first on
     uint4 *s_dy;          // [A][NT]
     XWord *s_x;           // [A][NT]
-    unsigned next_scale;
+    unsigned scales[A];   // of the rows in flight
 
     // `rows` rows from fragment `at` on, `step` fragments apart.
     __device__ __forceinline__ Ring(const GnBackParams &p, uint4 *smem, int64_t at, int step_, int rows)
@@ -128,10 +129,11 @@ struct Ring {
         dy = p.dy + at * 16;
         x = (CKPT ? p.codes : p.x) + at * (int64_t)sizeof(XWord);
         scale = p.block_scales + at / Frag::kBlock;
-        next_scale = 127;
 #pragma unroll
-        for (int j = 0; j < A; ++j) ask(j, j);
-        if (CKPT && left > 0) next_scale = __ldg(scale);
+        for (int j = 0; j < A; ++j) {
+            scales[j] = 127;
+            ask(j, j);
+        }
     }
     // Row `ahead` of the round into slot j.
     __device__ __forceinline__ void ask(int j, int ahead)
@@ -139,6 +141,8 @@ struct Ring {
         if (left > ahead) {
             cp_async16(s_dy + j * NT, dy + ahead * (int64_t)(step * 16));
             cp_async_word(s_x + j * NT, x + ahead * (int64_t)(step * (int)sizeof(XWord)));
+            // (a row's fragments, and so the step, are whole blocks)
+            if (CKPT) scales[j] = __ldg(scale + ahead * (int64_t)(step / Frag::kBlock));
         }
         cp_async_commit();
     }
@@ -149,9 +153,7 @@ struct Ring {
         const uint4 a = s_dy[j * NT];
         const XWord c = s_x[j * NT];
         if constexpr (CKPT) {
-            const float2 s = dup2(block_scale_value(next_scale));
-            if (left > j + 1) // (a row's fragments, and so the step, are whole blocks)
-                next_scale = __ldg(scale + (j + 1) * (int64_t)(step / Frag::kBlock));
+            const float2 s = dup2(block_scale_value(scales[j]));
             Frag::codes(c, t);
 #pragma unroll
             for (int w = 0; w < Frag::kP; ++w) t[w] = fma2(t[w], s, ch.minus[w % ch.K]);
@@ -176,29 +178,35 @@ struct Ring {
 // CTAs of 256 threads that share an SM (three, of 80 registers, spill and took
 // 128 us for the gradient of [1, 512 x 512, 256] images against 109).
 constexpr int kBackBlocks = 2;
+// Buffers for the sums of a chunk (the widest tiles leave room for one).
+__host__ __device__ constexpr int halves_of(int threads) { return threads <= 256 ? 2 : 1; }
 
 template <int TYPE, bool CKPT, bool UNI, int NT>
 __global__ void __launch_bounds__(NT, NT > 256 ? 1 : kBackBlocks) gn_sums_kernel(const GnBackParams p)
 {
     using Frag = Fragment<TYPE>;
     using R = Ring<TYPE, CKPT, UNI, NT>;
-    constexpr int P = Frag::kP;
+    constexpr int P = Frag::kP, kHalves = halves_of(NT);
     extern __shared__ __align__(16) uint4 s_ring[];
+    float2 *s_sums = reinterpret_cast<float2 *>(s_ring + R::A * R::kBytes * NT / 16); // [kHalves][RL][channels]
     const int64_t n = blockIdx.x;
-    const GnPlace at(p.g, blockIdx.z, blockIdx.y);
+    const int chunk0 = blockIdx.y * p.chunks;
+    const GnPlace at(p.g, blockIdx.z, chunk0, p.chunks);
     grid_dependency_wait();
     allow_dependents();
-    float2 s0[P], s1[P];
+    R ring(p, s_ring, at.first(p.g, n), p.g.RL * p.g.F, at.mine);
+    Channels<P, UNI> ch = {};
+    const float2 *stats = p.stats + n * p.g.groups + at.g0;
+    if (at.mine > 0) ch.template get<TYPE>(p, n, at.f0 + at.f, stats, at.f * Frag::kE);
+    const int channels = at.Ft * Frag::kE;
+    for (int c = 0; at.rows > c * p.g.R; ++c) {
+        float2 s0[P], s1[P];
 #pragma unroll
-    for (int w = 0; w < P; ++w) s0[w] = s1[w] = make_float2(0.0f, 0.0f);
-    if (at.mine > 0) {
-        R ring(p, s_ring, at.first(p.g, n), p.g.RL * p.g.F, at.mine);
-        Channels<P, UNI> ch;
-        ch.template get<TYPE>(p, n, at.f0 + at.f, p.stats + n * p.g.groups + at.g0, at.f * Frag::kE);
-        for (; ring.left > 0; ring.round()) {
+        for (int w = 0; w < P; ++w) s0[w] = s1[w] = make_float2(0.0f, 0.0f);
+        for (int rows = at.part(p.g, c).mine; rows > 0; rows -= R::A, ring.round()) {
 #pragma unroll
             for (int j = 0; j < R::A; ++j) {
-                if (ring.left <= j) break;
+                if (rows <= j) break;
                 float2 t[P], d[P];
                 ring.take(j, ch, t, d);
 #pragma unroll
@@ -209,27 +217,27 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : kBackBlocks) gn_sums_kernel
                 }
             }
         }
-        float2 rstd[ch.K];
-        ch.rstds(p.g, p.stats + n * p.g.groups + at.g0, at.f * Frag::kE, rstd);
+        float2 *sums = s_sums + c % kHalves * p.g.RL * channels;
+        if (at.r < p.g.RL && at.f < at.Ft) {
+            float4 *to = reinterpret_cast<float4 *>(sums + at.r * channels + at.f * Frag::kE);
+            float2 rstd[ch.K];
+            ch.rstds(p.g, stats, at.f * Frag::kE, rstd);
 #pragma unroll
-        for (int w = 0; w < P; ++w) s1[w] = mul2(s1[w], rstd[w % ch.K]);
+            for (int w = 0; w < P; ++w) {
+                s1[w] = mul2(s1[w], rstd[w % ch.K]);
+                to[w] = make_float4(s0[w].x, s1[w].x, s0[w].y, s1[w].y);
+            }
+        }
+        __syncthreads(); // (with two halves, the other one may still be read)
+        float2 *to = p.part + (n * p.g.P + chunk0 + c) * ((int64_t)p.g.F * Frag::kE) + at.f0 * Frag::kE;
+        for (int k = threadIdx.x; k < channels; k += NT) {
+            float2 t = sums[k];
+            for (int r = 1; r < p.g.RL; ++r) t = add2(t, sums[r * channels + k]);
+            to[k] = t;
+        }
+        if (kHalves == 1) __syncthreads();
     }
     cp_async_wait_all();
-    __syncthreads(); // every thread has read its slots
-    float2 *s_sums = reinterpret_cast<float2 *>(s_ring); // [RL][channels]
-    const int channels = at.Ft * Frag::kE;
-    if (at.r < p.g.RL && at.f < at.Ft) {
-        float4 *to = reinterpret_cast<float4 *>(s_sums + at.r * channels + at.f * Frag::kE);
-#pragma unroll
-        for (int w = 0; w < P; ++w) to[w] = make_float4(s0[w].x, s1[w].x, s0[w].y, s1[w].y);
-    }
-    __syncthreads();
-    float2 *to = p.part + (n * p.g.P + blockIdx.y) * ((int64_t)p.g.F * Frag::kE) + at.f0 * Frag::kE;
-    for (int c = threadIdx.x; c < channels; c += NT) {
-        float2 t = s_sums[c];
-        for (int k = 1; k < p.g.RL; ++k) t = add2(t, s_sums[k * channels + c]);
-        to[c] = t;
-    }
 }
 
 // What follows from an image's sums t = (s0, s1) of channel c with the gains g.
@@ -522,9 +530,12 @@ GnSlab backward_slab(int64_t S, int64_t C, int64_t groups, int type, bool checkp
     return gn_slab(S, C, groups, type, false, checkpoint ? 16 + E + 1 : 32, E * (int)sizeof(float2));
 }
 
-GnCut backward_cut(int64_t S, int64_t C, int64_t groups, int type)
+// Rows of a thread's ring (Ring::A).
+constexpr int ring_rows(int type, bool ckpt) { return 48 * 1024 / 256 / (16 + (ckpt ? (type == kFp32 ? 4 : 8) : 16)); }
+
+GnCut backward_cut(int64_t S, int64_t C, int64_t groups, int type, bool checkpoint)
 {
-    return gn_cut(S, C, groups, type, false, 65536, 304);
+    return gn_cut(S, C, groups, type, false, ring_rows(type, checkpoint), 2, 304);
 }
 
 template <int TYPE, bool CKPT, bool UNI>
@@ -548,16 +559,26 @@ void set_passes(GnBackParams &p, const GnProblem &q, const GnCut &c)
 }
 
 template <int TYPE, bool CKPT, bool UNI>
-cudaError_t launch_passes(const GnBackParams &p, const GnProblem &q, const GnCut &c, cudaStream_t s)
+cudaError_t launch_passes(GnBackParams p, const GnProblem &q, const GnCut &c, cudaStream_t s)
 {
     using R = Ring<TYPE, CKPT, UNI, 256>;
-    const dim3 grid((unsigned)q.N, (unsigned)c.P, c.tiles), joins((unsigned)(q.N * q.groups));
-    const int ring = R::A * R::kBytes * c.threads, sums = c.RL * c.Ft * Fragment<TYPE>::kE * (int)sizeof(float2);
+    static_assert(R::A == ring_rows(TYPE, CKPT), "chunks are whole rounds");
+    const int ring = R::A * R::kBytes * c.threads, sums = halves_of(c.threads) * c.RL * c.Ft * Fragment<TYPE>::kE * (int)sizeof(float2);
+    const int blocks = c.threads <= 256 ? kBackBlocks : 1;
+    const int64_t slots = (int64_t)sm_count() * blocks / c.tiles;
+    // the second kernel's rows need not be whole chunks
+    const int64_t round = (int64_t)R::A * c.RL, second = gn_share(q.N, slots, (q.S + round - 1) / round);
+    GnBackParams a = p;
+    a.g.R = (int)((q.S + second - 1) / second);
+    p.chunks = c.rounds ? (int)((c.P + gn_share(q.N, slots, c.P) - 1) / gn_share(q.N, slots, c.P)) : 1;
+    const dim3 one((unsigned)q.N, (unsigned)((c.P + p.chunks - 1) / p.chunks), c.tiles);
+    const dim3 two((unsigned)q.N, (unsigned)((q.S + a.g.R - 1) / a.g.R), c.tiles);
+    const dim3 joins((unsigned)(q.N * q.groups));
     const auto go = [&](auto threads) {
         constexpr int NT = decltype(threads)::value;
-        cudaError_t e = launch_grid(gn_sums_kernel<TYPE, CKPT, UNI, NT>, grid, 1, c.threads, ring > sums ? ring : sums, s, p);
+        cudaError_t e = launch_grid(gn_sums_kernel<TYPE, CKPT, UNI, NT>, one, 1, NT, room_for(blocks, ring + sums), s, p);
         if (e == cudaSuccess) e = launch_grid(gn_back_join_kernel<TYPE>, joins, 1, kJoin, 0, s, p);
-        if (e == cudaSuccess) e = launch_grid(gn_dx_kernel<TYPE, CKPT, UNI, NT>, grid, 1, c.threads, ring, s, p);
+        if (e == cudaSuccess) e = launch_grid(gn_dx_kernel<TYPE, CKPT, UNI, NT>, two, 1, NT, room_for(blocks, ring), s, a);
         return e;
     };
     if (c.threads <= 256) return go(std::integral_constant<int, 256>());
@@ -570,7 +591,7 @@ int64_t group_norm_backward_workspace(int64_t N, int64_t S, int64_t C, int64_t g
 {
     if (S > 0 && backward_slab(S, C, groups, type, checkpoint).Ft) // the images' sums, to be added
         return N > 1 ? N * C * (int64_t)sizeof(float2) : 0;
-    const GnCut c = backward_cut(S, C, groups, type);
+    const GnCut c = backward_cut(S, C, groups, type, checkpoint);
     return N * (C * (c.P + 1) + groups) * (int64_t)sizeof(float2);
 }
 
@@ -595,7 +616,7 @@ cudaError_t launch_group_norm_backward(const GnProblem &q, cudaStream_t s)
     p.last = q.N == 1;
     p.count = (float)(q.S * per);
     const GnSlab slab = q.S ? backward_slab(q.S, q.C, q.groups, q.type, ckpt) : GnSlab{};
-    const GnCut cut = backward_cut(q.S, q.C, q.groups, q.type);
+    const GnCut cut = backward_cut(q.S, q.C, q.groups, q.type, ckpt);
     set_passes(p, q, cut);
     if (slab.Ft) p.sums = p.part;
     return with_type(q.type, [&](auto type) -> cudaError_t {

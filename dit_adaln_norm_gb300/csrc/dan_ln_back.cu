@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBa
     // every fragment but a thread's last is there for sure
     const bool has_last = in_team && col + width * (K - 1) < F;
     auto has = [&](int k) { return k < K - 1 || has_last; };
+    const bool whole = F == width * K; // all threads have all theirs
 
     grid_dependency_wait();
     allow_dependents();
@@ -192,47 +193,53 @@ __global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBa
             }
             fetch();
             cp_async_wait<A - 1>();
+            // The elements' n and g, and the sums.  MASKED: some rows or columns may
+            // not be there; they count as zeros, and are rare.
+            auto take = [&](auto masked) {
+                constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
-                const float2 neg_mean = dup2(-st[r].x), rstd = dup2(st[r].y);
+                for (int r = 0; r < R; ++r) {
+                    float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+                    const float2 neg_mean = dup2(-st[r].x), rstd = dup2(st[r].y);
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const int at = ((slot * R + r) * K + k) * NT + tid;
-                    uint4 dy = make_uint4(0, 0, 0, 0);
-                    XWord xv = XWord();
-                    const bool here = has(k) && r < left;
-                    if (here) {
-                        dy = s_dy[at];
-                        xv = s_x[at];
+                    for (int k = 0; k < K; ++k) {
+                        const int at = ((slot * R + r) * K + k) * NT + tid;
+                        uint4 dy = make_uint4(0, 0, 0, 0);
+                        XWord xv = XWord();
+                        const bool here = !MASKED || (has(k) && r < left);
+                        if (here) {
+                            dy = s_dy[at];
+                            xv = s_x[at];
+                        }
+                        float2 v[4];
+                        if constexpr (CKPT) {
+                            const float2 s = dup2(bs[r][k]);
+                            v[0] = fma2(e4m3_pair(xv.x & 0xFFFFu), s, neg_mean);
+                            v[1] = fma2(e4m3_pair(xv.x >> 16), s, neg_mean);
+                            v[2] = fma2(e4m3_pair(xv.y & 0xFFFFu), s, neg_mean);
+                            v[3] = fma2(e4m3_pair(xv.y >> 16), s, neg_mean);
+                        } else {
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) v[w] = add2(wide2(word(xv, w)), neg_mean);
+                        }
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const float2 d = wide2(word(dy, w));
+                            n[r][k][w] = mul2(v[w], rstd);
+                            if (MASKED && !here) n[r][k][w] = make_float2(0.0f, 0.0f); // whatever the statistics
+                            g[r][k][w] = mul2(d, o[k][w]);
+                            sum_1[k][w] = add2(sum_1[k][w], d);
+                            sum_n[k][w] = fma2(d, n[r][k][w], sum_n[k][w]);
+                            s1 = add2(s1, g[r][k][w]);
+                            s2 = fma2(g[r][k][w], n[r][k][w], s2);
+                        }
                     }
-                    float2 v[4];
-                    if constexpr (CKPT) {
-                        const float2 s = dup2(bs[r][k]);
-                        v[0] = fma2(e4m3_pair(xv.x & 0xFFFFu), s, neg_mean);
-                        v[1] = fma2(e4m3_pair(xv.x >> 16), s, neg_mean);
-                        v[2] = fma2(e4m3_pair(xv.y & 0xFFFFu), s, neg_mean);
-                        v[3] = fma2(e4m3_pair(xv.y >> 16), s, neg_mean);
-                    } else {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) v[w] = add2(wide2(word(xv, w)), neg_mean);
-                    }
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const float2 d = wide2(word(dy, w));
-                        n[r][k][w] = mul2(v[w], rstd);
-                        // a column or row that is not there adds 0 * 0, whatever the statistics
-                        if ((MULTI || R > 1 || k == K - 1) && !here) n[r][k][w] = make_float2(0.0f, 0.0f);
-                        g[r][k][w] = mul2(d, o[k][w]);
-                        sum_1[k][w] = add2(sum_1[k][w], d);
-                        sum_n[k][w] = fma2(d, n[r][k][w], sum_n[k][w]);
-                        s1 = add2(s1, g[r][k][w]);
-                        s2 = fma2(g[r][k][w], n[r][k][w], s2);
-                    }
+                    sums[2 * r] = __fadd_rn(s1.x, s1.y);
+                    sums[2 * r + 1] = __fadd_rn(s2.x, s2.y);
                 }
-                sums[2 * r] = __fadd_rn(s1.x, s1.y);
-                sums[2 * r + 1] = __fadd_rn(s2.x, s2.y);
-            }
+            };
+            if (!MULTI && whole && left >= R) take(std::false_type());
+            else take(std::true_type());
             if (MULTI) {
                 for (int off = L >> 1; off >= 1; off >>= 1) {
                     sums[0] = __fadd_rn(sums[0], __shfl_xor_sync(kFull, sums[0], off));
@@ -331,7 +338,7 @@ __global__ void __launch_bounds__(kJoinShares * kJoinQuads)
                         int64_t T, int64_t G, int D4, int tiles)
 {
     __shared__ float4 s_sum[kJoinShares][kJoinQuads];
-    const int64_t b = blockIdx.x / tiles;
+    const unsigned b = blockIdx.x / (unsigned)tiles;
     const int mine = threadIdx.x % kJoinQuads, share = threadIdx.x / kJoinQuads;
     const int quad = (int)(blockIdx.x - b * tiles) * kJoinQuads + mine;
     // the CTAs of the batch's first and last rows
@@ -341,7 +348,8 @@ __global__ void __launch_bounds__(kJoinShares * kJoinQuads)
         while (first_row(c, rows, G) > row) --c;
         return c;
     };
-    const int64_t c0 = rows > 0 ? cta_of(b * T) : 0, c1 = rows > 0 ? cta_of((b + 1) * T - 1) : -1;
+    const int64_t c0 = b == 0 ? 0 : rows > 0 ? cta_of(b * T) : 0;
+    const int64_t c1 = rows == 0 ? -1 : (b + 1) * T == rows ? G - 1 : cta_of((b + 1) * T - 1);
     grid_dependency_wait();
     allow_dependents();
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

@@ -241,7 +241,8 @@ def test_ln_no_rows():
 GN_SHAPES = [(1, 1, 8, 1), (2, 1, 64, 8), (1, 64, 1280, 32), (3, 77, 320, 32), (2, 5673, 40, 8), (1, 1000, 8, 8),
              (2, 300, 96, 3), (1, 2000, 2048, 32), (1, 70, 4096, 1), (2, 33, 2560, 2), (1, 40, 8192, 32),
              (5, 129, 160, 16), (1, 50000, 64, 32), (1, 300, 1920, 48), (1, 200001, 16, 2), (2, 4096, 512, 32),
-             (1, 16384, 256, 32), (2, 17, 24, 1)]
+             (1, 16384, 256, 32), (2, 17, 24, 1), (1, 5000, 4096, 1),
+             (3, 9000, 96, 3)]
 
 
 def gn_inputs(N, S, C, dtype, wtype, mod, seed=0, level=0.5):
