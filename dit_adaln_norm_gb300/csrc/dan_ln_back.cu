@@ -103,21 +103,78 @@ __global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBa
     const int col = MULTI ? lane - sub * L : (warp - team * W) * 32 + lane;
     const int step = p.teams * per_warp; // rows of a CTA's step
     const int64_t c = blockIdx.x, G = gridDim.x;
-    const int64_t r_end = first_row(c + 1, p.rows, G);
+    const int64_t r_begin = first_row(c, p.rows, G), r_end = first_row(c + 1, p.rows, G);
     // every fragment but a thread's last is there for sure
     const bool has_last = in_team && col + width * (K - 1) < F;
     auto has = [&](int k) { return k < K - 1 || has_last; };
     const bool whole = F == width * K; // all threads have all theirs
 
+    // the CTA's first rows, hinted into the L2 before the dependency wait
+    // (prefetch_l2: it returns nothing), those of two steps; a warp a row
+    for (int64_t row = r_begin + warp; row < min(r_end, r_begin + 2 * step); row += NT / 32) {
+        if (lane == 0) prefetch_l2(p.dy + row * F, F * 16);
+        if (RES && lane == 1) prefetch_l2(p.dres + row * F, F * 16);
+        if (!CKPT && lane == 2) prefetch_l2(p.x + row * F, F * 16);
+        if (CKPT && lane == 2 && F % 2 == 0) prefetch_l2(p.codes + row * F, F * 8);
+        if (CKPT && lane == 3) prefetch_l2_line(p.block_scales + row * p.blocks);
+        if (lane == 4) prefetch_l2_line(p.stats + row);
+    }
     grid_dependency_wait();
     allow_dependents();
 
-    for (int64_t r0 = first_row(c, p.rows, G); r0 < r_end;) {
+    for (int64_t r0 = r_begin; r0 < r_end;) {
         const int64_t b = r0 / p.T;
         const int64_t r1 = min(r_end, (b + 1) * p.T);
         const int64_t first = r0 + team * per_warp + sub; // this lane's first row
         const int64_t team_first = r0 + team * per_warp;
         const int steps = in_team && team_first < r1 ? (int)((r1 - team_first + step - 1) / step) : 0;
+
+        // this lane's rows: those of a step begin at `row`, with `left` from there on
+        // (what is requested or fetched ahead follows from the two)
+        int64_t row = first;
+        int left = in_team ? (int)(r1 - first) : 0;
+        auto request = [&](int ahead, int slot) { // of the step `ahead` of this one
+            const int64_t at0 = (row + ahead * step) * F + col;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < left - ahead * step) {
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        if (has(k)) {
+                            const int64_t at = at0 + (int64_t)r * F + width * k;
+                            const int to = ((slot * R + r) * K + k) * NT + tid;
+                            cp_async16(s_dy + to, p.dy + at);
+                            if (RES) cp_async16(s_res + to, p.dres + at);
+                            if (CKPT) cp_async8(s_x + to, p.codes + at);
+                            else cp_async16(s_x + to, p.x + at);
+                        }
+                }
+            cp_async_commit();
+        };
+        float2 next_stats[R];
+        unsigned next_code[R][K];
+        auto fetch = [&](int ahead) { // its statistics and block scales
+            const int64_t next = row + ahead * step;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < left - ahead * step) {
+                    next_stats[r] = __ldg(p.stats + next + r);
+                    if (CKPT) {
+                        const uint8_t *scales = p.block_scales + (next + r) * p.blocks + (col >> 2);
+#pragma unroll
+                        for (int k = 0; k < K; ++k)
+                            if (has(k)) next_code[r][k] = __ldg(scales + (width >> 2) * k);
+                    }
+                }
+        };
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            next_stats[r] = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < K; ++k) next_code[r][k] = 127;
+        }
+        for (int i = 0; i < A; ++i) request(i, i);
+        fetch(0);
 
         float2 sum_n[K][4], sum_1[K][4], o[K][4]; // o: 1 + scale
 #pragma unroll
@@ -130,57 +187,6 @@ __global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBa
                 sum_n[k][w] = sum_1[k][w] = make_float2(0.0f, 0.0f);
             }
         }
-        // where this lane's next step to request, to fetch and to write begins, and
-        // the rows that are left from there on
-        int64_t ask = first * F + col, store = ask;
-        const int64_t stride = (int64_t)step * F;
-        const float2 *stats = p.stats + first;
-        const uint8_t *scales = p.block_scales + (CKPT ? first * p.blocks + (col >> 2) : 0);
-        int ask_left = in_team ? (int)(r1 - first) : 0, fetch_left = ask_left, left = ask_left;
-        auto request = [&](int slot) {
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r < ask_left) {
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        if (has(k)) {
-                            const int64_t at = ask + (int64_t)r * F + width * k;
-                            const int to = ((slot * R + r) * K + k) * NT + tid;
-                            cp_async16(s_dy + to, p.dy + at);
-                            if (RES) cp_async16(s_res + to, p.dres + at);
-                            if (CKPT) cp_async8(s_x + to, p.codes + at);
-                            else cp_async16(s_x + to, p.x + at);
-                        }
-                }
-            ask += stride;
-            ask_left -= step;
-            cp_async_commit();
-        };
-        float2 next_stats[R];
-        unsigned next_code[R][K];
-        auto fetch = [&]() { // the next step's statistics and block scales
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r < fetch_left) {
-                    next_stats[r] = __ldg(stats + r);
-                    if (CKPT)
-#pragma unroll
-                        for (int k = 0; k < K; ++k)
-                            if (has(k)) next_code[r][k] = __ldg(scales + (int64_t)r * p.blocks + (width >> 2) * k);
-                }
-            scales += (int64_t)step * p.blocks;
-            stats += step;
-            fetch_left -= step;
-        };
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            next_stats[r] = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < K; ++k) next_code[r][k] = 127;
-        }
-        for (int i = 0; i < A; ++i) request(i);
-        fetch();
-
         int slot = 0;
         for (int i = 0; i < steps; ++i) {
             float2 st[R], n[R][K][4], g[R][K][4];
@@ -191,8 +197,10 @@ __global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBa
 #pragma unroll
                 for (int k = 0; k < K; ++k) bs[r][k] = block_scale_value(next_code[r][k]);
             }
-            fetch();
+            fetch(1);
             cp_async_wait<A - 1>();
+            // one row at a time, a step's row is there
+            auto live = [&](int r) { return (!MULTI && R == 1) || r < left; };
             // The elements' n and g, and the sums.  MASKED: some rows or columns may
             // not be there; they count as zeros, and are rare.
             auto take = [&](auto masked) {
@@ -206,7 +214,7 @@ __global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBa
                         const int at = ((slot * R + r) * K + k) * NT + tid;
                         uint4 dy = make_uint4(0, 0, 0, 0);
                         XWord xv = XWord();
-                        const bool here = !MASKED || (has(k) && r < left);
+                        const bool here = !MASKED || (has(k) && live(r));
                         if (here) {
                             dy = s_dy[at];
                             xv = s_x[at];
@@ -276,12 +284,12 @@ __global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBa
                         if (RES) v = add2(v, wide2(word(res, w)));
                         set_word(out, w, pack_bf16(v.x, v.y));
                     }
-                    if (has(k) && r < left) st_stream(p.dx + store + (int64_t)r * F + width * k, out);
+                    if (has(k) && live(r)) st_stream(p.dx + (row + r) * F + col + width * k, out);
                 }
             }
-            request(slot); // into the slot that was read
+            request(A, slot); // into the slot that was read
             slot = slot + 1 == A ? 0 : slot + 1;
-            store += stride;
+            row += step;
             left -= step;
         }
         cp_async_wait_all();
@@ -329,17 +337,17 @@ __global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBa
 }
 
 // dscale and dshift of batch b: the partials c + b of the CTAs c that had rows
-// of it, added in order (32 threads a share of them each, then the shares): at
-// most five loads of a thread, all under way at once.  A block has 8 groups of
-// four columns of [dscale | dshift].
-constexpr int kJoinShares = 32, kJoinQuads = 8;
-__global__ void __launch_bounds__(kJoinShares * kJoinQuads)
+// of it, added in order: 64 threads a share of them each (at most three, all
+// under way at once), then the shares of a warp, then the warps'.  A block has 4
+// groups of four columns of [dscale | dshift].
+constexpr int kJoinThreads = 256, kJoinQuads = 4, kJoinShares = kJoinThreads / kJoinQuads;
+__global__ void __launch_bounds__(kJoinThreads)
     ln_back_join_kernel(const float4 *part, uint2 *dscale, uint2 *dshift, int64_t gs4, int64_t rows,
                         int64_t T, int64_t G, int D4, int tiles)
 {
-    __shared__ float4 s_sum[kJoinShares][kJoinQuads];
+    __shared__ float4 s_sum[kJoinThreads / 32][kJoinQuads];
     const unsigned b = blockIdx.x / (unsigned)tiles;
-    const int mine = threadIdx.x % kJoinQuads, share = threadIdx.x / kJoinQuads;
+    const int tid = threadIdx.x, mine = tid % kJoinQuads, share = tid / kJoinQuads;
     const int quad = (int)(blockIdx.x - b * tiles) * kJoinQuads + mine;
     // the CTAs of the batch's first and last rows
     auto cta_of = [&](int64_t row) {
@@ -360,14 +368,19 @@ __global__ void __launch_bounds__(kJoinShares * kJoinQuads)
         v.w = __fadd_rn(v.w, t.w);
     };
     if (quad < 2 * D4) {
-#pragma unroll 5
-        for (int64_t c = c0 + share; c <= c1; c += kJoinShares) add(__ldcg(part + (c + b) * 2 * D4 + quad));
+        const float4 *from = part + b * (int64_t)(2 * D4) + quad;
+#pragma unroll 3
+        for (int64_t c = c0 + share; c <= c1; c += kJoinShares) add(__ldcg(from + c * 2 * D4));
     }
-    s_sum[share][mine] = v;
-    __syncthreads();
-    if (share != 0 || quad >= 2 * D4) return;
 #pragma unroll
-    for (int j = 1; j < kJoinShares; ++j) add(s_sum[j][mine]);
+    for (int off = kJoinQuads; off < 32; off *= 2)
+        add(make_float4(__shfl_xor_sync(kFull, v.x, off), __shfl_xor_sync(kFull, v.y, off),
+                        __shfl_xor_sync(kFull, v.z, off), __shfl_xor_sync(kFull, v.w, off)));
+    if ((tid & 31) < kJoinQuads) s_sum[tid >> 5][mine] = v;
+    __syncthreads();
+    if (tid >= kJoinQuads || quad >= 2 * D4) return;
+#pragma unroll
+    for (int j = 1; j < kJoinThreads / 32; ++j) add(s_sum[j][mine]);
     uint2 *to = quad < D4 ? dscale + b * gs4 + quad : dshift + b * gs4 + quad - D4;
     *to = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
@@ -446,7 +459,7 @@ cudaError_t launch_ln_modulate_backward(const LnBackProblem &q, cudaStream_t s)
     }
     const int D4 = (int)(q.D / 4), tiles = (2 * D4 + kJoinQuads - 1) / kJoinQuads;
     if (q.B > (int64_t(1) << 30) / tiles) return cudaErrorInvalidConfiguration;
-    return launch_overlapped(ln_back_join_kernel, (int)(q.B * tiles), kJoinShares * kJoinQuads, 0, s,
+    return launch_overlapped(ln_back_join_kernel, (int)(q.B * tiles), kJoinThreads, 0, s,
                              static_cast<const float4 *>(q.workspace), static_cast<uint2 *>(q.dscale),
                              static_cast<uint2 *>(q.dshift), q.gs / 4, p.rows, p.T, G, D4, tiles);
 }
