@@ -1097,11 +1097,15 @@ cudaError_t launch_rms_shapes(const RowProblem &q, cudaStream_t s, unsigned *cta
 // GB300s); for the FP8 producer two CTAs of six per SM on contiguous blocks
 // (10.82 against 11.10 us at [1,4216,4096], 9.20 against 9.27 at
 // [1,4096,3072]; interleaved rows measured 0.1 to 0.25 us slower on one GB300
-// and as much faster on another).  With fewer rows: eight two-warp teams.
+// and as much faster on another); for the training form, whose checkpoint doubles
+// a row's instructions, eight two-warp teams (16.6 us at [1,4216,4096]; twelve
+// single-warp teams 18.6, four-warp teams 17.4 to 17.7, two CTAs of six 18.3).
+// With fewer rows: eight two-warp teams.
 template <int KIND, int FPT, bool RAGGED>
 cudaError_t launch_ln_many(const RowProblem &q, cudaStream_t s)
 {
     if constexpr (KIND == kLnFp8) return launch_ring<KIND, 4, FPT, 6, 1, 1, RAGGED, false, 0, 0, 2>(q, s);
+    else if constexpr (KIND == kLnSave) return launch_ring<KIND, 4, FPT, 16, 2, 1, RAGGED, false, 0, 0, 1, true>(q, s);
     else return launch_ring<KIND, 4, FPT, 12, 1, 1, RAGGED, false, 0, 0, 1, true>(q, s);
 }
 
