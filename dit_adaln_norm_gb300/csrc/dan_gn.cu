@@ -473,6 +473,8 @@ cudaError_t launch_slab(GnParams p, const GnProblem &q, const GnSlab &c, cudaStr
     p.log_cs = c.log_cs;
     p.M = c.M;
     p.stats = static_cast<float2 *>(q.stats);
+    const cudaError_t e = ready(gn_slab_kernel<TYPE, CKPT, UNI>, c.smem);
+    if (e != cudaSuccess) return e;
     return launch_grid(gn_slab_kernel<TYPE, CKPT, UNI>, dim3((unsigned)(q.N << c.log_cs), c.slabs), 1 << c.log_cs,
                        c.threads, c.smem, s, p);
 }
@@ -499,9 +501,15 @@ cudaError_t launch_passes(GnParams p, const GnProblem &q, const GnCut &c, cudaSt
     const dim3 two((unsigned)q.N, (unsigned)((q.S + a.g.R - 1) / a.g.R), c.tiles);
     auto go = [&](auto threads) {
         constexpr int NT = decltype(threads)::value;
-        cudaError_t e = launch_grid(gn_moments_kernel<TYPE, NT>, one, 1, NT, room_for(1024 / NT, ring + units), s, p);
+        const auto moments = gn_moments_kernel<TYPE, NT>;
+        const auto apply = gn_apply_kernel<TYPE, CKPT, UNI, NT>;
+        const int smem1 = room_for(1024 / NT, ring + units), smem2 = room_for(1024 / NT, ring);
+        cudaError_t e = ready(moments, smem1);
+        if (e == cudaSuccess) e = ready(gn_join_kernel, 0);
+        if (e == cudaSuccess) e = ready(apply, smem2);
+        if (e == cudaSuccess) e = launch_grid(moments, one, 1, NT, smem1, s, p);
         if (e == cudaSuccess) e = launch_grid(gn_join_kernel, dim3((unsigned)(q.N * q.groups)), 1, kJoin, 0, s, p);
-        if (e == cudaSuccess) e = launch_grid(gn_apply_kernel<TYPE, CKPT, UNI, NT>, two, 1, NT, room_for(1024 / NT, ring), s, a);
+        if (e == cudaSuccess) e = launch_grid(apply, two, 1, NT, smem2, s, a);
         return e;
     };
     if (c.threads <= 256) return go(std::integral_constant<int, 256>());

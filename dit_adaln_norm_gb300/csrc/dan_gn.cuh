@@ -401,13 +401,19 @@ inline GnGrid gn_grid(int64_t S, int64_t C, int64_t groups, int type, int64_t Ft
     return g;
 }
 
+// What a kernel's launch may fail on beforehand: a call makes sure of all its
+// kernels before it launches the first.
+template <typename... KArgs>
+cudaError_t ready(void (*fn)(KArgs...), int smem)
+{
+    return allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
+}
+
 // A launch with programmatic stream serialization on a grid of three dimensions,
-// in clusters of `cs` CTAs along x.
+// in clusters of `cs` CTAs along x (of a kernel that is ready).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_grid(void (*fn)(KArgs...), dim3 grid, int cs, int block, int smem, cudaStream_t s, Args... args)
 {
-    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)block);

@@ -545,6 +545,8 @@ cudaError_t launch_slab(GnBackParams p, const GnProblem &q, const GnSlab &c, cud
     p.log_cs = c.log_cs;
     p.M = c.M;
     p.sums = static_cast<float2 *>(q.workspace);
+    const cudaError_t e = ready(gn_back_slab_kernel<TYPE, CKPT, UNI>, c.smem);
+    if (e != cudaSuccess) return e;
     return launch_grid(gn_back_slab_kernel<TYPE, CKPT, UNI>, dim3((unsigned)(q.N << c.log_cs), c.slabs), 1 << c.log_cs,
                        c.threads, c.smem, s, p);
 }
@@ -576,9 +578,14 @@ cudaError_t launch_passes(GnBackParams p, const GnProblem &q, const GnCut &c, cu
     const dim3 joins((unsigned)(q.N * q.groups));
     const auto go = [&](auto threads) {
         constexpr int NT = decltype(threads)::value;
-        cudaError_t e = launch_grid(gn_sums_kernel<TYPE, CKPT, UNI, NT>, one, 1, NT, room_for(blocks, ring + sums), s, p);
+        const auto first = gn_sums_kernel<TYPE, CKPT, UNI, NT>, last = gn_dx_kernel<TYPE, CKPT, UNI, NT>;
+        const int smem1 = room_for(blocks, ring + sums), smem2 = room_for(blocks, ring);
+        cudaError_t e = ready(first, smem1);
+        if (e == cudaSuccess) e = ready(gn_back_join_kernel<TYPE>, 0);
+        if (e == cudaSuccess) e = ready(last, smem2);
+        if (e == cudaSuccess) e = launch_grid(first, one, 1, NT, smem1, s, p);
         if (e == cudaSuccess) e = launch_grid(gn_back_join_kernel<TYPE>, joins, 1, kJoin, 0, s, p);
-        if (e == cudaSuccess) e = launch_grid(gn_dx_kernel<TYPE, CKPT, UNI, NT>, two, 1, NT, room_for(blocks, ring), s, a);
+        if (e == cudaSuccess) e = launch_grid(last, two, 1, NT, smem2, s, a);
         return e;
     };
     if (c.threads <= 256) return go(std::integral_constant<int, 256>());
@@ -621,7 +628,9 @@ cudaError_t launch_group_norm_backward(const GnProblem &q, cudaStream_t s)
     if (slab.Ft) p.sums = p.part;
     return with_type(q.type, [&](auto type) -> cudaError_t {
         constexpr int T = decltype(type)::value;
-        cudaError_t e = cudaSuccess;
+        const bool params = !p.last && q.dweight;
+        cudaError_t e = params ? ready(gn_params_kernel<T>, 0) : cudaSuccess;
+        if (e != cudaSuccess) return e;
         if (q.N > 0 && q.S > 0) {
             e = with_bool(ckpt, [&](auto codes) {
                 return with_bool(per % E == 0, [&](auto uni) {
@@ -630,9 +639,10 @@ cudaError_t launch_group_norm_backward(const GnProblem &q, cudaStream_t s)
                 });
             });
         } else if (q.N > 0) { // no positions: sums of nothing
-            e = launch_grid(gn_back_join_kernel<T>, dim3((unsigned)(q.N * q.groups)), 1, kJoin, 0, s, p);
+            e = ready(gn_back_join_kernel<T>, 0);
+            if (e == cudaSuccess) e = launch_grid(gn_back_join_kernel<T>, dim3((unsigned)(q.N * q.groups)), 1, kJoin, 0, s, p);
         }
-        if (e != cudaSuccess || p.last || !q.dweight) return e;
+        if (e != cudaSuccess || !params) return e;
         return launch_grid(gn_params_kernel<T>, dim3((unsigned)((q.C + 31) / 32)), 1, 256, 0, s, p, q.N);
     });
 }

@@ -387,6 +387,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 int64_t back_grid(int64_t rows) { return rows < sm_count() ? rows : sm_count(); }
 
+cudaError_t ready_join() { return allow_dynamic_smem(reinterpret_cast<const void *>(ln_back_join_kernel), 0); }
+
 template <int K, int R, bool CKPT, bool RES, bool MULTI>
 cudaError_t launch_back(LnBackParams p, int grid, cudaStream_t s)
 {
@@ -395,7 +397,8 @@ cudaError_t launch_back(LnBackParams p, int grid, cudaStream_t s)
     const int smem = ahead_of(K, R, CKPT, RES) * R * K * NT * (16 + (CKPT ? 8 : 16) + (RES ? 16 : 0)) +
                      2 * (NT / 32) * 2 * R * (int)sizeof(float);
     const auto fn = ln_back_kernel<K, R, CKPT, RES, MULTI>;
-    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
+    if (e == cudaSuccess) e = ready_join(); // before the first launch
     return e != cudaSuccess ? e : launch_overlapped(fn, grid, NT, smem, s, p);
 }
 
@@ -426,6 +429,7 @@ cudaError_t launch_ln_modulate_backward(const LnBackProblem &q, cudaStream_t s)
     p.blocks = (int)((q.D + 31) / 32);
     p.inv_d = 1.0f / (float)q.D;
     const int64_t G = back_grid(p.rows);
+    const int D4 = (int)(q.D / 4), tiles = (2 * D4 + kJoinQuads - 1) / kJoinQuads;
     if (p.rows > 0) {
         // a warp per row up to five fragments a lane; else teams of up to eight warps,
         // several rows at a time where the registers last
@@ -457,8 +461,10 @@ cudaError_t launch_ln_modulate_backward(const LnBackProblem &q, cudaStream_t s)
                                                       : go(five, one, no);
         if (e != cudaSuccess) return e;
     }
-    const int D4 = (int)(q.D / 4), tiles = (2 * D4 + kJoinQuads - 1) / kJoinQuads;
-    if (q.B > (int64_t(1) << 30) / tiles) return cudaErrorInvalidConfiguration;
+    if (p.rows == 0) {
+        const cudaError_t e = ready_join();
+        if (e != cudaSuccess) return e;
+    }
     return launch_overlapped(ln_back_join_kernel, (int)(q.B * tiles), kJoinThreads, 0, s,
                              static_cast<const float4 *>(q.workspace), static_cast<uint2 *>(q.dscale),
                              static_cast<uint2 *>(q.dshift), q.gs / 4, p.rows, p.T, G, D4, tiles);

@@ -95,6 +95,7 @@ int validate_ln_back(const dan_bf16 *dy, const dan_bf16 *x, const uint8_t *codes
 {
     const int st = check_ln(B, T, D);
     if (st != DAN_OK || B == 0) return st;
+    if (B > (int64_t(1) << 30) / D) return DAN_EUNSUPPORTED; // blocks of the join
     const int64_t vec = strided(B, D, vs), grad = strided(B, D, gs);
     if (vec < 0 || grad < 0) return DAN_EINVAL;
     if (vs % 8 || gs % 8) return DAN_EALIGN;

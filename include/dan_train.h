@@ -17,12 +17,15 @@
  *    and each result is rounded once, to its own type.  A call's bits are the
  *    same every time (no atomics).  y, dx, the statistics, the checkpoints,
  *    and a group norm's dscale and dshift are batch invariant: a row's or
- *    image's bits do not depend on the others in the call.  dweight and dbias,
- *    and a LayerNorm's dscale and dshift, are sums over rows in an order that
- *    follows from the sizes and the GPU's SM count.
- *  - A call is one to four launches.
+ *    image's bits do not depend on the others in the call (a group norm's
+ *    follow from S, C, the groups, the type, and whether there is a checkpoint).
+ *    dweight and dbias, and a LayerNorm's dscale and dshift, are sums over rows
+ *    in an order that follows from the sizes and the GPU's SM count.
+ *  - A call is one to four launches; one that cannot run whole launches none.
  *  - Not a number and infinities pass as the formulas have them: a row or group
- *    that holds one gives NaN, others are not touched.
+ *    that holds one gives NaN, others are not touched.  Squares of differences
+ *    are summed in fp32: a row or group whose sum leaves its range (differences
+ *    of some 1e18 and more) is not normalised.
  *
  * Checkpoint of values v [rows, C] (C a multiple of 8): blocks of 32
  * neighbouring channels (the last one of a row may be shorter) share a power of
@@ -68,7 +71,7 @@ int dan_can_use_ln_modulate_save(const dan_bf16 *x, const dan_bf16 *scale, const
  * [B, D] with batch stride grad_bstride (>= D, a multiple of 8), e.g. their
  * slices of the embedding's gradient.  dres [B, T, D] (or NULL): a gradient
  * that reaches x by another way, added before the rounding.  In place: dx == dy
- * or dx == dres.  T == 0 writes zeros to dscale and dshift.
+ * or dx == dres.  T == 0 writes zeros to dscale and dshift.  B * D <= 2^30.
  * workspace: dan_ln_modulate_backward_workspace(B, T, D) bytes, of the current
  * device, 16-byte aligned, this call's alone until it has completed: two calls
  * that may run at the same time, or two captured graphs that may, need one

@@ -77,6 +77,7 @@ def test_ln_backward_validation(lib):
     need = lib.dan_ln_modulate_backward_workspace(1, 4216, 4096)
     assert need > 0 and f(size=need - 1) == EINVAL and f(wk=None) == EINVAL
     assert f(D=12) == EUNSUP and f(D=8200) == EUNSUP and f(T=-1, size=0) == EINVAL
+    assert f(B=(1 << 27) + 1, T=0, D=8, vs=8, gs=8) == EUNSUP
     assert f(B=0, dy=None, dx=None, g1=None, wk=None) == OK
     # rows of no tokens: the gradients are still written
     assert f(T=0, dy=None, dx=None, co=None, bs=None, st=None, sc=None, wk=None) == OK
