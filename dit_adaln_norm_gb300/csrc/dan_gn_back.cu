@@ -35,6 +35,7 @@ struct GnBackParams {
     bool last;     // the call's only image
     float count;   // values of a group
     int chunks;    // of a CTA of the first kernel
+    float keep;    // share of a chunk's rows that the L2 is to hold
     int log_cs, M; // slabs: CTAs of a cluster, rows of a thread at most
 };
 
@@ -115,13 +116,18 @@ struct Ring {
     const uint8_t *scale; // and its block's scale
     int step;             // fragments from a row to the next
     int left;             // rows from the round's first on
+    int keep;             // of them the last ones that the L2 is to hold (others are to go first)
+    uint64_t first, normal;
     uint4 *s_dy;          // [A][NT]
     XWord *s_x;           // [A][NT]
     unsigned scales[A];   // of the rows in flight
 
     // `rows` rows from fragment `at` on, `step` fragments apart.
-    __device__ __forceinline__ Ring(const GnBackParams &p, uint4 *smem, int64_t at, int step_, int rows)
+    __device__ __forceinline__ Ring(const GnBackParams &p, uint4 *smem, int64_t at, int step_, int rows, int keep_)
     {
+        keep = keep_;
+        first = evict_first();
+        normal = evict_normal();
         s_dy = smem + threadIdx.x;
         s_x = reinterpret_cast<XWord *>(smem + A * NT) + threadIdx.x;
         step = step_;
@@ -139,8 +145,10 @@ struct Ring {
     __device__ __forceinline__ void ask(int j, int ahead)
     {
         if (left > ahead) {
-            cp_async16(s_dy + j * NT, dy + ahead * (int64_t)(step * 16));
-            cp_async_word(s_x + j * NT, x + ahead * (int64_t)(step * (int)sizeof(XWord)));
+            const uint64_t policy = left - ahead > keep ? first : normal;
+            cp_async16(s_dy + j * NT, dy + ahead * (int64_t)(step * 16), policy);
+            if constexpr (CKPT) cp_async_word(s_x + j * NT, x + ahead * (int64_t)(step * (int)sizeof(XWord)));
+            else cp_async16(s_x + j * NT, x + ahead * (int64_t)(step * 16), policy);
             // (a row's fragments, and so the step, are whole blocks)
             if (CKPT) scales[j] = __ldg(scale + ahead * (int64_t)(step / Frag::kBlock));
         }
@@ -194,7 +202,7 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : kBackBlocks) gn_sums_kernel
     const GnPlace at(p.g, blockIdx.z, chunk0, p.chunks);
     grid_dependency_wait();
     allow_dependents();
-    R ring(p, s_ring, at.first(p.g, n), p.g.RL * p.g.F, at.mine);
+    R ring(p, s_ring, at.first(p.g, n), p.g.RL * p.g.F, at.mine, (int)((float)at.mine * p.keep));
     Channels<P, UNI> ch = {};
     const float2 *stats = p.stats + n * p.g.groups + at.g0;
     if (at.mine > 0) ch.template get<TYPE>(p, n, at.f0 + at.f, stats, at.f * Frag::kE);
@@ -326,7 +334,7 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : kBackBlocks) gn_dx_kernel(c
     char *dx = p.dx + to * 16;
     // dy, x, the statistics and the gains were complete before the kernel whose
     // results are waited for below let this one start
-    R ring(p, s_ring, to, step, at.mine);
+    R ring(p, s_ring, to, step, at.mine, 0); // (read for the last time)
     Channels<P, UNI> ch = {};
     if (at.mine > 0) ch.template get<TYPE>(p, n, at.f0 + at.f, p.stats + n * p.g.groups + at.g0, at.f * Frag::kE);
     grid_dependency_wait();
@@ -342,7 +350,7 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : kBackBlocks) gn_dx_kernel(c
             ring.take(j, ch, t, d);
 #pragma unroll
             for (int w = 0; w < P; ++w) d[w] = ch.dx(w, t[w], ch.dz(w, p.act, t[w], d[w]), m1, m2);
-            Frag::store(dx + j * (int64_t)(step * 16), d);
+            Frag::store(dx + j * (int64_t)(step * 16), d, ring.first);
         }
     }
 }
@@ -566,6 +574,10 @@ cudaError_t launch_passes(GnBackParams p, const GnProblem &q, const GnCut &c, cu
     using R = Ring<TYPE, CKPT, UNI, 256>;
     static_assert(R::A == ring_rows(TYPE, CKPT), "chunks are whole rounds");
     const int ring = R::A * R::kBytes * c.threads, sums = halves_of(c.threads) * c.RL * c.Ft * Fragment<TYPE>::kE * (int)sizeof(float2);
+    // Of all that the first kernel reads, what the L2 is found to hold for the
+    // second: some 64 MB.
+    const float all = (float)(q.N * q.S) * (float)q.C * (float)(type_bytes(TYPE) + (CKPT ? 1 : type_bytes(TYPE)));
+    p.keep = all > 64e6f ? 64e6f / all : 1.0f;
     const int blocks = c.threads <= 256 ? kBackBlocks : 1;
     const int64_t slots = (int64_t)sm_count() * blocks / c.tiles;
     // the second kernel's rows need not be whole chunks
