@@ -14,7 +14,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import math
 import os
 import re
 
@@ -670,9 +669,9 @@ def _images(t, name: str):
     if len(shape) not in (3, 4, 5) or not _last(t):
         raise ValueError(f"{name}: expected [N, C, H, W] (or [N, C, D, H, W]) in channels_last memory, or "
                          "a contiguous [N, S, C] tensor")
-    if len(shape) == 3:
-        return tuple(shape)
-    return shape[0], math.prod(shape[2:]), shape[1]
+    if len(shape) == 4:
+        return shape[0], shape[2] * shape[3], shape[1]
+    return tuple(shape) if len(shape) == 3 else (shape[0], shape[2] * shape[3] * shape[4], shape[1])
 
 
 def _like(t, name: str, dtype, shape, device: int, first: str):
@@ -739,6 +738,7 @@ def _group_norm(x, groups, weight, bias, eps, act, scale, shift, out, save: bool
     return out, (stats, codes, scales)
 
 
+@functools.lru_cache(maxsize=1024)
 def _scale_layout(shape):
     """Shape and (channels-last) strides of the checkpoint's scales."""
     shape = _scale_shape(shape)
