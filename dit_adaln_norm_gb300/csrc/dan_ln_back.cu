@@ -49,6 +49,7 @@ struct LnBackParams {
     int L;      // lanes per row (32 with W > 1)
     int teams;
     float inv_d;
+    bool hint_codes; // the codes' rows begin and end on 16 bytes, as the bulk hint wants them
 };
 
 // First row of CTA c of G.
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBa
         if (lane == 0) prefetch_l2(p.dy + row * F, F * 16);
         if (RES && lane == 1) prefetch_l2(p.dres + row * F, F * 16);
         if (!CKPT && lane == 2) prefetch_l2(p.x + row * F, F * 16);
-        if (CKPT && lane == 2 && F % 2 == 0) prefetch_l2(p.codes + row * F, F * 8);
+        if (CKPT && lane == 2 && p.hint_codes) prefetch_l2(p.codes + row * F, F * 8);
         if (CKPT && lane == 3) prefetch_l2_line(p.block_scales + row * p.blocks);
         if (lane == 4) prefetch_l2_line(p.stats + row);
     }
@@ -428,6 +429,7 @@ cudaError_t launch_ln_modulate_backward(const LnBackProblem &q, cudaStream_t s)
     p.F = (int)(q.D / 8);
     p.blocks = (int)((q.D + 31) / 32);
     p.inv_d = 1.0f / (float)q.D;
+    p.hint_codes = p.F % 2 == 0 && reinterpret_cast<uintptr_t>(q.codes) % 16 == 0;
     const int64_t G = back_grid(p.rows);
     const int D4 = (int)(q.D / 4), tiles = (2 * D4 + kJoinQuads - 1) / kJoinQuads;
     if (p.rows > 0) {

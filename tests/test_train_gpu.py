@@ -176,6 +176,32 @@ def test_ln_backward_of_x_beside_a_checkpoint():
     assert all(torch.equal(u, v) for u, v in zip(a, b))
 
 
+def shifted(t, by):
+    """The same bytes `by` bytes behind a 16-byte boundary."""
+    buf = torch.empty(t.numel() + 32, dtype=U8, device="cuda")
+    v = buf[by:by + t.numel()]
+    assert v.data_ptr() % 16 == by
+    return v.copy_(t.reshape(-1))
+
+
+@pytest.mark.parametrize("D", [64, 1160, 4096])
+def test_checkpoints_at_their_least_alignment(D):
+    """Codes on 8 bytes, scales on any."""
+    x, scale, saved, dy, _ = ln_back_case(2, 50, D, True, False)
+    kept = (saved[0], shifted(saved[1], 8).view(2, 50, D), shifted(saved[2], 5).view(2, 50, -1))
+    for u, v in zip(ops.ln_modulate_backward(dy, None, scale, kept), ops.ln_modulate_backward(dy, None, scale, saved)):
+        assert torch.equal(u, v)
+    for dtype in TYPES:
+        for S in (40, 9000):
+            C = 64
+            g, x, w, b, _, _ = gn_inputs(2, S, C, dtype, dtype, False)
+            saved = ops.group_norm_save(x, 8, w, b, EPS, act="silu")[1]
+            kept = (saved[0], shifted(saved[1], 8).view(2, S, C), shifted(saved[2], 5).view(2, S, C // 32))
+            for u, v in zip(ops.group_norm_backward(x, None, 8, w, b, kept, act="silu")[:3],
+                            ops.group_norm_backward(x, None, 8, w, b, saved, act="silu")[:3]):
+                assert torch.equal(u, v)
+
+
 @pytest.mark.parametrize("ckpt", [True, False])
 def test_ln_backward_in_place_and_into_slices(ckpt):
     B, T, D = 3, 50, 1160
