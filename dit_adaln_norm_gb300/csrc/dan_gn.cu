@@ -3,10 +3,13 @@
 //
 // A group's mean and variance need all of an image's rows before the first
 // output can be written.  Where a cluster of CTAs can hold a slab of whole groups
-// in shared memory, one launch reads x once.  Else three launches: the moments of
-// each chunk of rows (x read once), their join per group, and the normalisation,
-// which reads x again, in the opposite order so that what the first kernel read
-// last still lies in the L2.
+// in shared memory, one launch reads x once.  Else passes: the moments of each
+// chunk of rows (x read once), their join per group (a kernel, or where there are
+// few of them a part of the next one), and the normalisation, which reads x again,
+// in the opposite order so that what the first kernel read last still lies in the
+// L2.  Large images are bound by memory: at [1, 1024 x 1024, 128] bf16 the moments
+// take 46 us (5.8 TB/s) and the normalisation 82 (6.5 TB/s); images of some MB by
+// their instructions and the launches' latencies.
 //
 // Moments: a thread sums d and d^2 of its values' differences d from its first
 // one (so that a level far above the spread costs no accuracy), turns them into
@@ -37,6 +40,8 @@ struct GnParams {
     float count;   // values of a group
     float keep;    // share of a chunk's rows that the L2 is to hold
     int chunks;    // of a CTA of the first kernel
+    bool few;      // so few chunks that each CTA of the second kernel joins them itself
+    int chunk_R;   // rows of a chunk (the second kernel's R is its own)
     int log_cs, M; // slabs: CTAs of a cluster, rows of a thread at most
 };
 
@@ -296,6 +301,46 @@ __device__ __forceinline__ void store_codes(const GnParams &p, int64_t at, const
     if (at % Frag::kBlock == 0) p.block_scales[at / Frag::kBlock] = (uint8_t)code;
 }
 
+// A launch less, where an image's groups have few chunks (up to 128, and 4096 in
+// all): each CTA joins them itself, eight lanes a group, from sums about the first
+// chunk's mean.  `stats`: those of the CTA's groups; stored by the CTAs that say so.
+constexpr int kFewLanes = 8, kFewChunks = 128, kFewAll = 4096;
+__device__ __forceinline__ void join_few(const GnParams &p, const GnPlace &at, int64_t n, bool store, float2 *stats)
+{
+    const int lane = threadIdx.x & 31, from = lane % kFewLanes, at_once = 32 / kFewLanes, P = p.g.P;
+    const float last = (float)((p.g.S - (int64_t)(P - 1) * p.chunk_R) * p.g.per), whole = (float)p.chunk_R * p.g.per;
+    for (int g0 = (threadIdx.x >> 5) * at_once; g0 < at.groups; g0 += (blockDim.x >> 5) * at_once) {
+        const int g = g0 + lane / kFewLanes;
+        const float2 *part = p.part + (n * p.g.groups + at.g0 + min(g, at.groups - 1)) * P;
+        const float pivot = __ldcg(part).x;
+        float a = 0.0f, b = 0.0f;
+        constexpr int U = 8; // loads under way at once
+        for (int k = from; k < P; k += U * kFewLanes) {
+            float2 t[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (k + j * kFewLanes < P) t[j] = __ldcg(part + k + j * kFewLanes);
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (k + j * kFewLanes < P) {
+                    const float rows = k + j * kFewLanes + 1 < P ? whole : last;
+                    const float d = __fsub_rn(t[j].x, pivot), e = __fmul_rn(d, rows);
+                    a = __fadd_rn(a, e);
+                    b = __fadd_rn(b, __fmaf_rn(d, e, t[j].y));
+                }
+        }
+        a = lane_sum(a, kFewLanes);
+        b = lane_sum(b, kFewLanes);
+        const float d = __fdiv_rn(a, p.count);
+        const float m2 = fmaxf(__fmaf_rn(-a, d, b), 0.0f);
+        const float2 st = make_float2(__fadd_rn(pivot, d), defined_rsqrt(__fadd_rn(__fdiv_rn(m2, p.count), p.eps)));
+        if (from == 0 && g < at.groups) {
+            stats[g] = st;
+            if (store) p.stats[n * p.g.groups + at.g0 + g] = st;
+        }
+    }
+}
+
 template <int TYPE, bool CKPT, bool UNI, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) gn_apply_kernel(const GnParams p)
 {
@@ -325,7 +370,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) gn_apply_kernel(const GnParams 
     if (at.mine > 0) p.gains.get<TYPE>(n, at.f0 + at.f, norm.a, norm.b);
     grid_dependency_wait();
     allow_dependents();
-    if (at.mine > 0) norm.moments(p.g, p.stats + n * p.g.groups + at.g0, at.f * Frag::kE);
+    const float2 *stats = p.stats + n * p.g.groups + at.g0;
+    if (p.few) {
+        float2 *s_stats = reinterpret_cast<float2 *>(s_ring + kRing * NT);
+        join_few(p, at, n, p.stats && at.row0 == 0, s_stats);
+        __syncthreads();
+        stats = s_stats;
+    }
+    if (at.mine > 0) norm.moments(p.g, stats, at.f * Frag::kE);
     for (; left > 0; left -= kRing, to -= kRing * (int64_t)step, x -= kRing * (int64_t)(step * 16), y -= kRing * (int64_t)(step * 16)) {
 #pragma unroll
         for (int j = 0; j < kRing; ++j) {
@@ -346,7 +398,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) gn_apply_kernel(const GnParams 
 
 // ------------------------------------------------------------------- slabs
 
-// One launch, one read of x: a cluster holds a slab (whole groups of an image) in
+// One launch, one read of x (4.9 us for [1, 8 x 8, 1280], where the passes took
+// 10): a cluster holds a slab (whole groups of an image) in
 // its CTAs' shared memory.  Each thread copies its own fragments there, all at
 // once, and nobody else reads them; the CTAs exchange their groups' moments
 // through the cluster's shared memory.
@@ -485,7 +538,9 @@ cudaError_t launch_passes(GnParams p, const GnProblem &q, const GnCut &c, cudaSt
     p.g = gn_grid(q.S, q.C, q.groups, TYPE, c.Ft, c.R, c.P, c.RL);
     set_join(p);
     p.part = static_cast<float2 *>(q.workspace);
-    p.stats = q.stats ? static_cast<float2 *>(q.stats) : p.part + q.N * q.groups * c.P;
+    p.few = c.P <= kFewChunks && c.P * p.g.tile_groups <= kFewAll;
+    p.chunk_R = (int)c.R;
+    p.stats = q.stats || p.few ? static_cast<float2 *>(q.stats) : p.part + q.N * q.groups * c.P;
     // Of all that the first kernel reads, what the L2 is found to hold for the
     // second: some 64 MB.
     const float all = (float)(q.N * q.S) * (float)q.C * (float)type_bytes(TYPE);
@@ -503,12 +558,13 @@ cudaError_t launch_passes(GnParams p, const GnProblem &q, const GnCut &c, cudaSt
         constexpr int NT = decltype(threads)::value;
         const auto moments = gn_moments_kernel<TYPE, NT>;
         const auto apply = gn_apply_kernel<TYPE, CKPT, UNI, NT>;
-        const int smem1 = room_for(1024 / NT, ring + units), smem2 = room_for(1024 / NT, ring);
+        const int smem1 = room_for(1024 / NT, ring + units);
+        const int smem2 = room_for(1024 / NT, ring + (p.few ? p.g.tile_groups * (int)sizeof(float2) : 0));
         cudaError_t e = ready(moments, smem1);
         if (e == cudaSuccess) e = ready(gn_join_kernel, 0);
         if (e == cudaSuccess) e = ready(apply, smem2);
         if (e == cudaSuccess) e = launch_grid(moments, one, 1, NT, smem1, s, p);
-        if (e == cudaSuccess) e = launch_grid(gn_join_kernel, dim3((unsigned)(q.N * q.groups)), 1, kJoin, 0, s, p);
+        if (e == cudaSuccess && !p.few) e = launch_grid(gn_join_kernel, dim3((unsigned)(q.N * q.groups)), 1, kJoin, 0, s, p);
         if (e == cudaSuccess) e = launch_grid(apply, two, 1, NT, smem2, s, a);
         return e;
     };

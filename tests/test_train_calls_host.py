@@ -40,12 +40,14 @@ def gn_back(N=1, S=4096, C=512, G=32):
 
 
 def test_kernels_of_a_call(fake):
-    """One launch, the rows' and the join; a slab (and its images' sum); the passes and theirs."""
-    s, b, small, many, large, back, pair, passes, nothing = fake(CALLS + """
+    """One launch, the rows' and the join; a slab (and its images' sum); the passes and theirs, the
+    second one joining few chunks itself."""
+    s, b, small, many, large, back, pair, passes, nothing, few = fake(CALLS + """
 print(json.dumps([save(), ln_back(), gn(S=64), gn(N=7, S=64), gn(S=1 << 18), gn_back(S=64), gn_back(N=3, S=64),
-                  gn_back(N=3, S=1 << 18), ln_back(T=0)]))""")
-    assert all(r[0] == OK for r in (s, b, small, many, large, back, pair, passes, nothing))
-    assert [len(r[1]) for r in (s, b, small, many, large, back, pair, passes, nothing)] == [1, 2, 1, 1, 3, 1, 2, 4, 1]
+                  gn_back(N=3, S=1 << 18), ln_back(T=0), gn(S=6000, G=8)]))""")
+    assert all(r[0] == OK for r in (s, b, small, many, large, back, pair, passes, nothing, few))
+    assert [len(r[1]) for r in (s, b, small, many, large, back, pair, passes, nothing, few)] == \
+        [1, 2, 1, 1, 3, 1, 2, 4, 1, 2]
     # a slab's launch has the images along x and is cut the same for each
     assert many[1][0][0] == 7 * small[1][0][0] and many[1][0][1:] == small[1][0][1:]
     # the passes' first wave: a CTA in each of an SM's four places (two for the gradients)
