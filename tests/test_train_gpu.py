@@ -78,6 +78,15 @@ def test_ln_save_statistics_are_those_of_ln_modulate(D):
     assert torch.equal(ops.ln_modulate(x, scale, shift, EPS), n * (1 + scale)[:, None] + shift[:, None])
 
 
+@pytest.mark.parametrize("B,T,D", [(2, 300, 1160), (1, 100, 2048), (1, 4216, 4096), (2, 9, 8192)])
+def test_ln_save_in_place(B, T, D):
+    _, x, scale, shift = ln_inputs(B, T, D)
+    y, saved = ops.ln_modulate_save(x, scale, shift, EPS)
+    z = x.clone()
+    got, kept = ops.ln_modulate_save(z, scale, shift, EPS, out=z)
+    assert got is z and torch.equal(z, y) and all(torch.equal(u, v) for u, v in zip(kept, saved))
+
+
 def test_ln_save_level_far_above_the_spread():
     _, x, scale, shift = ln_inputs(1, 40, 2048, level=300.0)
     y, (stats, _, _) = ops.ln_modulate_save(x, scale, shift, EPS)
@@ -379,7 +388,20 @@ def test_group_norm_level_far_above_the_spread(dtype):
     assert not y.any() and bool((saved[0][..., 0] == 7.5).all())
 
 
-@pytest.mark.parametrize("S,C,groups", [(100, 320, 32), (5000, 64, 8), (70000, 32, 4)])
+@pytest.mark.parametrize("S", [50, 6000, 100000])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_group_norm_first_rows_far_off(S, dtype):
+    """Pivots that say nothing of the rest: the first rows of an image, and its middle ones, 3000
+    times the others' spread away."""
+    for rows in (slice(0, 1), slice(0, 40), slice(S // 2, S // 2 + 1)):
+        g, x, w, b, _, _ = gn_inputs(2, S, 512, dtype, dtype, False)
+        x[1, rows] += 3000
+        y, saved = ops.group_norm_save(x, 8, w, b, EPS, act="silu", checkpoint=False)
+        check_gn(y, saved, x, 8, w, b, "silu", None, None, False)
+        assert torch.equal(y[:1], ops.group_norm(x[:1], 8, w, b, EPS, act="silu"))
+
+
+@pytest.mark.parametrize("S,C,groups", [(100, 320, 32), (5000, 64, 8), (6000, 512, 8), (70000, 32, 4)])
 def test_images_do_not_follow_the_batch(S, C, groups):
     N = 5
     g, x, w, b, s, t = gn_inputs(N, S, C, BF16, BF16, True)
