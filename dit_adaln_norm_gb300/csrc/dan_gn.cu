@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) gn_moments_kernel(const GnParam
 
 // Mean and rstd of each group (a block's) from its chunks' moments: up to kU
 // chunks a thread, in registers.
-constexpr int kJoin = 128, kU = 5, kGnChunks = kJoin * kU;
+constexpr int kJoin = 128, kU = 5;
 __global__ void __launch_bounds__(kJoin) gn_join_kernel(const GnParams p)
 {
     __shared__ float s_warp[2][kJoin / 32];
@@ -332,7 +332,8 @@ __device__ __forceinline__ void join_few(const GnParams &p, const GnPlace &at, i
         a = lane_sum(a, kFewLanes);
         b = lane_sum(b, kFewLanes);
         const float d = __fdiv_rn(a, p.count);
-        const float m2 = fmaxf(__fmaf_rn(-a, d, b), 0.0f);
+        float m2 = __fmaf_rn(-a, d, b);
+        if (m2 < 0.0f) m2 = 0.0f; // (not fmaxf: what is not a number stays that)
         const float2 st = make_float2(__fadd_rn(pivot, d), defined_rsqrt(__fadd_rn(__fdiv_rn(m2, p.count), p.eps)));
         if (from == 0 && g < at.groups) {
             stats[g] = st;

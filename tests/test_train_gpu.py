@@ -423,6 +423,24 @@ def test_images_do_not_follow_the_batch(S, C, groups):
     assert bool(y2[bad].isnan().all()) and torch.equal(y2[~bad], y[~bad])
 
 
+@pytest.mark.parametrize("S,C,groups", [(100, 320, 32), (3000, 40, 40), (5000, 64, 8), (6000, 512, 8), (70000, 32, 4),
+                                        (400000, 32, 4)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_an_infinity_spoils_its_group(S, C, groups, dtype):
+    """Its group's outputs are not numbers, wherever the infinity lies, and the others are what they were."""
+    _, x, w, b, _, _ = gn_inputs(2, S, C, dtype, dtype, False)
+    y = ops.group_norm(x, groups, w, b, EPS)
+    per = C // groups
+    bad = torch.zeros((2, S, C), dtype=torch.bool, device="cuda")
+    bad[1, :, per:2 * per] = True
+    for row in (0, S // 2, S - 1):
+        z = x.clone()
+        z[1, row, 2 * per - 1] = float("-inf")
+        y2, (stats, _, _) = ops.group_norm_save(z, groups, w, b, EPS, checkpoint=False)
+        assert bool(y2[bad].isnan().all()) and torch.equal(y2[~bad], y[~bad]), row
+        assert bool(stats[1, 1, 1].isnan()), row
+
+
 def test_group_norm_no_positions():
     C = 40
     w = torch.ones(C, dtype=BF16, device="cuda")
