@@ -13,9 +13,11 @@
 // to eight fragments, on eight warps of up to 255 registers: what a step costs
 // apart from its elements, the exchange of the rows' sums above all, is spread
 // over 32 to 64 elements of a thread, and the rows' chains of shuffles and
-// barriers run side by side (at D = 4096, one row at a time by two teams of four
-// warps: 24.1 us for 4216 rows).  Each thread copies its own columns of the next
-// rows into shared memory with cp.async and nobody else reads them.  At the end
+// barriers run side by side (4216 x 4096: 24.0 us, 0.53 of the copy rate, some 8 us
+// of it the call's two ends; 33 with one or two fragments on sixteen warps; one row
+// at a time by two teams of four warps is no slower than four rows by one of eight).
+// Each thread copies its own columns of the next rows into shared memory with
+// cp.async and nobody else reads them.  At the end
 // of a batch, or of the CTA's rows, the teams' column sums are added in order and
 // stored as one partial of the batch; a second kernel adds the partials in order.
 #include "dan_train.cuh"
