@@ -359,7 +359,7 @@ inline GnSlab gn_slab(int64_t S, int64_t C, int64_t groups, int type, bool check
     for (int64_t segment = 128; segment >= 64; segment /= 2) {
         int64_t Ft = (segment / 16 + step - 1) / step * step;
         if (Ft > F) Ft = F;
-        if (Ft > 256) continue;
+        if (Ft > 256 || (F + Ft - 1) / Ft > 65535) continue; // (slabs lie along a grid's y)
         int log_cs = 0;
         while (log_cs < kSlabCluster && (2 << log_cs) <= S && S * Ft * bytes > (kSlabRows << log_cs)) ++log_cs;
         const int64_t rows = (S + (1 << log_cs) - 1) >> log_cs;

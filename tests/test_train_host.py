@@ -92,6 +92,18 @@ def gn(lib, x=X, ty=BF, w=W, b=B_, pt=BF, sc=None, sh=None, vs=512, act=1, y=Y, 
     return lib.dan_can_use_group_norm(x, ty, w, b, pt, sc, sh, vs, act, y, st, co, bs, N, S, C, G, eps, wk, size)
 
 
+def test_slabs_of_the_widest_images_fit_a_grid(lib):
+    """65536 slabs of 64 bytes a row are more than a grid has in y: such images go in passes, which
+    need a workspace; one step narrower, and with slabs of 128 bytes, they are slabs."""
+    forward, backward = lib.dan_group_norm_workspace, lib.dan_group_norm_backward_workspace
+    C = 1 << 20
+    for S in (5200, 8192):
+        assert forward(1, S, C, C // 4, F32, 0) > 0 and forward(1, S, C - 16, C // 4 - 4, F32, 0) == 0
+    assert forward(1, 4096, C, C // 4, F32, 0) == 0
+    for S in (2600, 4096):
+        assert backward(1, S, C, C // 4, F32, 0) > 0 and backward(1, S, C - 16, C // 4 - 4, F32, 0) == 0
+
+
 def test_group_norm_validation(lib):
     f = lambda **k: gn(lib, **k)  # noqa: E731
     assert f() == OK and f(w=None, b=None) == OK and f(sc=SC, sh=SH) == OK and f(st=ST, co=CO, bs=BS) == OK
