@@ -1,0 +1,115 @@
+"""The training operators over the whole of the ranges that they take: the narrowest rows, the
+shortest batches, many images, levels far above the spread, buffers of exactly their size; against
+64-bit references (tests/_train.py), the oracle's bits, and the plain form's time."""
+import numpy as np
+import pytest
+import torch
+
+import _train as ref
+from _gpu import from_dev
+from dit_adaln_norm_gb300 import ops
+
+pytestmark = pytest.mark.gpu
+BF16, FP16, FP32, U8 = torch.bfloat16, torch.float16, torch.float32, torch.uint8
+EPS = 1e-6
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def normal(g, *shape, std=1.0, mean=0.0, dtype=BF16):
+    return (torch.randn(*shape, generator=g, device="cuda") * std + mean).to(dtype)
+
+
+@pytest.fixture(autouse=True)
+def no_bad_status():
+    yield
+    torch.cuda.synchronize()
+    assert ops.device_status() == 0
+
+
+def device_us(f, reps=5):
+    """The least device time of a call, in microseconds."""
+    f()
+    times = []
+    for _ in range(reps):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    return min(times)
+
+
+def same_bits(a, b):
+    a, b = a.contiguous().view(torch.int32), b.contiguous().view(torch.int32)
+    nan = lambda t: (t & 0x7FFFFFFF) > 0x7F800000  # noqa: E731
+    return bool(((a == b) | (nan(a) & nan(b))).all())
+
+
+# ------------------------------------------------------------- LayerNorm of short rows
+
+SHORT = [8, 16, 24, 32, 40, 64, 72, 128, 136, 256, 264, 504, 512, 520, 768, 776, 1016, 1024, 1032]
+
+
+@pytest.mark.parametrize("D", SHORT)
+def test_short_rows_have_the_oracles_statistics(orc, D):
+    """Mean and 1/std of ln_modulate's definition bit for bit, whatever is in a row; the codes and
+    scales of the format, y within its rounding."""
+    B, T = 3, 67
+    g = gen(D)
+    x = normal(g, B, T, D, mean=0.5)
+    x[:, 1] *= 1e4
+    x[:, 2] = 0
+    x[:, 3] = -0.0
+    x[:, 4] = 1e-40
+    x[0, 5, -1], x[0, 6, 0], x[0, 7, D // 2], x[0, 8, :8] = float("nan"), float("inf"), float("-inf"), 3e38
+    emb = normal(g, B, 3 * D, std=0.3)
+    scale, shift = emb[:, :D], emb[:, 2 * D:]
+    for checkpoint in (True, False):
+        y, (stats, codes, scales) = ops.ln_modulate_save(x, scale, shift, EPS, checkpoint=checkpoint)
+        _, st = orc.ln_modulate(from_dev(x), from_dev(scale), from_dev(shift), EPS, with_stats=True)
+        want = torch.from_numpy(st[:, [0, 2]].copy()).view(B, T, 2).cuda()
+        assert same_bits(stats, want)
+        fine = [i for i in range(T) if not 5 <= i <= 8]
+        w, _, e, _ = ref.ln_forward(x[:, fine], scale, shift, EPS)
+        ref.assert_near(y[:, fine], w, e, "y")
+        assert bool(y[0, 5:8].isnan().all()) and bool(y[1:].isfinite().all())
+    c, s = ref.checkpoint(x)
+    codes, scales = ops.ln_modulate_save(x, scale, shift, EPS)[1][1:]
+    nan = (c & 0x7F == 0x7F) & (codes & 0x7F == 0x7F)
+    assert bool(((codes == c) | nan).all()) and torch.equal(scales, s)
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 1, 8), (1, 50000, 8), (7, 1, 16), (5000, 1, 24), (3, 9001, 40), (1001, 3, 64),
+                                   (2, 33, 256), (11, 31, 264), (400, 7, 1000)])
+def test_short_rows_of_any_batches(B, T, D):
+    """Batches of one row, of fewer rows than a warp takes, and of many; in place too."""
+    g = gen(1)
+    x, emb = normal(g, B, T, D, mean=0.5), normal(g, B, 2 * D, std=0.3)
+    y, saved = ops.ln_modulate_save(x, emb[:, :D], emb[:, D:], EPS)
+    want, st, ey, est = ref.ln_forward(x, emb[:, :D], emb[:, D:], EPS)
+    ref.assert_near(y, want, ey, "y")
+    ref.assert_near(saved[0], st, est, "stats")
+    c, s = ref.checkpoint(x)
+    assert torch.equal(saved[1], c) and torch.equal(saved[2], s)
+    z = x.clone()
+    assert ops.ln_modulate_save(z, emb[:, :D], emb[:, D:], EPS, out=z)[0] is z and torch.equal(z, y)
+
+
+@pytest.mark.parametrize("rows,D", [(500000, 8), (500000, 16), (300000, 64), (150000, 128)])
+def test_many_short_rows_take_less_than_torch(rows, D):
+    """A warp a row, one at a time, took 1.3 to 13 times as long as these five torch operations."""
+    g = gen(2)
+    x, scale, shift = normal(g, 1, rows, D), normal(g, 1, D), normal(g, 1, D)
+
+    def plain():
+        v = x.float()
+        d = v - v.mean(-1, keepdim=True)
+        r = (d.square().mean(-1, keepdim=True) + EPS).rsqrt()
+        return (d * r * (1 + scale.float()[:, None]) + shift.float()[:, None]).bfloat16()
+
+    for checkpoint in (False, True):
+        assert device_us(lambda: ops.ln_modulate_save(x, scale, shift, EPS, checkpoint=checkpoint)) < device_us(plain)
