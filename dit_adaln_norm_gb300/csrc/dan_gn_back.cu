@@ -384,6 +384,26 @@ __global__ void __launch_bounds__(256) gn_params_kernel(const GnBackParams p, in
     store_as(p.dbias, p.gains.param_type, c, t.x);
 }
 
+// The parameters' gradients of images without positions, or of no images: zeros,
+// whatever the parameters are (they are not read).
+__global__ void __launch_bounds__(256) gn_zeros_kernel(const GnBackParams p, int type, int64_t N, int64_t C)
+{
+    grid_dependency_wait();
+    allow_dependents();
+    const int64_t most = (N > 0 ? N : 1) * C;
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < most; i += gridDim.x * (int64_t)256) {
+        const int64_t n = i / C, c = i - n * C;
+        if (p.dscale && n < N) {
+            store_as(p.dscale, type, n * p.gs + c, 0.0f);
+            store_as(p.dshift, type, n * p.gs + c, 0.0f);
+        }
+        if (p.dweight && i < C) {
+            store_as(p.dweight, p.gains.param_type, i, 0.0f);
+            store_as(p.dbias, p.gains.param_type, i, 0.0f);
+        }
+    }
+}
+
 // ------------------------------------------------------------------- slabs
 
 // One launch, one read of dy and x: a cluster holds a slab (whole groups of an
@@ -613,7 +633,8 @@ cudaError_t launch_passes(GnBackParams p, const GnProblem &q, const GnCut &c, cu
 
 int64_t group_norm_backward_workspace(int64_t N, int64_t S, int64_t C, int64_t groups, int type, bool checkpoint)
 {
-    if (S > 0 && backward_slab(S, C, groups, type, checkpoint).Ft) // the images' sums, to be added
+    if (N * S == 0) return 0;
+    if (backward_slab(S, C, groups, type, checkpoint).Ft) // the images' sums, to be added
         return N > 1 ? N * C * (int64_t)sizeof(float2) : 0;
     const GnCut c = backward_cut(S, C, groups, type, checkpoint);
     return N * (C * (c.P + 1) + groups) * (int64_t)sizeof(float2);
@@ -639,7 +660,14 @@ cudaError_t launch_group_norm_backward(const GnProblem &q, cudaStream_t s)
     p.act = q.act;
     p.last = q.N == 1;
     p.count = (float)(q.S * per);
-    const GnSlab slab = q.S ? backward_slab(q.S, q.C, q.groups, q.type, ckpt) : GnSlab{};
+    if (q.N * q.S == 0) {
+        if (!q.dweight && (!q.dscale || q.N == 0)) return cudaSuccess;
+        const cudaError_t e = ready(gn_zeros_kernel, 0);
+        const int64_t blocks = ((q.N > 0 ? q.N : 1) * q.C + 255) / 256, most = 8 * (int64_t)sm_count();
+        if (e != cudaSuccess) return e;
+        return launch_grid(gn_zeros_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 1, 256, 0, s, p, q.type, q.N, q.C);
+    }
+    const GnSlab slab = backward_slab(q.S, q.C, q.groups, q.type, ckpt);
     const GnCut cut = backward_cut(q.S, q.C, q.groups, q.type, ckpt);
     set_passes(p, q, cut);
     if (slab.Ft) p.sums = p.part;
@@ -648,17 +676,12 @@ cudaError_t launch_group_norm_backward(const GnProblem &q, cudaStream_t s)
         const bool params = !p.last && q.dweight;
         cudaError_t e = params ? ready(gn_params_kernel<T>, 0) : cudaSuccess;
         if (e != cudaSuccess) return e;
-        if (q.N > 0 && q.S > 0) {
-            e = with_bool(ckpt, [&](auto codes) {
-                return with_bool(per % E == 0, [&](auto uni) {
-                    constexpr bool K = decltype(codes)::value, U = decltype(uni)::value;
-                    return slab.Ft ? launch_slab<T, K, U>(p, q, slab, s) : launch_passes<T, K, U>(p, q, cut, s);
-                });
+        e = with_bool(ckpt, [&](auto codes) {
+            return with_bool(per % E == 0, [&](auto uni) {
+                constexpr bool K = decltype(codes)::value, U = decltype(uni)::value;
+                return slab.Ft ? launch_slab<T, K, U>(p, q, slab, s) : launch_passes<T, K, U>(p, q, cut, s);
             });
-        } else if (q.N > 0) { // no positions: sums of nothing
-            e = ready(gn_back_join_kernel<T>, 0);
-            if (e == cudaSuccess) e = launch_grid(gn_back_join_kernel<T>, dim3((unsigned)(q.N * q.groups)), 1, kJoin, 0, s, p);
-        }
+        });
         if (e != cudaSuccess || !params) return e;
         return launch_grid(gn_params_kernel<T>, dim3((unsigned)((q.C + 31) / 32)), 1, 256, 0, s, p, q.N);
     });

@@ -136,7 +136,7 @@ int dan_can_use_group_norm(const void *x, int type, const void *weight, const vo
  * and scales (C % 32 == 0).  dx has `type`, dweight and dbias [C] param_type,
  * dscale and dshift [N, C] `type` with image stride grad_bstride; each pair is
  * there when its parameters are.  In place: dx == dy.  S == 0 writes zeros to
- * dscale and dshift, N * S == 0 to dweight and dbias.
+ * dscale and dshift, N * S == 0 to dweight and dbias, whatever the parameters are.
  * workspace: dan_group_norm_backward_workspace(...) bytes, on the same terms. */
 int64_t dan_group_norm_backward_workspace(int64_t N, int64_t S, int64_t C, int64_t groups, int type,
                                           int checkpoint);

@@ -113,3 +113,24 @@ def test_many_short_rows_take_less_than_torch(rows, D):
 
     for checkpoint in (False, True):
         assert device_us(lambda: ops.ln_modulate_save(x, scale, shift, EPS, checkpoint=checkpoint)) < device_us(plain)
+
+
+# ------------------------------------------------------------------------- group norm
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("N,S", [(1, 0), (2, 0), (5, 0), (0, 4), (0, 0)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_gradients_of_nothing_are_zeros_whatever_the_parameters(dtype, N, S, bad):
+    """Sums of no terms; the parameters are not looked at."""
+    C, groups = 320, 32
+    e = torch.empty((N, S, C), dtype=dtype, device="cuda")
+    w, b = (torch.full((C,), bad, dtype=dtype, device="cuda") for _ in range(2))
+    s, t = (torch.full((N, C), bad, dtype=dtype, device="cuda") for _ in range(2))
+    saved = (torch.full((N, groups, 2), bad, device="cuda"), None, None)
+    for act in (None, "silu"):
+        got = ops.group_norm_backward(e, e, groups, w, b, saved, act=act, scale=s, shift=t)
+        assert got[0].shape == e.shape
+        for g, like in zip(got[1:], (w, b, s, t)):
+            assert g.shape == like.shape and g.dtype is dtype and not g.any()
+        dw, db = ops.group_norm_backward(e, e, groups, w.float(), b.float(), saved, act=act)[1:3]
+        assert dw.dtype is FP32 and not dw.any() and not db.any()

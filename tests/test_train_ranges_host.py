@@ -22,3 +22,12 @@ def test_short_rows_that_cannot_run_launch_nothing(fake, D):
     for fail in ("SET", "LAUNCH"):
         first, again = fake(CALLS + f"fail_at[{fail}] = 1\nprint(json.dumps([save(D={D}), save(D={D})]))")
         assert first == [ECUDA, []] and again[0] == OK and len(again[1]) == 1
+
+
+def test_gradients_of_nothing(fake):
+    """One kernel that needs no workspace, and none where it cannot run."""
+    for sizes in ("N=1, S=0", "N=3, S=0", "N=0, S=7"):
+        call = f"gn_back({sizes})"
+        good, size = fake(CALLS + f"print(json.dumps([{call}, lib.dan_group_norm_backward_workspace(3, 0, 512, 32, 0, 0)]))")
+        assert good[0] == OK and len(good[1]) == 1 and size == 0
+        assert fake(CALLS + f"fail_at[SET] = 1\nprint(json.dumps({call}))") == [ECUDA, []]
