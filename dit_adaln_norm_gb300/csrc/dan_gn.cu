@@ -12,9 +12,11 @@
 // their instructions and the launches' latencies.
 //
 // Moments: a thread sums d and d^2 of its values' differences d from its first
-// one (so that a level far above the spread costs no accuracy), turns them into
-// a mean and a sum of squares about it, and these are joined in a fixed order:
-// first the means, then the squares about the joint mean.
+// one, turns them into a mean and a sum of squares about it, and these are joined in
+// a fixed order: first the means, then the squares about the joint mean.  Means
+// too are summed as differences from the first one of those that are joined.  So
+// a level far above the spread costs what a mean's own rounding does, half a step
+// of the level at each of up to three joins, and equal values have no spread.
 #include "dan_gn.cuh"
 
 namespace dan {
@@ -107,7 +109,8 @@ struct Sums {
 };
 
 // Mean and squared sum of each of a CTA's groups from its entries (the groups'
-// units of every row lane): their mean, then the squared sums about it.
+// units of every row lane): their mean, from the first one on, then the squared
+// sums about it.
 __device__ __forceinline__ void join_units(const GnParams &p, const GnPlace &at, const float2 *s_units, float2 *to,
                                            int64_t step)
 {
@@ -120,20 +123,21 @@ __device__ __forceinline__ void join_units(const GnParams &p, const GnPlace &at,
         const int g = g0 + lane / p.join;
         const float2 *from = s_units + g * p.per_group;
         const int last = g < at.groups ? end : 0;
+        const float pivot = last > 0 ? from->x : 0.0f; // (of a lane that has entries)
         float sum = 0.0f;
         for (int rl = rl0; rl < last; rl += p.deep)
             for (int u = u0; u < p.per_group; u += p.wide)
-                sum = __fmaf_rn(from[rl * units + u].x, (float)(at.whole + (rl < at.rest)), sum);
-        const float mean = __fmul_rn(lane_sum(sum, p.join), inv);
+                sum = __fmaf_rn(__fsub_rn(from[rl * units + u].x, pivot), (float)(at.whole + (rl < at.rest)), sum);
+        const float off = __fmul_rn(lane_sum(sum, p.join), inv); // the mean's, from the pivot
         float m2 = 0.0f;
         for (int rl = rl0; rl < last; rl += p.deep)
             for (int u = u0; u < p.per_group; u += p.wide) {
                 const float2 t = from[rl * units + u];
-                const float d = __fsub_rn(t.x, mean);
+                const float d = __fsub_rn(__fsub_rn(t.x, pivot), off);
                 m2 = __fadd_rn(m2, __fmaf_rn(__fmul_rn(d, d), (float)((at.whole + (rl < at.rest)) * p.unit), t.y));
             }
         m2 = lane_sum(m2, p.join);
-        if (mine == 0 && g < at.groups) to[g * step] = make_float2(mean, m2);
+        if (mine == 0 && g < at.groups) to[g * step] = make_float2(__fadd_rn(pivot, off), m2);
     }
 }
 
@@ -213,7 +217,8 @@ __global__ void __launch_bounds__(kJoin) gn_join_kernel(const GnParams p)
     float2 t[kU];
 #pragma unroll
     for (int j = 0; j < kU; ++j)
-        t[j] = tid + j * kJoin < p.g.P ? __ldcg(p.part + g * p.g.P + tid + j * kJoin) : make_float2(0.0f, 0.0f);
+        t[j] = __ldcg(p.part + g * p.g.P + (tid + j * kJoin < p.g.P ? tid + j * kJoin : 0)); // (n is 0 of no chunk)
+    const float pivot = __ldcg(p.part + g * p.g.P).x;
     auto block_sum = [&](float v, int at) {
         v = lane_sum(v, 32);
         if ((tid & 31) == 0) s_warp[at][tid >> 5] = v;
@@ -225,16 +230,16 @@ __global__ void __launch_bounds__(kJoin) gn_join_kernel(const GnParams p)
     };
     float v = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kU; ++j) v = __fmaf_rn(t[j].x, n[j], v);
-    const float mean = __fdiv_rn(block_sum(v, 0), p.count);
+    for (int j = 0; j < kU; ++j) v = __fmaf_rn(__fsub_rn(t[j].x, pivot), n[j], v);
+    const float off = __fdiv_rn(block_sum(v, 0), p.count); // the mean's, from the pivot
     v = 0.0f;
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
-        const float d = __fsub_rn(t[j].x, mean);
-        v = __fadd_rn(v, __fmaf_rn(__fmul_rn(d, d), n[j], t[j].y));
+        const float d = __fsub_rn(__fsub_rn(t[j].x, pivot), off);
+        v = __fadd_rn(v, __fmaf_rn(__fmul_rn(d, d), n[j], n[j] > 0.0f ? t[j].y : 0.0f));
     }
     v = __fdiv_rn(block_sum(v, 1), p.count);
-    if (tid == 0) p.stats[g] = make_float2(mean, defined_rsqrt(__fadd_rn(v, p.eps)));
+    if (tid == 0) p.stats[g] = make_float2(__fadd_rn(pivot, off), defined_rsqrt(__fadd_rn(v, p.eps)));
 }
 
 // --------------------------------------------------------------- normalise
@@ -475,10 +480,12 @@ __global__ void __launch_bounds__(512, 2) gn_slab_kernel(const GnParams p)
             const int g = g0 + (lane >> p.log_cs);
             const bool here = g < at.groups && share > 0.0f;
             const float2 t = here ? ld_cluster(s_group + g, from) : make_float2(0.0f, 0.0f);
-            const float mean = __fdiv_rn(lane_sum(__fmul_rn(t.x, share), cs), p.count);
-            const float d = __fsub_rn(t.x, mean);
+            const float pivot = __shfl_sync(kFull, t.x, lane - from); // the first CTA's (it has rows)
+            const float e = here ? __fsub_rn(t.x, pivot) : 0.0f;
+            const float off = __fdiv_rn(lane_sum(__fmul_rn(e, share), cs), p.count); // the mean's, from the pivot
+            const float d = here ? __fsub_rn(e, off) : 0.0f;
             const float m2 = lane_sum(__fmaf_rn(__fmul_rn(d, d), share, t.y), cs);
-            if (from == 0 && g < at.groups) finish(g, mean, m2);
+            if (from == 0 && g < at.groups) finish(g, __fadd_rn(pivot, off), m2);
         }
         cluster_arrive(); // nobody reads this CTA's moments after the wait below
     }

@@ -134,3 +134,35 @@ def test_gradients_of_nothing_are_zeros_whatever_the_parameters(dtype, N, S, bad
             assert g.shape == like.shape and g.dtype is dtype and not g.any()
         dw, db = ops.group_norm_backward(e, e, groups, w.float(), b.float(), saved, act=act)[1:3]
         assert dw.dtype is FP32 and not dw.any() and not db.any()
+
+
+# (N, S, C, groups): one CTA's slab, clusters, few chunks and many, whole tiles and narrow groups
+CUTS = [(2, 64, 320, 32), (1, 3, 96, 4), (1, 1000, 1280, 32), (2, 777, 640, 16), (1, 6000, 512, 8), (2, 9001, 96, 3),
+        (1, 100001, 64, 32), (1, 70000, 24, 1), (1, 300001, 16, 2)]
+
+
+@pytest.mark.parametrize("N,S,C,groups", CUTS)
+@pytest.mark.parametrize("level", [1000.1, -3001.7, 1.7e20])
+def test_equal_values_have_no_spread(N, S, C, groups, level):
+    """Whatever the bits of their level: the mean is exact, and what is normalised zero."""
+    x = torch.full((N, S, C), level, dtype=FP32, device="cuda")
+    x += torch.arange(groups, device="cuda").repeat_interleave(C // groups) * 0.7   # each group its own
+    y, saved = ops.group_norm_save(x, groups, None, None, EPS, checkpoint=False)
+    assert torch.equal(saved[0][..., 0], x[:, 0, ::C // groups])
+    assert not y.any() and bool((saved[0][..., 1].double() - EPS ** -0.5).abs().max() < 1e-3 * EPS ** -0.5)
+
+
+@pytest.mark.parametrize("N,S,C,groups", CUTS)
+def test_means_of_a_level_far_above_the_spread(N, S, C, groups):
+    """A mean is off by the roundings of the level at its three joins (a thread's values, a CTA's, the
+    image's), half a step each, and by the differences' own sums."""
+    x = normal(gen(4), N, S, C, mean=1e5, dtype=FP32)
+    mean, rstd = ops.group_norm_save(x, groups, None, None, EPS, checkpoint=False)[1][0].double().unbind(-1)
+    v = x.double().unflatten(2, (groups, -1))
+    want = v.mean((1, 3))
+    far = (v - want[:, None, :, None]).abs().amax((1, 3))
+    lim = 3 * 2.0 ** -24 * 2.0 ** 17 + ref.E * far          # (1e5 < 2^17)
+    assert bool(((mean - want).abs() <= lim).all())
+    std = (v - want[:, None, :, None]).square().mean((1, 3)).add(EPS).sqrt()
+    # each join's means are off by so much at most, and what they add to the squares too
+    assert bool(((rstd * std - 1).abs() <= 2 * lim * rstd + ref.E * (1 + far * rstd)).all())
