@@ -21,10 +21,10 @@ LIB = os.path.join(HERE, "libdan.so")
 SOURCES = ["dan_rows_rms.cu", "dan_rows_gated.cu", "dan_rows_ln.cu", "dan_rows_lnfp8.cu",
            "dan_rows_gatedln.cu", "dan_qk.cu", "dan_resid_t.cu", "dan_abi.cu", "dan_noalloc.cu",
            "dan_cache_rope.cu", "dan_attn_step.cu", "dan_attn_tile.cu",
-           "dan_cache_abi.cu", "dan_rows_lnsave.cu", "dan_ln_back.cu", "dan_gn.cu", "dan_gn_back.cu",
+           "dan_cache_abi.cu", "dan_rows_lnsave.cu", "dan_ln_back.cu", "dan_ln_back_short.cu", "dan_gn.cu", "dan_gn_back.cu",
            "dan_train_abi.cu"]
 HEADERS = ["dan_device.cuh", "dan_internal.h", "dan_ring.cuh", "dan_rows.cuh",
-           "dan_attn.cuh", "dan_attn_plan.cuh", "dan_attn_tma.cuh", "dan_train.cuh", "dan_gn.cuh"]
+           "dan_attn.cuh", "dan_attn_plan.cuh", "dan_attn_tma.cuh", "dan_train.cuh", "dan_gn.cuh", "dan_ln_back.cuh"]
 
 # Registers a thread that the kernels of a source must have: the attention's
 # tile kernel moves registers between its warps, and with fewer at launch than

@@ -20,7 +20,8 @@
 // cp.async and nobody else reads them.  At the end
 // of a batch, or of the CTA's rows, the teams' column sums are added in order and
 // stored as one partial of the batch; a second kernel adds the partials in order.
-#include "dan_train.cuh"
+// Many short batches go to dan_ln_back_short.cu.
+#include "dan_ln_back.cuh"
 
 namespace dan {
 namespace {
@@ -35,54 +36,8 @@ __host__ __device__ constexpr int ahead_of(int K, int R, bool ckpt, bool res)
     return 4 * step <= 220 * 1024 ? 4 : 3 * step <= 220 * 1024 ? 3 : 2;
 }
 
-struct LnBackParams {
-    const uint4 *dy, *x;
-    const uint2 *codes;
-    const uint8_t *block_scales;
-    const float2 *stats;
-    const uint4 *scale;
-    const uint4 *dres;
-    uint4 *dx;
-    float *part; // [grid + B][2][D] partial column sums; CTA c's of batch b is number c + b
-    int64_t rows, T, vs8;
-    int F;      // fragments (of eight columns) per row
-    int blocks; // checkpoint blocks per row
-    int W;      // warps per team
-    int L;      // lanes per row (32 with W > 1)
-    int teams;
-    float inv_d;
-    bool hint_codes; // the codes' rows begin and end on 16 bytes, as the bulk hint wants them
-};
-
 // First row of CTA c of G.
 __host__ __device__ inline int64_t first_row(int64_t c, int64_t rows, int64_t G) { return c * rows / G; }
-
-__device__ __forceinline__ void team_barrier(int team, int threads)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
-}
-
-// Sums of N values over a warp: each step halves the lanes' values, the lanes of
-// the one half of a pair going on with the one half of them.  Value i ends in the
-// lanes whose upper bits are i (32 / N lanes each).
-template <int N>
-__device__ __forceinline__ float warp_sums(float (&v)[N], int lane)
-{
-    int off = 16;
-#pragma unroll
-    for (int n = N; n > 1; n /= 2, off /= 2) {
-        const bool upper = lane & off;
-#pragma unroll
-        for (int i = 0; i < n / 2; ++i) {
-            const float mine = upper ? v[i + n / 2] : v[i], other = upper ? v[i] : v[i + n / 2];
-            v[i] = __fadd_rn(mine, __shfl_xor_sync(kFull, other, off));
-        }
-    }
-    float s = v[0];
-#pragma unroll
-    for (int k = 32 / N / 2; k >= 1; k /= 2) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, k));
-    return s;
-}
 
 // K fragments per thread, R rows at a time.  MULTI: several rows share a warp
 // (K == R == W == 1).
@@ -340,27 +295,32 @@ __global__ void __launch_bounds__(threads_of(K, R), 1) ln_back_kernel(const LnBa
 }
 
 // dscale and dshift of batch b: the partials c + b of the CTAs c that had rows
-// of it, added in order: 64 threads a share of them each (at most three, all
-// under way at once), then the shares of a warp, then the warps'.  A block has 4
-// groups of four columns of [dscale | dshift].
-constexpr int kJoinThreads = 256, kJoinQuads = 4, kJoinShares = kJoinThreads / kJoinQuads;
+// of it, added in order: SHARES threads a share of them each (a few, all under way at
+// once), then the shares of a warp, then the warps'.  A block has 256 / SHARES
+// groups of four columns of [dscale | dshift].  With 64 shares whatever their number, a
+// batch of 4096 columns had 512 blocks: 22 us for 16 batches, 85 for 61.
+constexpr int kJoinThreads = 256;
+template <int SHARES>
 __global__ void __launch_bounds__(kJoinThreads)
     ln_back_join_kernel(const float4 *part, uint2 *dscale, uint2 *dshift, int64_t gs4, int64_t rows,
                         int64_t T, int64_t G, int D4, int tiles)
 {
-    __shared__ float4 s_sum[kJoinThreads / 32][kJoinQuads];
+    constexpr int kQuads = kJoinThreads / SHARES, kWarps = kJoinThreads / 32, kAcross = kQuads < 32 ? kQuads : 32;
+    __shared__ float4 s_sum[SHARES > 1 ? kWarps : 1][kAcross];
+    __shared__ int64_t s_cta[2];
     const unsigned b = blockIdx.x / (unsigned)tiles;
-    const int tid = threadIdx.x, mine = tid % kJoinQuads, share = tid / kJoinQuads;
-    const int quad = (int)(blockIdx.x - b * tiles) * kJoinQuads + mine;
+    const int tid = threadIdx.x, mine = tid % kQuads, share = tid / kQuads;
+    const int quad = (int)(blockIdx.x - b * tiles) * kQuads + mine;
     // the CTAs of the batch's first and last rows
-    auto cta_of = [&](int64_t row) {
+    if (tid < 2) {
+        const int64_t row = (b + tid) * T - tid;
         int64_t c = row * G / rows;
         while (first_row(c + 1, rows, G) <= row) ++c;
         while (first_row(c, rows, G) > row) --c;
-        return c;
-    };
-    const int64_t c0 = b == 0 ? 0 : rows > 0 ? cta_of(b * T) : 0;
-    const int64_t c1 = rows == 0 ? -1 : (b + 1) * T == rows ? G - 1 : cta_of((b + 1) * T - 1);
+        s_cta[tid] = c;
+    }
+    __syncthreads();
+    const int64_t c0 = s_cta[0], c1 = s_cta[1];
     grid_dependency_wait();
     allow_dependents();
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -373,24 +333,35 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (quad < 2 * D4) {
         const float4 *from = part + b * (int64_t)(2 * D4) + quad;
 #pragma unroll 3
-        for (int64_t c = c0 + share; c <= c1; c += kJoinShares) add(__ldcg(from + c * 2 * D4));
+        for (int64_t c = c0 + share; c <= c1; c += SHARES) add(__ldcg(from + c * 2 * D4));
     }
 #pragma unroll
-    for (int off = kJoinQuads; off < 32; off *= 2)
+    for (int off = kQuads; off < 32; off *= 2)
         add(make_float4(__shfl_xor_sync(kFull, v.x, off), __shfl_xor_sync(kFull, v.y, off),
                         __shfl_xor_sync(kFull, v.z, off), __shfl_xor_sync(kFull, v.w, off)));
-    if ((tid & 31) < kJoinQuads) s_sum[tid >> 5][mine] = v;
-    __syncthreads();
-    if (tid >= kJoinQuads || quad >= 2 * D4) return;
+    if (SHARES > 1) {
+        if ((tid & 31) < kAcross) s_sum[tid >> 5][mine] = v;
+        __syncthreads();
+        if (tid >= kQuads) return;
 #pragma unroll
-    for (int j = 1; j < kJoinThreads / 32; ++j) add(s_sum[j][mine]);
+        for (int j = 1; j < kWarps; ++j) add(s_sum[j][mine]);
+    }
+    if (quad >= 2 * D4) return;
     uint2 *to = quad < D4 ? dscale + b * gs4 + quad : dshift + b * gs4 + quad - D4;
     *to = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
 int64_t back_grid(int64_t rows) { return rows < sm_count() ? rows : sm_count(); }
 
-cudaError_t ready_join() { return allow_dynamic_smem(reinterpret_cast<const void *>(ln_back_join_kernel), 0); }
+// Calls f with the shares of a batch's partials: up to G / B + 2 of them.
+template <typename F>
+cudaError_t with_shares(int64_t B, int64_t G, F f)
+{
+    const int64_t most = (G + B - 1) / B + 1;
+    if (most > 16) return f(std::integral_constant<int, 64>());
+    if (most > 4) return f(std::integral_constant<int, 8>());
+    return f(std::integral_constant<int, 1>());
+}
 
 template <int K, int R, bool CKPT, bool RES, bool MULTI>
 cudaError_t launch_back(LnBackParams p, int grid, cudaStream_t s)
@@ -400,20 +371,13 @@ cudaError_t launch_back(LnBackParams p, int grid, cudaStream_t s)
     const int smem = ahead_of(K, R, CKPT, RES) * R * K * NT * (16 + (CKPT ? 8 : 16) + (RES ? 16 : 0)) +
                      2 * (NT / 32) * 2 * R * (int)sizeof(float);
     const auto fn = ln_back_kernel<K, R, CKPT, RES, MULTI>;
-    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
-    if (e == cudaSuccess) e = ready_join(); // before the first launch
+    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(fn), smem);
     return e != cudaSuccess ? e : launch_overlapped(fn, grid, NT, smem, s, p);
 }
 
 } // namespace
 
-int64_t ln_modulate_backward_workspace(int64_t B, int64_t T, int64_t D)
-{
-    const int64_t rows = B * T;
-    return rows == 0 ? 0 : (back_grid(rows) + B) * 2 * D * (int64_t)sizeof(float);
-}
-
-cudaError_t launch_ln_modulate_backward(const LnBackProblem &q, cudaStream_t s)
+LnBackParams ln_back_params(const LnBackProblem &q)
 {
     LnBackParams p = {};
     p.dy = static_cast<const uint4 *>(q.dy);
@@ -432,46 +396,41 @@ cudaError_t launch_ln_modulate_backward(const LnBackProblem &q, cudaStream_t s)
     p.blocks = (int)((q.D + 31) / 32);
     p.inv_d = 1.0f / (float)q.D;
     p.hint_codes = p.F % 2 == 0 && reinterpret_cast<uintptr_t>(q.codes) % 16 == 0;
+    const LnBackCut c = ln_back_cut(p.F);
+    p.W = c.W;
+    p.L = c.L;
+    return p;
+}
+
+int64_t ln_modulate_backward_workspace(int64_t B, int64_t T, int64_t D)
+{
+    return ln_back_is_short(B, T, D) ? 0 : (back_grid(B * T) + B) * 2 * D * (int64_t)sizeof(float);
+}
+
+cudaError_t launch_ln_modulate_backward(const LnBackProblem &q, cudaStream_t s)
+{
+    if (ln_back_is_short(q.B, q.T, q.D)) return launch_ln_back_short(q, s);
+    const LnBackParams p = ln_back_params(q);
     const int64_t G = back_grid(p.rows);
-    const int D4 = (int)(q.D / 4), tiles = (2 * D4 + kJoinQuads - 1) / kJoinQuads;
-    if (p.rows > 0) {
-        // a warp per row up to five fragments a lane; else teams of up to eight warps,
-        // several rows at a time where the registers last
-        const int K = p.F <= 160 ? (p.F + 31) / 32 : p.F <= 256 ? 2 : p.F <= 384 ? 3 : p.F <= 512 ? 2 : 4;
-        p.W = (p.F + 32 * K - 1) / (32 * K);
-        p.L = 32;
-        while (p.W == 1 && p.L / 2 >= p.F) p.L /= 2;
-        const bool ckpt = q.x == nullptr, res = q.dres != nullptr;
-        auto go = [&](auto k, auto rows, auto multi) {
-            constexpr int KK = decltype(k)::value, R = decltype(rows)::value;
+    const int D4 = (int)(q.D / 4);
+    return with_shares(q.B, G, [&](auto shares) {
+        constexpr int kQuads = kJoinThreads / decltype(shares)::value;
+        const auto join = ln_back_join_kernel<decltype(shares)::value>;
+        const int tiles = (2 * D4 + kQuads - 1) / kQuads;
+        // the call's kernels are made ready before the first launch
+        cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(join), 0);
+        if (e != cudaSuccess) return e;
+        e = with_cut(ln_back_cut(p.F), [&](auto k, auto rows, auto multi) {
+            constexpr int K = decltype(k)::value, R = decltype(rows)::value;
             constexpr bool M = decltype(multi)::value;
-            const int grid = (int)G;
-            if (ckpt) return res ? launch_back<KK, R, true, true, M>(p, grid, s) : launch_back<KK, R, true, false, M>(p, grid, s);
-            return res ? launch_back<KK, R, false, true, M>(p, grid, s) : launch_back<KK, R, false, false, M>(p, grid, s);
-        };
-        const std::false_type no;
-        const std::integral_constant<int, 1> one;
-        const std::integral_constant<int, 2> two;
-        const std::integral_constant<int, 3> three;
-        const std::integral_constant<int, 4> four;
-        const std::integral_constant<int, 5> five;
-        const cudaError_t e = p.L < 32                ? go(one, one, std::true_type())
-                              : K == 1                ? go(one, one, no)
-                              : K == 2 && p.W == 1    ? go(two, one, no)
-                              : K == 2                ? go(two, four, no)
-                              : K == 3 && p.W == 1    ? go(three, one, no)
-                              : K == 3                ? go(three, two, no)
-                              : K == 4                ? go(four, one, no)
-                                                      : go(five, one, no);
+            if (!p.x) return p.dres ? launch_back<K, R, true, true, M>(p, (int)G, s) : launch_back<K, R, true, false, M>(p, (int)G, s);
+            return p.dres ? launch_back<K, R, false, true, M>(p, (int)G, s) : launch_back<K, R, false, false, M>(p, (int)G, s);
+        });
         if (e != cudaSuccess) return e;
-    }
-    if (p.rows == 0) {
-        const cudaError_t e = ready_join();
-        if (e != cudaSuccess) return e;
-    }
-    return launch_overlapped(ln_back_join_kernel, (int)(q.B * tiles), kJoinThreads, 0, s,
-                             static_cast<const float4 *>(q.workspace), static_cast<uint2 *>(q.dscale),
-                             static_cast<uint2 *>(q.dshift), q.gs / 4, p.rows, p.T, G, D4, tiles);
+        return launch_overlapped(join, (int)(q.B * tiles), kJoinThreads, 0, s, static_cast<const float4 *>(q.workspace),
+                                 static_cast<uint2 *>(q.dscale), static_cast<uint2 *>(q.dshift), q.gs / 4, p.rows, p.T, G,
+                                 D4, tiles);
+    });
 }
 
 } // namespace dan

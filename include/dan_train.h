@@ -72,8 +72,8 @@ int dan_can_use_ln_modulate_save(const dan_bf16 *x, const dan_bf16 *scale, const
  * slices of the embedding's gradient.  dres [B, T, D] (or NULL): a gradient
  * that reaches x by another way, added before the rounding.  In place: dx == dy
  * or dx == dres.  T == 0 writes zeros to dscale and dshift.  B * D <= 2^30.
- * workspace: dan_ln_modulate_backward_workspace(B, T, D) bytes, of the current
- * device, 16-byte aligned, this call's alone until it has completed: two calls
+ * workspace: dan_ln_modulate_backward_workspace(B, T, D) bytes (0 for many short
+ * batches), of the current device, 16-byte aligned, this call's alone until it has completed: two calls
  * that may run at the same time, or two captured graphs that may, need one
  * each. */
 int64_t dan_ln_modulate_backward_workspace(int64_t B, int64_t T, int64_t D);

@@ -166,3 +166,88 @@ def test_means_of_a_level_far_above_the_spread(N, S, C, groups):
     std = (v - want[:, None, :, None]).square().mean((1, 3)).add(EPS).sqrt()
     # each join's means are off by so much at most, and what they add to the squares too
     assert bool(((rstd * std - 1).abs() <= 2 * lim * rstd + ref.E * (1 + far * rstd)).all())
+
+
+# ------------------------------------------------------------- LayerNorm gradients
+
+def ln_back_case(B, T, D, ckpt, res, seed=0):
+    g = gen(seed)
+    x, emb = normal(g, B, T, D, mean=0.5), normal(g, B, 3 * D, std=0.3)
+    saved = ops.ln_modulate_save(x, emb[:, :D], emb[:, D:2 * D], EPS, checkpoint=ckpt)[1]
+    dy = normal(g, B, T, D, std=0.1, mean=0.02)
+    return x, emb[:, :D], saved, dy, normal(g, B, T, D, std=0.1) if res else None
+
+
+def check_ln_back(got, x, scale, saved, dy, dres):
+    B, T, D = dy.shape
+    v = x.double() if saved[1] is None else ref.restore(*saved[1:])
+    want, err = ref.ln_backward(dy, v, saved[0], scale, dres, min(T, -(-B * T // min(max(B * T, 1), 148))))
+    for a, w, e, name in zip(got, want, err, ("dx", "dscale", "dshift")):
+        ref.assert_near(a, w, e, name)
+
+
+# a width of each cut: several rows a warp, one to five fragments a lane, teams of three to eight warps
+CUT_WIDTHS = [8, 16, 40, 136, 256, 264, 520, 776, 1032, 1280, 1288, 2048, 2056, 3064, 3080, 4096, 4104, 6152, 8192]
+
+
+@pytest.mark.parametrize("D", CUT_WIDTHS)
+@pytest.mark.parametrize("ckpt,res", [(True, False), (False, True), (True, True), (False, False)])
+def test_many_short_batches(D, ckpt, res):
+    """Of one row each, of three, and of none, the gradients' places as slices of one embedding."""
+    for B, T in ((700, 1), (401, 3), (350, 0)):
+        x, scale, saved, dy, dres = ln_back_case(B, T, D, ckpt, res)
+        demb = torch.full((B, 4 * D), 77, dtype=BF16, device="cuda")
+        got = ops.ln_modulate_backward(dy, None if ckpt else x, scale, saved, dres=dres, dscale=demb[:, 2 * D:3 * D],
+                                       dshift=demb[:, D:2 * D])
+        check_ln_back(got, x, scale, saved, dy, dres)
+        assert bool((demb[:, :D] == 77).all()) and bool((demb[:, 3 * D:] == 77).all())
+
+
+@pytest.mark.parametrize("D", CUT_WIDTHS)
+@pytest.mark.parametrize("ckpt", [True, False])
+def test_a_rows_dx_is_its_own_at_every_width(D, ckpt):
+    """The same bits alone, among the rows of a long batch and of short ones, in place too; a bad
+    row spoils no other."""
+    x, scale, saved, dy, dres = ln_back_case(1, 900, D, ckpt, True)
+    keep = lambda s, at: tuple(None if t is None else t[:, at].contiguous() for t in s)  # noqa: E731
+    dx = ops.ln_modulate_backward(dy, None if ckpt else x, scale, saved, dres=dres)[0]
+    for at in (slice(0, 1), slice(17, 40), slice(899, 900), slice(100, 700)):
+        cut = lambda t: t[:, at].contiguous()  # noqa: E731
+        one = ops.ln_modulate_backward(cut(dy), None if ckpt else cut(x), scale, keep(saved, at), dres=cut(dres))[0]
+        assert torch.equal(one, dx[:, at]), at
+    for B, T in ((900, 1), (450, 2), (300, 3), (30, 30)):
+        as_batches = lambda t: None if t is None else t.view(B, T, -1)  # noqa: E731
+        d = as_batches(dy.clone())
+        got = ops.ln_modulate_backward(d, None if ckpt else as_batches(x), scale.expand(B, D).contiguous(),
+                                       tuple(map(as_batches, saved)), dres=as_batches(dres), dx=d)[0]
+        assert torch.equal(got.view(1, 900, D), dx), (B, T)
+        bad = as_batches(dy.clone())
+        bad[-1, 0, 3], bad[11, -1, D - 1] = float("nan"), float("inf")
+        got = ops.ln_modulate_backward(bad, None if ckpt else as_batches(x), scale.expand(B, D).contiguous(),
+                                       tuple(map(as_batches, saved)), dres=as_batches(dres))[0].view(1, 900, D)
+        rows = [i for i in range(900) if i not in ((B - 1) * T, 12 * T - 1)]
+        assert torch.equal(got[:, rows], dx[:, rows])
+
+
+@pytest.mark.parametrize("B", [2, 9, 11, 16, 50, 52, 153, 290, 310])
+@pytest.mark.parametrize("T,D", [(40, 264), (7, 4096), (300, 40)])
+def test_batches_of_few_and_many_partials(B, T, D):
+    """The joins of 64, of 8 and of one thread a column."""
+    case = ln_back_case(B, T, D, True, False)
+    check_ln_back(ops.ln_modulate_backward(case[3], None, case[1], case[2]), *case)
+
+
+@pytest.mark.parametrize("B,T,D", [(20000, 1, 64), (4000, 8, 64), (8000, 1, 1024), (1953, 8, 1024), (3906, 1, 4096),
+                                   (488, 8, 4096), (61, 64, 4096)])
+def test_short_batches_take_less_than_torch(B, T, D):
+    """A join of 64 threads a column and batch took up to nine times as long as these operations."""
+    x, scale, saved, dy, _ = ln_back_case(B, T, D, False, False)
+
+    def plain():
+        n = (x.float() - saved[0][..., :1]) * saved[0][..., 1:]
+        d = dy.float()
+        g = d * (1 + scale.float()[:, None])
+        dx = saved[0][..., 1:] * (g - g.mean(-1, keepdim=True) - n * (g * n).mean(-1, keepdim=True))
+        return dx.bfloat16(), (d * n).sum(1).bfloat16(), d.sum(1).bfloat16()
+
+    assert device_us(lambda: ops.ln_modulate_backward(dy, x, scale, saved)) < device_us(plain)

@@ -31,3 +31,26 @@ def test_gradients_of_nothing(fake):
         good, size = fake(CALLS + f"print(json.dumps([{call}, lib.dan_group_norm_backward_workspace(3, 0, 512, 32, 0, 0)]))")
         assert good[0] == OK and len(good[1]) == 1 and size == 0
         assert fake(CALLS + f"fail_at[SET] = 1\nprint(json.dumps({call}))") == [ECUDA, []]
+
+
+def test_gradients_of_short_and_long_batches(fake):
+    """Many short batches: one kernel without a workspace; else the rows' and a join whose blocks have
+    as many threads a column as a batch can have partials."""
+    sizes = [(65536, 1, 64), (1953, 8, 1024), (700, 0, 4096), (488, 32, 1024), (1, 4216, 4096), (16, 256, 4096),
+             (61, 64, 4096)]
+    calls = "".join(f"ln_back(B={b}, T={t}, D={d}), " for b, t, d in sizes)
+    works = "".join(f"lib.dan_ln_modulate_backward_workspace({b}, {t}, {d}), " for b, t, d in sizes)
+    got, work = fake(CALLS + f"print(json.dumps([[{calls}], [{works}]]))")
+    assert all(st == OK for st, _ in got)
+    assert [len(grids) for _, grids in got] == [1, 1, 1, 2, 2, 2, 2]
+    assert [w > 0 for w in work] == [False] * 3 + [True] * 4
+    assert got[0][1][0][0] == 3 * 152
+    # blocks of the join: 4, 32 and 256 columns' quads of [dscale | dshift] each
+    assert [grids[1][0] for _, grids in got[4:]] == [512, 16 * 64, 61 * 8]
+
+
+@pytest.mark.parametrize("call,sets", [("ln_back(B=4000, T=1, D=64)", 1), ("ln_back(B=61, T=64, D=4096)", 3)])
+def test_gradients_that_cannot_run_whole_launch_nothing(fake, call, sets):
+    for n in range(1, sets + 1):
+        first, counted, again = fake(CALLS + f"fail_at[SET] = {n}\na = {call}\nprint(json.dumps([a, count[SET], {call}]))")
+        assert first == [ECUDA, []] and counted == n and again[0] == OK, n
