@@ -21,7 +21,9 @@
  *    follow from S, C, the groups, the type, and whether there is a checkpoint).
  *    dweight and dbias, and a LayerNorm's dscale and dshift, are sums over rows
  *    in an order that follows from the sizes and the GPU's SM count.
- *  - A call is one to four launches; one that cannot run whole launches none.
+ *  - A call is one to four launches (gradients of parameters over more than 256
+ *    images one more for each further factor of 256); one that cannot run whole
+ *    launches none.
  *  - Not a number and infinities pass as the formulas have them: a row or group
  *    that holds one gives NaN, others are not touched.  Squares of differences
  *    are summed in fp32: a row or group whose sum leaves its range (differences

@@ -251,3 +251,50 @@ def test_short_batches_take_less_than_torch(B, T, D):
         return dx.bfloat16(), (d * n).sum(1).bfloat16(), d.sum(1).bfloat16()
 
     assert device_us(lambda: ops.ln_modulate_backward(dy, x, scale, saved)) < device_us(plain)
+
+
+# ------------------------------------------------------------- group norms of many images
+
+@pytest.mark.parametrize("N,S,C,groups", [(255, 2, 64, 8), (256, 1, 40, 5), (257, 3, 32, 4), (1000, 1, 96, 3),
+                                          (65537, 1, 16, 2), (70000, 2, 8, 1), (300, 700, 24, 3)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_parameter_gradients_of_many_images(N, S, C, groups, dtype):
+    """Sums of 256 images at a time; the same bits every time."""
+    g = gen(6)
+    x, dy = normal(g, N, S, C, mean=0.5, dtype=dtype), normal(g, N, S, C, std=0.1, mean=0.02, dtype=dtype)
+    w, b = normal(g, C, std=0.3, mean=1.0, dtype=dtype), normal(g, C, std=0.3, dtype=dtype)
+    emb = normal(g, N, 2 * C, std=0.3, dtype=dtype)
+    s, t = emb[:, :C], emb[:, C:]
+    saved = ops.group_norm_save(x, groups, w, b, 0.1, act="silu", scale=s, shift=t, checkpoint=False)[1]
+    got = ops.group_norm_backward(dy, x, groups, w, b, saved, act="silu", scale=s, shift=t)
+    want, err = ref.gn_backward(dy, x.double(), groups, w, b, saved[0], "silu", s, t)
+    for a, u, e, name in zip(got, want, err, ("dx", "dweight", "dbias", "dscale", "dshift")):
+        ref.assert_near(a, u, e, name)
+    again = ops.group_norm_backward(dy, x, groups, w, b, saved, act="silu", scale=s, shift=t)
+    assert all(torch.equal(u, v) for u, v in zip(got, again))
+
+
+def plain_group_norm_backward(dy, x, groups, w, b, saved):
+    """The formulas in elementary torch operations."""
+    N, S, C = x.shape
+    mean, rstd = (saved[0][:, None, :, i].repeat_interleave(C // groups, 2) for i in range(2))
+    n = (x.float() - mean) * rstd
+    z = n * w.float() + b.float()
+    p = 1 / (1 + (-z).exp())
+    dz = dy.float() * (p * (1 + z * (1 - p)))
+    g = dz * w.float()
+    avg = lambda v: v.unflatten(2, (groups, -1)).mean((1, 3)).repeat_interleave(C // groups, 1)[:, None]  # noqa: E731
+    dx = (rstd * (g - avg(g) - n * avg(g * n))).to(x.dtype)
+    return dx, (dz * n).sum((0, 1)).to(w.dtype), dz.sum((0, 1)).to(b.dtype)
+
+
+@pytest.mark.parametrize("N,S,C,groups", [(65536, 1, 64, 8), (4096, 16, 320, 32)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_gradients_of_many_images_take_less_than_torch(N, S, C, groups, dtype):
+    """A chain of N / 8 loads for each parameter took six times as long as these operations."""
+    g = gen(7)
+    x, dy = normal(g, N, S, C, dtype=dtype), normal(g, N, S, C, dtype=dtype)
+    w, b = normal(g, C, dtype=dtype), normal(g, C, dtype=dtype)
+    saved = ops.group_norm_save(x, groups, w, b, EPS, checkpoint=False)[1]
+    assert device_us(lambda: ops.group_norm_backward(dy, x, groups, w, b, saved, act="silu")) < \
+        device_us(lambda: plain_group_norm_backward(dy, x, groups, w, b, saved))

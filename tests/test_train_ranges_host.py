@@ -54,3 +54,14 @@ def test_gradients_that_cannot_run_whole_launch_nothing(fake, call, sets):
     for n in range(1, sets + 1):
         first, counted, again = fake(CALLS + f"fail_at[SET] = {n}\na = {call}\nprint(json.dumps([a, count[SET], {call}]))")
         assert first == [ECUDA, []] and counted == n and again[0] == OK, n
+
+
+def test_parameter_gradients_of_many_images(fake):
+    """A launch more for each further factor of 256 images; where one cannot be made ready, none."""
+    got = fake(CALLS + "print(json.dumps([gn_back(N=n, S=1) for n in (1, 2, 256, 257, 65536, 65537)]))")
+    assert all(st == OK for st, _ in got) and [len(grids) for _, grids in got] == [1, 2, 2, 3, 3, 4]
+    assert all(grids[-1][:2] == [1, 16] for _, grids in got[1:])
+    for n in range(1, 4):
+        first, counted, again = fake(CALLS + f"fail_at[SET] = {n}\na = gn_back(N=300, S=1)\n"
+                                     "print(json.dumps([a, count[SET], gn_back(N=300, S=1)]))")
+        assert first == [ECUDA, []] and counted == n and again[0] == OK and len(again[1]) == 3
