@@ -346,18 +346,21 @@ constexpr int kSlabCluster = 3; // log2 of the largest portable cluster
 // The shared memory of a CTA: up to 64 KB of rows and what joins them.
 constexpr int64_t kSlabRows = 64 * 1024, kSlabRoom = 80 * 1024;
 
-// bytes: of a fragment in shared memory; extra: further bytes per thread.
+// bytes: of a fragment in shared memory; extra: further bytes per thread; fill: a
+// slab of fewer fragments than that is made wider.
 // Segments of 128 bytes of a row where such slabs fit, else of 64 (of 32 they took
 // 17.6 us for a [1, 128 x 128, 512] image, the passes 11.7); as few CTAs, and as
 // few threads of eight fragments, as do: many small ones did better for one image
 // (a [1, 32 x 32, 640] one: 6.7 us with 32 KB and four fragments, 7.7 so), worse
 // for many (16 of them: 20.3 and 15.8), and which it is may not count.
-inline GnSlab gn_slab(int64_t S, int64_t C, int64_t groups, int type, bool checkpoint, int bytes, int extra)
+inline GnSlab gn_slab(int64_t S, int64_t C, int64_t groups, int type, bool checkpoint, int bytes, int extra,
+                      int64_t fill)
 {
     GnSlab c = {};
     const int64_t E = type_channels(type), F = C / E, step = gn_step(C / groups, checkpoint) / E;
     for (int64_t segment = 128; segment >= 64; segment /= 2) {
         int64_t Ft = (segment / 16 + step - 1) / step * step;
+        while (Ft < F && 2 * Ft * S <= fill) Ft *= 2;
         if (Ft > F) Ft = F;
         if (Ft > 256 || (F + Ft - 1) / Ft > 65535) continue; // (slabs lie along a grid's y)
         int log_cs = 0;

@@ -595,7 +595,9 @@ GnSlab backward_slab(int64_t S, int64_t C, int64_t groups, int type, bool checkp
 {
     const int E = (int)type_channels(type);
     // (a slab need not hold whole blocks: their scales are read only)
-    return gn_slab(S, C, groups, type, false, checkpoint ? 16 + E + 1 : 32, E * (int)sizeof(float2));
+    // (wider ones where there are few rows gained in many images, [16384, 1, 1024] 0.88 ->
+    // 0.42 ms, but lost in one, 3.8 -> 10.8 us: a thread's channels go one by one)
+    return gn_slab(S, C, groups, type, false, checkpoint ? 16 + E + 1 : 32, E * (int)sizeof(float2), 0);
 }
 
 // Rows of a thread's ring (Ring::A).

@@ -65,3 +65,13 @@ def test_parameter_gradients_of_many_images(fake):
         first, counted, again = fake(CALLS + f"fail_at[SET] = {n}\na = gn_back(N=300, S=1)\n"
                                      "print(json.dumps([a, count[SET], gn_back(N=300, S=1)]))")
         assert first == [ECUDA, []] and counted == n and again[0] == OK and len(again[1]) == 3
+
+
+def test_slabs_of_few_positions(fake):
+    """A fragment for each thread of the smallest CTA, whole groups; cut alike for any number of
+    images."""
+    got = fake(CALLS + "print(json.dumps([gn(N=n, S=s, C=1024) for s in (1, 2, 8, 64) for n in (1, 500)]))")
+    assert all(st == OK and len(grids) == 1 for st, grids in got)
+    # fragments of a row: 128
+    assert [grids[0][:3] for _, grids in got[::2]] == [[1, 2, 64], [1, 4, 64], [1, 16, 64], [1, 16, 64]]
+    assert all(b[1][0][0] == 500 * a[1][0][0] and b[1][0][1:] == a[1][0][1:] for a, b in zip(got[::2], got[1::2]))
