@@ -717,6 +717,8 @@ def _group_norm(x, groups, weight, bias, eps, act, scale, shift, out, save: bool
     N, S, C = _images(x, "x")
     device, dtype, shape = x.get_device(), x.dtype, x.shape
     groups, act = int(groups), _act(act)
+    if not 1 <= groups <= C:  # before anything is allocated by their number
+        raise DanError(DAN_EINVAL if groups < 1 else DAN_EUNSUPPORTED, "dan_group_norm")
     ptype, vs = _gains(weight, bias, scale, shift, dtype, N, C, device, "x")
     if out is None:
         out = torch.empty_like(x)
@@ -724,7 +726,7 @@ def _group_norm(x, groups, weight, bias, eps, act, scale, shift, out, save: bool
         _like(out, "out", dtype, shape, device, "x")
     stats = codes = scales = None
     if save:
-        stats = torch.empty((N, max(groups, 0), 2), dtype=_F32, device=x.device)
+        stats = torch.empty((N, groups, 2), dtype=_F32, device=x.device)
         if checkpoint:
             if C % 32:
                 raise ValueError(f"checkpoint: expected channels in blocks of 32, got {C}")

@@ -337,3 +337,17 @@ def test_group_norm_of_few_positions(S, C, groups, dtype):
         assert torch.equal(codes, c) and torch.equal(scales, s)
     one = ops.group_norm_save(x[5:6], groups, w, b, 0.1, act="silu", checkpoint=ckpt)
     assert torch.equal(one[0], y[5:6]) and torch.equal(one[1][0], stats[5:6])
+
+
+@pytest.mark.parametrize("groups", [65, 1 << 40, (1 << 64) + 8, 0, -8])
+def test_more_groups_than_channels_are_refused(groups):
+    """By their number alone, with nothing allocated for them."""
+    x = normal(gen(0), 4, 100, 64)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    for call in (lambda: ops.group_norm_save(x, groups, None, None, EPS, checkpoint=False),
+                 lambda: ops.group_norm(x, groups, None, None, EPS)):
+        with pytest.raises(ops.DanError):
+            call()
+    assert torch.cuda.max_memory_allocated() == before
