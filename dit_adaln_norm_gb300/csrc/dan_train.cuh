@@ -57,14 +57,4 @@ __device__ __forceinline__ void cp_async8(void *smem_dst, const void *gmem_src)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(smem_dst)), "l"(gmem_src) : "memory");
 }
 
-// The eight values of a fragment of codes, times their block's scale.
-__device__ __forceinline__ void decode8(const uint2 &c, float scale, float2 (&v)[4])
-{
-    const float2 s = dup2(scale);
-    v[0] = mul2(e4m3_pair(c.x & 0xFFFFu), s);
-    v[1] = mul2(e4m3_pair(c.x >> 16), s);
-    v[2] = mul2(e4m3_pair(c.y & 0xFFFFu), s);
-    v[3] = mul2(e4m3_pair(c.y >> 16), s);
-}
-
 } // namespace dan
