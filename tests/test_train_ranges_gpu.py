@@ -351,3 +351,116 @@ def test_more_groups_than_channels_are_refused(groups):
         with pytest.raises(ops.DanError):
             call()
     assert torch.cuda.max_memory_allocated() == before
+
+
+def gn_case(N, S, C, dtype, mod, seed=0):
+    g = gen(seed)
+    x = normal(g, N, S, C, mean=0.5, dtype=dtype)
+    x *= torch.exp(0.3 * torch.randn(C, generator=g, device="cuda")).to(dtype)
+    w, b = normal(g, C, std=0.3, mean=1.0, dtype=dtype), normal(g, C, std=0.3, dtype=dtype)
+    emb = normal(g, N, 2 * C, std=0.3, dtype=dtype)
+    s, t = (emb[:, :C], emb[:, C:]) if mod else (None, None)
+    return x, w, b, s, t, normal(g, N, S, C, std=0.1, mean=0.02, dtype=dtype)
+
+
+def check_gn_case(x, groups, w, b, s, t, dy, ckpt, terms=128):
+    """Both directions; `terms`: the roundings of a sum's longest chain."""
+    k = terms / 128
+    y, saved = ops.group_norm_save(x, groups, w, b, EPS, act="silu", scale=s, shift=t, checkpoint=ckpt)
+    want, st, ey, est = ref.gn_forward(x, groups, w, b, EPS, "silu", s, t)
+    ref.assert_near(y, want, k * ey, "y")
+    ref.assert_near(saved[0], st, k * est, "stats")
+    if ckpt:
+        c, q = ref.checkpoint(x)
+        assert torch.equal(saved[1], c) and torch.equal(saved[2], q)
+    del y, want, ey
+    v = ref.restore(*saved[1:]) if ckpt else x.double()
+    got = ops.group_norm_backward(dy, None if ckpt else x, groups, w, b, saved, act="silu", scale=s, shift=t)
+    want, err = ref.gn_backward(dy, v, groups, w, b, saved[0], "silu", s, t)
+    for a, u, e, name in zip(got, want, err, ("dx", "dweight", "dbias", "dscale", "dshift")):
+        if u is not None:
+            ref.assert_near(a, u, k * e, name)
+
+
+# in passes, with tiles of 250 and 230 fragments (fp32), 250 and 70, 240, 240 and 40, 255 and 225; in slabs
+# whose last one is narrower
+@pytest.mark.parametrize("N,S,C,groups", [(1, 20000, 1920, 48), (2, 9000, 2560, 32), (1, 6000, 4160, 13),
+                                          (1, 7001, 3840, 32), (1, 5000, 2600, 13), (3, 50, 2600, 13), (2, 300, 1000, 25),
+                                          (2, 70, 416, 13)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_tiles_whose_last_one_is_narrower(N, S, C, groups, dtype):
+    for ckpt in (True, False) if C % 32 == 0 else (False,):
+        x, w, b, s, t, dy = gn_case(N, S, C, dtype, ckpt)
+        check_gn_case(x, groups, w, b, s, t, dy, ckpt)
+
+
+@pytest.mark.parametrize("ckpt", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_large_images_in_64_bits(dtype, ckpt):
+    """Rows as wide as a CTA and so many that a thread adds some 165 of them in turn, in the gradients
+    330 (608 and 304 chunks), and a join as many chunks."""
+    x, w, b, s, t, dy = gn_case(1, 100000, 1024 if dtype is FP32 else 2048, dtype, True)
+    check_gn_case(x, 32, w, b, s, t, dy, ckpt, terms=330 + 128)
+
+
+class Buffers:
+    """Buffers of exactly the bytes that a call needs, between bytes that it must not write."""
+
+    def __init__(self):
+        self.all = []
+
+    def out(self, nbytes, align=16, pad=1024):
+        buf = torch.full((nbytes + 2 * pad + align,), 0xA5, dtype=U8, device="cuda")
+        at = pad + align if align < 16 else pad          # no better aligned than it needs
+        self.all.append((buf, at, nbytes))
+        assert (buf.data_ptr() + at) % align == 0
+        return buf.data_ptr() + at
+
+    def check(self):
+        torch.cuda.synchronize()
+        for buf, at, n in self.all:
+            assert bool((buf[:at] == 0xA5).all()) and bool((buf[at + n:] == 0xA5).all()), (n, at)
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 1, 8), (3, 41, 24), (2, 67, 1160), (500, 3, 40), (1, 333, 4104), (2, 9, 1016),
+                                   (16, 40, 520), (60, 7, 2056), (1, 200, 1024)])
+def test_ln_calls_stay_in_buffers_of_their_size(B, T, D):
+    x, scale, _, dy, _ = ln_back_case(B, T, D, False, False)
+    scale = scale.contiguous()
+    rows, blocks, lib = B * T, (D + 31) // 32, ops.load()
+    b = Buffers()
+    y, stats, codes, scales = b.out(rows * D * 2), b.out(rows * 8, 8), b.out(rows * D, 8), b.out(rows * blocks, 1)
+    ops._on(0, "dan_ln_modulate_save", x.data_ptr(), scale.data_ptr(), scale.data_ptr(), D, y, stats, codes, scales,
+            B, T, D, EPS)
+    b.check()
+    size = lib.dan_ln_modulate_backward_workspace(B, T, D)
+    for from_x in (False, True):
+        dx, dscale, dshift, work = b.out(rows * D * 2), b.out(B * D * 2), b.out(B * D * 2), b.out(size)
+        ops._on(0, "dan_ln_modulate_backward", dy.data_ptr(), x.data_ptr() if from_x else None,
+                None if from_x else codes, None if from_x else scales, stats, scale.data_ptr(), D, None, dx, dscale,
+                dshift, D, B, T, D, work if size else None, size)
+        b.check()
+
+
+@pytest.mark.parametrize("N,S,C,groups", [(1, 1, 8, 1), (3, 5, 96, 3), (2, 77, 320, 32), (300, 2, 64, 8), (1, 20001, 64, 8),
+                                          (2, 9001, 96, 3), (1, 5003, 2560, 32), (3, 3001, 1056, 33), (1, 300001, 8, 8)])
+@pytest.mark.parametrize("ty,dtype", [(0, BF16), (1, FP16), (2, FP32)])
+def test_gn_calls_stay_in_buffers_of_their_size(N, S, C, groups, ty, dtype):
+    x, w, b_, s, t, dy = gn_case(N, S, C, dtype, True)
+    s, t = s.contiguous(), t.contiguous()
+    es, lib, n = x.element_size(), ops.load(), N * S * C
+    ckpt = C % 32 == 0
+    b = Buffers()
+    y, stats = b.out(n * es), b.out(N * groups * 8, 8)
+    codes, scales = (b.out(n, 8), b.out(n // 32, 1)) if ckpt else (None, None)
+    size = lib.dan_group_norm_workspace(N, S, C, groups, ty, int(ckpt))
+    ops._on(0, "dan_group_norm", x.data_ptr(), ty, w.data_ptr(), b_.data_ptr(), ty, s.data_ptr(), t.data_ptr(), C, 1, y,
+            stats, codes, scales, N, S, C, groups, EPS, b.out(size) if size else None, size)
+    b.check()
+    for from_x in (True, False) if ckpt else (True,):
+        size = lib.dan_group_norm_backward_workspace(N, S, C, groups, ty, int(not from_x))
+        dx, dw, db, ds, dt = b.out(n * es), b.out(C * es), b.out(C * es), b.out(N * C * es), b.out(N * C * es)
+        ops._on(0, "dan_group_norm_backward", dy.data_ptr(), x.data_ptr() if from_x else None, ty,
+                None if from_x else codes, None if from_x else scales, stats, w.data_ptr(), b_.data_ptr(), ty, s.data_ptr(),
+                t.data_ptr(), C, 1, dx, dw, db, ds, dt, C, N, S, C, groups, b.out(size) if size else None, size)
+        b.check()
