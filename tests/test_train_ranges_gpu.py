@@ -464,3 +464,18 @@ def test_gn_calls_stay_in_buffers_of_their_size(N, S, C, groups, ty, dtype):
                 None if from_x else codes, None if from_x else scales, stats, w.data_ptr(), b_.data_ptr(), ty, s.data_ptr(),
                 t.data_ptr(), C, 1, dx, dw, db, ds, dt, C, N, S, C, groups, b.out(size) if size else None, size)
         b.check()
+
+
+def test_gradients_of_narrow_rows_take_about_as_long_as_of_wide_ones():
+    """Of as many bytes, replayed.  A hint to the L2 for each row at a call's start made it three times."""
+    times = []
+    for T, D in ((1 << 17, 8), (1 << 10, 1024)):
+        x, scale, saved, dy, dres = ln_back_case(1, T, D, False, True)
+        ops.ln_modulate_backward(dy, x, scale, saved, dres=dres)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                ops.ln_modulate_backward(dy, x, scale, saved, dres=dres)
+        times.append(device_us(graph.replay))
+    assert times[0] < 1.8 * times[1], times
