@@ -42,6 +42,7 @@ struct GnBackParams {
     int chunks;    // of a CTA of the first kernel
     float keep;    // share of a chunk's rows that the L2 is to hold
     int log_cs, M; // slabs: CTAs of a cluster, rows of a thread at most
+    int log_join;  // slabs: log2 of the lanes that add up a group's channels together
 };
 
 // A thread's P pairs of channels.  UNI: they lie in one group.
@@ -568,12 +569,28 @@ __global__ void __launch_bounds__(512, 1) gn_back_slab_kernel(const GnBackParams
     }
     if (cs > 1) cluster_arrive(); // nobody reads this CTA's sums after the wait below
     __syncthreads();
-    for (int g = tid >> 5; g < at.groups; g += NT >> 5) {
-        float2 t = make_float2(0.0f, 0.0f);
-        for (int c = lane; c < p.g.per; c += 32) t = add2(t, s_all[g * p.g.per + c]);
-        t.x = lane_sum(t.x, 32);
-        t.y = lane_sum(t.y, 32);
-        if (lane == 0) s_mean[g] = make_float2(__fdiv_rn(t.x, p.count), __fdiv_rn(t.y, p.count));
+    // a group's means, by a warp or, of up to 16 channels, by 2^log_join lanes (with a
+    // warp each, groups of one channel took most of a CTA's time: the gradient of
+    // [1, 8 x 8, 64] in 64 groups 16.1 us, so 6.3)
+    auto finish = [&](int g, float2 t) { s_mean[g] = make_float2(__fdiv_rn(t.x, p.count), __fdiv_rn(t.y, p.count)); };
+    if (p.log_join == 5) {
+        for (int g = tid >> 5; g < at.groups; g += NT >> 5) {
+            float2 t = make_float2(0.0f, 0.0f);
+            for (int c = lane; c < p.g.per; c += 32) t = add2(t, s_all[g * p.g.per + c]);
+            t.x = lane_sum(t.x, 32);
+            t.y = lane_sum(t.y, 32);
+            if (lane == 0) finish(g, t);
+        }
+    } else {
+        const int lanes = 1 << p.log_join, c = lane & (lanes - 1);
+        for (int g0 = tid - lane; g0 < at.groups << p.log_join; g0 += NT) {
+            const int g = (g0 + lane) >> p.log_join;
+            const bool here = g < at.groups && c < p.g.per;
+            float2 t = here ? s_all[g * p.g.per + c] : make_float2(0.0f, 0.0f);
+            t.x = lane_sum(t.x, lanes);
+            t.y = lane_sum(t.y, lanes);
+            if (here && c == 0) finish(g, t);
+        }
     }
     __syncthreads();
     if (at.mine > 0) {
@@ -614,6 +631,7 @@ cudaError_t launch_slab(GnBackParams p, const GnProblem &q, const GnSlab &c, cud
     p.g = gn_grid(q.S, q.C, q.groups, TYPE, c.Ft, c.R, 1 << c.log_cs, c.RL);
     p.log_cs = c.log_cs;
     p.M = c.M;
+    while (p.log_join < 5 && (1 << p.log_join) < p.g.per) ++p.log_join;
     p.sums = static_cast<float2 *>(q.workspace);
     const cudaError_t e = ready(gn_back_slab_kernel<TYPE, CKPT, UNI>, c.smem);
     if (e != cudaSuccess) return e;

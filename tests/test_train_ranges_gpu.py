@@ -479,3 +479,31 @@ def test_gradients_of_narrow_rows_take_about_as_long_as_of_wide_ones():
                 ops.ln_modulate_backward(dy, x, scale, saved, dres=dres)
         times.append(device_us(graph.replay))
     assert times[0] < 1.8 * times[1], times
+
+
+@pytest.mark.parametrize("per", [1, 2, 3, 4, 7, 8, 12, 16, 17, 32, 33, 40])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_gradients_of_small_images_in_groups_of_any_width(per, dtype):
+    """In one launch: lanes of a warp a group, or a warp; an image's are its own."""
+    groups = 8 if per > 4 else 40
+    for N, S in ((5, 9), (2, 200)):
+        x, w, b, s, t, dy = gn_case(N, S, groups * per, dtype, True)
+        check_gn_case(x, groups, w, b, s, t, dy, False)
+        saved = ops.group_norm_save(x, groups, w, b, EPS, checkpoint=False)[1]
+        got = ops.group_norm_backward(dy, x, groups, w, b, saved)[0]
+        one = ops.group_norm_backward(dy[1:2], x[1:2], groups, w, b, (saved[0][1:2], None, None))[0]
+        assert torch.equal(one, got[1:2])
+
+
+def test_gradients_in_groups_of_one_channel_take_less_than_torch():
+    N, S, C = 15184, 2, 200
+    x, w, b, _, _, dy = gn_case(N, S, C, FP32, False)
+    saved = ops.group_norm_save(x, C, w, b, EPS, checkpoint=False)[1]
+
+    def plain():
+        n = (x - saved[0][:, None, :, 0]) * saved[0][:, None, :, 1]
+        g = dy * w
+        dx = saved[0][:, None, :, 1] * (g - g.mean(1, keepdim=True) - n * (g * n).mean(1, keepdim=True))
+        return dx, (dy * n).sum((0, 1)), dy.sum((0, 1))
+
+    assert device_us(lambda: ops.group_norm_backward(dy, x, C, w, b, saved)) < device_us(plain)
