@@ -347,7 +347,8 @@ constexpr int kSlabCluster = 3; // log2 of the largest portable cluster
 constexpr int64_t kSlabRows = 64 * 1024, kSlabRoom = 80 * 1024;
 
 // bytes: of a fragment in shared memory; extra: further bytes per thread; fill: a
-// slab of fewer fragments than that is made wider.
+// slab of fewer fragments than that is made wider.  A warp has up to 32 (65536 images
+// of [1, 64] 114 us with two, 68 so).
 // Segments of 128 bytes of a row where such slabs fit, else of 64 (of 32 they took
 // 17.6 us for a [1, 128 x 128, 512] image, the passes 11.7); as few CTAs, and as
 // few threads of eight fragments, as do: many small ones did better for one image
@@ -366,7 +367,7 @@ inline GnSlab gn_slab(int64_t S, int64_t C, int64_t groups, int type, bool check
         int log_cs = 0;
         while (log_cs < kSlabCluster && (2 << log_cs) <= S && S * Ft * bytes > (kSlabRows << log_cs)) ++log_cs;
         const int64_t rows = (S + (1 << log_cs) - 1) >> log_cs;
-        int threads = 64;
+        int threads = rows * Ft <= 32 && (fill > 0 || E * Ft <= 32) ? 32 : 64; // (a channel each in the gradients)
         while (threads < 512 && (threads < Ft || rows * Ft > threads * (threads < 256 ? 8 : 16))) threads *= 2;
         const int64_t RL = threads / Ft, M = (rows + RL - 1) / RL;
         const int64_t smem = M * threads * bytes + (int64_t)threads * extra + E * Ft * 48;

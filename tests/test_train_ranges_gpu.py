@@ -507,3 +507,36 @@ def test_gradients_in_groups_of_one_channel_take_less_than_torch():
         return dx, (dy * n).sum((0, 1)), dy.sum((0, 1))
 
     assert device_us(lambda: ops.group_norm_backward(dy, x, C, w, b, saved)) < device_us(plain)
+
+
+@pytest.mark.parametrize("N,S,C,groups", [(47088, 1, 112, 112), (300000, 7, 8, 4), (65536, 1, 64, 8)])
+def test_many_images_of_a_warp_take_less_than_torch(N, S, C, groups):
+    """Images of up to 32 fragments in CTAs of two warps took up to 1.2 times as long as these operations."""
+    x, w, b, _, _, _ = gn_case(N, S, C, FP16, False)
+
+    def plain():
+        v = x.float().unflatten(2, (groups, -1))
+        d = v - v.mean((1, 3), keepdim=True)
+        n = (d * (d.square().mean((1, 3), keepdim=True) + EPS).rsqrt()).flatten(2)
+        z = n * w.float() + b.float()
+        return (z / (1 + (-z).exp())).to(x.dtype)
+
+    assert device_us(lambda: ops.group_norm(x, groups, w, b, EPS, act="silu")) < device_us(plain)
+
+
+@pytest.mark.parametrize("N,S,C,groups", [(3000, 2, 16, 16), (1000, 1, 24, 3), (500, 4, 32, 4), (700, 3, 8, 1), (300, 8, 32, 1)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_images_of_a_warp(N, S, C, groups, dtype):
+    x, w, b, s, t, dy = gn_case(N, S, C, dtype, True)
+    g = groups
+    for ckpt in (True, False) if C % 32 == 0 else (False,):
+        k = dict(act="silu", scale=s, shift=t)
+        y, saved = ops.group_norm_save(x, g, w, b, 0.1, checkpoint=ckpt, **k)
+        want, st, ey, est = ref.gn_forward(x, g, w, b, 0.1, "silu", s, t)
+        ref.assert_near(y, want, ey, "y")
+        ref.assert_near(saved[0], st, est, "stats")
+        got = ops.group_norm_backward(dy, None if ckpt else x, g, w, b, saved, **k)
+        v = ref.restore(*saved[1:]) if ckpt else x.double()
+        want, err = ref.gn_backward(dy, v, g, w, b, saved[0], "silu", s, t)
+        for a, u, e, name in zip(got, want, err, ("dx", "dweight", "dbias", "dscale", "dshift")):
+            ref.assert_near(a, u, e, name)
