@@ -540,3 +540,76 @@ def test_images_of_a_warp(N, S, C, groups, dtype):
         want, err = ref.gn_backward(dy, v, g, w, b, saved[0], "silu", s, t)
         for a, u, e, name in zip(got, want, err, ("dx", "dweight", "dbias", "dscale", "dshift")):
             ref.assert_near(a, u, e, name)
+
+
+# ------------------------------------------------------------------ streams and graphs
+
+def calls_of_the_ranges():
+    """Calls that take the forms for narrow rows, short batches, many images and no positions."""
+    x, scale, saved, dy, dres = ln_back_case(700, 2, 40, True, True)
+    u, w, b, s, t, du = gn_case(600, 2, 64, BF16, True)
+    kept = ops.group_norm_save(u, 8, w, b, EPS, act="silu", scale=s, shift=t)[1]
+    none = u[:, :0]
+    small, sw, sb, _, _, ds = gn_case(3, 30, 40, BF16, False)
+    keep = ops.group_norm_save(small, 40, sw, sb, EPS, checkpoint=False)[1]
+    wide = ln_back_case(20, 9, 4096, True, False)
+    return [lambda: ops.ln_modulate_save(x, scale, scale, EPS)[0],
+            lambda: ops.ln_modulate_backward(dy, None, scale, saved, dres=dres),
+            lambda: ops.ln_modulate_backward(wide[3], None, wide[1], wide[2]),
+            lambda: ops.group_norm(u, 8, w, b, EPS, act="silu", scale=s, shift=t),
+            lambda: ops.group_norm_backward(du, None, 8, w, b, kept, act="silu", scale=s, shift=t),
+            lambda: ops.group_norm_backward(none, none, 8, w, b, (kept[0], None, None), scale=s, shift=t),
+            lambda: ops.group_norm_backward(ds, small, 40, sw, sb, keep)]
+
+
+def tensors(v):
+    return [v] if isinstance(v, torch.Tensor) else [t for t in v if t is not None]
+
+
+def test_the_ranges_ends_on_streams_and_in_graphs():
+    """The same bits on three streams at once, and from two graphs replayed in turn."""
+    calls = calls_of_the_ranges()
+    want = [tensors(f()) for f in calls]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(3)], []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append([tensors(f()) for f in calls])
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = [tensors(f()) for f in calls]
+        graphs.append((graph, outs))
+    for _ in range(2):
+        for _, outs in graphs:
+            for run in outs:
+                for v in run:
+                    v.fill_(3)
+        for graph, _ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        got += [[[v.clone() for v in run] for run in outs] for _, outs in graphs]
+    for run in got:
+        for a, b in zip(run, want):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_a_call_follows_what_the_stream_does_before_it():
+    """Zeros for no positions, and short forms, on inputs that the kernel before still writes."""
+    x, scale, saved, dy, _ = ln_back_case(20000, 1, 64, False, False)
+    want = tensors(ops.ln_modulate_backward(dy, x, scale, saved))
+    y = ops.ln_modulate_save(x, scale, scale, EPS)[0]
+    src = [dy.clone(), x.clone(), scale.clone()]
+    for _ in range(5):
+        for v in (dy, x, scale):
+            v.fill_(float("nan"))
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200000)
+        for v, k in zip((dy, x, scale), src):
+            v.copy_(k)
+        a = ops.ln_modulate_save(x, scale, scale, EPS)[0]
+        b = tensors(ops.ln_modulate_backward(dy, x, scale, saved))
+        assert torch.equal(a, y) and all(torch.equal(u, v) for u, v in zip(b, want))
