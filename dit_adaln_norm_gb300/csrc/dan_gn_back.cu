@@ -11,10 +11,11 @@
 // the L2), and writes dx.  For several images one more (for over 256, a few) adds
 // their shares of dweight and dbias.
 //
-// Large images are bound by memory: at [1, 512 x 512, 256] bf16 the sums take 46 us
-// (5.8 TB/s), dx 57 (6.8 TB/s with what the L2 still holds); batches of images of
-// some MB by their instructions ([16, 64 x 64, 320] from checkpoints: 25 and 20 us,
-// half the issue slots).
+// Large images are bound by memory: at [1, 512 x 512, 256] bf16 the sums take 45 us
+// (268 MB read from DRAM, 6.0 TB/s), dx 58 (403 MB asked for and stored, 7.0 TB/s;
+// of them 356 in DRAM, 6.2 TB/s, the last stores still lying in the L2); both by ncu's
+// clock, cold.  Batches of images of some MB are bound by their instructions
+// ([16, 64 x 64, 320] from checkpoints: 25 and 20 us, half the issue slots).
 //
 // In the loops n = (x - mean) * rstd appears as t = x - mean, with rstd in the
 // factors of a channel: z = t * (a * rstd) + b, s1 = rstd * sum dz * t.
@@ -445,7 +446,11 @@ __global__ void __launch_bounds__(256) gn_zeros_kernel(const GnBackParams p, int
 // One launch, one read of dy and x: a cluster holds a slab (whole groups of an
 // image) of both in its CTAs' shared memory.  Each thread copies its own
 // fragments there and nobody else reads them; the channels' sums are joined in
-// the CTA, then over the cluster, each CTA for itself in the same order.
+// the CTA, then over the cluster, each CTA for itself in the same order.  From x, one
+// image and 16, in us: [8 x 8, 1280] 5.3 and 7.7 (passes 8.6 and 12.0), [16 x 16, 1280]
+// 7.0 and 18.7 (8.9 and 19.2), [32 x 32, 640] 7.6 and 38 (9.6 and 25: many large slabs
+// lose, of 13 to 16 warps an SM, and which form it is may not follow the batch).
+// Bound by the chain of latencies, of many images by their instructions.
 template <int TYPE, bool CKPT, bool UNI>
 __global__ void __launch_bounds__(512, 1) gn_back_slab_kernel(const GnBackParams p)
 {

@@ -61,7 +61,15 @@ struct LnBackCut {
     int K, R, W, L;
 };
 // A warp per row up to five fragments a lane; else teams of up to eight warps,
-// several rows at a time where the registers last.
+// several rows at a time where the registers last.  Replayed, in us, 16M elements from
+// checkpoints and from rows with dres (floor 12 and 19), this cut and the next best:
+//    264 (K 2)  27 29   K 1  44 44        2048 (K 2, R 4)  22 26   K 4  21 26
+//    520 (K 3)  25 28   K 2  31 32        2056 (K 3, R 2)  28 29   K 5  26 28   K 2  32 32
+//   1032 (K 5)  22 27   K 3  28 29        3072 (K 3, R 2)  22 27   K 2  25 27
+//   1288 (K 2, R 4)  29 29   K 3  24 28   4096 (K 2, R 4)  24 28   K 4  23 27
+//   4104 (K 4)  35 37   K 5  27 30        8192 (K 4)  26 31   K 5  28 31
+// Several rows a warp, 100000 rows of 8 and of 128 columns: 5.5 and 21 us, a warp a
+// row 27 and 33.
 inline LnBackCut ln_back_cut(int F)
 {
     LnBackCut c;

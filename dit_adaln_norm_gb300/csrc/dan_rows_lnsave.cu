@@ -17,9 +17,11 @@
 //    four, 64, they spill).
 // With checkpoints, row kernel against this one: 593750 rows of 64 columns 1891 and
 // 57 us (floor 29), 16000 of 264 59.0 and 14.2 (3.2), 16000 of 1000 78.4 and 24.0
-// (12); one row of 8 to 1000 columns 4.6 to 6.5 and 2.1 to 3.1.  Rows of 1024 are
-// whole: the row kernel folds them without divisions, 7.2 us for 4216 of them where
-// this one takes 8.1.
+// (12); one row of 8 to 1000 columns 4.6 to 6.5 and 2.1 to 3.1.  Bound by the issue of
+// instructions (64 to 73% of the slots): Welford's chain takes six an element, the
+// store and the codes as many, and where L or 32 J is not all of a row's fragments
+// the other lanes' are for nothing.  Rows of 1024 are whole: the row kernel folds
+// them without divisions, 7.2 us for 4216 of them where this one takes 8.1.
 #include "dan_rows.cuh"
 
 namespace dan {

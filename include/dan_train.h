@@ -110,7 +110,7 @@ int dan_can_use_ln_modulate_backward(const dan_bf16 *dy, const dan_bf16 *x, cons
  * S < 2^31, N < 2^28, N * groups < 2^31.  N == 0 or S == 0 launches nothing.
  * An image is one CTA's work at least (2 to 3 ns each on a GB300): hundreds of
  * thousands of images of some ten values each are better left to elementary
- * operations (882723 of 24 values take 2.2 ms, 1.0 so).
+ * operations (882723 of 24 bf16 values take 2.2 ms, 0.6 so).
  * workspace: dan_group_norm_workspace(...) bytes, on the terms of
  * dan_ln_modulate_backward's; 0 bytes where a call needs none. */
 typedef enum { DAN_BF16 = 0, DAN_FP16 = 1, DAN_FP32 = 2 } dan_type;
