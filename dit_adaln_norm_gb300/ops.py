@@ -775,13 +775,15 @@ def group_norm_save(x, groups: int, weight, bias, eps: float, act=None, scale=No
     return _group_norm(x, groups, weight, bias, eps, act, scale, shift, out, True, checkpoint)
 
 
-def group_norm_backward(dy, x, groups: int, weight, bias, saved, act=None, scale=None, shift=None, dx=None):
+def group_norm_backward(dy, x, groups: int, weight, bias, saved, act=None, scale=None, shift=None, dx=None,
+                        dscale=None, dshift=None):
     """The gradients of ``group_norm_save`` (include/dan_train.h).
 
     dy like the forward pass's x; x that input, or None to take it from the
-    checkpoint in ``saved``; the others as there.  dx may be dy itself.  Returns
-    (dx, dweight, dbias, dscale, dshift), each in the type of what it is the
-    gradient of, None where that is."""
+    checkpoint in ``saved``; the others as there.  dx may be dy itself; dscale,
+    dshift [N, C] (or [C] when N == 1): views that share one image stride, e.g. of
+    the embedding's gradient.  Returns (dx, dweight, dbias, dscale, dshift), each in
+    the type of what it is the gradient of, None where that is."""
     N, S, C = _images(dy, "dy")
     device, dtype, shape = dy.get_device(), dy.dtype, dy.shape
     groups, act = int(groups), _act(act)
@@ -803,14 +805,21 @@ def group_norm_backward(dy, x, groups: int, weight, bias, saved, act=None, scale
         dx = torch.empty_like(dy)
     else:
         _like(dx, "dx", dtype, shape, device, "dy")
-    dweight = dbias = dscale = dshift = None
+    dweight = dbias = None
     if weight is not None:
         dweight, dbias = _two((C,), weight.dtype, dy.device)
-    if scale is not None:
+    gs = C
+    if dscale is not None or dshift is not None:
+        if dscale is None or dshift is None:
+            raise ValueError("dscale and dshift: expected both or neither")
+        if scale is None:
+            raise ValueError("dscale and dshift: there is no scale and shift")
+        gs = _pair(dscale, dshift, ("dscale", "dshift"), dtype, N, C, device, "dy")
+    elif scale is not None:
         dscale, dshift = _two((N, C), dtype, dy.device)
     size = _bytes("dan_group_norm_backward_workspace", device, N, S, C, groups, _TYPES[dtype], 1 if x is None else 0)
     work = torch.empty(size, dtype=_U8, device=dy.device) if size else None
     _on(device, "dan_group_norm_backward", dy.data_ptr(), at[0], _TYPES[dtype], at[1], at[2], stats.data_ptr(),
         _ptr(weight), _ptr(bias), ptype, _ptr(scale), _ptr(shift), vs, act, dx.data_ptr(), _ptr(dweight),
-        _ptr(dbias), _ptr(dscale), _ptr(dshift), C, N, S, C, groups, _ptr(work), size)
+        _ptr(dbias), _ptr(dscale), _ptr(dshift), gs, N, S, C, groups, _ptr(work), size)
     return dx, dweight, dbias, dscale, dshift

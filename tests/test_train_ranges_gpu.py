@@ -613,3 +613,38 @@ def test_a_call_follows_what_the_stream_does_before_it():
         a = ops.ln_modulate_save(x, scale, scale, EPS)[0]
         b = tensors(ops.ln_modulate_backward(dy, x, scale, saved))
         assert torch.equal(a, y) and all(torch.equal(u, v) for u, v in zip(b, want))
+
+
+@pytest.mark.parametrize("N,S,C,groups", [(3, 40, 64, 8), (2, 9000, 320, 32), (300, 1, 96, 3), (4, 0, 64, 8), (1, 70, 32, 4)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_group_norm_gradients_into_slices(N, S, C, groups, dtype):
+    """dscale and dshift as slices of one embedding's gradient, the rest of it left as it was."""
+    x, w, b, s, t, dy = gn_case(N, S, C, dtype, True)
+    saved = ops.group_norm_save(x, groups, w, b, EPS, act="silu", scale=s, shift=t, checkpoint=False)[1]
+    k = dict(act="silu", scale=s, shift=t)
+    want = ops.group_norm_backward(dy, x, groups, w, b, saved, **k)
+    demb = torch.full((N, 5 * C), 77, dtype=dtype, device="cuda")
+    a, c = demb[:, 3 * C:4 * C], demb[:, C:2 * C]
+    got = ops.group_norm_backward(dy, x, groups, w, b, saved, dscale=a, dshift=c, **k)
+    assert got[3] is a and got[4] is c and all(torch.equal(u, v) for u, v in zip(got, want))
+    rest = [i for i in range(5 * C) if not (C <= i < 2 * C or 3 * C <= i < 4 * C)]
+    assert bool((demb[:, rest] == 77).all())
+
+
+def test_group_norm_gradients_into_slices_refuse():
+    x, w, b, s, t, dy = gn_case(2, 10, 64, BF16, True)
+    saved = ops.group_norm_save(x, 8, w, b, EPS, scale=s, shift=t, checkpoint=False)[1]
+    d = torch.zeros((2, 256), dtype=BF16, device="cuda")
+    f = lambda scale=s, shift=t, **k: ops.group_norm_backward(dy, x, 8, w, b, saved, scale=scale, shift=shift, **k)  # noqa: E731
+    for bad in (dict(dscale=d[:, :64]), dict(dshift=d[:, :64]), dict(dscale=d[:, :64], dshift=d[:, :32]),
+                dict(dscale=d[:, :64], dshift=torch.zeros_like(d[:, :64])),
+                dict(scale=None, shift=None, dscale=d[:, :64], dshift=d[:, 64:128])):
+        with pytest.raises(ValueError):
+            f(**bad)
+    with pytest.raises(TypeError):
+        f(dscale=d[:, :64].float(), dshift=d[:, 64:128].float())
+    with pytest.raises(ops.DanError):
+        f(dscale=d[:, :64], dshift=d[:, 32:96])               # they overlap
+    with pytest.raises(ops.DanError):
+        f(dscale=d[:, 4:68], dshift=d[:, 128:192])            # not on 16 bytes
+    assert not d.any()
